@@ -308,6 +308,132 @@ iq_status iq_mx_gemm(const iq_desc* d, const void* codes_w, const void* scales_w
 iq_status iq_mxw_gemm(const iq_desc* d, const void* codes, const void* scales, const void* x, int32_t x_dtype,
                       int64_t n1, float* z, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The feed-forward half of a transformer layer, around the quantized
+ * weights: layer norm, the gate and up projections with their activation,
+ * and the products of a few tokens with packed 4-bit weights.  A model
+ * trains with the BF16 forms, quantizes its weights with iq_quantize and
+ * answers with the packed ones.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Layer norm over the rows of x [rows, cols]:
+ *   mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   y = (x - mean) * rstd * weight + bias.
+ * Only d->in_dtype, rows, cols and ld_in are used.  x has row stride ld_in;
+ * y is dense [rows, cols] of x's type.
+ *   param_dtype  iq_dtype of weight and bias
+ *   weight, bias [cols]; NULL stands for ones / zeros
+ *   mean, rstd   float32 [rows]; NULL where they are not wanted
+ * Any cols >= 1 and any alignment that the element types need are accepted:
+ * rows of whole 16-byte words (base addresses, ld_in and cols) take vector
+ * loads, others single elements.  Statistics are held in FP32.  A NaN or an
+ * infinity makes its whole row NaN.  eps must be finite and >= 0.
+ */
+iq_status iq_layer_norm(const iq_desc* d, const void* x, const void* weight, const void* bias,
+                        int32_t param_dtype, float eps, void* y, float* mean, float* rstd, hipStream_t stream);
+
+/*
+ * Its backward pass.  With n = (x - mean) * rstd and a = dy * weight:
+ *   dx      = rstd * (a - sum a / cols - n * sum (a n) / cols)
+ *   dweight = sum over rows of dy * n,   dbias = sum over rows of dy
+ * x as above; dy and dx dense [rows, cols] of x's type; mean and rstd as
+ * iq_layer_norm wrote them; dweight and dbias [cols] of param_dtype.
+ * dx, dweight and dbias may each be NULL; weight NULL stands for ones.
+ * Row sums are added in FP32 in an order fixed by the shape, so every call
+ * returns the same bits.  rows == 0 writes zero gradients.
+ *   workspace  iq_layer_norm_workspace_bytes(d) bytes, 256-byte aligned,
+ *              of any content; may be NULL where dweight and dbias are.
+ */
+iq_status iq_layer_norm_backward(const iq_desc* d, const void* x, const void* dy, const void* weight,
+                                 int32_t param_dtype, const float* mean, const float* rstd, void* dx, void* dweight,
+                                 void* dbias, void* workspace, hipStream_t stream);
+size_t iq_layer_norm_workspace_bytes(const iq_desc* d);
+
+typedef enum {
+    IQ_ACT_SILU = 0,     /* g / (1 + e^-g) */
+    IQ_ACT_GELU = 1,     /* g (1 + erf(g / sqrt 2)) / 2 */
+    IQ_ACT_GELU_TANH = 2 /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+} iq_act;
+
+/* A gated block: `tokens` rows of x, `cols` input features, `features`
+ * rows of each weight. */
+typedef struct {
+    int32_t act;      /* iq_act */
+    int32_t dtype;    /* iq_dtype of every operand: IQ_BF16 */
+    int64_t tokens, cols, features;
+    int64_t ld_x;     /* row stride of x, in elements */
+    uint32_t flags;   /* 0 */
+    uint32_t reserved;
+} iq_gated_desc;
+
+/*
+ * The gate and up projections, the activation and the product in one kernel:
+ *   g = x w_gate^T, u = x w_up^T, h = act(g) * u.
+ * x [tokens, cols] with row stride ld_x, w_gate and w_up dense
+ * [features, cols], h dense [tokens, features], all BF16 and 16-byte
+ * aligned; cols, features and ld_x multiples of 8 (IQ_EINVAL; IQ_EALIGN
+ * for ld_x), cols and features at most 2^20, tokens below 2^31
+ * (IQ_EUNSUPPORTED).  Sums are held in FP32 and g and u are not rounded
+ * before h is.
+ *   saved  NULL, or iq_gated_saved_bytes(d) bytes, 16-byte aligned, that
+ *          receive what iq_gated_backward needs: g and u in FP32.  (Rounded
+ *          to BF16 they would add an error of the gradients' own rounding.)
+ */
+iq_status iq_gated_forward(const iq_gated_desc* d, const void* x, const void* w_gate, const void* w_up, void* h,
+                           void* saved, hipStream_t stream);
+
+/*
+ * Its backward pass, from dh dense [tokens, features]:
+ *   dg = dh * u * act'(g), du = dh * act(g)     (FP32, rounded once to BF16)
+ *   dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x
+ * dx dense [tokens, cols], dw_gate and dw_up dense [features, cols], BF16.
+ * dx, and the pair dw_gate, dw_up, may be NULL.  x is read only for the
+ * weights' gradients and w_gate, w_up only for dx.
+ *   workspace  iq_gated_workspace_bytes(d) bytes, 256-byte aligned, of any
+ *              content.
+ * Sums are FP32 in an order fixed by the shape.  tokens == 0 writes zero
+ * weight gradients.
+ */
+iq_status iq_gated_backward(const iq_gated_desc* d, const void* dh, const void* x, const void* w_gate,
+                            const void* w_up, const void* saved, void* dx, void* dw_gate, void* dw_up,
+                            void* workspace, hipStream_t stream);
+size_t iq_gated_saved_bytes(const iq_gated_desc* d);
+size_t iq_gated_workspace_bytes(const iq_gated_desc* d);
+
+/*
+ * A few tokens times packed 4-bit weights, the weights read once:
+ *   z[t, j] = sum_k x[t, k] w[j, k]
+ * with the weights of d (IQ_INT4, IQ_NVFP4 or IQ_MXFP4, IQ_PER_BLOCK; N0 =
+ * d->rows, K = d->cols), laid out as iq_quantize writes them; K a multiple
+ * of 32 (IQ_EINVAL).  global_scale is NVFP4's (ignored otherwise).
+ *   x        BF16 token-major [n1, K], 16-byte aligned (x_dtype IQ_BF16,
+ *            else IQ_EUNSUPPORTED), 1 to 64 tokens (more: IQ_EUNSUPPORTED;
+ *            many tokens go through iq_dequantize and a matrix product)
+ *   z        z_dtype [n1, N0] token-major, ready to be the next product's x
+ * Weights enter the matrix cores exactly (NVFP4 without the global scale,
+ * INT4 without the group scale, as 4 a + b with a in [-2, 1], b in [0, 3])
+ * and are summed in FP32: before z's own rounding |z - exact| <=
+ * (2 K + 8) 2^-24 sum_k |x| m, where m is |w|, for INT4 |w| plus six group
+ * scales.  MXFP4 scale bytes of 255 and NVFP4 ones of 0x7F or 0xFF are NaN
+ * and make their row's outputs NaN.
+ * d->in_dtype and d->ld_in are ignored.  n1 == 0 or N0 == 0 is legal and
+ * writes nothing, K == 0 writes zeros.  No workspace.
+ */
+iq_status iq_packed_gemv(const iq_desc* d, const void* codes, const void* scales, const float* global_scale,
+                         const void* x, int32_t x_dtype, int64_t n1, void* z, int32_t z_dtype, hipStream_t stream);
+
+/*
+ * The gated block for a few tokens with both weights packed, one launch:
+ *   h[t, j] = act(sum_k x[t, k] wg[j, k]) * sum_k x[t, k] wu[j, k]
+ * Both weights share d; other rules as for iq_packed_gemv.  h is h_dtype
+ * [n1, N0] token-major.
+ */
+iq_status iq_packed_gated(const iq_desc* d, int32_t act, const void* codes_gate, const void* scales_gate,
+                          const float* global_gate, const void* codes_up, const void* scales_up,
+                          const float* global_up, const void* x, int32_t x_dtype, int64_t n1, void* h,
+                          int32_t h_dtype, hipStream_t stream);
+
 const char* iq_status_str(iq_status s);
 int iq_abi_version(void);
 

@@ -3,16 +3,19 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(_HERE)
-SOURCES = [os.path.join(_HERE, "csrc", "iq_kernels.hip"), os.path.join(_HERE, "csrc", "iq_api.cpp")]
+SOURCES = [os.path.join(_HERE, "csrc", name) for name in
+           ("iq_kernels.hip", "iq_api.cpp", "iq_norm.hip", "iq_packed.hip", "iq_gated.hip", "iq_ffn_api.cpp")]
 OUT = os.path.join(_HERE, "libiq.so")
 BENCH_SOURCES = [os.path.join(_HERE, "csrc", "bench_copy.hip")]
 BENCH_OUT = os.path.join(_HERE, "libiq_bench.so")
 
 HIPCC_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # no FMA contraction: x - s*q and the statistics must round as written
     "-ffp-contract=off",
     # no packed FP32 (v_pk_fma_f32 / v_pk_mul_f32 / v_pk_add_f32) in device code
@@ -21,9 +24,7 @@ HIPCC_FLAGS = [
 ]
 
 
-def _hipcc(sources, out, verbose):
-    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    cmd = [hipcc, *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", out + ".tmp", *sources]
+def _run(cmd, verbose):
     r = subprocess.run(cmd, capture_output=True, text=True)
     noise = "'-packed-fp32-ops' is not a recognized feature"
     msgs = [ln for ln in (r.stdout + r.stderr).splitlines() if noise not in ln]
@@ -31,6 +32,18 @@ def _hipcc(sources, out, verbose):
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
+
+
+def _hipcc(sources, out, verbose):
+    """Compile every source to an object of its own, a few at a time, and link them."""
+    hipcc = [os.environ.get("HIPCC", "/opt/rocm/bin/hipcc"), *HIPCC_FLAGS]
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, os.path.basename(src) + ".o") for src in sources]
+        compiles = [[*hipcc, "-I", os.path.join(ROOT, "include"), "-c", "-o", obj, src]
+                    for src, obj in zip(sources, objects)]
+        with ThreadPoolExecutor(4) as pool:
+            list(pool.map(lambda cmd: _run(cmd, verbose), compiles))
+        _run([*hipcc, "-shared", "-o", out + ".tmp", *objects], verbose)
     os.replace(out + ".tmp", out)
     return out
 

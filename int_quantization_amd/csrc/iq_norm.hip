@@ -1,0 +1,379 @@
+// Layer norm for gfx950 (MI355X), forward and backward.
+//
+//   mean = sum x / C, r = 1 / sqrt(sum (x - mean)^2 / C + eps), n = (x - mean) r
+//   y  = n w + b
+//   dx = r (a - sum a / C - n sum (a n) / C),  a = dy w
+//   dw = sum over rows of dy n,  db = sum over rows of dy
+//
+// HBM bounds both passes: the forward reads x and writes y, the backward
+// reads x and dy and writes dx.  A row is therefore held in registers
+// between its statistics and its output, and read once.  The variance is
+// taken about the mean, not as a difference of squares, so that an offset
+// much larger than the spread costs no digits.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "iq_ffn_launch.h"
+#include "iq_launch.h"
+
+namespace iqk {
+namespace {
+
+typedef uint32_t u4v __attribute__((ext_vector_type(4)));
+typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float as_f(uint32_t u) { return __uint_as_float(u); }
+
+// FP32 to BF16 bits, to nearest even; NaN stays NaN.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    typedef __bf16 b2v __attribute__((ext_vector_type(2)));
+    const b2v v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+template <int T> struct Elem;
+template <> struct Elem<D_F32> { typedef float type; };
+template <> struct Elem<D_BF16> { typedef uint16_t type; };
+
+// N consecutive elements as FP32: 8 in 16-byte loads, or single ones.
+template <int T, int N> __device__ __forceinline__ void load_n(const void* base, int64_t i, float (&v)[N]) {
+    static_assert(N == 1 || N == 8, "a single element or whole 16-byte words");
+    if constexpr (T == D_F32) {
+        const float* p = static_cast<const float*>(base) + i;
+        if constexpr (N == 1) {
+            v[0] = *p;
+        } else {
+            const u4v a = *reinterpret_cast<const u4v*>(p), b = *reinterpret_cast<const u4v*>(p + 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) { v[k] = as_f(a[k]); v[4 + k] = as_f(b[k]); }
+        }
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(base) + i;
+        if constexpr (N == 1) {
+            v[0] = as_f((uint32_t)*p << 16);
+        } else {
+            const u4v a = *reinterpret_cast<const u4v*>(p);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) { v[2 * k] = as_f(a[k] << 16); v[2 * k + 1] = as_f(a[k] & 0xFFFF0000u); }
+        }
+    }
+}
+
+template <int T, int N> __device__ __forceinline__ void store_n(void* base, int64_t i, const float (&v)[N]) {
+    if constexpr (T == D_F32) {
+        float* p = static_cast<float*>(base) + i;
+        if constexpr (N == 1) {
+            *p = v[0];
+        } else {
+            typedef float f4v __attribute__((ext_vector_type(4)));
+            *reinterpret_cast<f4v*>(p) = f4v{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<f4v*>(p + 4) = f4v{v[4], v[5], v[6], v[7]};
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(base) + i;
+        if constexpr (N == 1)
+            *p = (uint16_t)bf16_pair(v[0], 0.f);
+        else
+            *reinterpret_cast<u4v*>(p) = u4v{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                                             bf16_pair(v[6], v[7])};
+    }
+}
+
+template <int N> __device__ __forceinline__ void load_param(const void* p, int type, int64_t i, float none, float (&v)[N]) {
+    if (!p) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = none;
+    } else if (type == D_F32) {
+        load_n<D_F32, N>(p, i, v);
+    } else {
+        load_n<D_BF16, N>(p, i, v);
+    }
+}
+
+__device__ __forceinline__ void store_param(void* p, int type, int64_t i, float v) {
+    const float one[1] = {v};
+    if (type == D_F32) store_n<D_F32, 1>(p, i, one);
+    else store_n<D_BF16, 1>(p, i, one);
+}
+
+// Sum over the wave; every lane returns it.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
+// Sums of two values over the NW waves of a workgroup, in wave order.  `red`
+// may be written again once every thread has passed a later barrier.
+template <int NW> __device__ __forceinline__ void block_sum2(float& a, float& b, float (&red)[NW][2]) {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (NW > 1) {
+        if ((threadIdx.x & 63) == 0) { red[threadIdx.x >> 6][0] = a; red[threadIdx.x >> 6][1] = b; }
+        __syncthreads();
+        a = red[0][0];
+        b = red[0][1];
+#pragma unroll
+        for (int k = 1; k < NW; ++k) { a += red[k][0]; b += red[k][1]; }
+    }
+}
+template <int NW> __device__ __forceinline__ float block_sum(float a, float (&red)[NW][2]) {
+    float b = 0.f;
+    block_sum2<NW>(a, b, red);
+    return a;
+}
+
+// One workgroup of NT threads per row (the grid strides over the rows).
+// HOLD vectors of N elements per thread stay in registers; HOLD == 0 is a
+// row of any length, read three times.
+template <int IN, int N, int NT, int HOLD>
+__global__ __launch_bounds__(NT) void k_norm(NormArgs a) {
+    constexpr int NW = NT / 64;
+    __shared__ float red[2][NW][2];
+    const int t = threadIdx.x;
+    const int64_t nv = a.cols / N;
+    const float inv = 1.f / (float)a.cols;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const int64_t xo = row * a.ld, yo = row * a.cols;
+        float v[HOLD > 0 ? HOLD : 1][N];
+        float s = 0.f;
+        auto each = [&](auto&& f) {
+            if constexpr (HOLD > 0) {
+#pragma unroll
+                for (int k = 0; k < HOLD; ++k)
+                    if (t + k * NT < nv) f(t + k * NT, v[k]);
+            } else {
+                for (int64_t c = t; c < nv; c += NT) {
+                    load_n<IN, N>(a.x, xo + c * N, v[0]);
+                    f(c, v[0]);
+                }
+            }
+        };
+        if constexpr (HOLD > 0) {
+#pragma unroll
+            for (int k = 0; k < HOLD; ++k)
+                if (t + k * NT < nv) load_n<IN, N>(a.x, xo + (int64_t)(t + k * NT) * N, v[k]);
+        }
+        each([&](int64_t, float (&e)[N]) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) s += e[i];
+        });
+        const float mean = block_sum<NW>(s, red[0]) * inv;
+        float q = 0.f;
+        each([&](int64_t, float (&e)[N]) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) { const float d = e[i] - mean; q = __builtin_fmaf(d, d, q); }
+        });
+        const float rstd = 1.f / sqrtf(block_sum<NW>(q, red[1]) * inv + a.eps);
+        each([&](int64_t c, float (&e)[N]) {
+            float w[N], b[N], y[N];
+            load_param<N>(a.weight, a.param_dtype, c * N, 1.f, w);
+            load_param<N>(a.bias, a.param_dtype, c * N, 0.f, b);
+#pragma unroll
+            for (int i = 0; i < N; ++i) y[i] = __builtin_fmaf((e[i] - mean) * rstd, w[i], b[i]);
+            store_n<IN, N>(a.y, yo + c * N, y);
+        });
+        if (t == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+    }
+}
+
+// Backward: workgroup p of the grid takes rows p, p + gridDim.x, ... and a
+// thread the same columns of every one of them, so the sums over rows stay
+// in registers until the workgroup's last row and one partial row per
+// workgroup reaches memory.
+template <int IN, int N, int NT, int HOLD>
+__global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
+    constexpr int NW = NT / 64;
+    __shared__ float red[2][NW][2];
+    const int t = threadIdx.x;
+    const int nv = (int)(a.cols / N);
+    const float inv = 1.f / (float)a.cols;
+    float w[HOLD][N], dw[HOLD][N], db[HOLD][N];
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) { w[k][i] = 0.f; dw[k][i] = 0.f; db[k][i] = 0.f; }
+        if (t + k * NT < nv) load_param<N>(a.weight, a.param_dtype, (int64_t)(t + k * NT) * N, 1.f, w[k]);
+    }
+    int odd = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, odd ^= 1) {
+        const int64_t xo = row * a.ld, yo = row * a.cols;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float x[HOLD][N], g[HOLD][N], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            if (t + k * NT < nv) {
+                load_n<IN, N>(a.x, xo + (int64_t)(t + k * NT) * N, x[k]);
+                load_n<IN, N>(a.dy, yo + (int64_t)(t + k * NT) * N, g[k]);
+            }
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            if (t + k * NT < nv) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float n = (x[k][i] - mean) * rstd, e = g[k][i] * w[k][i];
+                    x[k][i] = n;
+                    dw[k][i] = __builtin_fmaf(g[k][i], n, dw[k][i]);
+                    db[k][i] += g[k][i];
+                    g[k][i] = e;
+                    s1 += e;
+                    s2 = __builtin_fmaf(e, n, s2);
+                }
+            }
+        if (!a.dx) continue;
+        block_sum2<NW>(s1, s2, red[odd]);
+        s1 *= inv;
+        s2 *= inv;
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            if (t + k * NT < nv) {
+                float d[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) d[i] = rstd * (g[k][i] - __builtin_fmaf(x[k][i], s2, s1));
+                store_n<IN, N>(a.dx, yo + (int64_t)(t + k * NT) * N, d);
+            }
+    }
+    if (!a.dweight && !a.dbias) return;
+    float* pw = a.partial + (int64_t)blockIdx.x * 2 * a.cols;
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k)
+        if (t + k * NT < nv) {
+            store_n<D_F32, N>(pw, (int64_t)(t + k * NT) * N, dw[k]);
+            store_n<D_F32, N>(pw + a.cols, (int64_t)(t + k * NT) * N, db[k]);
+        }
+}
+
+// Rows longer than the registers hold: one pass for the sums, one for dx.
+// The sums over rows go through the partial rows in memory, each thread
+// adding to its own columns.
+template <int IN, int N, int NT>
+__global__ __launch_bounds__(NT) void k_norm_grad_long(NormGradArgs a) {
+    constexpr int NW = NT / 64;
+    __shared__ float red[2][NW][2];
+    const int t = threadIdx.x;
+    const int64_t nv = a.cols / N;
+    const float inv = 1.f / (float)a.cols;
+    const bool params = a.dweight || a.dbias;
+    float* pw = a.partial + (int64_t)blockIdx.x * 2 * a.cols;
+    int odd = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, odd ^= 1) {
+        const int64_t xo = row * a.ld, yo = row * a.cols;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        const bool first = row == blockIdx.x;
+        float x[N], g[N], w[N], s1 = 0.f, s2 = 0.f;
+        for (int64_t c = t; c < nv; c += NT) {
+            load_n<IN, N>(a.x, xo + c * N, x);
+            load_n<IN, N>(a.dy, yo + c * N, g);
+            load_param<N>(a.weight, a.param_dtype, c * N, 1.f, w);
+            float pdw[N], pdb[N];
+            if (params && !first) {
+                load_n<D_F32, N>(pw, c * N, pdw);
+                load_n<D_F32, N>(pw + a.cols, c * N, pdb);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float n = (x[i] - mean) * rstd, e = g[i] * w[i];
+                s1 += e;
+                s2 = __builtin_fmaf(e, n, s2);
+                pdw[i] = __builtin_fmaf(g[i], n, first ? 0.f : pdw[i]);
+                pdb[i] = first ? g[i] : pdb[i] + g[i];
+            }
+            if (params) {
+                store_n<D_F32, N>(pw, c * N, pdw);
+                store_n<D_F32, N>(pw + a.cols, c * N, pdb);
+            }
+        }
+        if (!a.dx) continue;
+        block_sum2<NW>(s1, s2, red[odd]);
+        s1 *= inv;
+        s2 *= inv;
+        for (int64_t c = t; c < nv; c += NT) {
+            load_n<IN, N>(a.x, xo + c * N, x);
+            load_n<IN, N>(a.dy, yo + c * N, g);
+            load_param<N>(a.weight, a.param_dtype, c * N, 1.f, w);
+            float d[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) d[i] = rstd * (g[i] * w[i] - __builtin_fmaf((x[i] - mean) * rstd, s2, s1));
+            store_n<IN, N>(a.dx, yo + c * N, d);
+        }
+    }
+}
+
+// The partial rows' sum: 64 columns per workgroup, 16 waves a sixteenth of
+// the rows each, added in row order and then in wave order.
+__global__ __launch_bounds__(1024) void k_norm_fold(const float* partial, int parts, int64_t cols, int type, void* dweight,
+                                                    void* dbias) {
+    __shared__ float red[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;      // of the 2 cols columns of a partial row
+    float s = 0.f;
+    if (c < 2 * cols)
+        for (int p = wave; p < parts; p += 16) s += partial[(int64_t)p * 2 * cols + c];
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || c >= 2 * cols) return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s += red[k][lane];
+    void* out = c < cols ? dweight : dbias;
+    if (out) store_param(out, type, c < cols ? c : c - cols, s);
+}
+
+bool words(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <int IN, int N, int NT, int HOLD> hipError_t run_norm(const NormArgs& a, hipStream_t s) {
+    k_norm<IN, N, NT, HOLD><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), NT, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int IN, int N> hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
+    const int64_t nv = a.cols / N;
+    if (nv <= 256) return run_norm<IN, N, 256, 1>(a, s);
+    if (nv <= 512) return run_norm<IN, N, 256, 2>(a, s);
+    if (nv <= 1024) return run_norm<IN, N, 256, 4>(a, s);
+    if (nv <= 2048) return run_norm<IN, N, 512, 4>(a, s);
+    return run_norm<IN, N, 512, 0>(a, s);
+}
+
+template <int IN, int N> hipError_t pick_grad(const NormGradArgs& a, unsigned grid, hipStream_t s) {
+    const int64_t nv = a.cols / N;
+    if (nv <= 256) k_norm_grad<IN, N, 256, 1><<<grid, 256, 0, s>>>(a);
+    else if (nv <= 512) k_norm_grad<IN, N, 512, 1><<<grid, 512, 0, s>>>(a);
+    else if (nv <= 1024) k_norm_grad<IN, N, 512, 2><<<grid, 512, 0, s>>>(a);
+    else if (nv <= 2048) k_norm_grad<IN, N, 1024, 2><<<grid, 1024, 0, s>>>(a);
+    else k_norm_grad_long<IN, N, 512><<<grid, 512, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Vectors of 8 where every row of every array starts on a 16-byte word.
+hipError_t launch_layer_norm(const NormArgs& a, hipStream_t s) {
+    if (a.rows == 0) return hipSuccess;
+    const bool wide = a.cols % 8 == 0 && (a.ld * (a.in_dtype == D_F32 ? 4 : 2)) % 16 == 0 && words(a.x) && words(a.y) &&
+                      words(a.weight) && words(a.bias);
+    if (a.in_dtype == D_F32) return wide ? pick_norm<D_F32, 8>(a, s) : pick_norm<D_F32, 1>(a, s);
+    return wide ? pick_norm<D_BF16, 8>(a, s) : pick_norm<D_BF16, 1>(a, s);
+}
+
+hipError_t launch_layer_norm_grad(const NormGradArgs& a, hipStream_t s) {
+    const int parts = (int)std::min<int64_t>(a.rows, kNormParts);
+    if (parts > 0) {
+        const bool wide = a.cols % 8 == 0 && (a.ld * (a.in_dtype == D_F32 ? 4 : 2)) % 16 == 0 && words(a.x) &&
+                          words(a.dy) && words(a.dx) && words(a.weight);
+        hipError_t e;
+        if (a.in_dtype == D_F32) e = wide ? pick_grad<D_F32, 8>(a, parts, s) : pick_grad<D_F32, 1>(a, parts, s);
+        else e = wide ? pick_grad<D_BF16, 8>(a, parts, s) : pick_grad<D_BF16, 1>(a, parts, s);
+        if (e != hipSuccess) return e;
+    }
+    if (a.dweight || a.dbias)
+        k_norm_fold<<<(unsigned)((2 * a.cols + 63) / 64), 1024, 0, s>>>(a.partial, parts, a.cols, a.param_dtype, a.dweight,
+                                                                      a.dbias);
+    return hipGetLastError();
+}
+
+}  // namespace iqk

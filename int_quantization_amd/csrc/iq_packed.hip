@@ -1,0 +1,308 @@
+// A few tokens against weights that are read once, for gfx950 (MI355X).
+//
+//   z[t, j] = sum_k x[t, k] w[j, k]                      one matrix
+//   h[t, j] = act(sum_k x[t, k] wg[j, k]) * sum_k x[t, k] wu[j, k]   gated
+//
+// Weights are packed in 4 bits (INT4 with an FP16 scale per 128, NVFP4 with
+// an E4M3 scale per 16 and one FP32 scale, MXFP4 with an E8M0 scale per 32)
+// or are BF16.  HBM bounds the call: a weight costs half a byte and 2 n1
+// flops, so up to 64 tokens the matrix cores have time to spare, and the
+// work per weight on the vector units is what has to be kept small.
+//
+// A workgroup takes 16 FR rows of each matrix and up to 16 NT tokens; its
+// four waves split k in steps of 128 and add their sums in LDS in wave
+// order, so every call returns the same bits.  Tokens are the MFMA's rows
+// and weight rows its columns: lane l holds weight row l % 16 at k block
+// l / 16 and receives results of that same row for tokens 4 (l / 16) .. + 3,
+// so its group scale is its own.  Codes go from memory to registers to the
+// matrix cores; only scales pass through LDS.
+//
+// Every code becomes exact BF16:
+//   E2M1   one convert per pair, the E8M0 scale applied by the convert;
+//   NVFP4  code times E4M3 has 6 significant bits: two FP32 values per
+//          convert, a product each, upper halves packed by a byte permute;
+//   INT4   a two's-complement nibble is 4 a + b, a = its upper two bits as a
+//          signed number, b = its lower two: both are E2M1 codes of halves
+//          (b: 0, 1/2, 1, 3/2; a: sign and 0, 1/2, 1), so the FP4 convert
+//          serves here too and two MFMAs add the parts.  14 instructions per
+//          8 weights, where unsigned converts and subtractions take 23.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "iq_ffn_launch.h"
+#include "iq_gate.h"
+#include "iq_launch.h"
+
+namespace iqk {
+namespace {
+
+using namespace gate;
+
+struct PackedK {
+    const uint8_t* codes[2];
+    const uint8_t* scales[2];
+    const float* gscale[2];
+    const uint16_t* x;
+    void* out;
+    float* saved;
+    int64_t ldx;
+    int32_t n0, n1, K;
+    int32_t f32_out;
+};
+
+constexpr int kStep = 128;            // k of one step: 64 code bytes per row
+constexpr int kChunkSteps = 32;       // steps whose scales are in LDS at once
+
+// Scale bytes per row and step.
+template <int FMT> constexpr int scale_bytes() { return FMT == F_INT4 ? 2 : FMT == F_NVFP4 ? 8 : FMT == F_MXFP4 ? 4 : 0; }
+
+template <int FMT> __device__ __forceinline__ int64_t row_bytes(int K) { return FMT == F_BF16W ? 2 * (int64_t)K : K / 2; }
+
+// 8 E2M1 codes times a power of two.
+__device__ __forceinline__ u4v fp4_bf16x8(uint32_t w, float sc) {
+    const bf2v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1);
+    const bf2v c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3);
+    return u4v{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
+               __builtin_bit_cast(uint32_t, d)};
+}
+
+// 8 E2M1 codes times an E4M3 scale: at most 2 + 4 significant bits, so the
+// upper half of each FP32 product is the whole of it.
+__device__ __forceinline__ u4v fp4_scaled_bf16x8(uint32_t w, float s) {
+    typedef float f2v __attribute__((ext_vector_type(2)));
+    u4v o;
+    const f2v a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 1);
+    const f2v c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 3);
+    auto pack = [&](f2v v) {
+        return __builtin_amdgcn_perm(__float_as_uint(v.y * s), __float_as_uint(v.x * s), 0x07060302u);
+    };
+    o.x = pack(a); o.y = pack(b); o.z = pack(c); o.w = pack(d);
+    return o;
+}
+
+// The upper parts of 8 two's-complement nibbles as E2M1 codes of halves.
+__device__ __forceinline__ uint32_t int4_upper(uint32_t w) {
+    const uint32_t b2 = (w >> 2) & 0x11111111u;                       // weight 4
+    const uint32_t b3 = (w >> 2) & ~(w >> 1) & 0x22222222u;           // weight -8 where b2 is clear
+    return (w & 0x88888888u) | b2 | b3;                               // sign, 10 (-2), 01 (+-1)
+}
+
+// One step's codes of one fragment, as loaded.
+template <int FMT> struct Codes { u4v v[FMT == F_BF16W ? 4 : 1]; };
+
+template <int FMT, int FR, int NT, bool GATED, int ACT>
+__global__ __launch_bounds__(256) void k_packed(PackedK a) {
+    constexpr int M = GATED ? 2 : 1;
+    constexpr int kRows = 16 * FR, SB = scale_bytes<FMT>();
+    constexpr int kPad = SB * kChunkSteps + 4;                        // row r starts r words further round the banks
+    __shared__ f4v red[4][M * FR][NT][64];
+    __shared__ __align__(16) uint8_t s_sc[SB ? M * kRows * kPad : 16];
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int i = lane & 15, h = lane >> 4;
+    const int j0 = (int)blockIdx.x * kRows, t0 = (int)blockIdx.y * 16 * NT;
+    const int steps = (a.K + kStep - 1) / kStep;
+    const int64_t rb = row_bytes<FMT>(a.K);
+
+    // Rows past n0 and tokens past n1 read the last one: their lanes feed
+    // only outputs that are not stored.
+    const uint8_t* crow[M][FR];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int f = 0; f < FR; ++f)
+            crow[m][f] = a.codes[m] + (int64_t)min(j0 + 16 * f + i, a.n0 - 1) * rb + 16 * h;
+    const uint16_t* xrow[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xrow[n] = a.x + (int64_t)min(t0 + 16 * n + i, a.n1 - 1) * a.ldx;
+
+    f4v acc[M][FR][NT];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int f = 0; f < FR; ++f)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[m][f][n] = f4v{0.f, 0.f, 0.f, 0.f};
+
+    for (int s0 = 0; s0 < steps; s0 += kChunkSteps) {
+        const int s1 = min(steps, s0 + kChunkSteps);
+        if constexpr (SB > 0) {
+            // scale bytes of the rows, whole rows of the chunk at a time
+            const int64_t per_row = FMT == F_INT4 ? a.K / 128 * 2 : FMT == F_NVFP4 ? a.K / 16 : a.K / 32;
+            const int take = (int)min((int64_t)(s1 - s0) * SB, per_row - (int64_t)s0 * SB);
+            __syncthreads();                                          // the previous chunk's are no longer read
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                for (int e = t; e < kRows * take; e += 256) {
+                    const int r = e / take, b = e - r * take;
+                    s_sc[(m * kRows + r) * kPad + b] = a.scales[m][(int64_t)min(j0 + r, a.n0 - 1) * per_row + (int64_t)s0 * SB + b];
+                }
+            __syncthreads();
+        }
+        for (int s = s0 + wave; s < s1; s += 4) {
+            // lane h's 32 elements of a packed step start at 32 h, whole or
+            // not at all; of a BF16 step, 8 elements at 32 q + 8 h
+            Codes<FMT> c[M][FR];
+            u4v xv[NT][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int k = s * kStep + (FMT == F_BF16W ? 32 * q + 8 * h : 32 * h + 8 * q);
+                const bool in = k < a.K;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    xv[n][q] = u4v{0u, 0u, 0u, 0u};
+                    if (in) xv[n][q] = *reinterpret_cast<const u4v*>(xrow[n] + k);
+                }
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+#pragma unroll
+                    for (int f = 0; f < FR; ++f) {
+                        if constexpr (FMT == F_BF16W) {
+                            c[m][f].v[q] = u4v{0u, 0u, 0u, 0u};
+                            if (in) c[m][f].v[q] = *reinterpret_cast<const u4v*>(crow[m][f] + (int64_t)s * 256 + 64 * q);
+                        } else if (q == 0) {
+                            c[m][f].v[0] = u4v{0u, 0u, 0u, 0u};
+                            if (in) c[m][f].v[0] = *reinterpret_cast<const u4v*>(crow[m][f] + (int64_t)s * 64);
+                        }
+                    }
+            }
+            const bool live = s * kStep + 32 * h < a.K;               // packed lanes past K have no scale
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int f = 0; f < FR; ++f) {
+                    const uint8_t* sc = s_sc + (m * kRows + 16 * f + i) * kPad + (s - s0) * SB;
+                    if constexpr (FMT == F_BF16W) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                acc[m][f][n] = mfma(__builtin_bit_cast(bf8v, xv[n][q]), __builtin_bit_cast(bf8v, c[m][f].v[q]),
+                                                    acc[m][f][n]);
+                    } else if constexpr (FMT == F_INT4) {
+                        const float scale = (float)*reinterpret_cast<const _Float16*>(sc);
+                        f4v part[NT];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) part[n] = f4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t w = c[m][f].v[0][q];
+                            const bf8v lo = __builtin_bit_cast(bf8v, fp4_bf16x8(w & 0x33333333u, 2.f));
+                            const bf8v up = __builtin_bit_cast(bf8v, fp4_bf16x8(int4_upper(w), 8.f));
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                part[n] = mfma(__builtin_bit_cast(bf8v, xv[n][q]), lo, part[n]);
+                                part[n] = mfma(__builtin_bit_cast(bf8v, xv[n][q]), up, part[n]);
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[m][f][n][e] = __builtin_fmaf(scale, part[n][e], acc[m][f][n][e]);
+                    } else {
+                        const uint32_t b = live ? (FMT == F_NVFP4 ? *reinterpret_cast<const uint16_t*>(sc + 2 * h) : sc[h]) : 0u;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            u4v v;
+                            if constexpr (FMT == F_NVFP4) {
+                                v = fp4_scaled_bf16x8(c[m][f].v[0][q], q < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)b, 0)
+                                                                            : __builtin_amdgcn_cvt_f32_fp8((int)b, 1));
+                            } else {
+                                // 2^(b - 127): b = 0 is the subnormal 2^-127; 255 is NaN
+                                v = fp4_bf16x8(c[m][f].v[0][q], __uint_as_float(b ? b << 23 : 0x00400000u));
+                                if (b == 255u) v = u4v{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+                            }
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                acc[m][f][n] = mfma(__builtin_bit_cast(bf8v, xv[n][q]), __builtin_bit_cast(bf8v, v), acc[m][f][n]);
+                        }
+                    }
+                }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int f = 0; f < FR; ++f)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) red[wave][m * FR + f][n][lane] = acc[m][f][n];
+    __syncthreads();
+    float gs[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) gs[m] = FMT == F_NVFP4 && a.K > 0 ? *a.gscale[m] : 1.f;
+    // thread (wave, lane): the (fragment, token tile) pairs congruent to wave
+#pragma unroll
+    for (int fn = 0; fn < FR * NT; ++fn) {
+        if (fn % 4 != wave) continue;
+        const int f = fn / NT, n = fn % NT, j = j0 + 16 * f + i;
+        if (j >= a.n0) continue;
+        f4v v[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            v[m] = (((red[0][m * FR + f][n][lane] + red[1][m * FR + f][n][lane]) + red[2][m * FR + f][n][lane]) +
+                    red[3][m * FR + f][n][lane]) * gs[m];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int tok = t0 + 16 * n + 4 * h + e;
+            if (tok >= a.n1) continue;
+            const int64_t o = (int64_t)tok * a.n0 + j;
+            float z = v[0][e];
+            if constexpr (GATED) {
+                if (a.saved) {
+                    a.saved[o] = v[0][e];
+                    a.saved[(int64_t)a.n1 * a.n0 + o] = v[1][e];
+                }
+                z = act<ACT>(z) * v[1][e];
+            }
+            if (a.f32_out) static_cast<float*>(a.out)[o] = z;
+            else static_cast<uint16_t*>(a.out)[o] = (uint16_t)bf16_pair(z, 0.f);
+        }
+    }
+}
+
+template <int FMT, int FR, int NT, bool GATED, int ACT> hipError_t run(const PackedK& k, hipStream_t s) {
+    const dim3 grid((unsigned)((k.n0 + 16 * FR - 1) / (16 * FR)), (unsigned)((k.n1 + 16 * NT - 1) / (16 * NT)));
+    k_packed<FMT, FR, NT, GATED, ACT><<<grid, 256, 0, s>>>(k);
+    return hipGetLastError();
+}
+
+template <int FMT, bool GATED, int ACT> hipError_t pick_tokens(const PackedK& k, hipStream_t s) {
+    constexpr int FR = GATED ? 1 : 2;
+    if (k.n1 <= 16) return run<FMT, FR, 1, GATED, ACT>(k, s);
+    if (k.n1 <= 32) return run<FMT, FR, 2, GATED, ACT>(k, s);
+    return run<FMT, FR, 4, GATED, ACT>(k, s);
+}
+
+template <int FMT> hipError_t pick(const PackedArgs& a, const PackedK& k, hipStream_t s) {
+    if (!a.gated) {
+        if constexpr (FMT == F_BF16W) return hipErrorInvalidValue;
+        else return pick_tokens<FMT, false, A_SILU>(k, s);
+    }
+    if (a.act == A_SILU) return pick_tokens<FMT, true, A_SILU>(k, s);
+    if (a.act == A_GELU) return pick_tokens<FMT, true, A_GELU>(k, s);
+    return pick_tokens<FMT, true, A_GELU_TANH>(k, s);
+}
+
+}  // namespace
+
+hipError_t launch_packed(const PackedArgs& a, hipStream_t s) {
+    PackedK k = {};
+    for (int m = 0; m < (a.gated ? 2 : 1); ++m) {
+        k.codes[m] = static_cast<const uint8_t*>(a.w[m].codes);
+        k.scales[m] = static_cast<const uint8_t*>(a.w[m].scales);
+        k.gscale[m] = a.w[m].global_scale;
+    }
+    k.x = static_cast<const uint16_t*>(a.x); k.out = a.out; k.saved = a.saved; k.ldx = a.ldx;
+    k.n0 = (int32_t)a.n0; k.n1 = (int32_t)a.n1; k.K = (int32_t)a.K;
+    k.f32_out = a.out_dtype == D_F32;
+    switch (a.fmt) {
+    case F_INT4: return pick<F_INT4>(a, k, s);
+    case F_NVFP4: return pick<F_NVFP4>(a, k, s);
+    case F_MXFP4: return pick<F_MXFP4>(a, k, s);
+    default: return pick<F_BF16W>(a, k, s);
+    }
+}
+
+}  // namespace iqk
