@@ -95,19 +95,23 @@ template <bool KC, int NI> struct Copy {
     }
 };
 
-// MFMA operand of rows (columns) rb .. rb + 15 at k 32 ks .. + 31: lane l has
-// row rb + l % 16 and k 32 ks + 8 (l / 16) .. + 7.
-template <bool KC> __device__ __forceinline__ bf8v fragment(const Half& t, int rb, int ks, int lane) {
-    const int i = lane & 15, h = lane >> 4;
+// MFMA operand of rows (columns) rb .. rb + 15 at k 32 ks .. + 31 of the Half
+// that starts `at` bytes into LDS object T: lane l has row rb + l % 16 and
+// k 32 ks + 8 (l / 16) .. + 7.  The address is one offset from the object,
+// not a chain of members: past a few links the compiler no longer sees which
+// object a read is from and lets it wait for copies into the others.
+template <bool KC, class T> __device__ __forceinline__ bf8v fragment(const T& t, uint32_t at, int rb, int ks, int lane) {
+    const uint32_t i = lane & 15, h = lane >> 4;
+    const char* base = reinterpret_cast<const char*>(&t);
     if constexpr (KC) {
-        return __builtin_bit_cast(bf8v, t.w[(rb + i) * 8 + ((4 * ks + h) ^ (i & 7))]);
+        return *reinterpret_cast<const bf8v*>(base + (at + (rb + i) * 128 + ((4 * ks + h) ^ (i & 7)) * 16));
     } else {
         // the transposing read gives lane i of 16 element i of the four rows
         // that its group's lanes 4 j + c name by column 4 c of row j
-        const int k = 32 * ks + 8 * h + (i >> 2), slot = (rb >> 4) ^ ((i >> 2) | ((h & 1) << 2));
-        const char* p = reinterpret_cast<const char*>(t.w) + k * 256 + slot * 32 + (i & 3) * 8;
-        const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)p);
-        const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(p + 4 * 256));
+        const uint32_t k = 32 * ks + 8 * h + (i >> 2), slot = (rb >> 4) ^ ((i >> 2) | ((h & 1) << 2));
+        const uint32_t o = at + k * 256 + slot * 32 + (i & 3) * 8;
+        const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(base + o));
+        const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(base + (o + 4 * 256)));
         return __builtin_bit_cast(bf8v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
 }
@@ -198,9 +202,9 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 2) void k_gemm(Ge
         for (int ks = 0; ks < 2; ++ks) {
             bf8v pf[4], qf[4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) pf[n] = fragment<PK>(P, row_of(n), ks, lane);
+            for (int n = 0; n < 4; ++n) pf[n] = fragment<PK>(P, 0, row_of(n), ks, lane);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) qf[m] = fragment<QK>(Q, wm * 64 + m * 16, ks, lane);
+            for (int m = 0; m < 4; ++m) qf[m] = fragment<QK>(Q, 0, wm * 64 + m * 16, ks, lane);
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -237,6 +241,208 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 2) void k_gemm(Ge
 #pragma unroll
             for (int t = 0; t < 4; t += 2) {
                 const int nb = n0 + wn * 64 + t * 16;
+                if (MODE == DX && a.parts > 1) {
+                    float* pr = in ? a.partial + ((int64_t)blockIdx.y * a.M + row) * a.N : nullptr;
+                    store_f4(pr, nb + 4 * (lane >> 4), a.N, acc[t][m]);
+                    store_f4(pr, nb + 16 + 4 * (lane >> 4), a.N, acc[t + 1][m]);
+                } else {
+                    store_pair(in ? a.out[sel] + (int64_t)row * a.N : nullptr, nb, a.N, lane, acc[t][m], acc[t + 1][m]);
+                }
+            }
+        }
+    }
+}
+
+// ---- 256 x 256 tiles ----------------------------------------------------------
+// Four waves of 128 x 128 results, one to a SIMD: the results fill 256
+// registers of a lane and every operand fragment serves 8 products, so that
+// the reads from LDS take half as long as the products.  (Waves of 64 x 64
+// read as long as they multiply.)  A lone wave hides nothing by itself, so a
+// step's instructions are laid out by hand, a few reads or copies between any
+// two groups of four products:
+//   products of k 0..31 of step s   | reads of its k 32..63
+//   wait for the copies of step s + 1, barrier
+//   products of k 32..63            | reads of k 0..31 of step s + 1,
+//                                     copies of step s + 2 over step s
+struct Tile { Half half[2]; };        // 128 rows or columns each
+
+// One wave's share of the copies of a Tile, instructions 4 wave .. + 3 of each half.
+template <bool KC> struct WideCopy {
+    uint32_t off[8];      // byte offset from the tile's first element
+    int32_t kk;           // KC: first k that the lane's words hold
+    // `left` as for Copy.  `pair`: the halves are 64 gate rows and 64 up rows
+    // each, and the wave's are from one of the two matrices.
+    __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int64_t left, bool pair) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int half = i >> 2, q = 4 * wave + (i & 3);
+            if constexpr (KC) {
+                const int r0 = 8 * q + (lane >> 3), r = pair ? 64 * half + (r0 & 63) : 128 * half + r0;
+                off[i] = r < left ? (uint32_t)(r * ld * 2) + 16u * ((lane & 7) ^ (lane >> 3)) : kOutside;
+            } else {
+                const int k = 4 * q + (lane >> 4), col = 128 * half + 8 * ((lane & 15) ^ (2 * ((k & 3) | ((k >> 1) & 4))));
+                off[i] = col < left ? (uint32_t)(k * ld * 2) + col * 2u : kOutside;
+            }
+        }
+        kk = 8 * ((lane & 7) ^ (lane >> 3));
+    }
+    // Buffer of one step from the tile's first element `base`, `left` k before
+    // the end (0: nothing is read and zeros are written): a k-strided
+    // operand's rows past k are beyond its range.
+    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint16_t* base, int left, int64_t ld) {
+        const uint32_t rows = KC ? kOutside : (uint32_t)(min(left, BK) * (int)ld * 2);
+        const int range = left <= 0 ? 0 : left >= BK ? (int)kOutside : (int)rows;
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, range, 0x00020000);
+    }
+    __device__ __forceinline__ void one(int i, __amdgpu_buffer_rsrc_t rsrc, int left, int wave, Tile& to) const {
+        const uint32_t o = !KC || kk < left ? off[i] : kOutside;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)&to.half[i >> 2].w[(4 * wave + (i & 3)) * 64], 16, o, 0, 0, 0);
+    }
+};
+
+// Four products whose sums stay where they are, in the upper half of the
+// registers: left to itself the compiler moves results between the halves in
+// every step.  It does not see inside, so the waits that the matrix cores need
+// are written out: two states from a write of an operand to its use ...
+__device__ __forceinline__ void mfma_2x2(f4v& c00, f4v& c01, f4v& c10, f4v& c11, bf8v p0, bf8v p1, bf8v q0, bf8v q1) {
+    asm volatile("s_nop 1\n"
+                 "v_mfma_f32_16x16x32_bf16 %0, %4, %6, %0\n"
+                 "v_mfma_f32_16x16x32_bf16 %1, %4, %7, %1\n"
+                 "v_mfma_f32_16x16x32_bf16 %2, %5, %6, %2\n"
+                 "v_mfma_f32_16x16x32_bf16 %3, %5, %7, %3"
+                 : "+a"(c00), "+a"(c01), "+a"(c10), "+a"(c11)
+                 : "v"(p0), "v"(p1), "v"(q0), "v"(q1));
+}
+// ... and 18 at most from the last product to a read of its result.
+__device__ __forceinline__ void settle(f4v (&acc)[8][8]) {
+    asm volatile("s_nop 15\ns_nop 15" ::: "memory");
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+        asm volatile("" : "+a"(acc[n][0]), "+a"(acc[n][1]), "+a"(acc[n][2]), "+a"(acc[n][3]), "+a"(acc[n][4]), "+a"(acc[n][5]),
+                     "+a"(acc[n][6]), "+a"(acc[n][7]));
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wide(GemmArgs a) {
+    constexpr bool PK = MODE == FWD, QK = MODE != DW;
+    constexpr int kTileN = MODE == FWD ? 128 : 256;
+    __shared__ Tile P0, P1, Q0, Q1;
+    int tn, tm;
+    if (!tile_of(a, tn, tm)) return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = wave & 1, wm = wave >> 1;
+    const int sel = MODE == DW && tm >= a.tiles_m / 2 ? 1 : 0;        // which weight's gradient
+    const int n0 = tn * kTileN, m0 = (MODE == DW ? tm - sel * (a.tiles_m / 2) : tm) * 256;
+    const int seg_steps = (a.K + BK - 1) / BK;
+    const int all = MODE == DX ? 2 * seg_steps : seg_steps;
+    const int first = MODE == DX ? (int)blockIdx.y * a.split_steps : 0;
+    const int last = MODE == DX ? min(all, first + a.split_steps) : all;
+
+    WideCopy<PK> cp;
+    WideCopy<QK> cq;
+    cp.init(wave, lane, a.ldp, (int64_t)a.N - n0, MODE == FWD);
+    cq.init(wave, lane, a.ldq, (int64_t)a.M - m0, false);
+
+    struct Source { __amdgpu_buffer_rsrc_t p, q; int left; };
+    auto source = [&](int s) {
+        const int seg = MODE == DX && s >= seg_steps ? 1 : 0;
+        const int k0 = (s - seg * seg_steps) * BK, left = s < last ? a.K - k0 : 0;
+        const uint16_t* pb = PK ? a.p[wave >= 2 ? 1 : 0] + (int64_t)n0 * a.ldp + k0 : a.p[seg] + (int64_t)k0 * a.ldp + n0;
+        const uint16_t* qb = QK ? a.q[seg] + (int64_t)m0 * a.ldq + k0 : a.q[sel] + (int64_t)k0 * a.ldq + m0;
+        return Source{WideCopy<PK>::buffer(pb, left, a.ldp), WideCopy<QK>::buffer(qb, left, a.ldq), left};
+    };
+    auto copy = [&](int i, const Source& src, Tile& P, Tile& Q) {     // i: 0 .. 15
+        if (i & 1) cq.one(i >> 1, src.q, src.left, wave, Q);
+        else cp.one(i >> 1, src.p, src.left, wave, P);
+    };
+    // row of the wave's P half that its 16-row fragment t starts at: gate
+    // features and then the same features of the up projection, or as they are
+    auto read = [&](int i, int ks, const Tile& P, const Tile& Q, bf8v (&pf)[8], bf8v (&qf)[8]) {   // i: 0 .. 15
+        if (i & 1) qf[i >> 1] = fragment<QK>(Q, wm * (uint32_t)sizeof(Half), (i >> 1) * 16, ks, lane);
+        else pf[i >> 1] = fragment<PK>(P, wn * (uint32_t)sizeof(Half), (i >> 1) * 16, ks, lane);
+    };
+
+    f4v acc[8][8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int m = 0; m < 8; ++m) acc[n][m] = f4v{0.f, 0.f, 0.f, 0.f};
+    // group g of 16: four products; a fragment is first used in a group no earlier than its read's
+    auto products = [&](int g, const bf8v (&pf)[8], const bf8v (&qf)[8]) {
+        const int n = 2 * (g >> 2), m = 2 * (g & 3);
+        mfma_2x2(acc[n][m], acc[n][m + 1], acc[n + 1][m], acc[n + 1][m + 1], pf[n], pf[n + 1], qf[m], qf[m + 1]);
+    };
+    bf8v pa[8], qa[8], pb[8], qb[8];
+    auto step = [&](int s, Tile& P, Tile& Q, const Tile& nP, const Tile& nQ) {
+#pragma unroll
+        for (int g = 0; g < 16; ++g) {
+            if (g < 8) {
+                read(2 * g, 1, P, Q, pb, qb);
+                read(2 * g + 1, 1, P, Q, pb, qb);
+            }
+            products(g, pa, qa);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0070);           // vmcnt(0), lgkmcnt(0): step s + 1 has landed, step s is read
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        const Source src = source(s + 2);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int g = 0; g < 16; ++g) {
+            read(g, 0, nP, nQ, pa, qa);
+            copy(g, src, P, Q);
+            products(g, pb, qb);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    {
+        const Source s0 = source(first), s1 = source(first + 1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) copy(i, s0, P0, Q0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) copy(i, s1, P1, Q1);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x4F70);           // vmcnt(16): this wave's copies of the first step have landed
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) read(i, 0, P0, Q0, pa, qa);
+    }
+    for (int s = first; s < last; s += 2) {           // a step past the last adds zeros
+        step(s, P0, Q0, P1, Q1);
+        step(s + 1, P1, Q1, P0, Q0);
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);               // the copies past the last step write LDS too
+    settle(acc);
+
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        const int row = m0 + wm * 128 + m * 16 + (lane & 15);
+        const bool in = row < a.M;
+        if constexpr (MODE == FWD) {
+            const int nb = n0 + wn * 64;
+            uint16_t* hr = in ? a.out[0] + (int64_t)row * a.N : nullptr;
+            float* gr = in && a.saved ? a.saved + (int64_t)row * a.N : nullptr;
+            float* ur = in && a.saved ? a.saved + ((int64_t)a.M + row) * a.N : nullptr;
+#pragma unroll
+            for (int t = 0; t < 4; t += 2) {
+                f4v h[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    store_f4(gr, nb + 16 * (t + e) + 4 * (lane >> 4), a.N, acc[t + e][m]);
+                    store_f4(ur, nb + 16 * (t + e) + 4 * (lane >> 4), a.N, acc[4 + t + e][m]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[e][j] = act<ACT>(acc[t + e][m][j]) * acc[4 + t + e][m][j];
+                }
+                store_pair(hr, nb + 16 * t, a.N, lane, h[0], h[1]);
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < 8; t += 2) {
+                const int nb = n0 + wn * 128 + t * 16;
                 if (MODE == DX && a.parts > 1) {
                     float* pr = in ? a.partial + ((int64_t)blockIdx.y * a.M + row) * a.N : nullptr;
                     store_f4(pr, nb + 4 * (lane >> 4), a.N, acc[t][m]);
@@ -302,25 +508,35 @@ __global__ __launch_bounds__(256) void k_clear(uint16_t* out, int64_t n) {
 unsigned wide_grid(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((n / 8 + 255) / 256, 8192)); }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Tiles of 256 where they fill the GPU.
+bool wide_tiles(int64_t N, int64_t M, int mode) {
+    return ceil_div(N, mode == FWD ? 128 : 256) * ceil_div(M, 256) * (mode == DW ? 2 : 1) >= 224;
+}
+
 hipError_t clear(void* p, int64_t n, hipStream_t s) {
     if (!p || n == 0) return hipSuccess;
     k_clear<<<wide_grid(n), 256, 0, s>>>(static_cast<uint16_t*>(p), n);
     return hipGetLastError();
 }
 
-template <int MODE, int ACT> hipError_t run_gemm(GemmArgs& a, int64_t tiles_n, int64_t tiles_m, hipStream_t s) {
+template <int MODE, int ACT> hipError_t run_gemm(GemmArgs& a, hipStream_t s) {
+    const int64_t side = wide_tiles(a.N, a.M, MODE) ? 256 : 128;
+    const int64_t tiles_n = ceil_div(a.N, MODE == FWD ? side / 2 : side), tiles_m = ceil_div(a.M, side) * (MODE == DW ? 2 : 1);
     const int64_t tiles = tiles_n * tiles_m;
     if (tiles > ((int64_t)1 << 31) - 64) return hipErrorInvalidConfiguration;
     a.tiles_n = (int32_t)tiles_n;
     a.tiles_m = (int32_t)tiles_m;
     a.tiles = (uint32_t)tiles;
     a.per_xcd = (int32_t)ceil_div(tiles, 8);
-    k_gemm<MODE, ACT><<<dim3((unsigned)(8 * (int64_t)a.per_xcd), MODE == DX ? a.parts : 1), 256, 0, s>>>(a);
+    const dim3 grid((unsigned)(8 * (int64_t)a.per_xcd), MODE == DX ? a.parts : 1);
+    if (side == 256) k_gemm_wide<MODE, ACT><<<grid, 256, 0, s>>>(a);
+    else k_gemm<MODE, ACT><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
 // Parts of dx's sum: enough workgroups for two per CU, at least 8 steps each.
 int dx_parts(int64_t tokens, int64_t cols, int64_t features) {
+    if (wide_tiles(cols, tokens, DX)) return 1;
     const int64_t tiles = ceil_div(tokens, 128) * ceil_div(cols, 128), steps = 2 * ceil_div(features, BK);
     return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, tiles), steps / 8, 16}));
 }
@@ -351,10 +567,9 @@ hipError_t launch_gated(const GatedArgs& g, hipStream_t s) {
     a.N = (int32_t)g.features; a.M = (int32_t)g.tokens; a.K = (int32_t)g.cols;
     a.out[0] = static_cast<uint16_t*>(g.h);
     a.saved = g.saved;
-    const int64_t tn = ceil_div(g.features, 64), tm = ceil_div(g.tokens, 128);
-    if (g.act == A_SILU) return run_gemm<FWD, A_SILU>(a, tn, tm, s);
-    if (g.act == A_GELU) return run_gemm<FWD, A_GELU>(a, tn, tm, s);
-    return run_gemm<FWD, A_GELU_TANH>(a, tn, tm, s);
+    if (g.act == A_SILU) return run_gemm<FWD, A_SILU>(a, s);
+    if (g.act == A_GELU) return run_gemm<FWD, A_GELU>(a, s);
+    return run_gemm<FWD, A_GELU_TANH>(a, s);
 }
 
 hipError_t launch_gated_grad(const GatedGradArgs& g, hipStream_t s) {
@@ -384,7 +599,7 @@ hipError_t launch_gated_grad(const GatedGradArgs& g, hipStream_t s) {
         a.parts = dx_parts(g.tokens, g.cols, g.features);
         a.split_steps = (int32_t)ceil_div(2 * ceil_div(g.features, BK), a.parts);
         a.partial = reinterpret_cast<float*>(ws + 2 * plane_bytes(g.tokens, g.features));
-        e = run_gemm<DX, 0>(a, ceil_div(g.cols, 128), ceil_div(g.tokens, 128), s);
+        e = run_gemm<DX, 0>(a, s);
         if (e != hipSuccess) return e;
         if (a.parts > 1) {
             const int64_t n = g.tokens * g.cols;
@@ -399,7 +614,7 @@ hipError_t launch_gated_grad(const GatedGradArgs& g, hipStream_t s) {
         a.ldp = g.ldx; a.ldq = g.features;
         a.N = (int32_t)g.cols; a.M = (int32_t)g.features; a.K = (int32_t)g.tokens;
         a.out[0] = static_cast<uint16_t*>(g.dwg); a.out[1] = static_cast<uint16_t*>(g.dwu);
-        e = run_gemm<DW, 0>(a, ceil_div(g.cols, 128), 2 * ceil_div(g.features, 128), s);
+        e = run_gemm<DW, 0>(a, s);
     }
     return e;
 }

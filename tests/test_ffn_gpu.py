@@ -168,6 +168,27 @@ def test_gated_large(iq, tokens, cols, features):
     check_gated(iq, *gated_inputs(tokens, cols, features, 1), "silu")
 
 
+@pytest.mark.parametrize("tokens,cols,features,act", [(2050, 328, 3336, "silu"), (2050, 6408, 264, "gelu"), (70, 1096, 5640, "silu"),
+                                                      (300, 2056, 3592, "gelu_tanh"), (1793, 8, 4096, "silu"), (1800, 6408, 8, "silu"),
+                                                      (2048, 4096, 3592, "silu")])
+def test_gated_wide_tiles(iq, tokens, cols, features, act):
+    """Products large enough for 256 x 256 tiles, forward or in one of the gradients, with ragged edges and odd numbers of steps."""
+    check_gated(iq, *gated_inputs(tokens, cols, features, 6), act)
+
+
+@pytest.mark.parametrize("tokens,features", [(2050, 3336), (300, 15000)])
+def test_gated_wide_tiles_strided_x_and_a_bad_token(iq, tokens, features):
+    """The space between rows of x and one token hold NaN: neither reaches another token."""
+    x, wg, wu, dh = gated_inputs(tokens, 328, features, 7, ld=344)
+    check_gated(iq, x, wg, wu, dh, "silu")
+    h0, s0 = iq.gated(x, wg, wu, save=True)
+    dx0 = iq.gated_backward(dh, x, wg, wu, s0)[0]
+    x[tokens - 1, 327] = float("nan")
+    h, saved = iq.gated(x, wg, wu, save=True)
+    assert torch.equal(h[:-1], h0[:-1]) and torch.isnan(h[-1]).all()
+    assert torch.equal(iq.gated_backward(dh, x, wg, wu, saved)[0][:-1], dx0[:-1])
+
+
 @pytest.mark.parametrize("tokens", [5, 40, 200, 600])
 def test_gated_strided_x(iq, tokens):
     """Rows of x further apart than its columns; the space between holds NaN."""
