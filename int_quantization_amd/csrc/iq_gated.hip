@@ -300,20 +300,15 @@ template <bool KC> struct WideCopy {
     }
 };
 
-// Four products whose sums stay where they are, in the upper half of the
-// registers: left to itself the compiler moves results between the halves in
-// every step.  It does not see inside, so the waits that the matrix cores need
-// are written out: two states from a write of an operand to its use ...
-__device__ __forceinline__ void mfma_2x2(f4v& c00, f4v& c01, f4v& c10, f4v& c11, bf8v p0, bf8v p1, bf8v q0, bf8v q1) {
-    asm volatile("s_nop 1\n"
-                 "v_mfma_f32_16x16x32_bf16 %0, %4, %6, %0\n"
-                 "v_mfma_f32_16x16x32_bf16 %1, %4, %7, %1\n"
-                 "v_mfma_f32_16x16x32_bf16 %2, %5, %6, %2\n"
-                 "v_mfma_f32_16x16x32_bf16 %3, %5, %7, %3"
-                 : "+a"(c00), "+a"(c01), "+a"(c10), "+a"(c11)
-                 : "v"(p0), "v"(p1), "v"(q0), "v"(q1));
+// A product whose sum stays where it is, in the upper half of the registers:
+// left to itself the compiler moves results between the halves in every step.
+// It does not see inside, so what the matrix cores ask for is kept here: an
+// operand comes from LDS reads alone (which are waited for; an operand written
+// by the vector units would need two wait states), and from the last product
+// to a read of its result pass at least 18 states.
+__device__ __forceinline__ void mfma_in_place(f4v& c, bf8v p, bf8v q) {
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(p), "v"(q));
 }
-// ... and 18 at most from the last product to a read of its result.
 __device__ __forceinline__ void settle(f4v (&acc)[8][8]) {
     asm volatile("s_nop 15\ns_nop 15" ::: "memory");
 #pragma unroll
@@ -368,34 +363,31 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wi
     for (int n = 0; n < 8; ++n)
 #pragma unroll
         for (int m = 0; m < 8; ++m) acc[n][m] = f4v{0.f, 0.f, 0.f, 0.f};
-    // group g of 16: four products; a fragment is first used in a group no earlier than its read's
-    auto products = [&](int g, const bf8v (&pf)[8], const bf8v (&qf)[8]) {
-        const int n = 2 * (g >> 2), m = 2 * (g & 3);
-        mfma_2x2(acc[n][m], acc[n][m + 1], acc[n + 1][m], acc[n + 1][m + 1], pf[n], pf[n + 1], qf[m], qf[m + 1]);
+    // product i of 64, in blocks of 2 x 2: a fragment's first use comes after its read in the order of `read`
+    auto product = [&](int i, const bf8v (&pf)[8], const bf8v (&qf)[8]) {
+        const int n = 2 * (i >> 4) + ((i >> 1) & 1), m = 2 * ((i >> 2) & 3) + (i & 1);
+        mfma_in_place(acc[n][m], pf[n], qf[m]);
+        __builtin_amdgcn_sched_barrier(0);
     };
     bf8v pa[8], qa[8], pb[8], qb[8];
+    Source src;
     auto step = [&](int s, Tile& P, Tile& Q, const Tile& nP, const Tile& nQ) {
 #pragma unroll
-        for (int g = 0; g < 16; ++g) {
-            if (g < 8) {
-                read(2 * g, 1, P, Q, pb, qb);
-                read(2 * g + 1, 1, P, Q, pb, qb);
-            }
-            products(g, pa, qa);
-            __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < 64; ++i) {
+            if (i % 3 == 0 && i < 48) read(i / 3, 1, P, Q, pb, qb);
+            if (i == 50) src = source(s + 2);
+            product(i, pa, qa);
         }
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0x0070);           // vmcnt(0), lgkmcnt(0): step s + 1 has landed, step s is read
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        const Source src = source(s + 2);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int g = 0; g < 16; ++g) {
-            read(g, 0, nP, nQ, pa, qa);
-            copy(g, src, P, Q);
-            products(g, pb, qb);
-            __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < 64; ++i) {
+            if (i % 4 == 0) read(i / 4, 0, nP, nQ, pa, qa);
+            if (i % 4 == 2) copy(i / 4, src, P, Q);
+            product(i, pb, qb);
         }
     };
     {
