@@ -257,46 +257,64 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 2) void k_gemm(Ge
 // Four waves of 128 x 128 results, one to a SIMD: the results fill 256
 // registers of a lane and every operand fragment serves 8 products, so that
 // the reads from LDS take half as long as the products.  (Waves of 64 x 64
-// read as long as they multiply.)  A lone wave hides nothing by itself, so a
-// step's instructions are laid out by hand, a few reads or copies between any
-// two groups of four products:
-//   products of k 0..31 of step s   | reads of its k 32..63
-//   wait for the copies of step s + 1, barrier
-//   products of k 32..63            | reads of k 0..31 of step s + 1,
-//                                     copies of step s + 2 over step s
-struct Tile { Half half[2]; };        // 128 rows or columns each
+// read as long as they multiply.)  A lone wave hides nothing by itself, so the
+// instructions are laid out by hand between single products.  A step of 64 k:
+//   products of its k 0..31   | reads of its k 32..63, copies of Q of step s + 2
+//   wait for step s + 1, barrier
+//   products of its k 32..63  | reads of k 0..31 of step s + 1, copies of P of
+//                               step s + 2 over P of step s
+// LDS holds two stages of P and three of Q, all of its 160 KB: the third lets
+// the copies run evenly, one in eight products.  (Sixteen in 64 products stall
+// the wave at the copies; steps of 32 k with four stages of both operands read
+// k-contiguous rows in halves of 128-byte lines, which costs as much.)
+constexpr uint32_t kStage = 32768;                 // 256 rows or columns of one operand, 64 k
+constexpr int kStagesP = 2, kStagesQ = 3;
 
-// One wave's share of the copies of a Tile, instructions 4 wave .. + 3 of each half.
+// One wave's share of the copies of a stage: instructions 4 wave .. + 3 of
+// each half, a half being 128 rows or columns, laid out like a Half.
 template <bool KC> struct WideCopy {
-    uint32_t off[8];      // byte offset from the tile's first element
+    uint32_t off[8];      // byte offset from the tile's first element of the step
     int32_t kk;           // KC: first k that the lane's words hold
-    // `left` as for Copy.  `pair`: the halves are 64 gate rows and 64 up rows
-    // each, and the wave's are from one of the two matrices.
-    __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int64_t left, bool pair) {
+    uint64_t base;        // address of the step's first element
+    int32_t left;         // k from there to the end
+    int32_t ld2;          // bytes of a row
+    // `rest` as `left` of Copy.  `pair`: the halves are 64 gate rows and 64 up
+    // rows each, and the wave's are from one of the two matrices.
+    __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int64_t rest, bool pair) {
+        ld2 = (int32_t)(2 * ld);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int half = i >> 2, q = 4 * wave + (i & 3);
             if constexpr (KC) {
                 const int r0 = 8 * q + (lane >> 3), r = pair ? 64 * half + (r0 & 63) : 128 * half + r0;
-                off[i] = r < left ? (uint32_t)(r * ld * 2) + 16u * ((lane & 7) ^ (lane >> 3)) : kOutside;
+                off[i] = r < rest ? (uint32_t)(r * ld * 2) + 16u * ((lane & 7) ^ (lane >> 3)) : kOutside;
             } else {
                 const int k = 4 * q + (lane >> 4), col = 128 * half + 8 * ((lane & 15) ^ (2 * ((k & 3) | ((k >> 1) & 4))));
-                off[i] = col < left ? (uint32_t)(k * ld * 2) + col * 2u : kOutside;
+                off[i] = col < rest ? (uint32_t)(k * ld * 2) + col * 2u : kOutside;
             }
         }
         kk = 8 * ((lane & 7) ^ (lane >> 3));
     }
-    // Buffer of one step from the tile's first element `base`, `left` k before
-    // the end (0: nothing is read and zeros are written): a k-strided
-    // operand's rows past k are beyond its range.
-    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint16_t* base, int left, int64_t ld) {
-        const uint32_t rows = KC ? kOutside : (uint32_t)(min(left, BK) * (int)ld * 2);
-        const int range = left <= 0 ? 0 : left >= BK ? (int)kOutside : (int)rows;
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, range, 0x00020000);
+    __device__ __forceinline__ void start(const uint16_t* first, int k, int to_end) {
+        base = reinterpret_cast<uint64_t>(first) + (KC ? 2 * (int64_t)k : (int64_t)k * ld2);
+        left = to_end;
     }
-    __device__ __forceinline__ void one(int i, __amdgpu_buffer_rsrc_t rsrc, int left, int wave, Tile& to) const {
+    __device__ __forceinline__ void advance() {
+        base += KC ? 2 * BK : (int64_t)BK * ld2;
+        left -= BK;
+    }
+    // Buffer of the step: a k-strided operand's rows past k are beyond its range.
+    __device__ __forceinline__ u4v buffer() const {
+        const int range = KC || left >= BK ? (int)kOutside : max(left, 0) * ld2;
+        return u4v{(uint32_t)base, (uint32_t)(base >> 32), (uint32_t)range, 0x00020000u};
+    }
+    // Copy i into the stage at byte `to` of LDS.  Written out, for the compiler
+    // would take every later read of LDS to depend on it; it has no output
+    // register, and the step's wait and barrier stand between it and the reads.
+    __device__ __forceinline__ void one(int i, u4v buf, int wave, uint32_t to) const {
         const uint32_t o = !KC || kk < left ? off[i] : kOutside;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)&to.half[i >> 2].w[(4 * wave + (i & 3)) * 64], 16, o, 0, 0, 0);
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                     :: "s"(to + (uint32_t)(i >> 2) * 16384u + (uint32_t)(4 * wave + (i & 3)) * 1024u), "v"(o), "s"(buf) : "memory");
     }
 };
 
@@ -321,7 +339,7 @@ __device__ __forceinline__ void settle(f4v (&acc)[8][8]) {
 template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wide(GemmArgs a) {
     constexpr bool PK = MODE == FWD, QK = MODE != DW;
     constexpr int kTileN = MODE == FWD ? 128 : 256;
-    __shared__ Tile P0, P1, Q0, Q1;
+    __shared__ __align__(1024) char lds[(kStagesP + kStagesQ) * kStage];
     int tn, tm;
     if (!tile_of(a, tn, tm)) return;
     const int lane = threadIdx.x & 63;
@@ -333,29 +351,29 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wi
     const int all = MODE == DX ? 2 * seg_steps : seg_steps;
     const int first = MODE == DX ? (int)blockIdx.y * a.split_steps : 0;
     const int last = MODE == DX ? min(all, first + a.split_steps) : all;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)lds;
 
     WideCopy<PK> cp;
     WideCopy<QK> cq;
     cp.init(wave, lane, a.ldp, (int64_t)a.N - n0, MODE == FWD);
     cq.init(wave, lane, a.ldq, (int64_t)a.M - m0, false);
+    // first elements of both operands; DX goes on to the second pair where the first ends
+    const uint16_t* p0 = a.p[MODE == FWD && wave >= 2 ? 1 : 0] + (PK ? (int64_t)n0 * a.ldp : n0);
+    const uint16_t* q0 = a.q[sel] + (QK ? (int64_t)m0 * a.ldq : m0);
+    const uint16_t* p1 = a.p[1] + (PK ? (int64_t)n0 * a.ldp : n0);
+    const uint16_t* q1 = a.q[1] + (QK ? (int64_t)m0 * a.ldq : m0);
+    {
+        const int seg = MODE == DX && first >= seg_steps ? 1 : 0, k0 = (first - seg * seg_steps) * BK;
+        cp.start(seg ? p1 : p0, k0, a.K - k0);
+        cq.start(seg ? q1 : q0, k0, a.K - k0);
+    }
+    int sp = first, sq = first;                                       // the steps that cp and cq are at
+    auto advance_p = [&] { cp.advance(); if (MODE == DX && ++sp == seg_steps) cp.start(p1, 0, a.K); };
+    auto advance_q = [&] { cq.advance(); if (MODE == DX && ++sq == seg_steps) cq.start(q1, 0, a.K); };
 
-    struct Source { __amdgpu_buffer_rsrc_t p, q; int left; };
-    auto source = [&](int s) {
-        const int seg = MODE == DX && s >= seg_steps ? 1 : 0;
-        const int k0 = (s - seg * seg_steps) * BK, left = s < last ? a.K - k0 : 0;
-        const uint16_t* pb = PK ? a.p[wave >= 2 ? 1 : 0] + (int64_t)n0 * a.ldp + k0 : a.p[seg] + (int64_t)k0 * a.ldp + n0;
-        const uint16_t* qb = QK ? a.q[seg] + (int64_t)m0 * a.ldq + k0 : a.q[sel] + (int64_t)k0 * a.ldq + m0;
-        return Source{WideCopy<PK>::buffer(pb, left, a.ldp), WideCopy<QK>::buffer(qb, left, a.ldq), left};
-    };
-    auto copy = [&](int i, const Source& src, Tile& P, Tile& Q) {     // i: 0 .. 15
-        if (i & 1) cq.one(i >> 1, src.q, src.left, wave, Q);
-        else cp.one(i >> 1, src.p, src.left, wave, P);
-    };
-    // row of the wave's P half that its 16-row fragment t starts at: gate
-    // features and then the same features of the up projection, or as they are
-    auto read = [&](int i, int ks, const Tile& P, const Tile& Q, bf8v (&pf)[8], bf8v (&qf)[8]) {   // i: 0 .. 15
-        if (i & 1) qf[i >> 1] = fragment<QK>(Q, wm * (uint32_t)sizeof(Half), (i >> 1) * 16, ks, lane);
-        else pf[i >> 1] = fragment<PK>(P, wn * (uint32_t)sizeof(Half), (i >> 1) * 16, ks, lane);
+    auto read = [&](int i, int ks, uint32_t p, uint32_t q, bf8v (&pf)[8], bf8v (&qf)[8]) {   // i: 0 .. 15; p, q: stages
+        if (i & 1) qf[i >> 1] = fragment<QK>(lds, q + wm * 16384u, (i >> 1) * 16, ks, lane);
+        else pf[i >> 1] = fragment<PK>(lds, p + wn * 16384u, (i >> 1) * 16, ks, lane);
     };
 
     f4v acc[8][8];
@@ -370,41 +388,58 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wi
         __builtin_amdgcn_sched_barrier(0);
     };
     bf8v pa[8], qa[8], pb[8], qb[8];
-    Source src;
-    auto step = [&](int s, Tile& P, Tile& Q, const Tile& nP, const Tile& nQ) {
+    uint32_t p = 0, q = kStagesP * kStage, q2 = q + 2 * kStage;       // stages of this step; of Q two steps on
+    {
+        u4v buf = cp.buffer();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cp.one(i, buf, wave, lds0 + p);
+        buf = cq.buffer();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cq.one(i, buf, wave, lds0 + q);
+        advance_q();
+        buf = cq.buffer();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cq.one(i, buf, wave, lds0 + q + kStage);
+        advance_p();
+        buf = cp.buffer();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cp.one(i, buf, wave, lds0 + p + kStage);
+        advance_p();
+        advance_q();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x4F70);           // vmcnt(16): this wave's copies of the first step have landed
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) read(i, 0, p, q, pa, qa);
+    }
+    u4v bufq = cq.buffer();
+    for (int s = first; s < last; ++s) {
+        const uint32_t np = p ^ kStage, nq = q == (kStagesP + kStagesQ - 1) * kStage ? kStagesP * kStage : q + kStage;
+        u4v bufp;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-            if (i % 3 == 0 && i < 48) read(i / 3, 1, P, Q, pb, qb);
-            if (i == 50) src = source(s + 2);
+            if (i % 3 == 0 && i < 48) read(i / 3, 1, p, q, pb, qb);
+            if (i % 8 == 5) cq.one(i / 8, bufq, wave, lds0 + q2);
+            if (i == 56) bufp = cp.buffer();
             product(i, pa, qa);
         }
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070);           // vmcnt(0), lgkmcnt(0): step s + 1 has landed, step s is read
+        __builtin_amdgcn_s_waitcnt(0x0078);           // vmcnt(8), lgkmcnt(0): step s + 1 has landed, step s is read
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-            if (i % 4 == 0) read(i / 4, 0, nP, nQ, pa, qa);
-            if (i % 4 == 2) copy(i / 4, src, P, Q);
+            if (i % 4 == 0) read(i / 4, 0, np, nq, pa, qa);
+            if (i % 8 == 5) cp.one(i / 8, bufp, wave, lds0 + p);
+            if (i == 26) advance_q();
+            if (i == 42) bufq = cq.buffer();
+            if (i == 63) advance_p();
             product(i, pb, qb);
         }
-    };
-    {
-        const Source s0 = source(first), s1 = source(first + 1);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) copy(i, s0, P0, Q0);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) copy(i, s1, P1, Q1);
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x4F70);           // vmcnt(16): this wave's copies of the first step have landed
-        lds_barrier();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) read(i, 0, P0, Q0, pa, qa);
-    }
-    for (int s = first; s < last; s += 2) {           // a step past the last adds zeros
-        step(s, P0, Q0, P1, Q1);
-        step(s + 1, P1, Q1, P0, Q0);
+        q2 = q;                                       // step s + 3 takes the stage of step s
+        p = np;
+        q = nq;
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0x0F70);               // the copies past the last step write LDS too
