@@ -24,6 +24,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "iq_ffn_launch.h"
 #include "iq_gate.h"
@@ -308,13 +309,39 @@ template <bool KC> struct WideCopy {
         const int range = KC || left >= BK ? (int)kOutside : max(left, 0) * ld2;
         return u4v{(uint32_t)base, (uint32_t)(base >> 32), (uint32_t)range, 0x00020000u};
     }
-    // Copy i into the stage at byte `to` of LDS.  Written out, for the compiler
-    // would take every later read of LDS to depend on it; it has no output
-    // register, and the step's wait and barrier stand between it and the reads.
-    __device__ __forceinline__ void one(int i, u4v buf, int wave, uint32_t to) const {
-        const uint32_t o = !KC || kk < left ? off[i] : kOutside;
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     :: "s"(to + (uint32_t)(i >> 2) * 16384u + (uint32_t)(4 * wave + (i & 3)) * 1024u), "v"(o), "s"(buf) : "memory");
+    // The lane's offset in copy i; a k-contiguous operand's words past k are outside.
+    __device__ __forceinline__ uint32_t at(int i) const { return !KC || kk < left ? off[i] : kOutside; }
+};
+
+// Copies are written out, for the compiler would take every later read of LDS
+// to depend on them; they have no output register, and the step's wait and
+// barrier stand between them and the reads.  Lane l's 16 bytes go to byte
+// `to` + 16 l of LDS.
+__device__ __forceinline__ void copy_1k(uint32_t off, u4v buf, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(buf) : "memory");
+}
+
+// LDS addresses of a wave's fragments of one operand in a stage: rows
+// (columns) 16 t .. + 15 of its half, k 32 ks .. + 31, as `fragment` has them.
+template <bool KC> struct WideRead {
+    uint32_t at[KC ? 2 : 8];       // KC: by ks; else by t, which the turn of a row's slots mixes with the lane
+    __device__ __forceinline__ void init(uint32_t stage, int half, int lane) {
+        const uint32_t i = lane & 15, h = lane >> 4;
+#pragma unroll
+        for (uint32_t e = 0; e < (KC ? 2 : 8); ++e)
+            at[e] = stage + half * 16384u + (KC ? i * 128 + ((4 * e + h) ^ (i & 7)) * 16
+                                                : (8 * h + (i >> 2)) * 256 + (e ^ ((i >> 2) | ((h & 1) << 2))) * 32 + (i & 3) * 8);
+    }
+    // part e of 8 of the way to another stage
+    __device__ __forceinline__ void move(int e, uint32_t by) { if (e < (KC ? 2 : 8)) at[e] += by; }
+    __device__ __forceinline__ bf8v get(int t, int ks) const {
+        if constexpr (KC) {
+            return *(__attribute__((address_space(3))) const bf8v*)(uintptr_t)(at[ks] + t * 2048);
+        } else {
+            const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(uintptr_t)(at[t] + ks * 8192));
+            const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(uintptr_t)(at[t] + ks * 8192 + 1024));
+            return __builtin_bit_cast(bf8v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
     }
 };
 
@@ -327,6 +354,12 @@ template <bool KC> struct WideCopy {
 __device__ __forceinline__ void mfma_in_place(f4v& c, bf8v p, bf8v q) {
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(p), "v"(q));
 }
+// With a copy behind it, the product being the state that lies between a write
+// of m0 and its use.
+template <uint32_t TO> __device__ __forceinline__ void mfma_and_copy(f4v& c, bf8v p, bf8v q, uint32_t off, u4v buf, uint32_t to) {
+    asm volatile("s_add_u32 m0, %3, %4\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %5, %6, 0 offen lds"
+                 : "+a"(c) : "v"(p), "v"(q), "s"(to), "i"(TO), "v"(off), "s"(buf) : "memory", "scc");
+}
 __device__ __forceinline__ void settle(f4v (&acc)[8][8]) {
     asm volatile("s_nop 15\ns_nop 15" ::: "memory");
 #pragma unroll
@@ -334,6 +367,11 @@ __device__ __forceinline__ void settle(f4v (&acc)[8][8]) {
         asm volatile("" : "+a"(acc[n][0]), "+a"(acc[n][1]), "+a"(acc[n][2]), "+a"(acc[n][3]), "+a"(acc[n][4]), "+a"(acc[n][5]),
                      "+a"(acc[n][6]), "+a"(acc[n][7]));
     __builtin_amdgcn_sched_barrier(0);
+}
+
+// f of the constants 0, 1, ... in turn.
+template <class F, int... I> __device__ __forceinline__ void in_turn(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
 }
 
 template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wide(GemmArgs a) {
@@ -368,12 +406,13 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wi
         cq.start(seg ? q1 : q0, k0, a.K - k0);
     }
     int sp = first, sq = first;                                       // the steps that cp and cq are at
-    auto advance_p = [&] { cp.advance(); if (MODE == DX && ++sp == seg_steps) cp.start(p1, 0, a.K); };
-    auto advance_q = [&] { cq.advance(); if (MODE == DX && ++sq == seg_steps) cq.start(q1, 0, a.K); };
-
-    auto read = [&](int i, int ks, uint32_t p, uint32_t q, bf8v (&pf)[8], bf8v (&qf)[8]) {   // i: 0 .. 15; p, q: stages
-        if (i & 1) qf[i >> 1] = fragment<QK>(lds, q + wm * 16384u, (i >> 1) * 16, ks, lane);
-        else pf[i >> 1] = fragment<PK>(lds, p + wn * 16384u, (i >> 1) * 16, ks, lane);
+    auto advance_p = [&] {
+        cp.advance();
+        if (MODE == DX && ++sp == seg_steps) cp.start(p1, 0, a.K);
+    };
+    auto advance_q = [&] {
+        cq.advance();
+        if (MODE == DX && ++sq == seg_steps) cq.start(q1, 0, a.K);
     };
 
     f4v acc[8][8];
@@ -381,62 +420,67 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wi
     for (int n = 0; n < 8; ++n)
 #pragma unroll
         for (int m = 0; m < 8; ++m) acc[n][m] = f4v{0.f, 0.f, 0.f, 0.f};
-    // product i of 64, in blocks of 2 x 2: a fragment's first use comes after its read in the order of `read`
-    auto product = [&](int i, const bf8v (&pf)[8], const bf8v (&qf)[8]) {
-        const int n = 2 * (i >> 4) + ((i >> 1) & 1), m = 2 * ((i >> 2) & 3) + (i & 1);
-        mfma_in_place(acc[n][m], pf[n], qf[m]);
-        __builtin_amdgcn_sched_barrier(0);
-    };
     bf8v pa[8], qa[8], pb[8], qb[8];
     uint32_t p = 0, q = kStagesP * kStage, q2 = q + 2 * kStage;       // stages of this step; of Q two steps on
-    {
-        u4v buf = cp.buffer();
+    WideRead<PK> rp;
+    WideRead<QK> rq;
+    rp.init(lds0 + p, wn, lane);
+    rq.init(lds0 + q, wm, lane);
+    auto read = [&](int i, int ks, bf8v (&pf)[8], bf8v (&qf)[8]) {    // i: 0 .. 15
+        if (i & 1) qf[i >> 1] = rq.get(i >> 1, ks);
+        else pf[i >> 1] = rp.get(i >> 1, ks);
+    };
+    const uint32_t to0 = lds0 + (uint32_t)wave * 4096u;               // byte of LDS that the wave's copies start at
+    auto copy_all = [&](const auto& c, uint32_t stage) {
+        const u4v buf = c.buffer();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cp.one(i, buf, wave, lds0 + p);
-        buf = cq.buffer();
+        for (int i = 0; i < 8; ++i) copy_1k(c.at(i), buf, to0 + stage + (i >> 2) * 16384u + (i & 3) * 1024u);
+    };
+    copy_all(cp, p);
+    copy_all(cq, q);
+    advance_q();
+    copy_all(cq, q + kStage);
+    advance_p();
+    copy_all(cp, p + kStage);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x4F70);               // vmcnt(16): this wave's copies of the first step have landed
+    lds_barrier();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cq.one(i, buf, wave, lds0 + q);
-        advance_q();
-        buf = cq.buffer();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cq.one(i, buf, wave, lds0 + q + kStage);
-        advance_p();
-        buf = cp.buffer();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cp.one(i, buf, wave, lds0 + p + kStage);
-        advance_p();
-        advance_q();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x4F70);           // vmcnt(16): this wave's copies of the first step have landed
-        lds_barrier();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) read(i, 0, p, q, pa, qa);
-    }
-    u4v bufq = cq.buffer();
+    for (int i = 0; i < 16; ++i) read(i, 0, pa, qa);
+
+    // Product i of 64, in blocks of 2 x 2: a fragment's first use comes after
+    // its read in the order of `read`.  One in eight has a copy behind it.
+    auto products = [&](const bf8v (&pf)[8], const bf8v (&qf)[8], const auto& copies, const u4v& buf, uint32_t stage, auto&& between) {
+        auto one = [&](auto index) {
+            constexpr int i = decltype(index)::value, c = i >> 3;
+            constexpr int n = 2 * (i >> 4) + ((i >> 1) & 1), m = 2 * ((i >> 2) & 3) + (i & 1);
+            between(i);
+            if constexpr (i % 8 == 5) mfma_and_copy<(c >> 2) * 16384u + (c & 3) * 1024u>(acc[n][m], pf[n], qf[m], copies.at(c), buf, to0 + stage);
+            else mfma_in_place(acc[n][m], pf[n], qf[m]);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        in_turn(one, std::make_integer_sequence<int, 64>{});
+    };
+    advance_q();
+    u4v bufp, bufq = cq.buffer();
     for (int s = first; s < last; ++s) {
         const uint32_t np = p ^ kStage, nq = q == (kStagesP + kStagesQ - 1) * kStage ? kStagesP * kStage : q + kStage;
-        u4v bufp;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            if (i % 3 == 0 && i < 48) read(i / 3, 1, p, q, pb, qb);
-            if (i % 8 == 5) cq.one(i / 8, bufq, wave, lds0 + q2);
-            if (i == 56) bufp = cp.buffer();
-            product(i, pa, qa);
-        }
+        products(pa, qa, cq, bufq, q2, [&](int i) {
+            if (i % 3 == 0 && i < 48) read(i / 3, 1, pb, qb);
+            if (i == 50) advance_p();
+            if (i == 54) bufp = cp.buffer();
+            if (i >= 56) { rp.move(i - 56, np - p); rq.move(i - 56, nq - q); }
+        });
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0x0078);           // vmcnt(8), lgkmcnt(0): step s + 1 has landed, step s is read
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            if (i % 4 == 0) read(i / 4, 0, np, nq, pa, qa);
-            if (i % 8 == 5) cp.one(i / 8, bufp, wave, lds0 + p);
-            if (i == 26) advance_q();
-            if (i == 42) bufq = cq.buffer();
-            if (i == 63) advance_p();
-            product(i, pb, qb);
-        }
+        products(pb, qb, cp, bufp, p, [&](int i) {
+            if (i % 4 == 0) read(i / 4, 0, pa, qa);
+            if (i == 42) advance_q();
+            if (i == 50) bufq = cq.buffer();
+        });
         q2 = q;                                       // step s + 3 takes the stage of step s
         p = np;
         q = nq;
