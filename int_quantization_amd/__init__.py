@@ -206,28 +206,28 @@ def iq_amax(d: IQDesc, x: int, amax_out: int, workspace: int, stream: int | None
 
 def iq_layer_norm(d: IQDesc, x: int, weight: int | None, bias: int | None, param_dtype: int, eps: float, y: int,
                   mean: int | None, rstd: int | None, stream: int | None) -> int:
-    return load_library().iq_layer_norm(ctypes.byref(d), x, weight, bias, param_dtype, eps, y, mean, rstd, stream)
+    return (_lib or load_library()).iq_layer_norm(ctypes.byref(d), x, weight, bias, param_dtype, eps, y, mean, rstd, stream)
 
 
 def iq_layer_norm_backward(d: IQDesc, x: int, dy: int, weight: int | None, param_dtype: int, mean: int, rstd: int,
                            dx: int | None, dweight: int | None, dbias: int | None, workspace: int | None,
                            stream: int | None) -> int:
-    return load_library().iq_layer_norm_backward(ctypes.byref(d), x, dy, weight, param_dtype, mean, rstd, dx,
+    return (_lib or load_library()).iq_layer_norm_backward(ctypes.byref(d), x, dy, weight, param_dtype, mean, rstd, dx,
                                                  dweight, dbias, workspace, stream)
 
 
 def iq_layer_norm_workspace_bytes(d: IQDesc) -> int:
-    return load_library().iq_layer_norm_workspace_bytes(ctypes.byref(d))
+    return (_lib or load_library()).iq_layer_norm_workspace_bytes(ctypes.byref(d))
 
 
 def iq_gated_forward(d: IQGatedDesc, x: int, w_gate: int, w_up: int, h: int, saved: int | None,
                      stream: int | None) -> int:
-    return load_library().iq_gated_forward(ctypes.byref(d), x, w_gate, w_up, h, saved, stream)
+    return (_lib or load_library()).iq_gated_forward(ctypes.byref(d), x, w_gate, w_up, h, saved, stream)
 
 
 def iq_gated_backward(d: IQGatedDesc, dh: int, x: int, w_gate: int, w_up: int, saved: int, dx: int | None,
                       dw_gate: int | None, dw_up: int | None, workspace: int, stream: int | None) -> int:
-    return load_library().iq_gated_backward(ctypes.byref(d), dh, x, w_gate, w_up, saved, dx, dw_gate, dw_up,
+    return (_lib or load_library()).iq_gated_backward(ctypes.byref(d), dh, x, w_gate, w_up, saved, dx, dw_gate, dw_up,
                                             workspace, stream)
 
 
@@ -236,19 +236,19 @@ def iq_gated_saved_bytes(d: IQGatedDesc) -> int:
 
 
 def iq_gated_workspace_bytes(d: IQGatedDesc) -> int:
-    return load_library().iq_gated_workspace_bytes(ctypes.byref(d))
+    return (_lib or load_library()).iq_gated_workspace_bytes(ctypes.byref(d))
 
 
 def iq_packed_gemv(d: IQDesc, codes: int, scales: int, global_scale: int | None, x: int, x_dtype: int, n1: int,
                    z: int, z_dtype: int, stream: int | None) -> int:
-    return load_library().iq_packed_gemv(ctypes.byref(d), codes, scales, global_scale, x, x_dtype, n1, z, z_dtype,
+    return (_lib or load_library()).iq_packed_gemv(ctypes.byref(d), codes, scales, global_scale, x, x_dtype, n1, z, z_dtype,
                                          stream)
 
 
 def iq_packed_gated(d: IQDesc, act: int, codes_gate: int, scales_gate: int, global_gate: int | None, codes_up: int,
                     scales_up: int, global_up: int | None, x: int, x_dtype: int, n1: int, h: int, h_dtype: int,
                     stream: int | None) -> int:
-    return load_library().iq_packed_gated(ctypes.byref(d), act, codes_gate, scales_gate, global_gate, codes_up,
+    return (_lib or load_library()).iq_packed_gated(ctypes.byref(d), act, codes_gate, scales_gate, global_gate, codes_up,
                                           scales_up, global_up, x, x_dtype, n1, h, h_dtype, stream)
 
 
@@ -537,179 +537,206 @@ def mxw_gemm(qw: "Quantized", x, out=None, stream=None):
 
 
 # ---- the feed-forward half of a layer ---------------------------------------
+# Calls of a few microseconds of GPU time: the checks below take the common
+# case in one expression each and name what is wrong only where it fails.
+_DTYPES = {}
+
+
+def _dtypes() -> dict:
+    """torch dtype -> iq_dtype."""
+    if not _DTYPES:
+        torch = _torch()
+        _DTYPES.update({torch.float32: IQ_F32, torch.bfloat16: IQ_BF16})
+    return _DTYPES
+
+
 def _dtype_of(t, what: str) -> int:
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return IQ_BF16
-    if t.dtype == torch.float32:
-        return IQ_F32
-    raise TypeError(f"{what} must be float32 or bfloat16")
+    code = _dtypes().get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what} must be float32 or bfloat16")
+    return code
 
 
 def _stream_for(x, stream):
     """The stream of a call on x, which has to be in GPU memory."""
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"x is on {x.device}, not on a GPU")
-    return _stream(stream)
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())     # current_stream() without its object
 
 
-def _result(out, shape: tuple, dtype, device, what: str = "out"):
-    """A new tensor, or the caller's after checks."""
+def _result(out, shape: tuple, dtype, x, what: str = "out"):
+    """A new tensor on x's device, or the caller's after checks."""
     if out is None:
-        return _torch().empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != shape:
-        raise ValueError(f"{what} must be {list(shape)}, got {list(out.shape)}")
-    if out.device != device:
-        raise ValueError(f"{what} is on {out.device}, the input on {device}")
-    if out.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}, got {out.dtype}")
-    if not out.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+        return x.new_empty(shape, dtype=dtype)
+    _check_dense(out, shape, dtype, x, what)
     return out
 
 
-def _check_dense(t, shape: tuple, dtype, device, what: str):
+def _check_dense(t, shape: tuple, dtype, x, what: str):
+    """t is contiguous, of this shape and type and on x's device."""
+    if t.shape == shape and t.dtype == dtype and t.device == x.device and t.is_contiguous():
+        return
     if tuple(t.shape) != shape:
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the input on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    if t.device != x.device:
+        raise ValueError(f"{what} is on {t.device}, the input on {x.device}")
+    raise ValueError(f"{what} must be contiguous")
 
 
-def _scratch(workspace, nbytes: int, device):
+def _scratch(workspace, nbytes: int, x):
     if workspace is None:
-        return _torch().empty((max(nbytes, 256),), dtype=_torch().uint8, device=device)
-    _check_buffer(workspace, nbytes, "workspace", device)
+        return x.new_empty((max(nbytes, 256),), dtype=_torch().uint8)
+    _check_buffer(workspace, nbytes, "workspace", x.device)
     return workspace
 
 
 def _norm_desc(x):
     """Descriptor of a layer norm's input (2-D, unit column stride)."""
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    if x.dim() != 2 or not (x.is_contiguous() or x.shape[1] == 1 or x.stride(1) == 1):
         raise ValueError("x must be 2-D with unit column stride")
     rows, cols = x.shape
     return IQDesc(0, 0, _dtype_of(x, "x"), 0, rows, cols, x.stride(0) if rows > 1 else cols, 0, 0)
 
 
-def _norm_params(x, weight, bias) -> int:
+def _norm_params(x, cols: int, weight, bias) -> int:
     """Checks of weight and bias (each [cols] or None); their iq_dtype."""
-    given = [p for p in (weight, bias) if p is not None]
-    for p in given:
-        _check_dense(p, (x.shape[1],), given[0].dtype, x.device, "weight and bias")
-    return _dtype_of(given[0], "weight and bias") if given else IQ_F32
+    first = weight if weight is not None else bias
+    if first is None:
+        return IQ_F32
+    if weight is not None:
+        _check_dense(weight, (cols,), first.dtype, x, "weight and bias")
+    if bias is not None:
+        _check_dense(bias, (cols,), first.dtype, x, "weight and bias")
+    return _dtype_of(first, "weight and bias")
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
     """y = (x - mean) * rstd * weight + bias over the rows of x [rows, cols]
     (float32 or bfloat16, unit column stride); returns y, mean and rstd."""
-    torch = _torch()
     d = _norm_desc(x)
-    pt = _norm_params(x, weight, bias)
-    y = _result(out, tuple(x.shape), x.dtype, x.device)
-    stats = torch.empty((2, d.rows), dtype=torch.float32, device=x.device)
-    mean, rstd = stats[0], stats[1]
+    rows, cols = d.rows, d.cols
+    pt = _norm_params(x, cols, weight, bias)
+    y = _torch().empty_like(x) if out is None and x.is_contiguous() else _result(out, (rows, cols), x.dtype, x)
+    mean, rstd = x.new_empty((2, rows), dtype=_torch().float32).unbind(0)
     st = iq_layer_norm(d, x.data_ptr(), _ptr(weight), _ptr(bias), pt, eps, y.data_ptr(), mean.data_ptr(),
                        rstd.data_ptr(), _stream_for(x, stream))
-    _check(st, "iq_layer_norm")
+    if st:
+        _check(st, "iq_layer_norm")
     return y, mean, rstd
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, workspace=None, stream=None):
     """Gradients of layer_norm: dx of x's type, dweight and dbias of weight's
     (of param_dtype, float32 by default, where weight is None)."""
-    torch = _torch()
+    f32 = _torch().float32
     d = _norm_desc(x)
-    pt = _norm_params(x, weight, None)
-    _check_dense(dy, tuple(x.shape), x.dtype, x.device, "dy")
-    _check_dense(mean, (d.rows,), torch.float32, x.device, "mean")
-    _check_dense(rstd, (d.rows,), torch.float32, x.device, "rstd")
-    pdt = weight.dtype if weight is not None else torch.float32 if param_dtype is None else param_dtype
-    dx = torch.empty(tuple(x.shape), dtype=x.dtype, device=x.device)
-    grads = torch.empty((2, d.cols), dtype=pdt, device=x.device)
-    dweight, dbias = grads[0], grads[1]
+    rows, cols = d.rows, d.cols
+    pt = _norm_params(x, cols, weight, None)
+    _check_dense(dy, (rows, cols), x.dtype, x, "dy")
+    _check_dense(mean, (rows,), f32, x, "mean")
+    _check_dense(rstd, (rows,), f32, x, "rstd")
+    pdt = weight.dtype if weight is not None else f32 if param_dtype is None else param_dtype
+    dx = _torch().empty_like(dy)
+    dweight, dbias = x.new_empty((2, cols), dtype=pdt).unbind(0)
     if weight is None:
         pt = _dtype_of(dweight, "param_dtype")
-    ws = _scratch(workspace, iq_layer_norm_workspace_bytes(d), x.device)
+    ws = _scratch(workspace, iq_layer_norm_workspace_bytes(d), x)
     st = iq_layer_norm_backward(d, x.data_ptr(), dy.data_ptr(), _ptr(weight), pt, mean.data_ptr(), rstd.data_ptr(),
                                 dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr(), _stream_for(x, stream))
-    _check(st, "iq_layer_norm_backward")
+    if st:
+        _check(st, "iq_layer_norm_backward")
     return dx, dweight, dbias
 
 
 def _gated_desc(x, w_gate, w_up, act: str):
-    torch = _torch()
+    bf16 = _torch().bfloat16
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or x.dtype != torch.bfloat16:
+    if x.dim() != 2 or x.dtype != bf16 or not (x.is_contiguous() or x.shape[1] == 1 or x.stride(1) == 1):
         raise ValueError("x must be a 2-D bfloat16 tensor with unit column stride")
-    if w_gate.dim() != 2 or w_gate.shape[1] != x.shape[1]:
-        raise ValueError("w_gate must be [features, cols]")
-    for w, what in ((w_gate, "w_gate"), (w_up, "w_up")):
-        _check_dense(w, tuple(w_gate.shape), torch.bfloat16, x.device, what)
     tokens, cols = x.shape
-    return IQGatedDesc(ACTS[act], IQ_BF16, tokens, cols, w_gate.shape[0],
-                       x.stride(0) if tokens > 1 and cols > 0 else cols, 0, 0)
+    if w_gate.dim() != 2 or w_gate.shape[1] != cols:
+        raise ValueError("w_gate must be [features, cols]")
+    features = w_gate.shape[0]
+    _check_dense(w_gate, (features, cols), bf16, x, "w_gate")
+    _check_dense(w_up, (features, cols), bf16, x, "w_up")
+    return IQGatedDesc(ACTS[act], IQ_BF16, tokens, cols, features, x.stride(0) if tokens > 1 and cols > 0 else cols, 0, 0)
 
 
 def gated(x, w_gate, w_up, act: str = "silu", *, save: bool = False, out=None, stream=None):
     """h = act(x w_gate^T) * (x w_up^T) in one kernel, for BF16 x [tokens,
     cols] and weights [features, cols]; with save=True returns h and what
     gated_backward needs."""
-    torch = _torch()
     d = _gated_desc(x, w_gate, w_up, act)
-    h = _result(out, (d.tokens, d.features), torch.bfloat16, x.device)
-    saved = torch.empty((2, d.tokens, d.features), dtype=torch.float32, device=x.device) if save else None
+    h = _result(out, (d.tokens, d.features), x.dtype, x)
+    saved = x.new_empty((2, d.tokens, d.features), dtype=_torch().float32) if save else None
     st = iq_gated_forward(d, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(), _ptr(saved),
                           _stream_for(x, stream))
-    _check(st, "iq_gated_forward")
+    if st:
+        _check(st, "iq_gated_forward")
     return (h, saved) if save else h
 
 
 def gated_backward(dh, x, w_gate, w_up, saved, act: str = "silu", *, workspace=None, stream=None):
     """Gradients of gated from dh [tokens, features] and the forward pass's
     saved values: dx, dw_gate and dw_up, BF16."""
-    torch = _torch()
     d = _gated_desc(x, w_gate, w_up, act)
-    _check_dense(dh, (d.tokens, d.features), torch.bfloat16, x.device, "dh")
-    _check_dense(saved, (2, d.tokens, d.features), torch.float32, x.device, "saved")
-    dx = torch.empty((d.tokens, d.cols), dtype=torch.bfloat16, device=x.device)
-    dw = torch.empty((2, d.features, d.cols), dtype=torch.bfloat16, device=x.device)
-    dwg, dwu = dw[0], dw[1]
-    ws = _scratch(workspace, iq_gated_workspace_bytes(d), x.device)
+    tokens, cols, features = d.tokens, d.cols, d.features
+    _check_dense(dh, (tokens, features), x.dtype, x, "dh")
+    _check_dense(saved, (2, tokens, features), _torch().float32, x, "saved")
+    dx = x.new_empty((tokens, cols))
+    dwg, dwu = x.new_empty((2, features, cols)).unbind(0)
+    ws = _scratch(workspace, iq_gated_workspace_bytes(d), x)
     st = iq_gated_backward(d, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), saved.data_ptr(),
                            dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), ws.data_ptr(), _stream_for(x, stream))
-    _check(st, "iq_gated_backward")
+    if st:
+        _check(st, "iq_gated_backward")
     return dx, dwg, dwu
 
 
-def _packed_operands(q: "Quantized", x, what: str = "weights"):
-    torch = _torch()
-    if q.fmt not in ("int4", "nvfp4", "mxfp4"):
-        raise ValueError(f"{what} must be INT4, NVFP4 or MXFP4")
-    if x.dim() != 2 or x.shape[1] != q.cols or x.dtype != torch.bfloat16 or not x.is_contiguous():
+# format -> codes and elements per scale, bytes per scale
+_PACKED = {"int4": (128, 2), "nvfp4": (16, 1), "mxfp4": (32, 1)}
+
+
+def _packed_x(x, cols: int):
+    if x.dim() != 2 or x.shape[1] != cols or x.dtype != _torch().bfloat16 or not x.is_contiguous():
         raise ValueError("x must be a contiguous BF16 [n1, K] tensor")
-    d = make_desc(q.fmt, "block", q.rows, q.cols)
-    _check_buffer(q.codes, q.rows * (q.cols // 2), f"{what}' codes", x.device, torch.uint8)
-    _check_buffer(q.scales, iq_scales_bytes(d), f"{what}' scales", x.device)
+
+
+def _packed_weights(q: "Quantized", x, what: str = "weights"):
+    """Checks of packed weights; the addresses of their codes, scales and global scale."""
+    if q.fmt not in _PACKED:
+        raise ValueError(f"{what} must be INT4, NVFP4 or MXFP4")
+    group, size = _PACKED[q.fmt]
+    codes, scales, uint8 = q.codes, q.scales, _torch().uint8
+    if codes.dtype != uint8 or codes.device != x.device or not codes.is_contiguous() or codes.numel() < q.rows * (q.cols // 2):
+        _check_buffer(codes, q.rows * (q.cols // 2), f"{what}' codes", x.device, uint8)
+    if (scales.device != x.device or not scales.is_contiguous()
+            or scales.numel() * scales.element_size() < q.rows * (q.cols // group) * size):
+        _check_buffer(scales, q.rows * (q.cols // group) * size, f"{what}' scales", x.device)
     if q.fmt == "nvfp4":
-        _check_buffer(q.global_scale, 4, f"{what}' global_scale", x.device, torch.float32)
-    return d
+        _check_buffer(q.global_scale, 4, f"{what}' global_scale", x.device, _torch().float32)
+    return codes.data_ptr(), scales.data_ptr(), _ptr(q.global_scale)
 
 
 def packed_gemv(q: "Quantized", x, out_dtype=None, out=None, stream=None):
     """z[t, j] = sum_k x[t, k] w[j, k] for 1 to 64 BF16 tokens x [n1, K] and
     INT4, NVFP4 or MXFP4 weights q [N0, K] (from quantize); z [n1, N0] is
     bfloat16 (by default) or float32, token-major."""
-    torch = _torch()
-    d = _packed_operands(q, x)
+    rows, cols = q.rows, q.cols
+    _packed_x(x, cols)
+    codes, scales, gscale = _packed_weights(q, x)
     n1 = x.shape[0]
-    z = _result(out, (n1, q.rows), torch.bfloat16 if out_dtype is None else out_dtype, x.device)
-    st = iq_packed_gemv(d, q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.global_scale), x.data_ptr(), IQ_BF16, n1,
+    z = _result(out, (n1, rows), x.dtype if out_dtype is None else out_dtype, x)
+    st = iq_packed_gemv(make_desc(q.fmt, "block", rows, cols), codes, scales, gscale, x.data_ptr(), IQ_BF16, n1,
                         z.data_ptr(), _dtype_of(z, "out"), _stream_for(x, stream))
-    _check(st, "iq_packed_gemv")
+    if st:
+        _check(st, "iq_packed_gemv")
     return z
 
 
@@ -717,17 +744,17 @@ def packed_gated(q_gate: "Quantized", q_up: "Quantized", x, act: str = "silu", o
     """h = act(x w_gate^T) * (x w_up^T) for 1 to 64 BF16 tokens with both
     weights packed in the same format, in one launch; h [n1, N0] is bfloat16
     (by default) or float32."""
-    torch = _torch()
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
-    if q_gate.fmt != q_up.fmt or q_gate.rows != q_up.rows or q_gate.cols != q_up.cols:
+    rows, cols = q_gate.rows, q_gate.cols
+    if q_gate.fmt != q_up.fmt or rows != q_up.rows or cols != q_up.cols:
         raise ValueError("gate and up weights disagree on format or shape")
-    d = _packed_operands(q_gate, x, "gate weights")
-    _packed_operands(q_up, x, "up weights")
+    _packed_x(x, cols)
+    gate, up = _packed_weights(q_gate, x, "gate weights"), _packed_weights(q_up, x, "up weights")
     n1 = x.shape[0]
-    h = _result(out, (n1, q_gate.rows), torch.bfloat16 if out_dtype is None else out_dtype, x.device)
-    st = iq_packed_gated(d, ACTS[act], q_gate.codes.data_ptr(), q_gate.scales.data_ptr(), _ptr(q_gate.global_scale),
-                         q_up.codes.data_ptr(), q_up.scales.data_ptr(), _ptr(q_up.global_scale), x.data_ptr(), IQ_BF16,
-                         n1, h.data_ptr(), _dtype_of(h, "out"), _stream_for(x, stream))
-    _check(st, "iq_packed_gated")
+    h = _result(out, (n1, rows), x.dtype if out_dtype is None else out_dtype, x)
+    st = iq_packed_gated(make_desc(q_gate.fmt, "block", rows, cols), ACTS[act], *gate, *up, x.data_ptr(), IQ_BF16, n1,
+                         h.data_ptr(), _dtype_of(h, "out"), _stream_for(x, stream))
+    if st:
+        _check(st, "iq_packed_gated")
     return h

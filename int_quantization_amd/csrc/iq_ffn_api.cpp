@@ -46,6 +46,10 @@ iq_status check_gated(const iq_gated_desc* d) {
     return IQ_OK;
 }
 
+// Launch grids count threads in 32 bits, at most 256 for 16 rows; byte offsets
+// among a workgroup's 32 rows and among 64 tokens stay below 2^31.
+constexpr int64_t kMaxRows = (int64_t)1 << 27, kMaxPackedK = (int64_t)1 << 22;
+
 // Rules shared by the packed products; *empty where nothing is to be done.
 iq_status check_packed(const iq_desc* d, int32_t x_dtype, int64_t n1, int32_t z_dtype, bool* empty) {
     if (!d) return IQ_EINVAL;
@@ -57,7 +61,7 @@ iq_status check_packed(const iq_desc* d, int32_t x_dtype, int64_t n1, int32_t z_
                            : d->fmt == IQ_NVFP4 ? IQ_FLAG_NV_SCALE_RNE : 0u;
     if (d->flags & ~rules) return IQ_EUNSUPPORTED;   // the rules shape the codes only, so they are not looked at
     if (x_dtype != IQ_BF16 || n1 > iqk::kPackedTokens) return IQ_EUNSUPPORTED;
-    if (d->rows > kMax31 - 1024 || d->cols > kMax31 - 65536) return IQ_EUNSUPPORTED;
+    if (d->rows > kMaxRows || d->cols > kMaxPackedK) return IQ_EUNSUPPORTED;
     *empty = d->rows == 0 || n1 == 0;
     return IQ_OK;
 }

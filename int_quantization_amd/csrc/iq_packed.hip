@@ -10,12 +10,14 @@
 // work per weight on the vector units is what has to be kept small.
 //
 // A workgroup takes 16 FR rows of each matrix and up to 16 NT tokens; its
-// four waves split k in steps of 128 and add their sums in LDS in wave
-// order, so every call returns the same bits.  Tokens are the MFMA's rows
-// and weight rows its columns: lane l holds weight row l % 16 at k block
-// l / 16 and receives results of that same row for tokens 4 (l / 16) .. + 3,
-// so its group scale is its own.  Codes go from memory to registers to the
-// matrix cores; only scales pass through LDS.
+// four waves take a quarter of k each, in steps of 128, and add their sums in
+// LDS in wave order, so every call returns the same bits.  Tokens are the
+// MFMA's rows and weight rows its columns: lane l holds weight row l % 16 at k
+// block l / 16 and receives results of that same row for tokens 4 (l / 16) ..
+// + 3, so its group scale is its own.  Codes go from memory to registers to
+// the matrix cores, the next batch of steps in flight while one is multiplied:
+// a wave's steps follow each other in memory, so a batch is whole 128-byte
+// lines.  Only scales pass through LDS.
 //
 // Every code becomes exact BF16:
 //   E2M1   one convert per pair, the E8M0 scale applied by the convert;
@@ -50,10 +52,12 @@ struct PackedK {
     int64_t ldx;
     int32_t n0, n1, K;
     int32_t f32_out;
+    int32_t scale_words;          // rows of scales are whole 4-byte words
 };
 
 constexpr int kStep = 128;            // k of one step: 64 code bytes per row
-constexpr int kChunkSteps = 32;       // steps whose scales are in LDS at once
+constexpr uint32_t kOutside = 0x80000000u;     // an offset beyond every buffer: loads zeros
+constexpr int kChunkSteps = 64;       // steps whose scales are in LDS at once
 
 // Scale bytes per row and step.
 template <int FMT> constexpr int scale_bytes() { return FMT == F_INT4 ? 2 : FMT == F_NVFP4 ? 8 : FMT == F_MXFP4 ? 4 : 0; }
@@ -92,13 +96,36 @@ __device__ __forceinline__ uint32_t int4_upper(uint32_t w) {
 // One step's codes of one fragment, as loaded.
 template <int FMT> struct Codes { u4v v[FMT == F_BF16W ? 4 : 1]; };
 
-template <int FMT, int FR, int NT, bool GATED, int ACT>
-__global__ __launch_bounds__(256) void k_packed(PackedK a) {
+// Bytes to LDS in words of W: `rows` rows of `take` bytes, `pitch` bytes apart
+// in memory and `pad` in LDS; the last row is `most`.
+template <class W>
+__device__ __forceinline__ void stage_rows(uint8_t* to, const uint8_t* from, int rows, int64_t j0, int64_t most, int take, int64_t pitch, int pad) {
+    const int per = take / (int)sizeof(W);
+    for (int r = threadIdx.x >> 4; r < rows; r += 16) {
+        const uint8_t* row = from + min(j0 + r, most) * pitch;
+        for (int c = threadIdx.x & 15; c < per; c += 16) {
+            const W w = reinterpret_cast<const W*>(row)[c];
+            __builtin_memcpy(to + r * pad + c * (int)sizeof(W), &w, sizeof(W));
+        }
+    }
+}
+
+// XR: token rows that a wave copies to LDS for every step (4 or 16, of one
+// token tile), or 0 where tokens are loaded as operands.
+template <int FMT, int FR, int NT, int XR, bool GATED, int ACT>
+__global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void k_packed(PackedK a) {
     constexpr int M = GATED ? 2 : 1;
     constexpr int kRows = 16 * FR, SB = scale_bytes<FMT>();
     constexpr int kPad = SB * kChunkSteps + 4;                        // row r starts r words further round the banks
-    __shared__ f4v red[4][M * FR][NT][64];
-    __shared__ __align__(16) uint8_t s_sc[SB ? M * kRows * kPad : 16];
+    constexpr int D = XR == 4 && FMT != F_BF16W ? 2 : 1;              // steps of a batch
+    constexpr int XW = XR ? D * XR * 16 : 1;                          // 16-byte words of a batch's tokens
+    struct Sums { f4v of[4][M * FR][NT][64]; };
+    __shared__ __align__(16) uint8_t s_sc[std::max<int>(SB ? M * kRows * kPad : 16, sizeof(Sums))];    // scales, then sums
+    // tokens of the batch at hand and of the next, a wave's own each: word w of
+    // row r at word w ^ turn(r) of its 256 bytes, so that the lanes that the
+    // LDS serves together (0-3, 12-15, 20-23, 24-27 and so on) are in
+    // different banks
+    __shared__ u4v s_x0[4][XW], s_x1[4][XW];
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int i = lane & 15, h = lane >> 4;
@@ -107,16 +134,18 @@ __global__ __launch_bounds__(256) void k_packed(PackedK a) {
     const int64_t rb = row_bytes<FMT>(a.K);
 
     // Rows past n0 and tokens past n1 read the last one: their lanes feed
-    // only outputs that are not stored.
-    const uint8_t* crow[M][FR];
+    // only outputs that are not stored.  Offsets from the workgroup's first
+    // row and token fit 32 bits.
+    const uint8_t* cbase[M];
+    uint32_t coff[FR], xoff[NT];
 #pragma unroll
-    for (int m = 0; m < M; ++m)
+    for (int m = 0; m < M; ++m) cbase[m] = a.codes[m] + j0 * rb;
 #pragma unroll
-        for (int f = 0; f < FR; ++f)
-            crow[m][f] = a.codes[m] + (int64_t)min(j0 + 16 * f + i, a.n0 - 1) * rb + 16 * h;
-    const uint16_t* xrow[NT];
+    for (int f = 0; f < FR; ++f) coff[f] = (uint32_t)min(16 * f + i, a.n0 - 1 - j0) * (uint32_t)rb + 16 * h;
+    const char* xbase = reinterpret_cast<const char*>(a.x + t0 * a.ldx);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) xrow[n] = a.x + (int64_t)min(t0 + 16 * n + i, a.n1 - 1) * a.ldx;
+    for (int n = 0; n < NT; ++n)
+        xoff[n] = (uint32_t)min(16 * n + i, a.n1 - 1 - t0) * (uint32_t)(2 * a.ldx) + (FMT == F_BF16W ? 16 * h : 64 * h);
 
     f4v acc[M][FR][NT];
 #pragma unroll
@@ -126,75 +155,93 @@ __global__ __launch_bounds__(256) void k_packed(PackedK a) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) acc[m][f][n] = f4v{0.f, 0.f, 0.f, 0.f};
 
-    for (int s0 = 0; s0 < steps; s0 += kChunkSteps) {
-        const int s1 = min(steps, s0 + kChunkSteps);
-        if constexpr (SB > 0) {
-            // scale bytes of the rows, whole rows of the chunk at a time
-            const int64_t per_row = FMT == F_INT4 ? a.K / 128 * 2 : FMT == F_NVFP4 ? a.K / 16 : a.K / 32;
-            const int take = (int)min((int64_t)(s1 - s0) * SB, per_row - (int64_t)s0 * SB);
-            __syncthreads();                                          // the previous chunk's are no longer read
+    // Lane h's 32 elements of a packed step start at 32 h, whole or not at
+    // all; of a BF16 step, 8 elements at 32 q + 8 h.  Loads from `limit` on
+    // are given an offset beyond their buffer's range and return zeros, so
+    // that the loop has no branches and the waits for it can be counted.
+    auto k_of = [&](int s, int q) { return s * kStep + (FMT == F_BF16W ? 32 * q + 8 * h : 32 * h); };
+    auto fetch = [](const void* base, uint32_t off) {
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)kOutside, 0x00020000);
+        return __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0);
+    };
+    struct Batch { Codes<FMT> c[D][M][FR]; };
+    struct Tokens { u4v v[D][NT][4]; };
+    auto load = [&](Batch& o, int s, int limit) {
 #pragma unroll
-            for (int m = 0; m < M; ++m)
-                for (int e = t; e < kRows * take; e += 256) {
-                    const int r = e / take, b = e - r * take;
-                    s_sc[(m * kRows + r) * kPad + b] = a.scales[m][(int64_t)min(j0 + r, a.n0 - 1) * per_row + (int64_t)s0 * SB + b];
-                }
-            __syncthreads();
-        }
-        for (int s = s0 + wave; s < s1; s += 4) {
-            // lane h's 32 elements of a packed step start at 32 h, whole or
-            // not at all; of a BF16 step, 8 elements at 32 q + 8 h
-            Codes<FMT> c[M][FR];
-            u4v xv[NT][4];
+        for (int d = 0; d < D; ++d)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int k = s * kStep + (FMT == F_BF16W ? 32 * q + 8 * h : 32 * h + 8 * q);
-                const bool in = k < a.K;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    xv[n][q] = u4v{0u, 0u, 0u, 0u};
-                    if (in) xv[n][q] = *reinterpret_cast<const u4v*>(xrow[n] + k);
-                }
+            for (int q = 0; q < (FMT == F_BF16W ? 4 : 1); ++q)
 #pragma unroll
                 for (int m = 0; m < M; ++m)
 #pragma unroll
-                    for (int f = 0; f < FR; ++f) {
-                        if constexpr (FMT == F_BF16W) {
-                            c[m][f].v[q] = u4v{0u, 0u, 0u, 0u};
-                            if (in) c[m][f].v[q] = *reinterpret_cast<const u4v*>(crow[m][f] + (int64_t)s * 256 + 64 * q);
-                        } else if (q == 0) {
-                            c[m][f].v[0] = u4v{0u, 0u, 0u, 0u};
-                            if (in) c[m][f].v[0] = *reinterpret_cast<const u4v*>(crow[m][f] + (int64_t)s * 64);
-                        }
-                    }
+                    for (int f = 0; f < FR; ++f)
+                        o.c[d][m][f].v[q] = fetch(cbase[m] + (int64_t)(s + d) * (FMT == F_BF16W ? 256 : 64),
+                                                  k_of(s + d, q) < limit ? coff[f] + 64 * q : kOutside);
+    };
+    auto turn = [](int r) { return 4 * ((0x78 >> ((r >> 1) & 6)) & 3) + (r & 3); };     // 0, 2, 3, 1 by fours of rows
+    auto load_x = [&](Tokens& x, int s, int limit) {
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    x.v[d][n][q] = fetch(xbase + (int64_t)(s + d) * (2 * kStep),
+                                         k_of(s + d, q) < limit ? xoff[n] + (FMT == F_BF16W ? 64 : 16) * q : kOutside);
+    };
+    // instruction c copies rows 4 c .. + 3 of a step, word lane % 16 of row 4 c + lane / 16
+    auto copy_x = [&](u4v (&to)[4][XW], int s, int limit) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(xbase + (int64_t)(s + d) * (2 * kStep)), 0, (int)kOutside, 0x00020000);
+#pragma unroll
+            for (int c = 0; c < XR / 4; ++c) {
+                const int r = 4 * c + h, w = i ^ turn(r);
+                const uint32_t off = r < a.n1 && (s + d) * kStep + 8 * w < limit ? (uint32_t)r * (uint32_t)(2 * a.ldx) + 16 * w : kOutside;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)&to[wave][(d * XR + 4 * c) * 16], 16, off, 0, 0, 0);
             }
-            const bool live = s * kStep + 32 * h < a.K;               // packed lanes past K have no scale
+        }
+    };
+    const int xr = min(i, min(XR, a.n1) - 1);
+    auto read_x = [&](Tokens& x, const u4v (&from)[4][XW]) {
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                x.v[d][0][q] = from[wave][(d * XR + xr) * 16 + ((FMT == F_BF16W ? 4 * q + h : 4 * h + q) ^ turn(xr))];
+    };
+    // `at`: the chunk's first step
+    auto multiply = [&](const Batch& o, const Tokens& x, int s, int at) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const bool live = (s + d) * kStep + 32 * h < a.K;         // packed lanes past K have no scale
 #pragma unroll
             for (int m = 0; m < M; ++m)
 #pragma unroll
                 for (int f = 0; f < FR; ++f) {
-                    const uint8_t* sc = s_sc + (m * kRows + 16 * f + i) * kPad + (s - s0) * SB;
+                    const Codes<FMT>& c = o.c[d][m][f];
+                    const uint8_t* sc = s_sc + (m * kRows + 16 * f + i) * kPad + min(s + d - at, kChunkSteps - 1) * SB;
                     if constexpr (FMT == F_BF16W) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                acc[m][f][n] = mfma(__builtin_bit_cast(bf8v, xv[n][q]), __builtin_bit_cast(bf8v, c[m][f].v[q]),
-                                                    acc[m][f][n]);
+                                acc[m][f][n] = mfma(__builtin_bit_cast(bf8v, x.v[d][n][q]), __builtin_bit_cast(bf8v, c.v[q]), acc[m][f][n]);
                     } else if constexpr (FMT == F_INT4) {
-                        const float scale = (float)*reinterpret_cast<const _Float16*>(sc);
+                        const float stored = (float)*reinterpret_cast<const _Float16*>(sc);
+                        const float scale = live ? stored : 0.f;
                         f4v part[NT];
 #pragma unroll
                         for (int n = 0; n < NT; ++n) part[n] = f4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const uint32_t w = c[m][f].v[0][q];
+                            const uint32_t w = c.v[0][q];
                             const bf8v lo = __builtin_bit_cast(bf8v, fp4_bf16x8(w & 0x33333333u, 2.f));
                             const bf8v up = __builtin_bit_cast(bf8v, fp4_bf16x8(int4_upper(w), 8.f));
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                part[n] = mfma(__builtin_bit_cast(bf8v, xv[n][q]), lo, part[n]);
-                                part[n] = mfma(__builtin_bit_cast(bf8v, xv[n][q]), up, part[n]);
+                                part[n] = mfma(__builtin_bit_cast(bf8v, x.v[d][n][q]), lo, part[n]);
+                                part[n] = mfma(__builtin_bit_cast(bf8v, x.v[d][n][q]), up, part[n]);
                             }
                         }
 #pragma unroll
@@ -202,26 +249,69 @@ __global__ __launch_bounds__(256) void k_packed(PackedK a) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) acc[m][f][n][e] = __builtin_fmaf(scale, part[n][e], acc[m][f][n][e]);
                     } else {
-                        const uint32_t b = live ? (FMT == F_NVFP4 ? *reinterpret_cast<const uint16_t*>(sc + 2 * h) : sc[h]) : 0u;
+                        const uint32_t stored = FMT == F_NVFP4 ? *reinterpret_cast<const uint16_t*>(sc + 2 * h) : sc[h];
+                        const uint32_t b = live ? stored : 0u;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             u4v v;
                             if constexpr (FMT == F_NVFP4) {
-                                v = fp4_scaled_bf16x8(c[m][f].v[0][q], q < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)b, 0)
-                                                                            : __builtin_amdgcn_cvt_f32_fp8((int)b, 1));
+                                v = fp4_scaled_bf16x8(c.v[0][q], q < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)b, 0)
+                                                                      : __builtin_amdgcn_cvt_f32_fp8((int)b, 1));
                             } else {
                                 // 2^(b - 127): b = 0 is the subnormal 2^-127; 255 is NaN
-                                v = fp4_bf16x8(c[m][f].v[0][q], __uint_as_float(b ? b << 23 : 0x00400000u));
+                                v = fp4_bf16x8(c.v[0][q], __uint_as_float(b ? b << 23 : 0x00400000u));
                                 if (b == 255u) v = u4v{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
                             }
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                acc[m][f][n] = mfma(__builtin_bit_cast(bf8v, xv[n][q]), __builtin_bit_cast(bf8v, v), acc[m][f][n]);
+                                acc[m][f][n] = mfma(__builtin_bit_cast(bf8v, x.v[d][n][q]), __builtin_bit_cast(bf8v, v), acc[m][f][n]);
                         }
                     }
                 }
         }
+    };
+
+    constexpr int kChunk = SB ? kChunkSteps : 1 << 30;
+    for (int s0 = 0; s0 < steps; s0 += kChunk) {
+        const int s1 = min(steps, s0 > steps - kChunk ? steps : s0 + kChunk);
+        const int share = ((s1 - s0 + 4 * D - 1) / (4 * D)) * D;      // whole batches
+        const int first = s0 + wave * share, end = min(s1, first + share);
+        Batch now, next;
+        const int limit = min(a.K, end * kStep);
+        if constexpr (XR > 0) copy_x(s_x0, first, limit);
+        load(now, first, limit);
+        if constexpr (SB > 0) {
+            const int64_t per_row = FMT == F_INT4 ? a.K / 128 * 2 : FMT == F_NVFP4 ? a.K / 16 : a.K / 32;
+            const int take = (int)min((int64_t)(s1 - s0) * SB, per_row - (int64_t)s0 * SB);
+            if (s0) __syncthreads();                                  // the previous chunk's are no longer read
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                uint8_t* to = s_sc + m * kRows * kPad;
+                const uint8_t* from = a.scales[m] + (int64_t)s0 * SB;
+                if (a.scale_words) stage_rows<uint32_t>(to, from, kRows, j0, a.n0 - 1, take, per_row, kPad);
+                else if (FMT != F_MXFP4) stage_rows<uint16_t>(to, from, kRows, j0, a.n0 - 1, take, per_row, kPad);
+                else stage_rows<uint8_t>(to, from, kRows, j0, a.n0 - 1, take, per_row, kPad);
+            }
+            __syncthreads();
+        }
+        // tokens that are loaded come from the caches and before the next
+        // codes, so that waiting for them does not wait for memory
+        auto batch = [&](Batch& o, Batch& ahead, u4v (&xo)[4][XW], u4v (&xa)[4][XW], int s) {
+            Tokens x;
+            if constexpr (XR > 0) copy_x(xa, s + D, limit);
+            else load_x(x, s, limit);
+            load(ahead, s + D, limit);
+            __builtin_amdgcn_sched_barrier(0);        // the compiler would put them off
+            if constexpr (XR > 0) read_x(x, xo);
+            multiply(o, x, s, s0);
+        };
+        for (int s = first; s < end; s += 2 * D) {
+            batch(now, next, s_x0, s_x1, s);
+            batch(next, now, s_x1, s_x0, s + D);
+        }
     }
+    auto& red = reinterpret_cast<Sums*>(s_sc)->of;
+    if constexpr (SB > 0) __syncthreads();                            // scales are no longer read
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -262,17 +352,18 @@ __global__ __launch_bounds__(256) void k_packed(PackedK a) {
     }
 }
 
-template <int FMT, int FR, int NT, bool GATED, int ACT> hipError_t run(const PackedK& k, hipStream_t s) {
+template <int FMT, int FR, int NT, int XR, bool GATED, int ACT> hipError_t run(const PackedK& k, hipStream_t s) {
     const dim3 grid((unsigned)((k.n0 + 16 * FR - 1) / (16 * FR)), (unsigned)((k.n1 + 16 * NT - 1) / (16 * NT)));
-    k_packed<FMT, FR, NT, GATED, ACT><<<grid, 256, 0, s>>>(k);
+    k_packed<FMT, FR, NT, XR, GATED, ACT><<<grid, 256, 0, s>>>(k);
     return hipGetLastError();
 }
 
 template <int FMT, bool GATED, int ACT> hipError_t pick_tokens(const PackedK& k, hipStream_t s) {
     constexpr int FR = GATED ? 1 : 2;
-    if (k.n1 <= 16) return run<FMT, FR, 1, GATED, ACT>(k, s);
-    if (k.n1 <= 32) return run<FMT, FR, 2, GATED, ACT>(k, s);
-    return run<FMT, FR, 4, GATED, ACT>(k, s);
+    if (k.n1 <= 4) return run<FMT, FR, 1, 4, GATED, ACT>(k, s);
+    if (k.n1 <= 16) return run<FMT, FR, 1, 16, GATED, ACT>(k, s);
+    if (k.n1 <= 32) return run<FMT, FR, 2, 0, GATED, ACT>(k, s);
+    return run<FMT, FR, 4, 0, GATED, ACT>(k, s);
 }
 
 template <int FMT> hipError_t pick(const PackedArgs& a, const PackedK& k, hipStream_t s) {
@@ -297,6 +388,7 @@ hipError_t launch_packed(const PackedArgs& a, hipStream_t s) {
     k.x = static_cast<const uint16_t*>(a.x); k.out = a.out; k.saved = a.saved; k.ldx = a.ldx;
     k.n0 = (int32_t)a.n0; k.n1 = (int32_t)a.n1; k.K = (int32_t)a.K;
     k.f32_out = a.out_dtype == D_F32;
+    k.scale_words = a.K % (a.fmt == F_INT4 ? 256 : a.fmt == F_NVFP4 ? 64 : 128) == 0;
     switch (a.fmt) {
     case F_INT4: return pick<F_INT4>(a, k, s);
     case F_NVFP4: return pick<F_NVFP4>(a, k, s);
