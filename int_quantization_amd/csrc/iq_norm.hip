@@ -7,7 +7,9 @@
 //
 // HBM bounds both passes: the forward reads x and writes y, the backward
 // reads x and dy and writes dx.  A row is therefore held in registers
-// between its statistics and its output, and read once.  The variance is
+// between its statistics and its output, and read once; a workgroup holds
+// the parameters of its columns, goes over many rows and has the next one
+// in flight while it works on this.  The variance is
 // taken about the mean, not as a difference of squares, so that an offset
 // much larger than the spread costs no digits.
 #include <hip/hip_runtime.h>
@@ -60,6 +62,14 @@ template <int T, int N> __device__ __forceinline__ void load_n(const void* base,
         }
     }
 }
+
+// The same elements as they lie in memory, to be taken apart later.
+template <int T, int N> struct Raw { u4v w[T == D_F32 ? 2 : 1]; };
+template <int T> struct Raw<T, 1> { typename Elem<T>::type w; };
+template <int T, int N> __device__ __forceinline__ Raw<T, N> raw(const void* base, int64_t i) {
+    return *reinterpret_cast<const Raw<T, N>*>(static_cast<const typename Elem<T>::type*>(base) + i);
+}
+template <int T, int N> __device__ __forceinline__ void unpack(const Raw<T, N>& r, float (&v)[N]) { load_n<T, N>(&r, 0, v); }
 
 template <int T, int N> __device__ __forceinline__ void store_n(void* base, int64_t i, const float (&v)[N]) {
     if constexpr (T == D_F32) {
@@ -125,11 +135,67 @@ template <int NW> __device__ __forceinline__ float block_sum(float a, float (&re
     return a;
 }
 
-// One workgroup of NT threads per row (the grid strides over the rows).
-// HOLD vectors of N elements per thread stay in registers; HOLD == 0 is a
-// row of any length, read three times.
+// A workgroup of NT threads takes rows blockIdx.x, + gridDim.x, ...; a thread
+// holds HOLD vectors of N elements of one.
 template <int IN, int N, int NT, int HOLD>
 __global__ __launch_bounds__(NT) void k_norm(NormArgs a) {
+    constexpr int NW = NT / 64;
+    __shared__ float red[2][2][NW][2];
+    const int t = threadIdx.x, nv = (int)(a.cols / N);
+    const float inv = 1.f / (float)a.cols;
+    Raw<IN, N> next[HOLD] = {};
+    float w[HOLD][N], b[HOLD][N];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            if (t + k * NT < nv) next[k] = raw<IN, N>(a.x, row * a.ld + (int64_t)(t + k * NT) * N);
+    };
+    fetch(blockIdx.x);
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k)
+        if (t + k * NT < nv) {
+            load_param<N>(a.weight, a.param_dtype, (int64_t)(t + k * NT) * N, 1.f, w[k]);
+            load_param<N>(a.bias, a.param_dtype, (int64_t)(t + k * NT) * N, 0.f, b[k]);
+        }
+    int odd = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, odd ^= 1) {
+        float v[HOLD][N], s = 0.f;
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k) unpack<IN, N>(next[k], v[k]);
+        if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            if (t + k * NT < nv) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) s += v[k][i];
+            }
+        const float mean = block_sum<NW>(s, red[odd][0]) * inv;
+        float q = 0.f;
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            if (t + k * NT < nv) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) { v[k][i] -= mean; q = __builtin_fmaf(v[k][i], v[k][i], q); }
+            }
+        const float rstd = 1.f / sqrtf(block_sum<NW>(q, red[odd][1]) * inv + a.eps);
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            if (t + k * NT < nv) {
+                float y[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) y[i] = __builtin_fmaf(v[k][i] * rstd, w[k][i], b[k][i]);
+                store_n<IN, N>(a.y, row * a.cols + (int64_t)(t + k * NT) * N, y);
+            }
+        if (t == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+    }
+}
+
+// Rows longer than the registers hold, read three times.
+template <int IN, int N, int NT>
+__global__ __launch_bounds__(NT) void k_norm_long(NormArgs a) {
     constexpr int NW = NT / 64;
     __shared__ float red[2][NW][2];
     const int t = threadIdx.x;
@@ -137,44 +203,28 @@ __global__ __launch_bounds__(NT) void k_norm(NormArgs a) {
     const float inv = 1.f / (float)a.cols;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const int64_t xo = row * a.ld, yo = row * a.cols;
-        float v[HOLD > 0 ? HOLD : 1][N];
-        float s = 0.f;
-        auto each = [&](auto&& f) {
-            if constexpr (HOLD > 0) {
-#pragma unroll
-                for (int k = 0; k < HOLD; ++k)
-                    if (t + k * NT < nv) f(t + k * NT, v[k]);
-            } else {
-                for (int64_t c = t; c < nv; c += NT) {
-                    load_n<IN, N>(a.x, xo + c * N, v[0]);
-                    f(c, v[0]);
-                }
-            }
-        };
-        if constexpr (HOLD > 0) {
-#pragma unroll
-            for (int k = 0; k < HOLD; ++k)
-                if (t + k * NT < nv) load_n<IN, N>(a.x, xo + (int64_t)(t + k * NT) * N, v[k]);
-        }
-        each([&](int64_t, float (&e)[N]) {
+        float e[N], s = 0.f, q = 0.f;
+        for (int64_t c = t; c < nv; c += NT) {
+            load_n<IN, N>(a.x, xo + c * N, e);
 #pragma unroll
             for (int i = 0; i < N; ++i) s += e[i];
-        });
+        }
         const float mean = block_sum<NW>(s, red[0]) * inv;
-        float q = 0.f;
-        each([&](int64_t, float (&e)[N]) {
+        for (int64_t c = t; c < nv; c += NT) {
+            load_n<IN, N>(a.x, xo + c * N, e);
 #pragma unroll
             for (int i = 0; i < N; ++i) { const float d = e[i] - mean; q = __builtin_fmaf(d, d, q); }
-        });
+        }
         const float rstd = 1.f / sqrtf(block_sum<NW>(q, red[1]) * inv + a.eps);
-        each([&](int64_t c, float (&e)[N]) {
+        for (int64_t c = t; c < nv; c += NT) {
             float w[N], b[N], y[N];
+            load_n<IN, N>(a.x, xo + c * N, e);
             load_param<N>(a.weight, a.param_dtype, c * N, 1.f, w);
             load_param<N>(a.bias, a.param_dtype, c * N, 0.f, b);
 #pragma unroll
             for (int i = 0; i < N; ++i) y[i] = __builtin_fmaf((e[i] - mean) * rstd, w[i], b[i]);
             store_n<IN, N>(a.y, yo + c * N, y);
-        });
+        }
         if (t == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
@@ -189,6 +239,7 @@ __global__ __launch_bounds__(NT) void k_norm(NormArgs a) {
 template <int IN, int N, int NT, int HOLD>
 __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
     constexpr int NW = NT / 64;
+    constexpr bool AHEAD = NT < 1024;     // 1024 threads have no registers for the next row
     __shared__ float red[2][NW][2];
     const int t = threadIdx.x;
     const int nv = (int)(a.cols / N);
@@ -200,17 +251,31 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
         for (int i = 0; i < N; ++i) { w[k][i] = 0.f; dw[k][i] = 0.f; db[k][i] = 0.f; }
         if (t + k * NT < nv) load_param<N>(a.weight, a.param_dtype, (int64_t)(t + k * NT) * N, 1.f, w[k]);
     }
-    int odd = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, odd ^= 1) {
-        const int64_t xo = row * a.ld, yo = row * a.cols;
-        const float mean = a.mean[row], rstd = a.rstd[row];
-        float x[HOLD][N], g[HOLD][N], s1 = 0.f, s2 = 0.f;
+    Raw<IN, N> nx[HOLD] = {}, ng[HOLD] = {};
+    float next_mean = 0.f, next_rstd = 0.f;
+    auto fetch = [&](int64_t row) {
+        next_mean = a.mean[row];
+        next_rstd = a.rstd[row];
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
             if (t + k * NT < nv) {
-                load_n<IN, N>(a.x, xo + (int64_t)(t + k * NT) * N, x[k]);
-                load_n<IN, N>(a.dy, yo + (int64_t)(t + k * NT) * N, g[k]);
+                nx[k] = raw<IN, N>(a.x, row * a.ld + (int64_t)(t + k * NT) * N);
+                ng[k] = raw<IN, N>(a.dy, row * a.cols + (int64_t)(t + k * NT) * N);
             }
+    };
+    if (AHEAD) fetch(blockIdx.x);
+    int odd = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, odd ^= 1) {
+        const int64_t yo = row * a.cols;
+        if (!AHEAD) fetch(row);
+        const float mean = next_mean, rstd = next_rstd;
+        float x[HOLD][N], g[HOLD][N], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k) {
+            unpack<IN, N>(nx[k], x[k]);
+            unpack<IN, N>(ng[k], g[k]);
+        }
+        if (AHEAD && row + gridDim.x < a.rows) fetch(row + gridDim.x);
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
             if (t + k * NT < nv) {
@@ -325,18 +390,18 @@ __global__ __launch_bounds__(1024) void k_norm_fold(const float* partial, int pa
 
 bool words(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <int IN, int N, int NT, int HOLD> hipError_t run_norm(const NormArgs& a, hipStream_t s) {
-    k_norm<IN, N, NT, HOLD><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), NT, 0, s>>>(a);
-    return hipGetLastError();
-}
+// Workgroups of the forward pass: a row each while they fill the GPU twice
+// over at most, then as many as stay resident, each with several rows.
+unsigned norm_grid(int64_t rows, int threads) { return (unsigned)std::min<int64_t>(rows, 256 * (2048 / threads)); }
 
 template <int IN, int N> hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
     const int64_t nv = a.cols / N;
-    if (nv <= 256) return run_norm<IN, N, 256, 1>(a, s);
-    if (nv <= 512) return run_norm<IN, N, 256, 2>(a, s);
-    if (nv <= 1024) return run_norm<IN, N, 256, 4>(a, s);
-    if (nv <= 2048) return run_norm<IN, N, 512, 4>(a, s);
-    return run_norm<IN, N, 512, 0>(a, s);
+    if (nv <= 256) k_norm<IN, N, 256, 1><<<norm_grid(a.rows, 256), 256, 0, s>>>(a);
+    else if (nv <= 512) k_norm<IN, N, 512, 1><<<norm_grid(a.rows, 512), 512, 0, s>>>(a);
+    else if (nv <= 1024) k_norm<IN, N, 512, 2><<<norm_grid(a.rows, 512), 512, 0, s>>>(a);
+    else if (nv <= 2048) k_norm<IN, N, 1024, 2><<<norm_grid(a.rows, 1024), 1024, 0, s>>>(a);
+    else k_norm_long<IN, N, 512><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 512, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 template <int IN, int N> hipError_t pick_grad(const NormGradArgs& a, unsigned grid, hipStream_t s) {

@@ -310,6 +310,7 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
             batch(next, now, s_x1, s_x0, s + D);
         }
     }
+    __builtin_amdgcn_s_waitcnt(0x0F70);                               // copies past the last step write LDS too
     auto& red = reinterpret_cast<Sums*>(s_sc)->of;
     if constexpr (SB > 0) __syncthreads();                            // scales are no longer read
 #pragma unroll
