@@ -20,13 +20,14 @@ static_assert(iqk::A_SILU == IQ_ACT_SILU && iqk::A_GELU == IQ_ACT_GELU && iqk::A
 
 constexpr int64_t kMax31 = ((int64_t)1 << 31) - 1;
 
-// Rows and columns of a layer norm: 31 bits each, and a stride whose
+// Rows of a layer norm: 31 bits; columns: 26, the fold's grid counting threads
+// in 32 bits; and a stride whose
 // products stay far inside 64 bits.
 iq_status check_norm(const iq_desc* d) {
     if (!d) return IQ_EINVAL;
     if (!known_dtype(d->in_dtype)) return IQ_EINVAL;
     if (d->rows < 0 || d->cols < 0 || d->ld_in < d->cols) return IQ_EINVAL;
-    if (d->rows > kMax31 || d->cols > ((int64_t)1 << 30) || d->ld_in > ((int64_t)1 << 40)) return IQ_EUNSUPPORTED;
+    if (d->rows > kMax31 || d->cols > ((int64_t)1 << 26) || d->ld_in > ((int64_t)1 << 40)) return IQ_EUNSUPPORTED;
     int64_t span = 0;
     if (__builtin_mul_overflow(d->rows, d->ld_in, &span) || span > ((int64_t)1 << 59)) return IQ_EUNSUPPORTED;
     return IQ_OK;

@@ -580,7 +580,11 @@ unsigned wide_grid(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<i
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tiles of 256 where they fill the GPU.
+#ifndef FORCE
+#define FORCE -1
+#endif
 bool wide_tiles(int64_t N, int64_t M, int mode) {
+    if (FORCE >= 0) return FORCE;
     return ceil_div(N, mode == FWD ? 128 : 256) * ceil_div(M, 256) * (mode == DW ? 2 : 1) >= 224;
 }
 
@@ -607,9 +611,9 @@ template <int MODE, int ACT> hipError_t run_gemm(GemmArgs& a, hipStream_t s) {
 
 // Parts of dx's sum: enough workgroups for two per CU, at least 8 steps each.
 int dx_parts(int64_t tokens, int64_t cols, int64_t features) {
-    if (wide_tiles(cols, tokens, DX)) return 1;
-    const int64_t tiles = ceil_div(tokens, 128) * ceil_div(cols, 128), steps = 2 * ceil_div(features, BK);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, tiles), steps / 8, 16}));
+    const bool wide = wide_tiles(cols, tokens, DX);
+    const int64_t side = wide ? 256 : 128, tiles = ceil_div(tokens, side) * ceil_div(cols, side), steps = 2 * ceil_div(features, BK);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({(wide ? 256 : 512) / std::max<int64_t>(1, tiles), steps / 8, 16}));
 }
 
 constexpr int64_t kAlign = 256;

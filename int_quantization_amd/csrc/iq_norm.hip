@@ -235,7 +235,7 @@ __global__ __launch_bounds__(NT) void k_norm_long(NormArgs a) {
 // Backward: workgroup p of the grid takes rows p, p + gridDim.x, ... and a
 // thread the same columns of every one of them, so the sums over rows stay
 // in registers until the workgroup's last row and one partial row per
-// workgroup reaches memory.
+// workgroup reaches memory; a lone workgroup writes the gradients.
 template <int IN, int N, int NT, int HOLD>
 __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
     constexpr int NW = NT / 64;
@@ -267,13 +267,17 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
     int odd = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, odd ^= 1) {
         const int64_t yo = row * a.cols;
-        if (!AHEAD) fetch(row);
-        const float mean = next_mean, rstd = next_rstd;
+        const float mean = AHEAD ? next_mean : a.mean[row], rstd = AHEAD ? next_rstd : a.rstd[row];
         float x[HOLD][N], g[HOLD][N], s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
-            unpack<IN, N>(nx[k], x[k]);
-            unpack<IN, N>(ng[k], g[k]);
+            if constexpr (AHEAD) {
+                unpack<IN, N>(nx[k], x[k]);
+                unpack<IN, N>(ng[k], g[k]);
+            } else if (t + k * NT < nv) {
+                load_n<IN, N>(a.x, row * a.ld + (int64_t)(t + k * NT) * N, x[k]);
+                load_n<IN, N>(a.dy, yo + (int64_t)(t + k * NT) * N, g[k]);
+            }
         }
         if (AHEAD && row + gridDim.x < a.rows) fetch(row + gridDim.x);
 #pragma unroll
@@ -308,8 +312,17 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
 #pragma unroll
     for (int k = 0; k < HOLD; ++k)
         if (t + k * NT < nv) {
-            store_n<D_F32, N>(pw, (int64_t)(t + k * NT) * N, dw[k]);
-            store_n<D_F32, N>(pw + a.cols, (int64_t)(t + k * NT) * N, db[k]);
+            const int64_t c = (int64_t)(t + k * NT) * N;
+            if (gridDim.x == 1) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    if (a.dweight) store_param(a.dweight, a.param_dtype, c + i, dw[k][i]);
+                    if (a.dbias) store_param(a.dbias, a.param_dtype, c + i, db[k][i]);
+                }
+            } else {
+                store_n<D_F32, N>(pw, c, dw[k]);
+                store_n<D_F32, N>(pw + a.cols, c, db[k]);
+            }
         }
 }
 
@@ -376,9 +389,12 @@ __global__ __launch_bounds__(1024) void k_norm_fold(const float* partial, int pa
     __shared__ float red[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;      // of the 2 cols columns of a partial row
+    float v[kNormParts / 16];                               // loads of all rows in flight at once
+#pragma unroll
+    for (int k = 0; k < kNormParts / 16; ++k) v[k] = wave + 16 * k < parts && c < 2 * cols ? partial[(wave + 16 * k) * 2 * cols + c] : 0.f;
     float s = 0.f;
-    if (c < 2 * cols)
-        for (int p = wave; p < parts; p += 16) s += partial[(int64_t)p * 2 * cols + c];
+#pragma unroll
+    for (int k = 0; k < kNormParts / 16; ++k) s += v[k];
     red[wave][lane] = s;
     __syncthreads();
     if (wave != 0 || c >= 2 * cols) return;
@@ -390,6 +406,8 @@ __global__ __launch_bounds__(1024) void k_norm_fold(const float* partial, int pa
 
 bool words(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+constexpr int64_t kNormHeld = 2048;      // vectors of a row that a workgroup's registers hold
+
 // Workgroups of the forward pass: a row each while they fill the GPU twice
 // over at most, then as many as stay resident, each with several rows.
 unsigned norm_grid(int64_t rows, int threads) { return (unsigned)std::min<int64_t>(rows, 256 * (2048 / threads)); }
@@ -399,17 +417,20 @@ template <int IN, int N> hipError_t pick_norm(const NormArgs& a, hipStream_t s) 
     if (nv <= 256) k_norm<IN, N, 256, 1><<<norm_grid(a.rows, 256), 256, 0, s>>>(a);
     else if (nv <= 512) k_norm<IN, N, 512, 1><<<norm_grid(a.rows, 512), 512, 0, s>>>(a);
     else if (nv <= 1024) k_norm<IN, N, 512, 2><<<norm_grid(a.rows, 512), 512, 0, s>>>(a);
-    else if (nv <= 2048) k_norm<IN, N, 1024, 2><<<norm_grid(a.rows, 1024), 1024, 0, s>>>(a);
+    else if (nv <= kNormHeld) k_norm<IN, N, 1024, 2><<<norm_grid(a.rows, 1024), 1024, 0, s>>>(a);
     else k_norm_long<IN, N, 512><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 512, 0, s>>>(a);
     return hipGetLastError();
 }
+
+// Rows that one workgroup takes in less time than the fold's launch.
+constexpr int64_t kNormLone = 4;
 
 template <int IN, int N> hipError_t pick_grad(const NormGradArgs& a, unsigned grid, hipStream_t s) {
     const int64_t nv = a.cols / N;
     if (nv <= 256) k_norm_grad<IN, N, 256, 1><<<grid, 256, 0, s>>>(a);
     else if (nv <= 512) k_norm_grad<IN, N, 512, 1><<<grid, 512, 0, s>>>(a);
     else if (nv <= 1024) k_norm_grad<IN, N, 512, 2><<<grid, 512, 0, s>>>(a);
-    else if (nv <= 2048) k_norm_grad<IN, N, 1024, 2><<<grid, 1024, 0, s>>>(a);
+    else if (nv <= kNormHeld) k_norm_grad<IN, N, 1024, 2><<<grid, 1024, 0, s>>>(a);
     else k_norm_grad_long<IN, N, 512><<<grid, 512, 0, s>>>(a);
     return hipGetLastError();
 }
@@ -426,16 +447,17 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_layer_norm_grad(const NormGradArgs& a, hipStream_t s) {
-    const int parts = (int)std::min<int64_t>(a.rows, kNormParts);
+    const bool wide = a.cols % 8 == 0 && (a.ld * (a.in_dtype == D_F32 ? 4 : 2)) % 16 == 0 && words(a.x) && words(a.dy) &&
+                      words(a.dx) && words(a.weight);
+    const bool lone = a.rows > 0 && a.rows <= kNormLone && a.cols / (wide ? 8 : 1) <= kNormHeld;
+    const int parts = lone ? 1 : (int)std::min<int64_t>(a.rows, kNormParts);
     if (parts > 0) {
-        const bool wide = a.cols % 8 == 0 && (a.ld * (a.in_dtype == D_F32 ? 4 : 2)) % 16 == 0 && words(a.x) &&
-                          words(a.dy) && words(a.dx) && words(a.weight);
         hipError_t e;
         if (a.in_dtype == D_F32) e = wide ? pick_grad<D_F32, 8>(a, parts, s) : pick_grad<D_F32, 1>(a, parts, s);
         else e = wide ? pick_grad<D_BF16, 8>(a, parts, s) : pick_grad<D_BF16, 1>(a, parts, s);
         if (e != hipSuccess) return e;
     }
-    if (a.dweight || a.dbias)
+    if ((a.dweight || a.dbias) && !lone)
         k_norm_fold<<<(unsigned)((2 * a.cols + 63) / 64), 1024, 0, s>>>(a.partial, parts, a.cols, a.param_dtype, a.dweight,
                                                                       a.dbias);
     return hipGetLastError();
