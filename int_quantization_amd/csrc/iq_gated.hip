@@ -52,70 +52,12 @@ struct GemmArgs {
     int32_t tiles_n, tiles_m;     // tiles_m counts both weights in DW
     uint32_t tiles;
     int32_t per_xcd;
-    int32_t split_steps;          // DX: steps of one part of k
-    int32_t parts;                // DX: parts of k; above 1 the sums go to `partial`
+    int32_t split_steps;          // DX, DW: steps of one part of k
+    int32_t parts;                // DX, DW: parts of k; above 1 the sums go to `partial`
     uint16_t* out[2];
     float* saved;                 // FWD: g and u [2][M][N], may be null
-    float* partial;               // DX: [parts][M][N]
+    float* partial;               // DX: [parts][M][N], DW: [parts][2][M][N]
 };
-
-// A tile of 128 rows (or columns) by 64 k in LDS: 16 KB.
-//   k-contiguous: 16-byte slot s of row r at slot s ^ (r & 7) of its 128 bytes;
-//   k-strided:    32-byte slot c of row k at slot c ^ (k & 3 | k >> 1 & 4) of
-//                 its 256 bytes: the 8 rows that half a wave reads at a time
-//                 fall into the 8 different slots.
-struct Half { u4v w[1024]; };
-
-// One wave's share of the copies of a Half: NI instructions of 64 x 16 bytes.
-template <bool KC, int NI> struct Copy {
-    uint32_t off[NI];     // byte offset from the tile's first element
-    int32_t kk;           // first k that the lane's word holds (KC: of every instruction; else of instruction 0)
-    // `left`: rows (KC) or columns (else) from the tile's first to the matrix's last
-    __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int64_t left) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int q = wave * NI + i;
-            if constexpr (KC) {
-                const int r = 8 * q + (lane >> 3), slot = (lane & 7) ^ (lane >> 3);
-                off[i] = r < left ? (uint32_t)(r * ld * 2) + slot * 16u : kOutside;
-            } else {
-                const int k = 4 * q + (lane >> 4), col = 8 * ((lane & 15) ^ (2 * ((k & 3) | ((k >> 1) & 4))));
-                off[i] = col < left ? (uint32_t)(k * ld * 2) + col * 2u : kOutside;
-            }
-        }
-        kk = KC ? 8 * ((lane & 7) ^ (lane >> 3)) : 4 * wave * NI + (lane >> 4);
-    }
-    // `base`: the tile's first element at this step; `left`: k from there to the end
-    __device__ __forceinline__ void issue(const uint16_t* base, int left, int wave, Half& to) const {
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, (int)kOutside, 0x00020000);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const uint32_t o = kk + (KC ? 0 : 4 * i) < left ? off[i] : kOutside;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)&to.w[(wave * NI + i) * 64], 16, o, 0, 0, 0);
-        }
-    }
-};
-
-// MFMA operand of rows (columns) rb .. rb + 15 at k 32 ks .. + 31 of the Half
-// that starts `at` bytes into LDS object T: lane l has row rb + l % 16 and
-// k 32 ks + 8 (l / 16) .. + 7.  The address is one offset from the object,
-// not a chain of members: past a few links the compiler no longer sees which
-// object a read is from and lets it wait for copies into the others.
-template <bool KC, class T> __device__ __forceinline__ bf8v fragment(const T& t, uint32_t at, int rb, int ks, int lane) {
-    const uint32_t i = lane & 15, h = lane >> 4;
-    const char* base = reinterpret_cast<const char*>(&t);
-    if constexpr (KC) {
-        return *reinterpret_cast<const bf8v*>(base + (at + (rb + i) * 128 + ((4 * ks + h) ^ (i & 7)) * 16));
-    } else {
-        // the transposing read gives lane i of 16 element i of the four rows
-        // that its group's lanes 4 j + c name by column 4 c of row j
-        const uint32_t k = 32 * ks + 8 * h + (i >> 2), slot = (rb >> 4) ^ ((i >> 2) | ((h & 1) << 2));
-        const uint32_t o = at + k * 256 + slot * 32 + (i & 3) * 8;
-        const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(base + o));
-        const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(base + (o + 4 * 256)));
-        return __builtin_bit_cast(bf8v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    }
-}
 
 // Two neighbouring 16 x 16 results (n 0..15 in a, 16..31 in b; the lane's m)
 // to BF16 memory: the lanes of even and odd 16s exchange halves so that each
@@ -145,121 +87,13 @@ __device__ __forceinline__ bool tile_of(const GemmArgs& a, int& tn, int& tm) {
     return true;
 }
 
-// 128 x 128 tiles (FWD: 64 features of each weight), 4 waves of 64 x 64, two
-// LDS stages: the copies of step s + 1 are in flight during step s.
-template <int MODE, int ACT> __global__ __launch_bounds__(256, 2) void k_gemm(GemmArgs a) {
-    constexpr bool PK = MODE == FWD, QK = MODE != DW;
-    constexpr int kTileN = MODE == FWD ? 64 : 128;
-    __shared__ Half P0, P1, Q0, Q1;
-    int tn, tm;
-    if (!tile_of(a, tn, tm)) return;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wn = wave & 1, wm = wave >> 1;
-    const int sel = MODE == DW && tm >= a.tiles_m / 2 ? 1 : 0;        // which weight's gradient
-    const int n0 = tn * kTileN, m0 = (MODE == DW ? tm - sel * (a.tiles_m / 2) : tm) * 128;
-    const int seg_steps = (a.K + BK - 1) / BK;
-    const int all = MODE == DX ? 2 * seg_steps : seg_steps;
-    const int first = MODE == DX ? (int)blockIdx.y * a.split_steps : 0;
-    const int last = MODE == DX ? min(all, first + a.split_steps) : all;
-
-    Copy<PK, 4> cp;
-    Copy<QK, 4> cq;
-    // FWD: waves 0 and 1 copy the gate's 64 rows, 2 and 3 the up projection's
-    if (MODE == FWD) {
-        cp.init(wave, lane, a.ldp, (wave >= 2 ? 64 : 0) + (int64_t)a.N - n0);
-        if (wave < 2)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (8 * (4 * wave + i) + (lane >> 3) >= a.N - n0) cp.off[i] = kOutside;
-    } else {
-        cp.init(wave, lane, a.ldp, (int64_t)a.N - n0);
-    }
-    cq.init(wave, lane, a.ldq, (int64_t)a.M - m0);
-
-    auto issue = [&](int s, Half& P, Half& Q) {
-        const int seg = MODE == DX && s >= seg_steps ? 1 : 0;
-        const int k0 = (s - seg * seg_steps) * BK, left = a.K - k0;
-        const uint16_t* pb;
-        if (MODE == FWD) pb = wave < 2 ? a.p[0] + (int64_t)n0 * a.ldp + k0 : a.p[1] + ((int64_t)n0 - 64) * a.ldp + k0;
-        else pb = a.p[MODE == DX ? seg : 0] + (int64_t)k0 * a.ldp + n0;
-        const uint16_t* qb = QK ? a.q[seg] + (int64_t)m0 * a.ldq + k0 : a.q[sel] + (int64_t)k0 * a.ldq + m0;
-        cp.issue(pb, left, wave, P);
-        cq.issue(qb, left, wave, Q);
-    };
-    auto row_of = [&](int t) { return MODE == FWD ? (t >> 1) * 64 + wn * 32 + (t & 1) * 16 : wn * 64 + t * 16; };
-
-    f4v acc[4][4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int m = 0; m < 4; ++m) acc[n][m] = f4v{0.f, 0.f, 0.f, 0.f};
-    auto step = [&](int s, const Half& P, const Half& Q, Half& nP, Half& nQ) {
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0F70);           // vmcnt(0): this wave's copies of step s have landed
-        lds_barrier();                                // every wave's have; step s - 1's tiles are free
-        if (s + 1 < last) issue(s + 1, nP, nQ);
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf8v pf[4], qf[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) pf[n] = fragment<PK>(P, 0, row_of(n), ks, lane);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) qf[m] = fragment<QK>(Q, 0, wm * 64 + m * 16, ks, lane);
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) acc[n][m] = mfma(pf[n], qf[m], acc[n][m]);
-        }
-    };
-    if (first < last) issue(first, P0, Q0);
-    for (int s = first; s < last; s += 2) {
-        step(s, P0, Q0, P1, Q1);
-        if (s + 1 < last) step(s + 1, P1, Q1, P0, Q0);
-    }
-
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const int row = m0 + wm * 64 + m * 16 + (lane & 15);
-        const bool in = row < a.M;
-        if constexpr (MODE == FWD) {
-            const int nb = n0 + wn * 32;
-            uint16_t* hr = in ? a.out[0] + (int64_t)row * a.N : nullptr;
-            f4v h[2];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (a.saved) {
-                    float* gr = in ? a.saved + (int64_t)row * a.N : nullptr;
-                    float* ur = in ? a.saved + ((int64_t)a.M + row) * a.N : nullptr;
-                    store_f4(gr, nb + 16 * t + 4 * (lane >> 4), a.N, acc[t][m]);
-                    store_f4(ur, nb + 16 * t + 4 * (lane >> 4), a.N, acc[2 + t][m]);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) h[t][e] = act<ACT>(acc[t][m][e]) * acc[2 + t][m][e];
-            }
-            store_pair(hr, nb, a.N, lane, h[0], h[1]);
-        } else {
-#pragma unroll
-            for (int t = 0; t < 4; t += 2) {
-                const int nb = n0 + wn * 64 + t * 16;
-                if (MODE == DX && a.parts > 1) {
-                    float* pr = in ? a.partial + ((int64_t)blockIdx.y * a.M + row) * a.N : nullptr;
-                    store_f4(pr, nb + 4 * (lane >> 4), a.N, acc[t][m]);
-                    store_f4(pr, nb + 16 + 4 * (lane >> 4), a.N, acc[t + 1][m]);
-                } else {
-                    store_pair(in ? a.out[sel] + (int64_t)row * a.N : nullptr, nb, a.N, lane, acc[t][m], acc[t + 1][m]);
-                }
-            }
-        }
-    }
-}
-
-// ---- 256 x 256 tiles ----------------------------------------------------------
-// Four waves of 128 x 128 results, one to a SIMD: the results fill 256
-// registers of a lane and every operand fragment serves 8 products, so that
-// the reads from LDS take half as long as the products.  (Waves of 64 x 64
-// read as long as they multiply.)  A lone wave hides nothing by itself, so the
-// instructions are laid out by hand between single products.  A step of 64 k:
+// Tiles of 2 W x 2 W results, W = 16 T: four waves of W x W.
+//
+// T = 8, one workgroup on a CU: the results fill 256 registers of a lane and
+// every operand fragment serves 8 products, so that the reads from LDS take
+// half as long as the products.  A lone wave on a SIMD hides nothing by
+// itself, so the instructions are laid out by hand between single products.
+// A step of 64 k:
 //   products of its k 0..31   | reads of its k 32..63, copies of Q of step s + 2
 //   wait for step s + 1, barrier
 //   products of its k 32..63  | reads of k 0..31 of step s + 1, copies of P of
@@ -268,29 +102,42 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 2) void k_gemm(Ge
 // the copies run evenly, one in eight products.  (Sixteen in 64 products stall
 // the wave at the copies; steps of 32 k with four stages of both operands read
 // k-contiguous rows in halves of 128-byte lines, which costs as much.)
-constexpr uint32_t kStage = 32768;                 // 256 rows or columns of one operand, 64 k
+//
+// T = 4, two workgroups on a CU: the same for grids that T = 8 leaves too
+// small; the reads take as long as the products.
 constexpr int kStagesP = 2, kStagesQ = 3;
 
-// One wave's share of the copies of a stage: instructions 4 wave .. + 3 of
-// each half, a half being 128 rows or columns, laid out like a Half.
-template <bool KC> struct WideCopy {
-    uint32_t off[8];      // byte offset from the tile's first element of the step
+// A half of a stage: W rows (columns) by 64 k of one operand.
+//   k-contiguous: 16-byte slot s of row r at slot s ^ (r & 7) of its 128 bytes;
+//   k-strided:    32-byte slot c of row k at slot c ^ turn(k) of its 2 W
+//                 bytes, so that the 8 rows that half a wave reads at a time
+//                 (k 0-3 and 8-11 and so on) are in different banks.
+template <int T> constexpr uint32_t kHalf = 2048 * T;
+template <int T> __device__ __forceinline__ int turn(int k) {
+    return T == 8 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
+}
+
+// One wave's share of the copies of a stage: T / 2 instructions of each half.
+template <bool KC, int T> struct Copy {
+    static constexpr int NI = T / 2;
+    uint32_t off[T];      // byte offset from the tile's first element of the step
     int32_t kk;           // KC: first k that the lane's words hold
     uint64_t base;        // address of the step's first element
     int32_t left;         // k from there to the end
     int32_t ld2;          // bytes of a row
-    // `rest` as `left` of Copy.  `pair`: the halves are 64 gate rows and 64 up
-    // rows each, and the wave's are from one of the two matrices.
+    // `rest`: rows (KC) or columns (else) from the tile's first to the
+    // matrix's last.  `pair`: the halves are W / 2 gate rows and W / 2 up rows
+    // each, and the wave's are from one of the two matrices.
     __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int64_t rest, bool pair) {
         ld2 = (int32_t)(2 * ld);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int half = i >> 2, q = 4 * wave + (i & 3);
+        for (int i = 0; i < T; ++i) {
+            const int half = i / NI, q = NI * wave + i % NI;
             if constexpr (KC) {
-                const int r0 = 8 * q + (lane >> 3), r = pair ? 64 * half + (r0 & 63) : 128 * half + r0;
+                const int r0 = 8 * q + (lane >> 3), r = pair ? 8 * T * half + (r0 & (8 * T - 1)) : 16 * T * half + r0;
                 off[i] = r < rest ? (uint32_t)(r * ld * 2) + 16u * ((lane & 7) ^ (lane >> 3)) : kOutside;
             } else {
-                const int k = 4 * q + (lane >> 4), col = 128 * half + 8 * ((lane & 15) ^ (2 * ((k & 3) | ((k >> 1) & 4))));
+                const int k = (32 / T) * q + lane / (2 * T), col = 16 * T * half + 8 * ((lane & (2 * T - 1)) ^ (2 * turn<T>(k)));
                 off[i] = col < rest ? (uint32_t)(k * ld * 2) + col * 2u : kOutside;
             }
         }
@@ -311,6 +158,8 @@ template <bool KC> struct WideCopy {
     }
     // The lane's offset in copy i; a k-contiguous operand's words past k are outside.
     __device__ __forceinline__ uint32_t at(int i) const { return !KC || kk < left ? off[i] : kOutside; }
+    // The byte of copy i in a stage, from that of the wave's first.
+    static constexpr uint32_t to(int i) { return (i / NI) * kHalf<T> + (i % NI) * 1024u; }
 };
 
 // Copies are written out, for the compiler would take every later read of LDS
@@ -321,25 +170,29 @@ __device__ __forceinline__ void copy_1k(uint32_t off, u4v buf, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(buf) : "memory");
 }
 
-// LDS addresses of a wave's fragments of one operand in a stage: rows
-// (columns) 16 t .. + 15 of its half, k 32 ks .. + 31, as `fragment` has them.
-template <bool KC> struct WideRead {
-    uint32_t at[KC ? 2 : 8];       // KC: by ks; else by t, which the turn of a row's slots mixes with the lane
+// LDS addresses of a wave's fragments of one operand in a stage: fragment t is
+// rows (columns) 16 t .. + 15 of its half; lane l has row 16 t + l % 16 and
+// k 32 ks + 8 (l / 16) .. + 7.
+template <bool KC, int T> struct Read {
+    uint32_t at[KC ? 2 : T];       // KC: by ks; else by t, which the turn of a row's slots mixes with the lane
     __device__ __forceinline__ void init(uint32_t stage, int half, int lane) {
         const uint32_t i = lane & 15, h = lane >> 4;
 #pragma unroll
-        for (uint32_t e = 0; e < (KC ? 2 : 8); ++e)
-            at[e] = stage + half * 16384u + (KC ? i * 128 + ((4 * e + h) ^ (i & 7)) * 16
-                                                : (8 * h + (i >> 2)) * 256 + (e ^ ((i >> 2) | ((h & 1) << 2))) * 32 + (i & 3) * 8);
+        for (uint32_t e = 0; e < (KC ? 2 : T); ++e)
+            at[e] = stage + half * kHalf<T> + (KC ? i * 128 + ((4 * e + h) ^ (i & 7)) * 16
+                                                  : (8 * h + (i >> 2)) * (32 * T) + (e ^ turn<T>(8 * h + (i >> 2))) * 32 + (i & 3) * 8);
     }
-    // part e of 8 of the way to another stage
-    __device__ __forceinline__ void move(int e, uint32_t by) { if (e < (KC ? 2 : 8)) at[e] += by; }
+    // part e of T of the way to another stage
+    __device__ __forceinline__ void move(int e, uint32_t by) { if (e < (KC ? 2 : T)) at[e] += by; }
     __device__ __forceinline__ bf8v get(int t, int ks) const {
         if constexpr (KC) {
             return *(__attribute__((address_space(3))) const bf8v*)(uintptr_t)(at[ks] + t * 2048);
         } else {
-            const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(uintptr_t)(at[t] + ks * 8192));
-            const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(uintptr_t)(at[t] + ks * 8192 + 1024));
+            // the transposing read gives lane i of 16 element i of the four
+            // rows that its group's lanes 4 j + c name by column 4 c of row j;
+            // four rows on, a row's slots are turned alike
+            const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(uintptr_t)(at[t] + ks * 1024 * T));
+            const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(uintptr_t)(at[t] + ks * 1024 * T + 128 * T));
             return __builtin_bit_cast(bf8v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
     }
@@ -360,12 +213,12 @@ template <uint32_t TO> __device__ __forceinline__ void mfma_and_copy(f4v& c, bf8
     asm volatile("s_add_u32 m0, %3, %4\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %5, %6, 0 offen lds"
                  : "+a"(c) : "v"(p), "v"(q), "s"(to), "i"(TO), "v"(off), "s"(buf) : "memory", "scc");
 }
-__device__ __forceinline__ void settle(f4v (&acc)[8][8]) {
+template <int T> __device__ __forceinline__ void settle(f4v (&acc)[T][T]) {
     asm volatile("s_nop 15\ns_nop 15" ::: "memory");
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
-        asm volatile("" : "+a"(acc[n][0]), "+a"(acc[n][1]), "+a"(acc[n][2]), "+a"(acc[n][3]), "+a"(acc[n][4]), "+a"(acc[n][5]),
-                     "+a"(acc[n][6]), "+a"(acc[n][7]));
+    for (int n = 0; n < T; ++n)
+#pragma unroll
+        for (int m = 0; m < T; m += 4) asm volatile("" : "+a"(acc[n][m]), "+a"(acc[n][m + 1]), "+a"(acc[n][m + 2]), "+a"(acc[n][m + 3]));
     __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -374,9 +227,10 @@ template <class F, int... I> __device__ __forceinline__ void in_turn(F&& f, std:
     (f(std::integral_constant<int, I>{}), ...);
 }
 
-template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wide(GemmArgs a) {
+template <int MODE, int ACT, int T> __global__ __launch_bounds__(256, T == 8 ? 1 : 2) void k_gemm(GemmArgs a) {
     constexpr bool PK = MODE == FWD, QK = MODE != DW;
-    constexpr int kTileN = MODE == FWD ? 128 : 256;
+    constexpr int W = 16 * T, kTileN = MODE == FWD ? W : 2 * W;
+    constexpr uint32_t kStage = 2 * kHalf<T>;
     __shared__ __align__(1024) char lds[(kStagesP + kStagesQ) * kStage];
     int tn, tm;
     if (!tile_of(a, tn, tm)) return;
@@ -384,15 +238,15 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wi
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave & 1, wm = wave >> 1;
     const int sel = MODE == DW && tm >= a.tiles_m / 2 ? 1 : 0;        // which weight's gradient
-    const int n0 = tn * kTileN, m0 = (MODE == DW ? tm - sel * (a.tiles_m / 2) : tm) * 256;
+    const int n0 = tn * kTileN, m0 = (MODE == DW ? tm - sel * (a.tiles_m / 2) : tm) * 2 * W;
     const int seg_steps = (a.K + BK - 1) / BK;
     const int all = MODE == DX ? 2 * seg_steps : seg_steps;
-    const int first = MODE == DX ? (int)blockIdx.y * a.split_steps : 0;
-    const int last = MODE == DX ? min(all, first + a.split_steps) : all;
+    const int first = MODE == FWD ? 0 : (int)blockIdx.y * a.split_steps;
+    const int last = MODE == FWD ? all : min(all, first + a.split_steps);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)lds;
 
-    WideCopy<PK> cp;
-    WideCopy<QK> cq;
+    Copy<PK, T> cp;
+    Copy<QK, T> cq;
     cp.init(wave, lane, a.ldp, (int64_t)a.N - n0, MODE == FWD);
     cq.init(wave, lane, a.ldq, (int64_t)a.M - m0, false);
     // first elements of both operands; DX goes on to the second pair where the first ends
@@ -415,26 +269,26 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wi
         if (MODE == DX && ++sq == seg_steps) cq.start(q1, 0, a.K);
     };
 
-    f4v acc[8][8];
+    f4v acc[T][T];
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+    for (int n = 0; n < T; ++n)
 #pragma unroll
-        for (int m = 0; m < 8; ++m) acc[n][m] = f4v{0.f, 0.f, 0.f, 0.f};
-    bf8v pa[8], qa[8], pb[8], qb[8];
+        for (int m = 0; m < T; ++m) acc[n][m] = f4v{0.f, 0.f, 0.f, 0.f};
+    bf8v pa[T], qa[T], pb[T], qb[T];
     uint32_t p = 0, q = kStagesP * kStage, q2 = q + 2 * kStage;       // stages of this step; of Q two steps on
-    WideRead<PK> rp;
-    WideRead<QK> rq;
+    Read<PK, T> rp;
+    Read<QK, T> rq;
     rp.init(lds0 + p, wn, lane);
     rq.init(lds0 + q, wm, lane);
-    auto read = [&](int i, int ks, bf8v (&pf)[8], bf8v (&qf)[8]) {    // i: 0 .. 15
+    auto read = [&](int i, int ks, bf8v (&pf)[T], bf8v (&qf)[T]) {    // i: 0 .. 2 T - 1
         if (i & 1) qf[i >> 1] = rq.get(i >> 1, ks);
         else pf[i >> 1] = rp.get(i >> 1, ks);
     };
-    const uint32_t to0 = lds0 + (uint32_t)wave * 4096u;               // byte of LDS that the wave's copies start at
+    const uint32_t to0 = lds0 + (uint32_t)wave * (512u * T);              // byte of LDS that the wave's copies start at
     auto copy_all = [&](const auto& c, uint32_t stage) {
         const u4v buf = c.buffer();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) copy_1k(c.at(i), buf, to0 + stage + (i >> 2) * 16384u + (i & 3) * 1024u);
+        for (int i = 0; i < T; ++i) copy_1k(c.at(i), buf, to0 + stage + c.to(i));
     };
     copy_all(cp, p);
     copy_all(cq, q);
@@ -443,43 +297,45 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wi
     advance_p();
     copy_all(cp, p + kStage);
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x4F70);               // vmcnt(16): this wave's copies of the first step have landed
+    __builtin_amdgcn_s_waitcnt(T == 8 ? 0x4F70 : 0x0F78);     // vmcnt(2 T): this wave's copies of the first step have landed
     lds_barrier();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) read(i, 0, pa, qa);
+    for (int i = 0; i < 2 * T; ++i) read(i, 0, pa, qa);
 
-    // Product i of 64, in blocks of 2 x 2: a fragment's first use comes after
-    // its read in the order of `read`.  One in eight has a copy behind it.
-    auto products = [&](const bf8v (&pf)[8], const bf8v (&qf)[8], const auto& copies, const u4v& buf, uint32_t stage, auto&& between) {
+    // Product i of T^2, in blocks of 2 x 2: a fragment's first use comes after
+    // its read in the order of `read`.  One in T has a copy behind it.
+    auto products = [&](const bf8v (&pf)[T], const bf8v (&qf)[T], const auto& copies, const u4v& buf, uint32_t stage, auto&& between) {
         auto one = [&](auto index) {
-            constexpr int i = decltype(index)::value, c = i >> 3;
-            constexpr int n = 2 * (i >> 4) + ((i >> 1) & 1), m = 2 * ((i >> 2) & 3) + (i & 1);
+            constexpr int i = decltype(index)::value, c = i / T;
+            constexpr int n = 2 * (i / (2 * T)) + ((i >> 1) & 1), m = 2 * ((i >> 2) % (T / 2)) + (i & 1);
             between(i);
-            if constexpr (i % 8 == 5) mfma_and_copy<(c >> 2) * 16384u + (c & 3) * 1024u>(acc[n][m], pf[n], qf[m], copies.at(c), buf, to0 + stage);
+            if constexpr (i % T == T - 3) mfma_and_copy<Copy<true, T>::to(c)>(acc[n][m], pf[n], qf[m], copies.at(c), buf, to0 + stage);
             else mfma_in_place(acc[n][m], pf[n], qf[m]);
             __builtin_amdgcn_sched_barrier(0);
         };
-        in_turn(one, std::make_integer_sequence<int, 64>{});
+        in_turn(one, std::make_integer_sequence<int, T * T>{});
     };
+    // reads: all of a step's before its wait, and spread over what follows it
+    constexpr int kBefore = T == 8 ? 3 : 1, kAfter = T == 8 ? 4 : 1, kEnd = T * T;
     advance_q();
     u4v bufp, bufq = cq.buffer();
     for (int s = first; s < last; ++s) {
         const uint32_t np = p ^ kStage, nq = q == (kStagesP + kStagesQ - 1) * kStage ? kStagesP * kStage : q + kStage;
         products(pa, qa, cq, bufq, q2, [&](int i) {
-            if (i % 3 == 0 && i < 48) read(i / 3, 1, pb, qb);
-            if (i == 50) advance_p();
-            if (i == 54) bufp = cp.buffer();
-            if (i >= 56) { rp.move(i - 56, np - p); rq.move(i - 56, nq - q); }
+            if (i % kBefore == 0 && i < 2 * T * kBefore) read(i / kBefore, 1, pb, qb);
+            if (i == kEnd - T - 6) advance_p();
+            if (i == kEnd - T - 2) bufp = cp.buffer();
+            if (i >= kEnd - T) { rp.move(i - kEnd + T, np - p); rq.move(i - kEnd + T, nq - q); }
         });
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0078);           // vmcnt(8), lgkmcnt(0): step s + 1 has landed, step s is read
+        __builtin_amdgcn_s_waitcnt(0x0070 + T);       // vmcnt(T), lgkmcnt(0): step s + 1 has landed, step s is read
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
         products(pb, qb, cp, bufp, p, [&](int i) {
-            if (i % 4 == 0) read(i / 4, 0, pa, qa);
-            if (i == 42) advance_q();
-            if (i == 50) bufq = cq.buffer();
+            if (i % kAfter == 0 && i < 2 * T * kAfter) read(i / kAfter, 0, pa, qa);
+            if (i == kEnd - T - 6) advance_q();
+            if (i == kEnd - T - 2) bufq = cq.buffer();
         });
         q2 = q;                                       // step s + 3 takes the stage of step s
         p = np;
@@ -487,35 +343,35 @@ template <int MODE, int ACT> __global__ __launch_bounds__(256, 1) void k_gemm_wi
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0x0F70);               // the copies past the last step write LDS too
-    settle(acc);
+    settle<T>(acc);
 
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-        const int row = m0 + wm * 128 + m * 16 + (lane & 15);
+    for (int m = 0; m < T; ++m) {
+        const int row = m0 + wm * W + m * 16 + (lane & 15);
         const bool in = row < a.M;
         if constexpr (MODE == FWD) {
-            const int nb = n0 + wn * 64;
+            const int nb = n0 + wn * (W / 2);
             uint16_t* hr = in ? a.out[0] + (int64_t)row * a.N : nullptr;
             float* gr = in && a.saved ? a.saved + (int64_t)row * a.N : nullptr;
             float* ur = in && a.saved ? a.saved + ((int64_t)a.M + row) * a.N : nullptr;
 #pragma unroll
-            for (int t = 0; t < 4; t += 2) {
+            for (int t = 0; t < T / 2; t += 2) {
                 f4v h[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     store_f4(gr, nb + 16 * (t + e) + 4 * (lane >> 4), a.N, acc[t + e][m]);
-                    store_f4(ur, nb + 16 * (t + e) + 4 * (lane >> 4), a.N, acc[4 + t + e][m]);
+                    store_f4(ur, nb + 16 * (t + e) + 4 * (lane >> 4), a.N, acc[T / 2 + t + e][m]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) h[e][j] = act<ACT>(acc[t + e][m][j]) * acc[4 + t + e][m][j];
+                    for (int j = 0; j < 4; ++j) h[e][j] = act<ACT>(acc[t + e][m][j]) * acc[T / 2 + t + e][m][j];
                 }
                 store_pair(hr, nb + 16 * t, a.N, lane, h[0], h[1]);
             }
         } else {
 #pragma unroll
-            for (int t = 0; t < 8; t += 2) {
-                const int nb = n0 + wn * 128 + t * 16;
-                if (MODE == DX && a.parts > 1) {
-                    float* pr = in ? a.partial + ((int64_t)blockIdx.y * a.M + row) * a.N : nullptr;
+            for (int t = 0; t < T; t += 2) {
+                const int nb = n0 + wn * W + t * 16;
+                if (a.parts > 1) {
+                    float* pr = in ? a.partial + (((int64_t)blockIdx.y * (MODE == DW ? 2 : 1) + sel) * a.M + row) * a.N : nullptr;
                     store_f4(pr, nb + 4 * (lane >> 4), a.N, acc[t][m]);
                     store_f4(pr, nb + 16 + 4 * (lane >> 4), a.N, acc[t + 1][m]);
                 } else {
@@ -558,16 +414,17 @@ template <int ACT> __global__ __launch_bounds__(256) void k_gate_grad(const uint
     }
 }
 
-// The parts of dx added in order and rounded, 8 elements per thread.
-__global__ __launch_bounds__(256) void k_join(const float* partial, int parts, int64_t n, uint16_t* out) {
+// The parts of a product added in order and rounded, 8 elements per thread;
+// elements from `first` on go to the second output.
+__global__ __launch_bounds__(256) void k_join(const float* partial, int parts, int64_t n, int64_t first, uint16_t* out, uint16_t* second) {
     for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 256 * 8) {
         f4v s0 = *reinterpret_cast<const f4v*>(partial + i), s1 = *reinterpret_cast<const f4v*>(partial + i + 4);
         for (int p = 1; p < parts; ++p) {
             s0 += *reinterpret_cast<const f4v*>(partial + p * n + i);
             s1 += *reinterpret_cast<const f4v*>(partial + p * n + i + 4);
         }
-        *reinterpret_cast<u4v*>(out + i) = u4v{bf16_pair(s0[0], s0[1]), bf16_pair(s0[2], s0[3]), bf16_pair(s1[0], s1[1]),
-                                              bf16_pair(s1[2], s1[3])};
+        *reinterpret_cast<u4v*>(i < first ? out + i : second + (i - first)) =
+            u4v{bf16_pair(s0[0], s0[1]), bf16_pair(s0[2], s0[3]), bf16_pair(s1[0], s1[1]), bf16_pair(s1[2], s1[3])};
     }
 }
 
@@ -579,41 +436,58 @@ __global__ __launch_bounds__(256) void k_clear(uint16_t* out, int64_t n) {
 unsigned wide_grid(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((n / 8 + 255) / 256, 8192)); }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tiles of 256 where they fill the GPU.
-#ifndef FORCE
-#define FORCE -1
-#endif
-bool wide_tiles(int64_t N, int64_t M, int mode) {
-    if (FORCE >= 0) return FORCE;
-    return ceil_div(N, mode == FWD ? 128 : 256) * ceil_div(M, 256) * (mode == DW ? 2 : 1) >= 224;
-}
-
 hipError_t clear(void* p, int64_t n, hipStream_t s) {
     if (!p || n == 0) return hipSuccess;
     k_clear<<<wide_grid(n), 256, 0, s>>>(static_cast<uint16_t*>(p), n);
     return hipGetLastError();
 }
 
-template <int MODE, int ACT> hipError_t run_gemm(GemmArgs& a, hipStream_t s) {
-    const int64_t side = wide_tiles(a.N, a.M, MODE) ? 256 : 128;
-    const int64_t tiles_n = ceil_div(a.N, MODE == FWD ? side / 2 : side), tiles_m = ceil_div(a.M, side) * (MODE == DW ? 2 : 1);
-    const int64_t tiles = tiles_n * tiles_m;
-    if (tiles > ((int64_t)1 << 31) - 64) return hipErrorInvalidConfiguration;
-    a.tiles_n = (int32_t)tiles_n;
-    a.tiles_m = (int32_t)tiles_m;
-    a.tiles = (uint32_t)tiles;
-    a.per_xcd = (int32_t)ceil_div(tiles, 8);
-    const dim3 grid((unsigned)(8 * (int64_t)a.per_xcd), MODE == DX ? a.parts : 1);
-    if (side == 256) k_gemm_wide<MODE, ACT><<<grid, 256, 0, s>>>(a);
-    else k_gemm<MODE, ACT><<<grid, 256, 0, s>>>(a);
-    return hipGetLastError();
+// Tiles of one product and the parts of its sum.  T = 8 where its tiles fill
+// the GPU; else T = 4 and, for the gradients, the sum split into parts of 8
+// steps and more until two workgroups per CU are busy.
+#ifndef FORCE
+#define FORCE -1
+#endif
+struct Plan {
+    int T, parts;
+    int64_t tiles_n, tiles_m;
+};
+Plan plan(int mode, int64_t N, int64_t M, int64_t K) {
+    Plan p;
+    for (p.T = 8;; p.T = 4) {
+        p.tiles_n = ceil_div(N, (mode == FWD ? 16 : 32) * p.T);
+        p.tiles_m = ceil_div(M, 32 * p.T) * (mode == DW ? 2 : 1);
+        if (FORCE >= 0 ? p.T == FORCE : (p.T == 4 || p.tiles_n * p.tiles_m >= 224)) break;
+    }
+    const int64_t steps = ceil_div(K, BK) * (mode == DX ? 2 : 1), tiles = std::max<int64_t>(1, p.tiles_n * p.tiles_m);
+    p.parts = mode == FWD ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({(p.T == 8 ? 256 : 512) / tiles, steps / 8, 16}));
+    return p;
 }
 
-// Parts of dx's sum: enough workgroups for two per CU, at least 8 steps each.
-int dx_parts(int64_t tokens, int64_t cols, int64_t features) {
-    const bool wide = wide_tiles(cols, tokens, DX);
-    const int64_t side = wide ? 256 : 128, tiles = ceil_div(tokens, side) * ceil_div(cols, side), steps = 2 * ceil_div(features, BK);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({(wide ? 256 : 512) / std::max<int64_t>(1, tiles), steps / 8, 16}));
+// Bytes of the parts' sums.
+int64_t part_bytes(int mode, int64_t N, int64_t M, int64_t K) {
+    const int parts = plan(mode, N, M, K).parts;
+    return parts > 1 ? parts * M * N * 4 * (mode == DW ? 2 : 1) : 0;
+}
+
+template <int MODE, int ACT> hipError_t run_gemm(GemmArgs& a, hipStream_t s) {
+    const Plan p = plan(MODE, a.N, a.M, a.K);
+    const int64_t tiles = p.tiles_n * p.tiles_m, steps = ceil_div(a.K, BK) * (MODE == DX ? 2 : 1);
+    if (tiles > ((int64_t)1 << 24) - 64) return hipErrorInvalidConfiguration;      // 256 threads each, counted in 32 bits
+    a.tiles_n = (int32_t)p.tiles_n;
+    a.tiles_m = (int32_t)p.tiles_m;
+    a.tiles = (uint32_t)tiles;
+    a.per_xcd = (int32_t)ceil_div(tiles, 8);
+    a.parts = p.parts;
+    a.split_steps = (int32_t)ceil_div(steps, p.parts);
+    const dim3 grid((unsigned)(8 * (int64_t)a.per_xcd), (unsigned)p.parts);
+    if (p.T == 8) k_gemm<MODE, ACT, 8><<<grid, 256, 0, s>>>(a);
+    else k_gemm<MODE, ACT, 4><<<grid, 256, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.parts == 1) return e;
+    const int64_t n = (int64_t)a.M * a.N;
+    k_join<<<wide_grid(n * (MODE == DW ? 2 : 1)), 256, 0, s>>>(a.partial, p.parts, n * (MODE == DW ? 2 : 1), n, a.out[0], a.out[1]);
+    return hipGetLastError();
 }
 
 constexpr int64_t kAlign = 256;
@@ -621,9 +495,10 @@ int64_t plane_bytes(int64_t tokens, int64_t features) { return ceil_div(tokens *
 
 }  // namespace
 
+// dg and du, then the parts of dx, and after it those of dw_gate and dw_up.
 size_t gated_workspace_bytes(int64_t tokens, int64_t cols, int64_t features) {
-    const int parts = dx_parts(tokens, cols, features);
-    return (size_t)(2 * plane_bytes(tokens, features) + (parts > 1 ? parts * tokens * cols * 4 : 0));
+    return (size_t)(2 * plane_bytes(tokens, features) +
+                    std::max(part_bytes(DX, cols, tokens, features), part_bytes(DW, cols, features, tokens)));
 }
 
 hipError_t launch_gated(const GatedArgs& g, hipStream_t s) {
@@ -658,6 +533,7 @@ hipError_t launch_gated_grad(const GatedGradArgs& g, hipStream_t s) {
     char* ws = static_cast<char*>(g.workspace);
     uint16_t* dg = reinterpret_cast<uint16_t*>(ws);
     uint16_t* du = reinterpret_cast<uint16_t*>(ws + plane_bytes(g.tokens, g.features));
+    float* partial = reinterpret_cast<float*>(ws + 2 * plane_bytes(g.tokens, g.features));
     const uint16_t* dh = static_cast<const uint16_t*>(g.dh);
     if (g.act == A_SILU) k_gate_grad<A_SILU><<<wide_grid(tf), 256, 0, s>>>(dh, g.saved, dg, du, tf);
     else if (g.act == A_GELU) k_gate_grad<A_GELU><<<wide_grid(tf), 256, 0, s>>>(dh, g.saved, dg, du, tf);
@@ -671,16 +547,9 @@ hipError_t launch_gated_grad(const GatedGradArgs& g, hipStream_t s) {
         a.ldp = g.cols; a.ldq = g.features;
         a.N = (int32_t)g.cols; a.M = (int32_t)g.tokens; a.K = (int32_t)g.features;
         a.out[0] = static_cast<uint16_t*>(g.dx);
-        a.parts = dx_parts(g.tokens, g.cols, g.features);
-        a.split_steps = (int32_t)ceil_div(2 * ceil_div(g.features, BK), a.parts);
-        a.partial = reinterpret_cast<float*>(ws + 2 * plane_bytes(g.tokens, g.features));
+        a.partial = partial;
         e = run_gemm<DX, 0>(a, s);
         if (e != hipSuccess) return e;
-        if (a.parts > 1) {
-            const int64_t n = g.tokens * g.cols;
-            k_join<<<wide_grid(n), 256, 0, s>>>(a.partial, a.parts, n, a.out[0]);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
     }
     if (g.dwg) {
         GemmArgs a = {};
@@ -689,6 +558,7 @@ hipError_t launch_gated_grad(const GatedGradArgs& g, hipStream_t s) {
         a.ldp = g.ldx; a.ldq = g.features;
         a.N = (int32_t)g.cols; a.M = (int32_t)g.features; a.K = (int32_t)g.tokens;
         a.out[0] = static_cast<uint16_t*>(g.dwg); a.out[1] = static_cast<uint16_t*>(g.dwu);
+        a.partial = partial;
         e = run_gemm<DW, 0>(a, s);
     }
     return e;
