@@ -51,7 +51,7 @@ struct PackedK {
     float* saved;
     int64_t ldx;
     int32_t n0, n1, K;
-    int32_t f32_out;
+    int32_t f32_out, act;
     int32_t scale_words;          // rows of scales are whole 4-byte words
 };
 
@@ -110,9 +110,9 @@ __device__ __forceinline__ void stage_rows(uint8_t* to, const uint8_t* from, int
     }
 }
 
-// XR: token rows that a wave copies to LDS for every step (4 or 16, of one
+// XR: token rows that a wave copies to LDS for every step (4, 8 or 16, of one
 // token tile), or 0 where tokens are loaded as operands.
-template <int FMT, int FR, int NT, int XR, bool GATED, int ACT>
+template <int FMT, int FR, int NT, int XR, bool GATED>
 __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void k_packed(PackedK a) {
     constexpr int M = GATED ? 2 : 1;
     constexpr int kRows = 16 * FR, SB = scale_bytes<FMT>();
@@ -136,13 +136,14 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
     // Rows past n0 and tokens past n1 read the last one: their lanes feed
     // only outputs that are not stored.  Offsets from the workgroup's first
     // row and token fit 32 bits.
-    const uint8_t* cbase[M];
+    __amdgpu_buffer_rsrc_t cbuf[M];
     uint32_t coff[FR], xoff[NT];
 #pragma unroll
-    for (int m = 0; m < M; ++m) cbase[m] = a.codes[m] + j0 * rb;
+    for (int m = 0; m < M; ++m)
+        cbuf[m] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.codes[m] + j0 * rb), 0, (int)(min(kRows, a.n0 - j0) * rb), 0x00020000);
 #pragma unroll
     for (int f = 0; f < FR; ++f) coff[f] = (uint32_t)min(16 * f + i, a.n0 - 1 - j0) * (uint32_t)rb + 16 * h;
-    const char* xbase = reinterpret_cast<const char*>(a.x + t0 * a.ldx);
+    const auto xbuf = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(a.x + t0 * a.ldx), 0, (int)kOutside, 0x00020000);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
         xoff[n] = (uint32_t)min(16 * n + i, a.n1 - 1 - t0) * (uint32_t)(2 * a.ldx) + (FMT == F_BF16W ? 16 * h : 64 * h);
@@ -156,51 +157,52 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
             for (int n = 0; n < NT; ++n) acc[m][f][n] = f4v{0.f, 0.f, 0.f, 0.f};
 
     // Lane h's 32 elements of a packed step start at 32 h, whole or not at
-    // all; of a BF16 step, 8 elements at 32 q + 8 h.  Loads from `limit` on
-    // are given an offset beyond their buffer's range and return zeros, so
-    // that the loop has no branches and the waits for it can be counted.
+    // all; of a BF16 step, 8 elements at 32 q + 8 h.  Tokens past K are given
+    // an offset beyond their buffer and return zeros, and so are BF16 weights,
+    // which need not be finite; codes past a row's end are the next row's and
+    // meet zeros, and the last row's end that of their buffer.  A step past
+    // the matrix stands for its end, so that no offset exceeds a buffer.
     auto k_of = [&](int s, int q) { return s * kStep + (FMT == F_BF16W ? 32 * q + 8 * h : 32 * h); };
-    auto fetch = [](const void* base, uint32_t off) {
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)kOutside, 0x00020000);
-        return __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0);
-    };
     struct Batch { Codes<FMT> c[D][M][FR]; };
     struct Tokens { u4v v[D][NT][4]; };
-    auto load = [&](Batch& o, int s, int limit) {
+    auto load = [&](Batch& o, int s) {
 #pragma unroll
-        for (int d = 0; d < D; ++d)
+        for (int d = 0; d < D; ++d) {
+            const uint32_t at = (uint32_t)min(s + d, steps) * (FMT == F_BF16W ? 256 : 64);
 #pragma unroll
             for (int q = 0; q < (FMT == F_BF16W ? 4 : 1); ++q)
 #pragma unroll
                 for (int m = 0; m < M; ++m)
 #pragma unroll
-                    for (int f = 0; f < FR; ++f)
-                        o.c[d][m][f].v[q] = fetch(cbase[m] + (int64_t)(s + d) * (FMT == F_BF16W ? 256 : 64),
-                                                  k_of(s + d, q) < limit ? coff[f] + 64 * q : kOutside);
+                    for (int f = 0; f < FR; ++f) {
+                        const uint32_t off = FMT != F_BF16W || k_of(s + d, q) < a.K ? coff[f] + 64 * q : kOutside;
+                        o.c[d][m][f].v[q] = FMT == F_BF16W ? __builtin_amdgcn_raw_buffer_load_b128(cbuf[m], off + (off == kOutside ? 0 : at), 0, 0)
+                                                           : __builtin_amdgcn_raw_buffer_load_b128(cbuf[m], off, at, 0);
+                    }
+        }
     };
-    auto turn = [](int r) { return 4 * ((0x78 >> ((r >> 1) & 6)) & 3) + (r & 3); };     // 0, 2, 3, 1 by fours of rows
-    auto load_x = [&](Tokens& x, int s, int limit) {
+    auto load_x = [&](Tokens& x, int s) {
 #pragma unroll
         for (int d = 0; d < D; ++d)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    x.v[d][n][q] = fetch(xbase + (int64_t)(s + d) * (2 * kStep),
-                                         k_of(s + d, q) < limit ? xoff[n] + (FMT == F_BF16W ? 64 : 16) * q : kOutside);
+                    x.v[d][n][q] = __builtin_amdgcn_raw_buffer_load_b128(
+                        xbuf, k_of(s + d, q) < a.K ? xoff[n] + (FMT == F_BF16W ? 64 : 16) * q : kOutside, (uint32_t)(s + d) * (2 * kStep), 0);
     };
     // instruction c copies rows 4 c .. + 3 of a step, word lane % 16 of row 4 c + lane / 16
-    auto copy_x = [&](u4v (&to)[4][XW], int s, int limit) {
+    auto turn = [](int r) { return 4 * ((0x78 >> ((r >> 1) & 6)) & 3) + (r & 3); };     // 0, 2, 3, 1 by fours of rows
+    auto copy_x = [&](u4v (&to)[4][XW], int s) {
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(xbase + (int64_t)(s + d) * (2 * kStep)), 0, (int)kOutside, 0x00020000);
+        for (int d = 0; d < D; ++d)
 #pragma unroll
             for (int c = 0; c < XR / 4; ++c) {
                 const int r = 4 * c + h, w = i ^ turn(r);
-                const uint32_t off = r < a.n1 && (s + d) * kStep + 8 * w < limit ? (uint32_t)r * (uint32_t)(2 * a.ldx) + 16 * w : kOutside;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)&to[wave][(d * XR + 4 * c) * 16], 16, off, 0, 0, 0);
+                const uint32_t off = r < a.n1 && (s + d) * kStep + 8 * w < a.K ? (uint32_t)r * (uint32_t)(2 * a.ldx) + 16 * w : kOutside;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(xbuf, (__attribute__((address_space(3))) void*)&to[wave][(d * XR + 4 * c) * 16], 16, off,
+                                                         (uint32_t)(s + d) * (2 * kStep), 0, 0);
             }
-        }
     };
     const int xr = min(i, min(XR, a.n1) - 1);
     auto read_x = [&](Tokens& x, const u4v (&from)[4][XW]) {
@@ -228,8 +230,7 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
                             for (int n = 0; n < NT; ++n)
                                 acc[m][f][n] = mfma(__builtin_bit_cast(bf8v, x.v[d][n][q]), __builtin_bit_cast(bf8v, c.v[q]), acc[m][f][n]);
                     } else if constexpr (FMT == F_INT4) {
-                        const float stored = (float)*reinterpret_cast<const _Float16*>(sc);
-                        const float scale = live ? stored : 0.f;
+                        const float scale = (float)*reinterpret_cast<const _Float16*>(sc);
                         f4v part[NT];
 #pragma unroll
                         for (int n = 0; n < NT; ++n) part[n] = f4v{0.f, 0.f, 0.f, 0.f};
@@ -275,11 +276,10 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
     for (int s0 = 0; s0 < steps; s0 += kChunk) {
         const int s1 = min(steps, s0 > steps - kChunk ? steps : s0 + kChunk);
         const int share = ((s1 - s0 + 4 * D - 1) / (4 * D)) * D;      // whole batches
-        const int first = s0 + wave * share, end = min(s1, first + share);
+        const int first = s0 + wave * share, end = min(s1, first + share);      // past s1: no steps
         Batch now, next;
-        const int limit = min(a.K, end * kStep);
-        if constexpr (XR > 0) copy_x(s_x0, first, limit);
-        load(now, first, limit);
+        if constexpr (XR > 0) copy_x(s_x0, first);
+        load(now, first);
         if constexpr (SB > 0) {
             const int64_t per_row = FMT == F_INT4 ? a.K / 128 * 2 : FMT == F_NVFP4 ? a.K / 16 : a.K / 32;
             const int take = (int)min((int64_t)(s1 - s0) * SB, per_row - (int64_t)s0 * SB);
@@ -298,10 +298,11 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
         // codes, so that waiting for them does not wait for memory
         auto batch = [&](Batch& o, Batch& ahead, u4v (&xo)[4][XW], u4v (&xa)[4][XW], int s) {
             Tokens x;
-            if constexpr (XR > 0) copy_x(xa, s + D, limit);
-            else load_x(x, s, limit);
-            load(ahead, s + D, limit);
+            if constexpr (XR > 0) copy_x(xa, s + D);
+            else load_x(x, s);
+            load(ahead, s + D);
             __builtin_amdgcn_sched_barrier(0);        // the compiler would put them off
+            if (s >= end) return;
             if constexpr (XR > 0) read_x(x, xo);
             multiply(o, x, s, s0);
         };
@@ -345,7 +346,7 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
                     a.saved[o] = v[0][e];
                     a.saved[(int64_t)a.n1 * a.n0 + o] = v[1][e];
                 }
-                z = act<ACT>(z) * v[1][e];
+                z = (a.act == A_SILU ? act<A_SILU>(z) : a.act == A_GELU ? act<A_GELU>(z) : act<A_GELU_TANH>(z)) * v[1][e];
             }
             if (a.f32_out) static_cast<float*>(a.out)[o] = z;
             else static_cast<uint16_t*>(a.out)[o] = (uint16_t)bf16_pair(z, 0.f);
@@ -353,28 +354,23 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
     }
 }
 
-template <int FMT, int FR, int NT, int XR, bool GATED, int ACT> hipError_t run(const PackedK& k, hipStream_t s) {
+template <int FMT, int FR, int NT, int XR, bool GATED> hipError_t run(const PackedK& k, hipStream_t s) {
     const dim3 grid((unsigned)((k.n0 + 16 * FR - 1) / (16 * FR)), (unsigned)((k.n1 + 16 * NT - 1) / (16 * NT)));
-    k_packed<FMT, FR, NT, XR, GATED, ACT><<<grid, 256, 0, s>>>(k);
+    k_packed<FMT, FR, NT, XR, GATED><<<grid, 256, 0, s>>>(k);
     return hipGetLastError();
 }
 
-template <int FMT, bool GATED, int ACT> hipError_t pick_tokens(const PackedK& k, hipStream_t s) {
+template <int FMT, bool GATED> hipError_t pick(const PackedK& k, hipStream_t s) {
     constexpr int FR = GATED ? 1 : 2;
-    if (k.n1 <= 4) return run<FMT, FR, 1, 4, GATED, ACT>(k, s);
-    if (k.n1 <= 16) return run<FMT, FR, 1, 16, GATED, ACT>(k, s);
-    if (k.n1 <= 32) return run<FMT, FR, 2, 0, GATED, ACT>(k, s);
-    return run<FMT, FR, 4, 0, GATED, ACT>(k, s);
+    if (k.n1 <= 4) return run<FMT, FR, 1, 4, GATED>(k, s);
+    if (k.n1 <= 8) return run<FMT, FR, 1, 8, GATED>(k, s);
+    if (k.n1 <= 16) return run<FMT, FR, 1, 16, GATED>(k, s);
+    if (k.n1 <= 32) return run<FMT, FR, 2, 0, GATED>(k, s);
+    return run<FMT, FR, 4, 0, GATED>(k, s);
 }
 
-template <int FMT> hipError_t pick(const PackedArgs& a, const PackedK& k, hipStream_t s) {
-    if (!a.gated) {
-        if constexpr (FMT == F_BF16W) return hipErrorInvalidValue;
-        else return pick_tokens<FMT, false, A_SILU>(k, s);
-    }
-    if (a.act == A_SILU) return pick_tokens<FMT, true, A_SILU>(k, s);
-    if (a.act == A_GELU) return pick_tokens<FMT, true, A_GELU>(k, s);
-    return pick_tokens<FMT, true, A_GELU_TANH>(k, s);
+template <int FMT> hipError_t pick(bool gated, const PackedK& k, hipStream_t s) {
+    return gated ? pick<FMT, true>(k, s) : pick<FMT, false>(k, s);
 }
 
 }  // namespace
@@ -390,11 +386,12 @@ hipError_t launch_packed(const PackedArgs& a, hipStream_t s) {
     k.n0 = (int32_t)a.n0; k.n1 = (int32_t)a.n1; k.K = (int32_t)a.K;
     k.f32_out = a.out_dtype == D_F32;
     k.scale_words = a.K % (a.fmt == F_INT4 ? 256 : a.fmt == F_NVFP4 ? 64 : 128) == 0;
+    k.act = a.act;
     switch (a.fmt) {
-    case F_INT4: return pick<F_INT4>(a, k, s);
-    case F_NVFP4: return pick<F_NVFP4>(a, k, s);
-    case F_MXFP4: return pick<F_MXFP4>(a, k, s);
-    default: return pick<F_BF16W>(a, k, s);
+    case F_INT4: return pick<F_INT4>(a.gated, k, s);
+    case F_NVFP4: return pick<F_NVFP4>(a.gated, k, s);
+    case F_MXFP4: return pick<F_MXFP4>(a.gated, k, s);
+    default: return a.gated ? pick<F_BF16W, true>(k, s) : hipErrorInvalidValue;
     }
 }
 
