@@ -17,7 +17,8 @@
 // + 3, so its group scale is its own.  Codes go from memory to registers to
 // the matrix cores, the next batch of steps in flight while one is multiplied:
 // a wave's steps follow each other in memory, so a batch is whole 128-byte
-// lines.  Only scales pass through LDS.
+// lines.  Scales and up to 16 tokens are copied to LDS by the wave that needs
+// them, so that nothing but the sums is shared and no wave waits for another.
 //
 // Every code becomes exact BF16:
 //   E2M1   one convert per pair, the E8M0 scale applied by the convert;
@@ -57,7 +58,7 @@ struct PackedK {
 
 constexpr int kStep = 128;            // k of one step: 64 code bytes per row
 constexpr uint32_t kOutside = 0x80000000u;     // an offset beyond every buffer: loads zeros
-constexpr int kChunkSteps = 64;       // steps whose scales are in LDS at once
+constexpr int kChunkSteps = 64;       // steps whose scales are in LDS at once, 16 for each wave
 
 // Scale bytes per row and step.
 template <int FMT> constexpr int scale_bytes() { return FMT == F_INT4 ? 2 : FMT == F_NVFP4 ? 8 : FMT == F_MXFP4 ? 4 : 0; }
@@ -96,18 +97,12 @@ __device__ __forceinline__ uint32_t int4_upper(uint32_t w) {
 // One step's codes of one fragment, as loaded.
 template <int FMT> struct Codes { u4v v[FMT == F_BF16W ? 4 : 1]; };
 
-// Bytes to LDS in words of W: `rows` rows of `take` bytes, `pitch` bytes apart
-// in memory and `pad` in LDS; the last row is `most`.
-template <class W>
-__device__ __forceinline__ void stage_rows(uint8_t* to, const uint8_t* from, int rows, int64_t j0, int64_t most, int take, int64_t pitch, int pad) {
-    const int per = take / (int)sizeof(W);
-    for (int r = threadIdx.x >> 4; r < rows; r += 16) {
-        const uint8_t* row = from + min(j0 + r, most) * pitch;
-        for (int c = threadIdx.x & 15; c < per; c += 16) {
-            const W w = reinterpret_cast<const W*>(row)[c];
-            __builtin_memcpy(to + r * pad + c * (int)sizeof(W), &w, sizeof(W));
-        }
-    }
+// Waits until at most N loads and copies of the wave are outstanding.
+template <int N> __device__ __forceinline__ void wait_for_all_but() {
+    static_assert(N < 64, "six bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+    asm volatile("" ::: "memory");
 }
 
 // XR: token rows that a wave copies to LDS for every step (4, 8 or 16, of one
@@ -116,11 +111,14 @@ template <int FMT, int FR, int NT, int XR, bool GATED>
 __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void k_packed(PackedK a) {
     constexpr int M = GATED ? 2 : 1;
     constexpr int kRows = 16 * FR, SB = scale_bytes<FMT>();
-    constexpr int kPad = SB * kChunkSteps + 4;                        // row r starts r words further round the banks
+    constexpr int kScRow = 128;                                       // bytes of a row's scales for a wave's share of a chunk
     constexpr int D = XR == 4 && FMT != F_BF16W ? 2 : 1;              // steps of a batch
+    constexpr int NC = D * M * FR * (FMT == F_BF16W ? 4 : 1), NX = D * XR / 4;      // loads of a batch's codes, copies of its tokens
     constexpr int XW = XR ? D * XR * 16 : 1;                          // 16-byte words of a batch's tokens
     struct Sums { f4v of[4][M * FR][NT][64]; };
-    __shared__ __align__(16) uint8_t s_sc[std::max<int>(SB ? M * kRows * kPad : 16, sizeof(Sums))];    // scales, then sums
+    // scales, a wave's own share (16-byte word w of row r at word w ^ r % 8, as the
+    // rows' words of one step would else be in one bank), then sums
+    __shared__ __align__(16) uint8_t s_sc[std::max<int>(SB ? 4 * M * kRows * kScRow : 16, sizeof(Sums))];
     // tokens of the batch at hand and of the next, a wave's own each: word w of
     // row r at word w ^ turn(r) of its 256 bytes, so that the lanes that the
     // LDS serves together (0-3, 12-15, 20-23, 24-27 and so on) are in
@@ -212,17 +210,23 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
             for (int q = 0; q < 4; ++q)
                 x.v[d][0][q] = from[wave][(d * XR + xr) * 16 + ((FMT == F_BF16W ? 4 * q + h : 4 * h + q) ^ turn(xr))];
     };
-    // `at`: the chunk's first step
+    // `at`: the wave's first step of the chunk
     auto multiply = [&](const Batch& o, const Tokens& x, int s, int at) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
             const bool live = (s + d) * kStep + 32 * h < a.K;         // packed lanes past K have no scale
+            const uint32_t byte = (uint32_t)min(s + d - at, 16 - 1) * SB;
+            uint32_t sc_at = (uint32_t)((wave * M * kRows + i) * kScRow + (FMT == F_NVFP4 ? 2 * h : FMT == F_MXFP4 ? h : 0)) +
+                                   ((byte >> 4) ^ (uint32_t)(i & 7)) * 16 + (byte & 15);
+            // kept whole: of an address in several parts the compiler no longer tells
+            // which array it is in, and waits for the copies under way into others
+            asm("" : "+v"(sc_at));
 #pragma unroll
             for (int m = 0; m < M; ++m)
 #pragma unroll
                 for (int f = 0; f < FR; ++f) {
                     const Codes<FMT>& c = o.c[d][m][f];
-                    const uint8_t* sc = s_sc + (m * kRows + 16 * f + i) * kPad + min(s + d - at, kChunkSteps - 1) * SB;
+                    const uint32_t sc = sc_at + (uint32_t)((m * kRows + 16 * f) * kScRow);
                     if constexpr (FMT == F_BF16W) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
@@ -230,7 +234,7 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
                             for (int n = 0; n < NT; ++n)
                                 acc[m][f][n] = mfma(__builtin_bit_cast(bf8v, x.v[d][n][q]), __builtin_bit_cast(bf8v, c.v[q]), acc[m][f][n]);
                     } else if constexpr (FMT == F_INT4) {
-                        const float scale = (float)*reinterpret_cast<const _Float16*>(sc);
+                        const float scale = (float)*reinterpret_cast<const _Float16*>(s_sc + sc);
                         f4v part[NT];
 #pragma unroll
                         for (int n = 0; n < NT; ++n) part[n] = f4v{0.f, 0.f, 0.f, 0.f};
@@ -250,7 +254,7 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
 #pragma unroll
                             for (int e = 0; e < 4; ++e) acc[m][f][n][e] = __builtin_fmaf(scale, part[n][e], acc[m][f][n][e]);
                     } else {
-                        const uint32_t stored = FMT == F_NVFP4 ? *reinterpret_cast<const uint16_t*>(sc + 2 * h) : sc[h];
+                        const uint32_t stored = FMT == F_NVFP4 ? *reinterpret_cast<const uint16_t*>(s_sc + sc) : s_sc[sc];
                         const uint32_t b = live ? stored : 0u;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -275,36 +279,52 @@ __global__ __launch_bounds__(256, NT > 2 ? 2 : NT > 1 || XR == 16 ? 3 : 4) void 
     constexpr int kChunk = SB ? kChunkSteps : 1 << 30;
     for (int s0 = 0; s0 < steps; s0 += kChunk) {
         const int s1 = min(steps, s0 > steps - kChunk ? steps : s0 + kChunk);
-        const int share = ((s1 - s0 + 4 * D - 1) / (4 * D)) * D;      // whole batches
+        const int unit = FMT == F_INT4 ? 2 : D;                       // whole batches, and whole 4-byte words of scales
+        const int share = (s1 - s0 + 4 * unit - 1) / (4 * unit) * unit;
         const int first = s0 + wave * share, end = min(s1, first + share);      // past s1: no steps
-        Batch now, next;
-        if constexpr (XR > 0) copy_x(s_x0, first);
-        load(now, first);
         if constexpr (SB > 0) {
-            const int64_t per_row = FMT == F_INT4 ? a.K / 128 * 2 : FMT == F_NVFP4 ? a.K / 16 : a.K / 32;
-            const int take = (int)min((int64_t)(s1 - s0) * SB, per_row - (int64_t)s0 * SB);
-            if (s0) __syncthreads();                                  // the previous chunk's are no longer read
+            const uint32_t per_row = (uint32_t)(FMT == F_INT4 ? a.K / 128 * 2 : FMT == F_NVFP4 ? a.K / 16 : a.K / 32);
+            const uint32_t most = (uint32_t)min(kRows, a.n0 - j0);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                uint8_t* to = s_sc + m * kRows * kPad;
-                const uint8_t* from = a.scales[m] + (int64_t)s0 * SB;
-                if (a.scale_words) stage_rows<uint32_t>(to, from, kRows, j0, a.n0 - 1, take, per_row, kPad);
-                else if (FMT != F_MXFP4) stage_rows<uint16_t>(to, from, kRows, j0, a.n0 - 1, take, per_row, kPad);
-                else stage_rows<uint8_t>(to, from, kRows, j0, a.n0 - 1, take, per_row, kPad);
+                const uint8_t* from = a.scales[m] + (int64_t)j0 * per_row;
+                if (a.scale_words) {
+                    const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(from), 0, (int)(most * per_row), 0x00020000);
+#pragma unroll
+                    for (int c = 0; c < kRows / 8; ++c) {
+                        const uint32_t r = 8 * c + (lane >> 3);
+                        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (__attribute__((address_space(3))) void*)(s_sc + ((wave * M + m) * kRows + 8 * c) * kScRow), 16,
+                                                                 min(r, most - 1) * per_row + first * SB + 16 * ((lane & 7) ^ (r & 7)), 0, 0, 0);
+                    }
+                } else {                                              // rows that 4-byte words do not divide
+                    const int take = max(0, min((end - first) * SB, (int)per_row - first * SB));
+                    for (int r = lane; r < kRows; r += 64) {
+                        const uint8_t* row = from + (int64_t)min((uint32_t)r, most - 1) * per_row + first * SB;
+                        for (int b = 0; b < take; ++b) s_sc[((wave * M + m) * kRows + r) * kScRow + ((b >> 4) ^ (r & 7)) * 16 + (b & 15)] = row[b];
+                    }
+                }
             }
-            __syncthreads();
         }
+        Batch now, next;
+        if constexpr (XR > 0) copy_x(s_x0, first);
+        __builtin_amdgcn_sched_barrier(0);
+        load(now, first);
+        // The wave's copies are waited for here and in `batch` by their
+        // number: the compiler's own waits for them may come out too weak.
+        if constexpr (SB > 0) wait_for_all_but<NX + NC>();
         // tokens that are loaded come from the caches and before the next
         // codes, so that waiting for them does not wait for memory
         auto batch = [&](Batch& o, Batch& ahead, u4v (&xo)[4][XW], u4v (&xa)[4][XW], int s) {
             Tokens x;
             if constexpr (XR > 0) copy_x(xa, s + D);
             else load_x(x, s);
+            __builtin_amdgcn_sched_barrier(0);        // in this order, and not put off
             load(ahead, s + D);
-            __builtin_amdgcn_sched_barrier(0);        // the compiler would put them off
+            __builtin_amdgcn_sched_barrier(0);
             if (s >= end) return;
+            if constexpr (XR > 0) wait_for_all_but<2 * NC + NX>();
             if constexpr (XR > 0) read_x(x, xo);
-            multiply(o, x, s, s0);
+            multiply(o, x, s, first);
         };
         for (int s = first; s < end; s += 2 * D) {
             batch(now, next, s_x0, s_x1, s);
