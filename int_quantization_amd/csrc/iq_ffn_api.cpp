@@ -47,9 +47,9 @@ iq_status check_gated(const iq_gated_desc* d) {
     return IQ_OK;
 }
 
-// Launch grids count threads in 32 bits, at most 256 for 16 rows; byte offsets
+// Launch grids count threads in 32 bits, at most 4 x 256 for 16 rows; byte offsets
 // among a workgroup's 32 rows and among 64 tokens stay below 2^31.
-constexpr int64_t kMaxRows = (int64_t)1 << 27, kMaxPackedK = (int64_t)1 << 22;
+constexpr int64_t kMaxRows = (int64_t)1 << 25, kMaxPackedK = (int64_t)1 << 22;
 
 // Rules shared by the packed products; *empty where nothing is to be done.
 iq_status check_packed(const iq_desc* d, int32_t x_dtype, int64_t n1, int32_t z_dtype, bool* empty) {

@@ -502,7 +502,11 @@ size_t gated_workspace_bytes(int64_t tokens, int64_t cols, int64_t features) {
 }
 
 hipError_t launch_gated(const GatedArgs& g, hipStream_t s) {
-    if (g.tokens <= kPackedTokens) {
+    // A few tokens go with the weights' rows, 16 to a workgroup.  Beyond one
+    // tile of 16 tokens, 64 to a workgroup are faster once they fill the GPU
+    // (33 tokens, 4096 x 14336: 59 us by 16 rows, 37 by 64; 8192 x 28672: 253
+    // and 182; 8192 x 8192: 61 and 83).
+    if (g.tokens <= 16 || (g.tokens <= kPackedTokens && ceil_div(g.features, 64) < 192)) {
         PackedArgs p = {};
         p.fmt = F_BF16W; p.gated = true; p.act = g.act;
         p.w[0].codes = g.wg; p.w[1].codes = g.wu;
