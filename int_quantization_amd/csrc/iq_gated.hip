@@ -48,7 +48,8 @@ struct GemmArgs {
     const uint16_t* p[2];
     const uint16_t* q[2];
     int64_t ldp, ldq;
-    int32_t N, M, K;              // of one of the two weights
+    int32_t N, M, K;              // of one of the two weights; N of this launch's columns
+    int64_t ldo;                  // elements of a row of C
     int32_t tiles_n, tiles_m;     // tiles_m counts both weights in DW
     uint32_t tiles;
     int32_t per_xcd;
@@ -351,9 +352,9 @@ template <int MODE, int ACT, int T> __global__ __launch_bounds__(256, T == 8 ? 1
         const bool in = row < a.M;
         if constexpr (MODE == FWD) {
             const int nb = n0 + wn * (W / 2);
-            uint16_t* hr = in ? a.out[0] + (int64_t)row * a.N : nullptr;
-            float* gr = in && a.saved ? a.saved + (int64_t)row * a.N : nullptr;
-            float* ur = in && a.saved ? a.saved + ((int64_t)a.M + row) * a.N : nullptr;
+            uint16_t* hr = in ? a.out[0] + (int64_t)row * a.ldo : nullptr;
+            float* gr = in && a.saved ? a.saved + (int64_t)row * a.ldo : nullptr;
+            float* ur = in && a.saved ? a.saved + ((int64_t)a.M + row) * a.ldo : nullptr;
 #pragma unroll
             for (int t = 0; t < T / 2; t += 2) {
                 f4v h[2];
@@ -371,11 +372,11 @@ template <int MODE, int ACT, int T> __global__ __launch_bounds__(256, T == 8 ? 1
             for (int t = 0; t < T; t += 2) {
                 const int nb = n0 + wn * W + t * 16;
                 if (a.parts > 1) {
-                    float* pr = in ? a.partial + (((int64_t)blockIdx.y * (MODE == DW ? 2 : 1) + sel) * a.M + row) * a.N : nullptr;
+                    float* pr = in ? a.partial + (((int64_t)blockIdx.y * (MODE == DW ? 2 : 1) + sel) * a.M + row) * a.ldo : nullptr;
                     store_f4(pr, nb + 4 * (lane >> 4), a.N, acc[t][m]);
                     store_f4(pr, nb + 16 + 4 * (lane >> 4), a.N, acc[t + 1][m]);
                 } else {
-                    store_pair(in ? a.out[sel] + (int64_t)row * a.N : nullptr, nb, a.N, lane, acc[t][m], acc[t + 1][m]);
+                    store_pair(in ? a.out[sel] + (int64_t)row * a.ldo : nullptr, nb, a.N, lane, acc[t][m], acc[t + 1][m]);
                 }
             }
         }
@@ -445,22 +446,30 @@ hipError_t clear(void* p, int64_t n, hipStream_t s) {
 // Tiles of one product and the parts of its sum.  T = 8 where its tiles fill
 // the GPU; else T = 4 and, for the gradients, the sum split into parts of 8
 // steps and more until two workgroups per CU are busy.
-#ifndef FORCE
-#define FORCE -1
-#endif
+//
+// T = 8 tiles take a CU each, so 256 of them are a round.  Where the last round
+// would be half full or less, its columns go to T = 4 tiles, a quarter as large
+// and two to a CU, in a launch of their own.
 struct Plan {
     int T, parts;
-    int64_t tiles_n, tiles_m;
+    int32_t tail;          // columns left to T = 4
 };
 Plan plan(int mode, int64_t N, int64_t M, int64_t K) {
-    Plan p;
-    for (p.T = 8;; p.T = 4) {
-        p.tiles_n = ceil_div(N, (mode == FWD ? 16 : 32) * p.T);
-        p.tiles_m = ceil_div(M, 32 * p.T) * (mode == DW ? 2 : 1);
-        if (FORCE >= 0 ? p.T == FORCE : (p.T == 4 || p.tiles_n * p.tiles_m >= 224)) break;
+    const int64_t width = mode == FWD ? 128 : 256, both = mode == DW ? 2 : 1;
+    const int64_t tiles_n = ceil_div(N, width), tiles_m = ceil_div(M, 256) * both, tiles = tiles_n * tiles_m;
+    const int64_t steps = ceil_div(K, BK) * (mode == DX ? 2 : 1);
+    Plan p = {8, 1, 0};
+    if (tiles >= 224) {
+        const int64_t over = tiles % 256;
+        if (tiles > 256 && over > 0 && over <= 128) {
+            const int64_t first = (tiles - over) / tiles_m * width, rest = N - first;
+            if (first > 0 && ceil_div(rest, width / 2) * ceil_div(M, 128) * both <= 512) p.tail = (int32_t)rest;
+        }
+    } else {
+        p.T = 4;
+        const int64_t small = std::max<int64_t>(1, ceil_div(N, width / 2) * ceil_div(M, 128) * both);
+        if (mode != FWD) p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({512 / small, steps / 8, 16}));
     }
-    const int64_t steps = ceil_div(K, BK) * (mode == DX ? 2 : 1), tiles = std::max<int64_t>(1, p.tiles_n * p.tiles_m);
-    p.parts = mode == FWD ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({(p.T == 8 ? 256 : 512) / tiles, steps / 8, 16}));
     return p;
 }
 
@@ -470,22 +479,43 @@ int64_t part_bytes(int mode, int64_t N, int64_t M, int64_t K) {
     return parts > 1 ? parts * M * N * 4 * (mode == DW ? 2 : 1) : 0;
 }
 
-template <int MODE, int ACT> hipError_t run_gemm(GemmArgs& a, hipStream_t s) {
-    const Plan p = plan(MODE, a.N, a.M, a.K);
-    const int64_t tiles = p.tiles_n * p.tiles_m, steps = ceil_div(a.K, BK) * (MODE == DX ? 2 : 1);
+template <int MODE, int ACT, int T> hipError_t run_tiles(GemmArgs a, int64_t parts, hipStream_t s) {
+    const int64_t tiles_n = ceil_div(a.N, (MODE == FWD ? 16 : 32) * T), tiles_m = ceil_div(a.M, 32 * T) * (MODE == DW ? 2 : 1);
+    const int64_t tiles = tiles_n * tiles_m;
     if (tiles > ((int64_t)1 << 24) - 64) return hipErrorInvalidConfiguration;      // 256 threads each, counted in 32 bits
-    a.tiles_n = (int32_t)p.tiles_n;
-    a.tiles_m = (int32_t)p.tiles_m;
+    a.tiles_n = (int32_t)tiles_n;
+    a.tiles_m = (int32_t)tiles_m;
     a.tiles = (uint32_t)tiles;
     a.per_xcd = (int32_t)ceil_div(tiles, 8);
+    k_gemm<MODE, ACT, T><<<dim3((unsigned)(8 * (int64_t)a.per_xcd), (unsigned)parts), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int MODE, int ACT> hipError_t run_gemm(GemmArgs& a, hipStream_t s) {
+    const Plan p = plan(MODE, a.N, a.M, a.K);
+    const int64_t steps = ceil_div(a.K, BK) * (MODE == DX ? 2 : 1), n = (int64_t)a.M * a.N;
     a.parts = p.parts;
     a.split_steps = (int32_t)ceil_div(steps, p.parts);
-    const dim3 grid((unsigned)(8 * (int64_t)a.per_xcd), (unsigned)p.parts);
-    if (p.T == 8) k_gemm<MODE, ACT, 8><<<grid, 256, 0, s>>>(a);
-    else k_gemm<MODE, ACT, 4><<<grid, 256, 0, s>>>(a);
-    const hipError_t e = hipGetLastError();
+    a.ldo = a.N;
+    hipError_t e;
+    if (p.T == 4) {
+        e = run_tiles<MODE, ACT, 4>(a, p.parts, s);
+    } else if (p.tail == 0) {
+        e = run_tiles<MODE, ACT, 8>(a, p.parts, s);
+    } else {
+        const int32_t first = a.N - p.tail;
+        GemmArgs t = a;
+        a.N = first;
+        if ((e = run_tiles<MODE, ACT, 8>(a, 1, s)) != hipSuccess) return e;
+        t.N = p.tail;
+        for (int w = 0; w < 2; ++w) {
+            t.p[w] += MODE == FWD ? first * t.ldp : first;
+            if (t.out[w]) t.out[w] += first;
+        }
+        if (t.saved) t.saved += first;
+        return run_tiles<MODE, ACT, 4>(t, 1, s);
+    }
     if (e != hipSuccess || p.parts == 1) return e;
-    const int64_t n = (int64_t)a.M * a.N;
     k_join<<<wide_grid(n * (MODE == DW ? 2 : 1)), 256, 0, s>>>(a.partial, p.parts, n * (MODE == DW ? 2 : 1), n, a.out[0], a.out[1]);
     return hipGetLastError();
 }

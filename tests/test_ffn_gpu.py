@@ -106,6 +106,22 @@ def test_layer_norm_non_finite_rows_stay_apart(iq, bad, cols):
     assert torch.isnan(dx[3]).all() and torch.isfinite(dx[keep]).all()
 
 
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 6])
+def test_layer_norm_few_rows(iq, rows):
+    """Around the number of rows whose sums one workgroup writes itself."""
+    g = gen(rows)
+    for cols in (96, 1001, 8192, 16384, 20008):
+        check_norm(iq, rand(g, rows, cols), rand(g, cols), rand(g, cols), rand(g, rows, cols), 1e-5)
+
+
+def test_layer_norm_rows_beyond_the_grid(iq):
+    """More rows than workgroups, so that each goes over several with the next in flight."""
+    g = gen(9)
+    for rows, cols, dtype in ((5000, 64, BF), (2100, 2560, F32), (1030, 4104, BF), (1030, 9000, F32), (520, 12288, BF)):
+        check_norm(iq, rand(g, rows, cols, dtype=dtype), rand(g, cols, dtype=F32), rand(g, cols, dtype=F32),
+                   rand(g, rows, cols, dtype=dtype), 1e-5)
+
+
 def test_layer_norm_empty(iq):
     x = torch.empty((0, 40), dtype=BF, device="cuda")
     y, mean, rstd = iq.layer_norm(x)
@@ -170,7 +186,11 @@ def test_gated_large(iq, tokens, cols, features):
 
 @pytest.mark.parametrize("tokens,cols,features,act", [(2050, 328, 3336, "silu"), (2050, 6408, 264, "gelu"), (70, 1096, 5640, "silu"),
                                                       (300, 2056, 3592, "gelu_tanh"), (1793, 8, 4096, "silu"), (1800, 6408, 8, "silu"),
-                                                      (2048, 4096, 3592, "silu")])
+                                                      (2048, 4096, 3592, "silu"),
+                                                      # a last round of tiles that smaller ones take: forward, x's gradient, the weights'
+                                                      (2050, 200, 3752, "gelu"), (2050, 7496, 136, "silu"), (200, 1096, 6952, "gelu_tanh"),
+                                                      # few tiles and a long sum: x's gradient and the weights' in parts
+                                                      (3000, 264, 392, "silu"), (72, 136, 5000, "gelu"), (5001, 24, 16, "silu")])
 def test_gated_wide_tiles(iq, tokens, cols, features, act):
     """Products large enough for 256 x 256 tiles, forward or in one of the gradients, with ragged edges and odd numbers of steps."""
     check_gated(iq, *gated_inputs(tokens, cols, features, 6), act)
@@ -300,6 +320,37 @@ def test_packed_short_rows(iq, fmt, cols):
         x = rand(gen(n1), n1, cols)
         q = any_weights(iq, 19, cols, fmt, 4)
         fo.assert_within(iq.packed_gemv(q, x, F32), *fo.packed(x, values(q)), "z")
+
+
+@pytest.mark.parametrize("fmt", ["int4", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("n1", [1, 4, 5, 8, 9, 16, 17, 48, 49, 64])
+def test_packed_token_counts(iq, fmt, n1):
+    """Every way the tokens are staged, in wide and narrow matrices and over more k than one round of scales."""
+    for rows, cols in ((130, 768), (4133, 512), (40, 8832 if fmt == "int4" else 8864)):
+        cols -= cols % (128 if fmt == "int4" else 32)
+        x = rand(gen(n1), n1, cols)
+        q, q2 = any_weights(iq, rows, cols, fmt, 5), random_weights(iq, rows, cols, fmt, 6)
+        fo.assert_within(iq.packed_gemv(q, x, F32), *fo.packed(x, values(q)), "z")
+        (g, eg), h = fo.packed(x, values(q2)), iq.packed_gated(q2, q2, x, "silu", F32)
+        fo.assert_within(h, *fo.gate(g, g, eg, eg, "silu"), "h")
+
+
+@pytest.mark.parametrize("fmt", ["int4", "nvfp4", "mxfp4"])
+def test_packed_infinities_stay_infinite(iq, fmt):
+    """An infinite activation gives infinities of its weights' signs, whichever step of k it is in."""
+    rows, cols = 33, 896
+    q = random_weights(iq, rows, cols, fmt, 12)
+    w = values(q)[0]
+    for n1, k in ((1, 0), (3, 895), (6, 500), (20, 130), (64, 640)):
+        x = rand(gen(k), n1, cols)
+        x[n1 - 1, k] = float("inf")
+        z = iq.packed_gemv(q, x, F32)[n1 - 1].double()
+        want = w[:, k] * float("inf")                  # NaN where the weight is zero
+        assert torch.equal(torch.isnan(z), torch.isnan(want)) or fmt == "int4"
+        there = w[:, k] != 0
+        if fmt != "int4":                              # INT4's two parts of a weight may both be infinite, with either sign
+            assert torch.equal(z[there], want[there])
+        assert not torch.isfinite(z[there]).any()
 
 
 def test_packed_empty(iq):
