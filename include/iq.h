@@ -325,8 +325,8 @@ iq_status iq_mxw_gemm(const iq_desc* d, const void* codes, const void* scales, c
  *   param_dtype  iq_dtype of weight and bias
  *   weight, bias [cols]; NULL stands for ones / zeros
  *   mean, rstd   float32 [rows]; NULL where they are not wanted
- * Any cols >= 1 and any alignment that the element types need are accepted:
- * rows of whole 16-byte words (base addresses, ld_in and cols) take vector
+ * Any cols >= 1 up to 2^26 (more: IQ_EUNSUPPORTED) and any alignment that the
+ * element types need are accepted: rows of whole 16-byte words (base addresses, ld_in and cols) take vector
  * loads, others single elements.  Statistics are held in FP32.  A NaN or an
  * infinity makes its whole row NaN.  eps must be finite and >= 0.
  */
@@ -392,7 +392,8 @@ iq_status iq_gated_forward(const iq_gated_desc* d, const void* x, const void* w_
  * weights' gradients and w_gate, w_up only for dx.
  *   workspace  iq_gated_workspace_bytes(d) bytes, 256-byte aligned, of any
  *              content.
- * Sums are FP32 in an order fixed by the shape.  tokens == 0 writes zero
+ * Sums are FP32 in an order fixed by the shape; those of few tiles and many
+ * terms are added in parts that the workspace holds.  tokens == 0 writes zero
  * weight gradients.
  */
 iq_status iq_gated_backward(const iq_gated_desc* d, const void* dh, const void* x, const void* w_gate,
@@ -411,12 +412,15 @@ size_t iq_gated_workspace_bytes(const iq_gated_desc* d);
  *            else IQ_EUNSUPPORTED), 1 to 64 tokens (more: IQ_EUNSUPPORTED;
  *            many tokens go through iq_dequantize and a matrix product)
  *   z        z_dtype [n1, N0] token-major, ready to be the next product's x
+ * N0 up to 2^25 and K up to 2^22 (IQ_EUNSUPPORTED).
  * Weights enter the matrix cores exactly (NVFP4 without the global scale,
  * INT4 without the group scale, as 4 a + b with a in [-2, 1], b in [0, 3])
  * and are summed in FP32: before z's own rounding |z - exact| <=
  * (2 K + 8) 2^-24 sum_k |x| m, where m is |w|, for INT4 |w| plus six group
  * scales.  MXFP4 scale bytes of 255 and NVFP4 ones of 0x7F or 0xFF are NaN
- * and make their row's outputs NaN.
+ * and make their row's outputs NaN.  An infinity in a token makes that
+ * token's outputs infinite where the weight is not zero, or NaN for INT4,
+ * whose two parts may pull either way.
  * d->in_dtype and d->ld_in are ignored.  n1 == 0 or N0 == 0 is legal and
  * writes nothing, K == 0 writes zeros.  No workspace.
  */

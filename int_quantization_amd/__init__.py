@@ -253,9 +253,15 @@ def iq_packed_gated(d: IQDesc, act: int, codes_gate: int, scales_gate: int, glob
 
 
 # ---- torch-facing helpers (allocation with torch.empty + the calls above) ---
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def make_desc(fmt: str, gran: str, rows: int, cols: int, in_dtype: int = IQ_BF16, ld: int | None = None,
@@ -577,7 +583,7 @@ def _result(out, shape: tuple, dtype, x, what: str = "out"):
 
 def _check_dense(t, shape: tuple, dtype, x, what: str):
     """t is contiguous, of this shape and type and on x's device."""
-    if t.shape == shape and t.dtype == dtype and t.device == x.device and t.is_contiguous():
+    if t.shape == shape and t.dtype is dtype and t.get_device() == x.get_device() and t.is_contiguous():
         return
     if tuple(t.shape) != shape:
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
@@ -714,9 +720,9 @@ def _packed_weights(q: "Quantized", x, what: str = "weights"):
         raise ValueError(f"{what} must be INT4, NVFP4 or MXFP4")
     group, size = _PACKED[q.fmt]
     codes, scales, uint8 = q.codes, q.scales, _torch().uint8
-    if codes.dtype != uint8 or codes.device != x.device or not codes.is_contiguous() or codes.numel() < q.rows * (q.cols // 2):
+    if codes.dtype is not uint8 or codes.get_device() != x.get_device() or not codes.is_contiguous() or codes.numel() < q.rows * (q.cols // 2):
         _check_buffer(codes, q.rows * (q.cols // 2), f"{what}' codes", x.device, uint8)
-    if (scales.device != x.device or not scales.is_contiguous()
+    if (scales.get_device() != x.get_device() or not scales.is_contiguous()
             or scales.numel() * scales.element_size() < q.rows * (q.cols // group) * size):
         _check_buffer(scales, q.rows * (q.cols // group) * size, f"{what}' scales", x.device)
     if q.fmt == "nvfp4":

@@ -229,3 +229,51 @@ def test_binding_refusals(iq):
         iq.packed_gated(q, iq.Quantized(q.codes, q.scales, None, None, None, "mxfp4", "block", 16, 64), x)
     with pytest.raises(ValueError):
         iq.packed_gated(q, q, x, act="tanh")
+
+
+# ---- what the compiler makes of the products written out -----------------------------------
+def test_products_read_only_operands_that_lds_reads_wrote(tmp_path):
+    """The tiles' products are written out, so the compiler keeps no wait states before them: no vector instruction may
+    write one of their operands within the two states before, none may use scratch memory between them, and 18 states
+    lie between the last product and the first read of a result."""
+    import os
+    import re
+    import subprocess
+
+    from int_quantization_amd import build
+    out = tmp_path / "gated.s"
+    subprocess.run(["/opt/rocm/bin/hipcc", *build.HIPCC_FLAGS, "-I", os.path.join(build.ROOT, "include"), "--cuda-device-only", "-S",
+                    "-o", str(out), os.path.join(build.ROOT, "int_quantization_amd", "csrc", "iq_gated.hip")], check=True,
+                   capture_output=True)
+
+    def registers(operand):
+        m = re.match(r"v\[(\d+):(\d+)\]$|v(\d+)$", operand)
+        return set() if not m else set(range(int(m[1]), int(m[2]) + 1)) if m[1] else {int(m[3])}
+
+    kernels, products = 0, 0
+    code = None
+    for line in out.read_text().splitlines():
+        if re.match(r"_Z\S*k_gemm\S*:", line):
+            code, kernels = [], kernels + 1
+        elif line.startswith(".Lfunc_end") and code is not None:
+            at = [i for i, c in enumerate(code) if c.startswith("v_mfma")]
+            assert not any(c.startswith("scratch") for c in code)
+            for i in at:
+                name, *args = re.split(r"[ ,]+", code[i])
+                assert args[0].startswith("a[") and args[0] == args[3], code[i]
+                reads = registers(args[1]) | registers(args[2])
+                for c in code[max(0, i - 2): i]:
+                    if c.startswith("v_") and not c.startswith("v_mfma"):
+                        assert not registers(re.split(r"[ ,]+", c)[1]) & reads, (c, code[i])
+            after, states = code[at[-1] + 1:], 0
+            for c in after:
+                if c.startswith("v_accvgpr_read"):
+                    break
+                states += int(c.split()[1]) + 1 if c.startswith("s_nop") else 1
+            assert states >= 18, states
+            products, code = products + len(at), None
+        elif code is not None:
+            c = line.split(";")[0].strip()
+            if c and not c.startswith(".") and not c.endswith(":"):
+                code.append(c)
+    assert kernels == 10 and products == 5 * (128 + 32)

@@ -469,3 +469,57 @@ def test_graph_replays_equal_eager_calls(iq):
         for a, b in zip(outs, block(iq, *args)):
             assert torch.equal(a, b), f"replay {k}"
         torch.cuda.synchronize()
+
+
+# ---- the operators together, as the example has them ----------------------------------------
+@pytest.fixture(scope="module")
+def example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "examples", "feed_forward.py")
+    spec = importlib.util.spec_from_file_location("feed_forward", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_example_gradients(iq, example):
+    """The layer's gradients against those of its formula in 64 bits.  Six values between input and gradient are rounded
+    to BF16 (the norm, h, dh, dg or du, dn and the gradient itself), each by half a step at most, and so are the weights
+    in both; the errors of one tensor's elements point every way, so its norm is off by at most the sum of the six."""
+    layer = example.FeedForward(264, 712, act="gelu", seed=4)
+    g = gen(50)
+    x, dy = rand(g, 300, 264), rand(g, 300, 264)
+    y, kept = layer.forward(x)
+    got = layer.backward(dy, kept)
+    got = (y, got[0], *got[1])
+    leaves = [t.double().requires_grad_() for t in (x, layer.weight, layer.bias, layer.gate.to(BF), layer.up.to(BF), layer.down.to(BF))]
+    xd, w, b, wg, wu, wd = leaves
+    c = xd - xd.mean(1, keepdim=True)
+    n = c / torch.sqrt((c * c).mean(1, keepdim=True) + 1e-5) * w + b
+    pre = n @ wg.t()
+    out = xd + (pre * 0.5 * torch.erfc(-pre / 2 ** 0.5) * (n @ wu.t())) @ wd.t()
+    out.backward(dy.double())
+    for o, r in zip(got, (out, *(t.grad for t in leaves))):
+        assert ((o.double() - r).norm() / r.norm()).item() <= 6 * fo.HALF[BF]
+
+
+def test_example_learns(iq, example):
+    losses = example.train(cols=256, features=704, tokens=512, steps=12)[1]
+    assert losses[-1] < losses[0], losses
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4", "int4"])
+def test_example_answers_from_packed_weights(iq, example, fmt):
+    layer = example.FeedForward(256, 768, seed=3)
+    packed = layer.packed(fmt)
+    x = rand(gen(40), 5, 256)
+    n = iq.layer_norm(x, layer.weight, layer.bias)[0]
+    (wg, mg), (wu, mu), (wd, md) = (values(q) for q in packed)
+    (g, eg), (u, eu) = fo.packed(n, (wg, mg)), fo.packed(n, (wu, mu))
+    h, eh = fo.gate(g, u, eg, eu, "silu")
+    eh = eh + fo.HALF[BF] * (h.abs() + eh)                        # h is rounded to BF16
+    z = h @ wd.t().contiguous()
+    ez = eh @ md.t().contiguous() + (2 * 768 + 8) * fo.U * ((h.abs() + eh) @ md.t().contiguous()) + fo.TINY
+    ez = ez + fo.HALF[BF] * (z.abs() + ez)                        # and so is z, and then its sum with x
+    fo.assert_within(layer.answer(x, packed), x.double() + z, ez, fmt)
