@@ -1,7 +1,8 @@
 """Python binding of libiq (block-scaled quantization on MI355X).
 
 A thin ctypes layer over the C ABI declared in include/iq.h: the functions
-below carry the C names and only marshal arguments.  torch provides device
+below carry the C names and only marshal arguments (_fast.so does the same for
+short calls).  torch provides device
 memory (torch.empty) and the current HIP stream; every step of quantization
 runs in the HIP kernels of libiq.so.  There is no CPU fallback: importing
 works anywhere, but any call raises if the library is missing.
@@ -543,8 +544,31 @@ def mxw_gemm(qw: "Quantized", x, out=None, stream=None):
 
 
 # ---- the feed-forward half of a layer ---------------------------------------
-# Calls of a few microseconds of GPU time: the checks below take the common
-# case in one expression each and name what is wrong only where it fails.
+# Calls of a few microseconds of GPU time.  The common case (dense tensors on
+# the current device, results allocated here, torch's current stream) is
+# checked, allocated and called in _fast.so, which returns None for any other;
+# the code below it here serves those and says what is wrong.
+_fast_calls = None
+
+
+def _bind_fast():
+    """The module of _fast.so, bound to the loaded library."""
+    global _fast_calls
+    if _fast_calls is None:
+        import importlib
+        lib = load_library()
+        _torch()
+        path = os.path.join(_HERE, "_fast.so")
+        if not os.path.exists(path):
+            raise OSError(f"_fast.so not found at {path}: build it with __graft_entry__.build()")
+        module = importlib.import_module(__name__ + "._fast")
+        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "iq_layer_norm", "iq_layer_norm_backward", "iq_layer_norm_workspace_bytes", "iq_gated_forward",
+            "iq_gated_backward", "iq_gated_workspace_bytes", "iq_packed_gemv", "iq_packed_gated")))
+        _fast_calls = module
+    return _fast_calls
+
+
 _DTYPES = {}
 
 
@@ -624,6 +648,10 @@ def _norm_params(x, cols: int, weight, bias) -> int:
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
     """y = (x - mean) * rstd * weight + bias over the rows of x [rows, cols]
     (float32 or bfloat16, unit column stride); returns y, mean and rstd."""
+    if out is None and stream is None:
+        done = (_fast_calls or _bind_fast()).layer_norm(x, weight, bias, eps)
+        if done is not None:
+            return done
     d = _norm_desc(x)
     rows, cols = d.rows, d.cols
     pt = _norm_params(x, cols, weight, bias)
@@ -639,6 +667,10 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
 def layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, workspace=None, stream=None):
     """Gradients of layer_norm: dx of x's type, dweight and dbias of weight's
     (of param_dtype, float32 by default, where weight is None)."""
+    if param_dtype is None and workspace is None and stream is None:
+        done = (_fast_calls or _bind_fast()).layer_norm_backward(dy, x, weight, mean, rstd)
+        if done is not None:
+            return done
     f32 = _torch().float32
     d = _norm_desc(x)
     rows, cols = d.rows, d.cols
@@ -678,6 +710,10 @@ def gated(x, w_gate, w_up, act: str = "silu", *, save: bool = False, out=None, s
     """h = act(x w_gate^T) * (x w_up^T) in one kernel, for BF16 x [tokens,
     cols] and weights [features, cols]; with save=True returns h and what
     gated_backward needs."""
+    if out is None and stream is None and act in ACTS:
+        done = (_fast_calls or _bind_fast()).gated(x, w_gate, w_up, ACTS[act], save)
+        if done is not None:
+            return done
     d = _gated_desc(x, w_gate, w_up, act)
     h = _result(out, (d.tokens, d.features), x.dtype, x)
     saved = x.new_empty((2, d.tokens, d.features), dtype=_torch().float32) if save else None
@@ -691,6 +727,10 @@ def gated(x, w_gate, w_up, act: str = "silu", *, save: bool = False, out=None, s
 def gated_backward(dh, x, w_gate, w_up, saved, act: str = "silu", *, workspace=None, stream=None):
     """Gradients of gated from dh [tokens, features] and the forward pass's
     saved values: dx, dw_gate and dw_up, BF16."""
+    if workspace is None and stream is None and act in ACTS:
+        done = (_fast_calls or _bind_fast()).gated_backward(dh, x, w_gate, w_up, saved, ACTS[act])
+        if done is not None:
+            return done
     d = _gated_desc(x, w_gate, w_up, act)
     tokens, cols, features = d.tokens, d.cols, d.features
     _check_dense(dh, (tokens, features), x.dtype, x, "dh")
@@ -707,6 +747,12 @@ def gated_backward(dh, x, w_gate, w_up, saved, act: str = "silu", *, workspace=N
 
 # format -> codes and elements per scale, bytes per scale
 _PACKED = {"int4": (128, 2), "nvfp4": (16, 1), "mxfp4": (32, 1)}
+
+
+def _packed_f32(out_dtype):
+    """Whether the result is float32 (not bfloat16); None for any other type."""
+    code = IQ_BF16 if out_dtype is None else _dtypes().get(out_dtype)
+    return None if code is None else code == IQ_F32
 
 
 def _packed_x(x, cols: int):
@@ -735,6 +781,11 @@ def packed_gemv(q: "Quantized", x, out_dtype=None, out=None, stream=None):
     INT4, NVFP4 or MXFP4 weights q [N0, K] (from quantize); z [n1, N0] is
     bfloat16 (by default) or float32, token-major."""
     rows, cols = q.rows, q.cols
+    f32 = _packed_f32(out_dtype)
+    if out is None and stream is None and f32 is not None and q.fmt in _PACKED:
+        done = (_fast_calls or _bind_fast()).packed_gemv(x, FORMATS[q.fmt], rows, cols, f32, q.codes, q.scales, q.global_scale)
+        if done is not None:
+            return done
     _packed_x(x, cols)
     codes, scales, gscale = _packed_weights(q, x)
     n1 = x.shape[0]
@@ -755,6 +806,12 @@ def packed_gated(q_gate: "Quantized", q_up: "Quantized", x, act: str = "silu", o
     rows, cols = q_gate.rows, q_gate.cols
     if q_gate.fmt != q_up.fmt or rows != q_up.rows or cols != q_up.cols:
         raise ValueError("gate and up weights disagree on format or shape")
+    f32 = _packed_f32(out_dtype)
+    if out is None and stream is None and f32 is not None and q_gate.fmt in _PACKED:
+        done = (_fast_calls or _bind_fast()).packed_gated(x, FORMATS[q_gate.fmt], rows, cols, f32, ACTS[act], q_gate.codes, q_gate.scales,
+                                                     q_gate.global_scale, q_up.codes, q_up.scales, q_up.global_scale)
+        if done is not None:
+            return done
     _packed_x(x, cols)
     gate, up = _packed_weights(q_gate, x, "gate weights"), _packed_weights(q_up, x, "up weights")
     n1 = x.shape[0]

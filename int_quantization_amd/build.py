@@ -13,6 +13,8 @@ SOURCES = [os.path.join(_HERE, "csrc", name) for name in
 OUT = os.path.join(_HERE, "libiq.so")
 BENCH_SOURCES = [os.path.join(_HERE, "csrc", "bench_copy.hip")]
 BENCH_OUT = os.path.join(_HERE, "libiq_bench.so")
+FAST_SOURCE = os.path.join(_HERE, "csrc", "iq_fast.cpp")
+FAST_OUT = os.path.join(_HERE, "_fast.so")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -48,10 +50,24 @@ def _hipcc(sources, out, verbose):
     return out
 
 
+def _host_module(source, out, verbose):
+    """Compile a Python module of host code against torch's headers and libraries."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    _run([os.environ.get("HIPCC", "/opt/rocm/bin/hipcc"), "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+          "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", os.path.join(ROOT, "include"), "-I", os.path.join(home, "include"),
+          "-I", "/opt/rocm/include", "-I", sysconfig.get_path("include"), "-o", out + ".tmp", source,
+          "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"], verbose)
+    os.replace(out + ".tmp", out)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile libiq.so (the library) and libiq_bench.so (the benchmark's
-    reference copy kernel)."""
+    """Compile libiq.so (the library), libiq_bench.so (the benchmark's
+    reference copy kernel) and _fast.so (the binding's short calls)."""
     _hipcc(BENCH_SOURCES, BENCH_OUT, verbose)
+    _host_module(FAST_SOURCE, FAST_OUT, verbose)
     return _hipcc(SOURCES, OUT, verbose)
 
 

@@ -440,6 +440,45 @@ def test_calls_repeat_bit_for_bit(iq):
         assert torch.equal(a, b)
 
 
+def test_short_calls_and_checked_calls_agree(iq):
+    """With a stream named every call goes through the checks in Python; without, dense tensors do not."""
+    x, w, b, wg, wu, dh, qg, qu, qd = block_inputs(iq)
+    s = torch.cuda.current_stream()
+    y, mean, rstd = iq.layer_norm(x, w, b)
+    h, saved = iq.gated(y, wg, wu, "gelu", save=True)
+    few = y[:7].contiguous()
+    for p in (w, None):
+        pairs = [(iq.layer_norm(x, p, b), iq.layer_norm(x, p, b, stream=s)),
+                 (iq.layer_norm_backward(y, x, p, mean, rstd), iq.layer_norm_backward(y, x, p, mean, rstd, stream=s)),
+                 (iq.gated(y, wg, wu, "gelu", save=True), iq.gated(y, wg, wu, "gelu", save=True, stream=s)),
+                 ([iq.gated(y, wg, wu)], [iq.gated(y, wg, wu, stream=s)]),
+                 (iq.gated_backward(dh, y, wg, wu, saved, "gelu"), iq.gated_backward(dh, y, wg, wu, saved, "gelu", stream=s)),
+                 ([iq.packed_gated(qg, qu, few, "gelu_tanh", F32)], [iq.packed_gated(qg, qu, few, "gelu_tanh", F32, stream=s)]),
+                 ([iq.packed_gemv(qg, few)], [iq.packed_gemv(qg, few, stream=s)])]
+        for a, c in pairs:
+            assert len(a) == len(c)
+            for t, u in zip(a, c):
+                assert t.dtype == u.dtype and t.shape == u.shape and torch.equal(t, u)
+    assert iq._bind_fast().layer_norm(x, w, b, 1e-5) is not None and iq._bind_fast().layer_norm(x.t(), w, b, 1e-5) is None
+
+
+def test_refusals_on_the_gpu(iq):
+    """What is wrong is still said, whichever way a call goes first."""
+    x, w, b, wg, wu, dh, qg, qu, qd = block_inputs(iq)
+    y, mean, rstd = iq.layer_norm(x, w, b)
+    h, saved = iq.gated(y, wg, wu, save=True)
+    for error, call in ((ValueError, lambda: iq.layer_norm(x, w[:-1], b)), (TypeError, lambda: iq.layer_norm(x, w, b.float())),
+                        (TypeError, lambda: iq.layer_norm(x.half())), (iq.IQError, lambda: iq.layer_norm(x, w, b, -1.0)),
+                        (ValueError, lambda: iq.layer_norm(x, w.cpu(), b)), (ValueError, lambda: iq.layer_norm_backward(y[1:], x, w, mean, rstd)),
+                        (ValueError, lambda: iq.gated(y, wg, wu, "relu")), (ValueError, lambda: iq.gated(y, wg[:, 1:], wu)),
+                        (iq.IQError, lambda: iq.gated(y[:, :4].contiguous(), wg[:, :4].contiguous(), wu[:, :4].contiguous())),
+                        (TypeError, lambda: iq.gated_backward(dh, y, wg, wu, saved.half())), (ValueError, lambda: iq.packed_gemv(qg, y.float())),
+                        (iq.IQError, lambda: iq.packed_gemv(qg, y)), (TypeError, lambda: iq.packed_gemv(qg, y[:3].contiguous(), torch.float16)),
+                        (ValueError, lambda: iq.packed_gated(qg, qd, y[:3].contiguous())), (ValueError, lambda: iq.packed_gemv(qg, y[:3].cpu()))):
+        with pytest.raises(error):
+            call()
+
+
 def test_another_stream(iq):
     args = block_inputs(iq)
     first = block(iq, *args)
