@@ -35,6 +35,14 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// Waits until at most N loads and copies of the wave are outstanding.
+template <int N> __device__ __forceinline__ void wait_for_all_but() {
+    static_assert(N < 64, "six bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+    asm volatile("" ::: "memory");
+}
+
 // 1 / (1 + e^-v), also for both infinities.
 __device__ __forceinline__ float logistic(float v) { return 1.f / (1.f + __expf(-v)); }
 

@@ -101,20 +101,19 @@ __device__ __forceinline__ bool tile_of(const GemmArgs& a, int& tn, int& tm) {
 // every operand fragment serves 8 products, so that the reads from LDS take
 // half as long as the products.  A lone wave on a SIMD hides nothing by
 // itself, so the instructions are laid out by hand between single products.
-// A step of 64 k:
-//   products of its k 0..31   | reads of its k 32..63, copies of Q of step s + 2
+// A step of 64 k, with copies A = AHEAD steps ahead:
+//   products of its k 0..31   | reads of its k 32..63, copies of Q of step s + A
 //   wait for step s + 1, barrier
 //   products of its k 32..63  | reads of k 0..31 of step s + 1, copies of P of
-//                               step s + 2 over P of step s
-// LDS holds two stages of P and three of Q, all of its 160 KB: the third lets
-// the copies run evenly, one in eight products.  (Sixteen in 64 products stall
+//                               step s + A over P of step s
+// A is 2: LDS holds two stages of P and three of Q, all of its 160 KB.  The
+// third lets the copies run evenly, one in eight products.  (Sixteen in 64 products stall
 // the wave at the copies; steps of 32 k with four stages of both operands read
 // k-contiguous rows in halves of 128-byte lines, which costs as much.)
 //
-// T = 4, two workgroups on a CU: the same for grids that T = 8 leaves too
-// small; the reads take as long as the products.  (1024 tokens, 1024 x 1024,
+// T = 4, two workgroups on a CU (or one, and A = 4): the same for grids that
+// T = 8 leaves too small; the reads take as long as the products.  (1024 tokens, 1024 x 1024,
 // forward: 10 us, and 26 with T = 8, whose prologue alone takes 10.)
-constexpr int kStagesP = 2, kStagesQ = 3;
 
 // A half of a stage: W rows (columns) by 64 k of one operand.
 //   k-contiguous: 16-byte slot s of row r at slot s ^ (r & 7) of its 128 bytes;
@@ -236,10 +235,11 @@ template <class F, int... I> __device__ __forceinline__ void in_turn(F&& f, std:
     (f(std::integral_constant<int, I>{}), ...);
 }
 
-template <int MODE, int ACT, int T> __global__ __launch_bounds__(256, T == 8 ? 1 : 2) void k_gemm(GemmArgs a) {
+template <int MODE, int ACT, int T, int AHEAD> __global__ __launch_bounds__(256, T == 8 || AHEAD > 2 ? 1 : 2) void k_gemm(GemmArgs a) {
     constexpr bool PK = MODE == FWD, QK = MODE != DW;
     constexpr int W = 16 * T, kTileN = MODE == FWD ? W : 2 * W;
     constexpr uint32_t kStage = 2 * kHalf<T>;
+    constexpr int kStagesP = AHEAD, kStagesQ = AHEAD + 1;
     __shared__ __align__(1024) char lds[(kStagesP + kStagesQ) * kStage];
     int tn, tm;
     if (!tile_of(a, tn, tm)) return;
@@ -284,7 +284,7 @@ template <int MODE, int ACT, int T> __global__ __launch_bounds__(256, T == 8 ? 1
 #pragma unroll
         for (int m = 0; m < T; ++m) acc[n][m] = f4v{0.f, 0.f, 0.f, 0.f};
     bf8v pa[T], qa[T], pb[T], qb[T];
-    uint32_t p = 0, q = kStagesP * kStage, q2 = q + 2 * kStage;       // stages of this step; of Q two steps on
+    uint32_t p = 0, q = kStagesP * kStage, q2 = q + AHEAD * kStage;   // stages of this step; of Q's copies
     Read<PK, T> rp;
     Read<QK, T> rq;
     rp.init(lds0 + p, wn, lane);
@@ -301,12 +301,14 @@ template <int MODE, int ACT, int T> __global__ __launch_bounds__(256, T == 8 ? 1
     };
     copy_all(cp, p);
     copy_all(cq, q);
-    advance_q();
-    copy_all(cq, q + kStage);
-    advance_p();
-    copy_all(cp, p + kStage);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(T == 8 ? 0x4F70 : 0x0F78);     // vmcnt(2 T): this wave's copies of the first step have landed
+#pragma unroll
+    for (int d = 1; d < AHEAD; ++d) {
+        advance_q();
+        copy_all(cq, q + d * kStage);
+        advance_p();
+        copy_all(cp, p + d * kStage);
+    }
+    wait_for_all_but<2 * (AHEAD - 1) * T>();          // this wave's copies of the first step have landed
     lds_barrier();
 #pragma unroll
     for (int i = 0; i < 2 * T; ++i) read(i, 0, pa, qa);
@@ -332,15 +334,15 @@ template <int MODE, int ACT, int T> __global__ __launch_bounds__(256, T == 8 ? 1
     // `settle` from the loop alone, without copies that would read them early.
     int s = first;
     do {
-        const uint32_t np = p ^ kStage, nq = q == (kStagesP + kStagesQ - 1) * kStage ? kStagesP * kStage : q + kStage;
+        const uint32_t np = p == (kStagesP - 1) * kStage ? 0 : p + kStage, nq = q == (kStagesP + kStagesQ - 1) * kStage ? kStagesP * kStage : q + kStage;
         products(pa, qa, cq, bufq, q2, [&](int i) {
             if (i % kBefore == 0 && i < 2 * T * kBefore) read(i / kBefore, 1, pb, qb);
             if (i == kEnd - T - 6) advance_p();
             if (i == kEnd - T - 2) bufp = cp.buffer();
             if (i >= kEnd - T) { rp.move(i - kEnd + T, np - p); rq.move(i - kEnd + T, nq - q); }
         });
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070 + T);       // vmcnt(T), lgkmcnt(0): step s + 1 has landed, step s is read
+        __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt(0): step s is read
+        wait_for_all_but<(2 * AHEAD - 3) * T>();      // step s + 1 has landed
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
@@ -349,7 +351,7 @@ template <int MODE, int ACT, int T> __global__ __launch_bounds__(256, T == 8 ? 1
             if (i == kEnd - T - 6) advance_q();
             if (i == kEnd - T - 2) bufq = cq.buffer();
         });
-        q2 = q;                                       // step s + 3 takes the stage of step s
+        q2 = q;                                       // the next step's copies of Q take the stage of this
         p = np;
         q = nq;
     } while (++s < last);
@@ -457,23 +459,29 @@ hipError_t clear(void* p, int64_t n, hipStream_t s) {
 // Tiles of one product and the parts of its sum.  T = 8 where its tiles fill
 // the GPU (2048 tokens, 2048 x 8192, forward, 512 tiles: 110 us, 123 with
 // T = 4; 1024 tokens, 4096 x 4096, 128 tiles: 78 and 61).  Else T = 4 and, for
-// the gradients, the sum split into parts of 8 steps and more until two
-// workgroups per CU are busy (8192 tokens, 256 x 512, the weights' gradients:
-// 88 us in one part, 31 in 16).
+// the gradients, the sum split into parts of 8 steps and more until every CU
+// has a workgroup (8192 tokens, 256 x 512, the weights' gradients: 88 us in one
+// part, 31 in 16; two workgroups to a CU: x's gradient at 512 tokens, 8192 x
+// 1024, 33 us, 23 with one).
+//
+// T = 4 tiles that have their CU alone keep four steps ahead instead of two
+// where the sum is long enough to gain from it (512 tokens, 8192 x 1024,
+// forward, 128 steps: 44 us, 56 with two; 1024 tokens, 1024 x 1024, 16 steps:
+// 10.3 and 9.8).
 //
 // T = 8 tiles take a CU each, so 256 of them are a round.  Where the last round
 // would be half full or less, its columns go to T = 4 tiles, a quarter as large
 // and two to a CU, in a launch of their own (1000 tokens, 4096 x 10000,
 // forward: 129 us, 159 without; 2048 tokens, 4096 x 14336: 354 and 361).
 struct Plan {
-    int T, parts;
+    int T, parts, ahead;
     int32_t tail;          // columns left to T = 4
 };
 Plan plan(int mode, int64_t N, int64_t M, int64_t K) {
     const int64_t width = mode == FWD ? 128 : 256, both = mode == DW ? 2 : 1;
     const int64_t tiles_n = ceil_div(N, width), tiles_m = ceil_div(M, 256) * both, tiles = tiles_n * tiles_m;
     const int64_t steps = ceil_div(K, BK) * (mode == DX ? 2 : 1);
-    Plan p = {8, 1, 0};
+    Plan p = {8, 1, 2, 0};
     if (tiles >= 224) {
         const int64_t over = tiles % 256;
         if (tiles > 256 && over > 0 && over <= 128) {
@@ -483,7 +491,8 @@ Plan plan(int mode, int64_t N, int64_t M, int64_t K) {
     } else {
         p.T = 4;
         const int64_t small = std::max<int64_t>(1, ceil_div(N, width / 2) * ceil_div(M, 128) * both);
-        if (mode != FWD) p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({512 / small, steps / 8, 16}));
+        if (mode != FWD) p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({256 / small, steps / 8, 16}));
+        if (small * p.parts <= 256 && steps / p.parts >= 20) p.ahead = 4;
     }
     return p;
 }
@@ -494,7 +503,7 @@ int64_t part_bytes(int mode, int64_t N, int64_t M, int64_t K) {
     return parts > 1 ? parts * M * N * 4 * (mode == DW ? 2 : 1) : 0;
 }
 
-template <int MODE, int ACT, int T> hipError_t run_tiles(GemmArgs a, int64_t parts, hipStream_t s) {
+template <int MODE, int ACT, int T, int AHEAD> hipError_t run_tiles(GemmArgs a, int64_t parts, hipStream_t s) {
     const int64_t tiles_n = ceil_div(a.N, (MODE == FWD ? 16 : 32) * T), tiles_m = ceil_div(a.M, 32 * T) * (MODE == DW ? 2 : 1);
     const int64_t tiles = tiles_n * tiles_m;
     if (tiles > ((int64_t)1 << 24) - 64) return hipErrorInvalidConfiguration;      // 256 threads each, counted in 32 bits
@@ -502,7 +511,7 @@ template <int MODE, int ACT, int T> hipError_t run_tiles(GemmArgs a, int64_t par
     a.tiles_m = (int32_t)tiles_m;
     a.tiles = (uint32_t)tiles;
     a.per_xcd = (int32_t)ceil_div(tiles, 8);
-    k_gemm<MODE, ACT, T><<<dim3((unsigned)(8 * (int64_t)a.per_xcd), (unsigned)parts), 256, 0, s>>>(a);
+    k_gemm<MODE, ACT, T, AHEAD><<<dim3((unsigned)(8 * (int64_t)a.per_xcd), (unsigned)parts), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -514,21 +523,21 @@ template <int MODE, int ACT> hipError_t run_gemm(GemmArgs& a, hipStream_t s) {
     a.ldo = a.N;
     hipError_t e;
     if (p.T == 4) {
-        e = run_tiles<MODE, ACT, 4>(a, p.parts, s);
+        e = p.ahead == 4 ? run_tiles<MODE, ACT, 4, 4>(a, p.parts, s) : run_tiles<MODE, ACT, 4, 2>(a, p.parts, s);
     } else if (p.tail == 0) {
-        e = run_tiles<MODE, ACT, 8>(a, p.parts, s);
+        e = run_tiles<MODE, ACT, 8, 2>(a, p.parts, s);
     } else {
         const int32_t first = a.N - p.tail;
         GemmArgs t = a;
         a.N = first;
-        if ((e = run_tiles<MODE, ACT, 8>(a, 1, s)) != hipSuccess) return e;
+        if ((e = run_tiles<MODE, ACT, 8, 2>(a, 1, s)) != hipSuccess) return e;
         t.N = p.tail;
         for (int w = 0; w < 2; ++w) {
             t.p[w] += MODE == FWD ? first * t.ldp : first;
             if (t.out[w]) t.out[w] += first;
         }
         if (t.saved) t.saved += first;
-        return run_tiles<MODE, ACT, 4>(t, 1, s);
+        return run_tiles<MODE, ACT, 4, 2>(t, 1, s);
     }
     if (e != hipSuccess || p.parts == 1) return e;
     k_join<<<wide_grid(n * (MODE == DW ? 2 : 1)), 256, 0, s>>>(a.partial, p.parts, n * (MODE == DW ? 2 : 1), n, a.out[0], a.out[1]);

@@ -107,14 +107,6 @@ __device__ __forceinline__ uint32_t int4_upper(uint32_t w) {
 // One step's codes of one fragment, as loaded.
 template <int FMT> struct Codes { u4v v[FMT == F_BF16W ? 4 : 1]; };
 
-// Waits until at most N loads and copies of the wave are outstanding.
-template <int N> __device__ __forceinline__ void wait_for_all_but() {
-    static_assert(N < 64, "six bits");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
-    asm volatile("" ::: "memory");
-}
-
 // XR: token rows that a wave copies to LDS for every step: 4, 8 or 16.
 template <int FMT, int FR, int XR, bool GATED>
 __global__ __launch_bounds__(256, XR > 4 && FMT != F_BF16W ? 3 : 4) void k_packed(PackedK a) {

@@ -276,4 +276,4 @@ def test_products_read_only_operands_that_lds_reads_wrote(tmp_path):
             c = line.split(";")[0].strip()
             if c and not c.startswith(".") and not c.endswith(":"):
                 code.append(c)
-    assert kernels == 10 and products == 5 * (128 + 32)
+    assert kernels == 15 and products == 5 * (128 + 2 * 32)
