@@ -42,73 +42,78 @@ template <int T> struct Elem;
 template <> struct Elem<D_F32> { typedef float type; };
 template <> struct Elem<D_BF16> { typedef uint16_t type; };
 
-// N consecutive elements as FP32: 8 in 16-byte loads, or single ones.
-template <int T, int N> __device__ __forceinline__ void load_n(const void* base, int64_t i, float (&v)[N]) {
-    static_assert(N == 1 || N == 8, "a single element or whole 16-byte words");
-    if constexpr (T == D_F32) {
-        const float* p = static_cast<const float*>(base) + i;
-        if constexpr (N == 1) {
-            v[0] = *p;
-        } else {
-            const u4v a = *reinterpret_cast<const u4v*>(p), b = *reinterpret_cast<const u4v*>(p + 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) { v[k] = as_f(a[k]); v[4 + k] = as_f(b[k]); }
-        }
+// Eight consecutive elements as they lie in memory.  A row may start at any
+// element, so a load is not aligned to its 16 bytes (the hardware takes global
+// loads and stores at any address); of the last vector of a row only the first
+// `have` elements are touched, and the others read as zeros.
+template <int T> struct Raw { u4v w[T == D_F32 ? 2 : 1]; };
+template <int T> __device__ __forceinline__ Raw<T> raw(const void* base, int64_t i, int have) {
+    typedef typename Elem<T>::type E;
+    const E* p = static_cast<const E*>(base) + i;
+    Raw<T> r = {};
+    if (have >= 8) {
+        __builtin_memcpy(&r, p, 8 * sizeof(E));
     } else {
-        const uint16_t* p = static_cast<const uint16_t*>(base) + i;
-        if constexpr (N == 1) {
-            v[0] = as_f((uint32_t)*p << 16);
-        } else {
-            const u4v a = *reinterpret_cast<const u4v*>(p);
+        E e[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) { v[2 * k] = as_f(a[k] << 16); v[2 * k + 1] = as_f(a[k] & 0xFFFF0000u); }
+        for (int k = 0; k < 8; ++k) e[k] = k < have ? p[k] : E(0);
+        __builtin_memcpy(&r, e, 8 * sizeof(E));
+    }
+    return r;
+}
+template <int T> __device__ __forceinline__ void unpack(const Raw<T>& r, float (&v)[8]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (T == D_F32) {
+            v[k] = as_f(r.w[0][k]);
+            v[4 + k] = as_f(r.w[1][k]);
+        } else {
+            v[2 * k] = as_f(r.w[0][k] << 16);
+            v[2 * k + 1] = as_f(r.w[0][k] & 0xFFFF0000u);
         }
     }
 }
-
-// The same elements as they lie in memory, to be taken apart later.
-template <int T, int N> struct Raw { u4v w[T == D_F32 ? 2 : 1]; };
-template <int T> struct Raw<T, 1> { typename Elem<T>::type w; };
-template <int T, int N> __device__ __forceinline__ Raw<T, N> raw(const void* base, int64_t i) {
-    return *reinterpret_cast<const Raw<T, N>*>(static_cast<const typename Elem<T>::type*>(base) + i);
-}
-template <int T, int N> __device__ __forceinline__ void unpack(const Raw<T, N>& r, float (&v)[N]) { load_n<T, N>(&r, 0, v); }
-
-template <int T, int N> __device__ __forceinline__ void store_n(void* base, int64_t i, const float (&v)[N]) {
+template <int T> __device__ __forceinline__ void load8(const void* base, int64_t i, int have, float (&v)[8]) { unpack<T>(raw<T>(base, i, have), v); }
+template <int T> __device__ __forceinline__ void store8(void* base, int64_t i, int have, const float (&v)[8]) {
+    typedef typename Elem<T>::type E;
+    E* p = static_cast<E*>(base) + i;
+    Raw<T> r;
     if constexpr (T == D_F32) {
-        float* p = static_cast<float*>(base) + i;
-        if constexpr (N == 1) {
-            *p = v[0];
-        } else {
-            typedef float f4v __attribute__((ext_vector_type(4)));
-            *reinterpret_cast<f4v*>(p) = f4v{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<f4v*>(p + 4) = f4v{v[4], v[5], v[6], v[7]};
-        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) { r.w[0][k] = __float_as_uint(v[k]); r.w[1][k] = __float_as_uint(v[4 + k]); }
     } else {
-        uint16_t* p = static_cast<uint16_t*>(base) + i;
-        if constexpr (N == 1)
-            *p = (uint16_t)bf16_pair(v[0], 0.f);
-        else
-            *reinterpret_cast<u4v*>(p) = u4v{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
-                                             bf16_pair(v[6], v[7])};
+        r.w[0] = u4v{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+    }
+    if (have >= 8) {
+        __builtin_memcpy(p, &r, 8 * sizeof(E));
+    } else {
+        E e[8];
+        __builtin_memcpy(e, &r, 8 * sizeof(E));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < have) p[k] = e[k];
     }
 }
 
-template <int N> __device__ __forceinline__ void load_param(const void* p, int type, int64_t i, float none, float (&v)[N]) {
+__device__ __forceinline__ void load_param(const void* p, int type, int64_t i, int have, float none, float (&v)[8]) {
     if (!p) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = none;
+        for (int k = 0; k < 8; ++k) v[k] = none;
     } else if (type == D_F32) {
-        load_n<D_F32, N>(p, i, v);
+        load8<D_F32>(p, i, have, v);
     } else {
-        load_n<D_BF16, N>(p, i, v);
+        load8<D_BF16>(p, i, have, v);
     }
 }
 
 __device__ __forceinline__ void store_param(void* p, int type, int64_t i, float v) {
-    const float one[1] = {v};
-    if (type == D_F32) store_n<D_F32, 1>(p, i, one);
-    else store_n<D_BF16, 1>(p, i, one);
+    if (type == D_F32) static_cast<float*>(p)[i] = v;
+    else static_cast<uint16_t*>(p)[i] = (uint16_t)bf16_pair(v, 0.f);
+}
+__device__ __forceinline__ void store_param8(void* p, int type, int64_t i, int have, const float (&v)[8]) {
+    if (!p) return;
+    if (type == D_F32) store8<D_F32>(p, i, have, v);
+    else store8<D_BF16>(p, i, have, v);
 }
 
 // Sum over the wave; every lane returns it.
@@ -139,55 +144,62 @@ template <int NW> __device__ __forceinline__ float block_sum(float a, float (&re
 }
 
 // A workgroup of NT threads takes rows blockIdx.x, + gridDim.x, ...; a thread
-// holds HOLD vectors of N elements of one.
-template <int IN, int N, int NT, int HOLD>
+// holds HOLD vectors of 8 elements of one.
+template <int IN, int NT, int HOLD>
 __global__ __launch_bounds__(NT) void k_norm(NormArgs a) {
     constexpr int NW = NT / 64;
     __shared__ float red[2][2][NW][2];
-    const int t = threadIdx.x, nv = (int)(a.cols / N);
+    const int t = threadIdx.x, nv = (int)((a.cols + 7) / 8);
+    auto have = [&](int64_t c) { return (int)min((int64_t)8, a.cols - 8 * c); };      // elements of vector c
     const float inv = 1.f / (float)a.cols;
-    Raw<IN, N> next[HOLD] = {};
-    float w[HOLD][N], b[HOLD][N];
+    Raw<IN> next[HOLD] = {};
+    float w[HOLD][8], b[HOLD][8];
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
-            if (t + k * NT < nv) next[k] = raw<IN, N>(a.x, row * a.ld + (int64_t)(t + k * NT) * N);
+            if (t + k * NT < nv) next[k] = raw<IN>(a.x, row * a.ld + (int64_t)(t + k * NT) * 8, have(t + k * NT));
     };
     fetch(blockIdx.x);
 #pragma unroll
     for (int k = 0; k < HOLD; ++k)
         if (t + k * NT < nv) {
-            load_param<N>(a.weight, a.param_dtype, (int64_t)(t + k * NT) * N, 1.f, w[k]);
-            load_param<N>(a.bias, a.param_dtype, (int64_t)(t + k * NT) * N, 0.f, b[k]);
+            load_param(a.weight, a.param_dtype, (int64_t)(t + k * NT) * 8, have(t + k * NT), 1.f, w[k]);
+            load_param(a.bias, a.param_dtype, (int64_t)(t + k * NT) * 8, have(t + k * NT), 0.f, b[k]);
         }
     int odd = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, odd ^= 1) {
-        float v[HOLD][N], s = 0.f;
+        float v[HOLD][8], s = 0.f;
 #pragma unroll
-        for (int k = 0; k < HOLD; ++k) unpack<IN, N>(next[k], v[k]);
+        for (int k = 0; k < HOLD; ++k) unpack<IN>(next[k], v[k]);
         if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
             if (t + k * NT < nv) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) s += v[k][i];
+                for (int i = 0; i < 8; ++i) s += v[k][i];
             }
         const float mean = block_sum<NW>(s, red[odd][0]) * inv;
         float q = 0.f;
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
+            if (const int n = have(t + k * NT); n < 8) {              // past the row's end: nothing off the mean
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] = i < n ? v[k][i] : mean;
+            }
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
             if (t + k * NT < nv) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) { v[k][i] -= mean; q = __builtin_fmaf(v[k][i], v[k][i], q); }
+                for (int i = 0; i < 8; ++i) { v[k][i] -= mean; q = __builtin_fmaf(v[k][i], v[k][i], q); }
             }
         const float rstd = 1.f / sqrtf(block_sum<NW>(q, red[odd][1]) * inv + a.eps);
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
             if (t + k * NT < nv) {
-                float y[N];
+                float y[8];
 #pragma unroll
-                for (int i = 0; i < N; ++i) y[i] = __builtin_fmaf(v[k][i] * rstd, w[k][i], b[k][i]);
-                store_n<IN, N>(a.y, row * a.cols + (int64_t)(t + k * NT) * N, y);
+                for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(v[k][i] * rstd, w[k][i], b[k][i]);
+                store8<IN>(a.y, row * a.cols + (int64_t)(t + k * NT) * 8, have(t + k * NT), y);
             }
         if (t == 0) {
             if (a.mean) a.mean[row] = mean;
@@ -197,36 +209,37 @@ __global__ __launch_bounds__(NT) void k_norm(NormArgs a) {
 }
 
 // Rows longer than the registers hold, read three times.
-template <int IN, int N, int NT>
+template <int IN, int NT>
 __global__ __launch_bounds__(NT) void k_norm_long(NormArgs a) {
     constexpr int NW = NT / 64;
     __shared__ float red[2][NW][2];
     const int t = threadIdx.x;
-    const int64_t nv = a.cols / N;
+    const int64_t nv = (a.cols + 7) / 8;
+    auto have = [&](int64_t c) { return (int)min((int64_t)8, a.cols - 8 * c); };      // elements of vector c
     const float inv = 1.f / (float)a.cols;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const int64_t xo = row * a.ld, yo = row * a.cols;
-        float e[N], s = 0.f, q = 0.f;
+        float e[8], s = 0.f, q = 0.f;
         for (int64_t c = t; c < nv; c += NT) {
-            load_n<IN, N>(a.x, xo + c * N, e);
+            load8<IN>(a.x, xo + c * 8, have(c), e);
 #pragma unroll
-            for (int i = 0; i < N; ++i) s += e[i];
+            for (int i = 0; i < 8; ++i) s += e[i];
         }
         const float mean = block_sum<NW>(s, red[0]) * inv;
         for (int64_t c = t; c < nv; c += NT) {
-            load_n<IN, N>(a.x, xo + c * N, e);
+            load8<IN>(a.x, xo + c * 8, have(c), e);
 #pragma unroll
-            for (int i = 0; i < N; ++i) { const float d = e[i] - mean; q = __builtin_fmaf(d, d, q); }
+            for (int i = 0; i < 8; ++i) { const float d = i < have(c) ? e[i] - mean : 0.f; q = __builtin_fmaf(d, d, q); }
         }
         const float rstd = 1.f / sqrtf(block_sum<NW>(q, red[1]) * inv + a.eps);
         for (int64_t c = t; c < nv; c += NT) {
-            float w[N], b[N], y[N];
-            load_n<IN, N>(a.x, xo + c * N, e);
-            load_param<N>(a.weight, a.param_dtype, c * N, 1.f, w);
-            load_param<N>(a.bias, a.param_dtype, c * N, 0.f, b);
+            float w[8], b[8], y[8];
+            load8<IN>(a.x, xo + c * 8, have(c), e);
+            load_param(a.weight, a.param_dtype, c * 8, have(c), 1.f, w);
+            load_param(a.bias, a.param_dtype, c * 8, have(c), 0.f, b);
 #pragma unroll
-            for (int i = 0; i < N; ++i) y[i] = __builtin_fmaf((e[i] - mean) * rstd, w[i], b[i]);
-            store_n<IN, N>(a.y, yo + c * N, y);
+            for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf((e[i] - mean) * rstd, w[i], b[i]);
+            store8<IN>(a.y, yo + c * 8, have(c), y);
         }
         if (t == 0) {
             if (a.mean) a.mean[row] = mean;
@@ -239,22 +252,23 @@ __global__ __launch_bounds__(NT) void k_norm_long(NormArgs a) {
 // thread the same columns of every one of them, so the sums over rows stay
 // in registers until the workgroup's last row and one partial row per
 // workgroup reaches memory; a lone workgroup writes the gradients.
-template <int IN, int N, int NT, int HOLD>
+template <int IN, int NT, int HOLD>
 __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
     constexpr int NW = NT / 64;
     constexpr bool AHEAD = NT < 1024;     // 1024 threads have no registers for the next row
     __shared__ float red[2][NW][2];
     const int t = threadIdx.x;
-    const int nv = (int)(a.cols / N);
+    const int nv = (int)((a.cols + 7) / 8);
+    auto have = [&](int64_t c) { return (int)min((int64_t)8, a.cols - 8 * c); };      // elements of vector c
     const float inv = 1.f / (float)a.cols;
-    float w[HOLD][N], dw[HOLD][N], db[HOLD][N];
+    float w[HOLD][8], dw[HOLD][8], db[HOLD][8];
 #pragma unroll
     for (int k = 0; k < HOLD; ++k) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) { w[k][i] = 0.f; dw[k][i] = 0.f; db[k][i] = 0.f; }
-        if (t + k * NT < nv) load_param<N>(a.weight, a.param_dtype, (int64_t)(t + k * NT) * N, 1.f, w[k]);
+        for (int i = 0; i < 8; ++i) { w[k][i] = 0.f; dw[k][i] = 0.f; db[k][i] = 0.f; }
+        if (t + k * NT < nv) load_param(a.weight, a.param_dtype, (int64_t)(t + k * NT) * 8, have(t + k * NT), 1.f, w[k]);
     }
-    Raw<IN, N> nx[HOLD] = {}, ng[HOLD] = {};
+    Raw<IN> nx[HOLD] = {}, ng[HOLD] = {};
     float next_mean = 0.f, next_rstd = 0.f;
     auto fetch = [&](int64_t row) {
         next_mean = a.mean[row];
@@ -262,8 +276,8 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
             if (t + k * NT < nv) {
-                nx[k] = raw<IN, N>(a.x, row * a.ld + (int64_t)(t + k * NT) * N);
-                ng[k] = raw<IN, N>(a.dy, row * a.cols + (int64_t)(t + k * NT) * N);
+                nx[k] = raw<IN>(a.x, row * a.ld + (int64_t)(t + k * NT) * 8, have(t + k * NT));
+                ng[k] = raw<IN>(a.dy, row * a.cols + (int64_t)(t + k * NT) * 8, have(t + k * NT));
             }
     };
     if (AHEAD) fetch(blockIdx.x);
@@ -271,15 +285,15 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, odd ^= 1) {
         const int64_t yo = row * a.cols;
         const float mean = AHEAD ? next_mean : a.mean[row], rstd = AHEAD ? next_rstd : a.rstd[row];
-        float x[HOLD][N], g[HOLD][N], s1 = 0.f, s2 = 0.f;
+        float x[HOLD][8], g[HOLD][8], s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
             if constexpr (AHEAD) {
-                unpack<IN, N>(nx[k], x[k]);
-                unpack<IN, N>(ng[k], g[k]);
+                unpack<IN>(nx[k], x[k]);
+                unpack<IN>(ng[k], g[k]);
             } else if (t + k * NT < nv) {
-                load_n<IN, N>(a.x, row * a.ld + (int64_t)(t + k * NT) * N, x[k]);
-                load_n<IN, N>(a.dy, yo + (int64_t)(t + k * NT) * N, g[k]);
+                load8<IN>(a.x, row * a.ld + (int64_t)(t + k * NT) * 8, have(t + k * NT), x[k]);
+                load8<IN>(a.dy, yo + (int64_t)(t + k * NT) * 8, have(t + k * NT), g[k]);
             }
         }
         if (AHEAD && row + gridDim.x < a.rows) fetch(row + gridDim.x);
@@ -287,7 +301,7 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
         for (int k = 0; k < HOLD; ++k)
             if (t + k * NT < nv) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     const float n = (x[k][i] - mean) * rstd, e = g[k][i] * w[k][i];
                     x[k][i] = n;
                     dw[k][i] = __builtin_fmaf(g[k][i], n, dw[k][i]);
@@ -304,10 +318,10 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
             if (t + k * NT < nv) {
-                float d[N];
+                float d[8];
 #pragma unroll
-                for (int i = 0; i < N; ++i) d[i] = rstd * (g[k][i] - __builtin_fmaf(x[k][i], s2, s1));
-                store_n<IN, N>(a.dx, yo + (int64_t)(t + k * NT) * N, d);
+                for (int i = 0; i < 8; ++i) d[i] = rstd * (g[k][i] - __builtin_fmaf(x[k][i], s2, s1));
+                store8<IN>(a.dx, yo + (int64_t)(t + k * NT) * 8, have(t + k * NT), d);
             }
     }
     if (!a.dweight && !a.dbias) return;
@@ -315,16 +329,14 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
 #pragma unroll
     for (int k = 0; k < HOLD; ++k)
         if (t + k * NT < nv) {
-            const int64_t c = (int64_t)(t + k * NT) * N;
+            const int64_t c = (int64_t)(t + k * NT) * 8;
+            const int n = have(t + k * NT);
             if (gridDim.x == 1) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    if (a.dweight) store_param(a.dweight, a.param_dtype, c + i, dw[k][i]);
-                    if (a.dbias) store_param(a.dbias, a.param_dtype, c + i, db[k][i]);
-                }
+                store_param8(a.dweight, a.param_dtype, c, n, dw[k]);
+                store_param8(a.dbias, a.param_dtype, c, n, db[k]);
             } else {
-                store_n<D_F32, N>(pw, c, dw[k]);
-                store_n<D_F32, N>(pw + a.cols, c, db[k]);
+                store8<D_F32>(pw, c, n, dw[k]);
+                store8<D_F32>(pw + a.cols, c, n, db[k]);
             }
         }
 }
@@ -332,12 +344,13 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
 // Rows longer than the registers hold: one pass for the sums, one for dx.
 // The sums over rows go through the partial rows in memory, each thread
 // adding to its own columns.
-template <int IN, int N, int NT>
+template <int IN, int NT>
 __global__ __launch_bounds__(NT) void k_norm_grad_long(NormGradArgs a) {
     constexpr int NW = NT / 64;
     __shared__ float red[2][NW][2];
     const int t = threadIdx.x;
-    const int64_t nv = a.cols / N;
+    const int64_t nv = (a.cols + 7) / 8;
+    auto have = [&](int64_t c) { return (int)min((int64_t)8, a.cols - 8 * c); };      // elements of vector c
     const float inv = 1.f / (float)a.cols;
     const bool params = a.dweight || a.dbias;
     float* pw = a.partial + (int64_t)blockIdx.x * 2 * a.cols;
@@ -346,18 +359,18 @@ __global__ __launch_bounds__(NT) void k_norm_grad_long(NormGradArgs a) {
         const int64_t xo = row * a.ld, yo = row * a.cols;
         const float mean = a.mean[row], rstd = a.rstd[row];
         const bool first = row == blockIdx.x;
-        float x[N], g[N], w[N], s1 = 0.f, s2 = 0.f;
+        float x[8], g[8], w[8], s1 = 0.f, s2 = 0.f;
         for (int64_t c = t; c < nv; c += NT) {
-            load_n<IN, N>(a.x, xo + c * N, x);
-            load_n<IN, N>(a.dy, yo + c * N, g);
-            load_param<N>(a.weight, a.param_dtype, c * N, 1.f, w);
-            float pdw[N], pdb[N];
+            load8<IN>(a.x, xo + c * 8, have(c), x);
+            load8<IN>(a.dy, yo + c * 8, have(c), g);
+            load_param(a.weight, a.param_dtype, c * 8, have(c), 1.f, w);
+            float pdw[8], pdb[8];
             if (params && !first) {
-                load_n<D_F32, N>(pw, c * N, pdw);
-                load_n<D_F32, N>(pw + a.cols, c * N, pdb);
+                load8<D_F32>(pw, c * 8, have(c), pdw);
+                load8<D_F32>(pw + a.cols, c * 8, have(c), pdb);
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const float n = (x[i] - mean) * rstd, e = g[i] * w[i];
                 s1 += e;
                 s2 = __builtin_fmaf(e, n, s2);
@@ -365,8 +378,8 @@ __global__ __launch_bounds__(NT) void k_norm_grad_long(NormGradArgs a) {
                 pdb[i] = first ? g[i] : pdb[i] + g[i];
             }
             if (params) {
-                store_n<D_F32, N>(pw, c * N, pdw);
-                store_n<D_F32, N>(pw + a.cols, c * N, pdb);
+                store8<D_F32>(pw, c * 8, have(c), pdw);
+                store8<D_F32>(pw + a.cols, c * 8, have(c), pdb);
             }
         }
         if (!a.dx) continue;
@@ -374,13 +387,13 @@ __global__ __launch_bounds__(NT) void k_norm_grad_long(NormGradArgs a) {
         s1 *= inv;
         s2 *= inv;
         for (int64_t c = t; c < nv; c += NT) {
-            load_n<IN, N>(a.x, xo + c * N, x);
-            load_n<IN, N>(a.dy, yo + c * N, g);
-            load_param<N>(a.weight, a.param_dtype, c * N, 1.f, w);
-            float d[N];
+            load8<IN>(a.x, xo + c * 8, have(c), x);
+            load8<IN>(a.dy, yo + c * 8, have(c), g);
+            load_param(a.weight, a.param_dtype, c * 8, have(c), 1.f, w);
+            float d[8];
 #pragma unroll
-            for (int i = 0; i < N; ++i) d[i] = rstd * (g[i] * w[i] - __builtin_fmaf((x[i] - mean) * rstd, s2, s1));
-            store_n<IN, N>(a.dx, yo + c * N, d);
+            for (int i = 0; i < 8; ++i) d[i] = rstd * (g[i] * w[i] - __builtin_fmaf((x[i] - mean) * rstd, s2, s1));
+            store8<IN>(a.dx, yo + c * 8, have(c), d);
         }
     }
 }
@@ -407,21 +420,19 @@ __global__ __launch_bounds__(1024) void k_norm_fold(const float* partial, int pa
     if (out) store_param(out, type, c < cols ? c : c - cols, s);
 }
 
-bool words(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 constexpr int64_t kNormHeld = 2048;      // vectors of a row that a workgroup's registers hold
 
 // Workgroups of the forward pass: a row each while they fill the GPU twice
 // over at most, then as many as stay resident, each with several rows.
 unsigned norm_grid(int64_t rows, int threads) { return (unsigned)std::min<int64_t>(rows, 256 * (2048 / threads)); }
 
-template <int IN, int N> hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
-    const int64_t nv = a.cols / N;
-    if (nv <= 256) k_norm<IN, N, 256, 1><<<norm_grid(a.rows, 256), 256, 0, s>>>(a);
-    else if (nv <= 512) k_norm<IN, N, 512, 1><<<norm_grid(a.rows, 512), 512, 0, s>>>(a);
-    else if (nv <= 1024) k_norm<IN, N, 512, 2><<<norm_grid(a.rows, 512), 512, 0, s>>>(a);
-    else if (nv <= kNormHeld) k_norm<IN, N, 1024, 2><<<norm_grid(a.rows, 1024), 1024, 0, s>>>(a);
-    else k_norm_long<IN, N, 512><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 512, 0, s>>>(a);
+template <int IN> hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
+    const int64_t nv = (a.cols + 7) / 8;
+    if (nv <= 256) k_norm<IN, 256, 1><<<norm_grid(a.rows, 256), 256, 0, s>>>(a);
+    else if (nv <= 512) k_norm<IN, 512, 1><<<norm_grid(a.rows, 512), 512, 0, s>>>(a);
+    else if (nv <= 1024) k_norm<IN, 512, 2><<<norm_grid(a.rows, 512), 512, 0, s>>>(a);
+    else if (nv <= kNormHeld) k_norm<IN, 1024, 2><<<norm_grid(a.rows, 1024), 1024, 0, s>>>(a);
+    else k_norm_long<IN, 512><<<(unsigned)std::min<int64_t>(a.rows, 1 << 20), 512, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -429,36 +440,28 @@ template <int IN, int N> hipError_t pick_norm(const NormArgs& a, hipStream_t s) 
 // call for one row, 17 with the fold).
 constexpr int64_t kNormLone = 4;
 
-template <int IN, int N> hipError_t pick_grad(const NormGradArgs& a, unsigned grid, hipStream_t s) {
-    const int64_t nv = a.cols / N;
-    if (nv <= 256) k_norm_grad<IN, N, 256, 1><<<grid, 256, 0, s>>>(a);
-    else if (nv <= 512) k_norm_grad<IN, N, 512, 1><<<grid, 512, 0, s>>>(a);
-    else if (nv <= 1024) k_norm_grad<IN, N, 512, 2><<<grid, 512, 0, s>>>(a);
-    else if (nv <= kNormHeld) k_norm_grad<IN, N, 1024, 2><<<grid, 1024, 0, s>>>(a);
-    else k_norm_grad_long<IN, N, 512><<<grid, 512, 0, s>>>(a);
+template <int IN> hipError_t pick_grad(const NormGradArgs& a, unsigned grid, hipStream_t s) {
+    const int64_t nv = (a.cols + 7) / 8;
+    if (nv <= 256) k_norm_grad<IN, 256, 1><<<grid, 256, 0, s>>>(a);
+    else if (nv <= 512) k_norm_grad<IN, 512, 1><<<grid, 512, 0, s>>>(a);
+    else if (nv <= 1024) k_norm_grad<IN, 512, 2><<<grid, 512, 0, s>>>(a);
+    else if (nv <= kNormHeld) k_norm_grad<IN, 1024, 2><<<grid, 1024, 0, s>>>(a);
+    else k_norm_grad_long<IN, 512><<<grid, 512, 0, s>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-// Vectors of 8 where every row of every array starts on a 16-byte word.
 hipError_t launch_layer_norm(const NormArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
-    const bool wide = a.cols % 8 == 0 && (a.ld * (a.in_dtype == D_F32 ? 4 : 2)) % 16 == 0 && words(a.x) && words(a.y) &&
-                      words(a.weight) && words(a.bias);
-    if (a.in_dtype == D_F32) return wide ? pick_norm<D_F32, 8>(a, s) : pick_norm<D_F32, 1>(a, s);
-    return wide ? pick_norm<D_BF16, 8>(a, s) : pick_norm<D_BF16, 1>(a, s);
+    return a.in_dtype == D_F32 ? pick_norm<D_F32>(a, s) : pick_norm<D_BF16>(a, s);
 }
 
 hipError_t launch_layer_norm_grad(const NormGradArgs& a, hipStream_t s) {
-    const bool wide = a.cols % 8 == 0 && (a.ld * (a.in_dtype == D_F32 ? 4 : 2)) % 16 == 0 && words(a.x) && words(a.dy) &&
-                      words(a.dx) && words(a.weight);
-    const bool lone = a.rows > 0 && a.rows <= kNormLone && a.cols / (wide ? 8 : 1) <= kNormHeld;
+    const bool lone = a.rows > 0 && a.rows <= kNormLone && (a.cols + 7) / 8 <= kNormHeld;
     const int parts = lone ? 1 : (int)std::min<int64_t>(a.rows, kNormParts);
     if (parts > 0) {
-        hipError_t e;
-        if (a.in_dtype == D_F32) e = wide ? pick_grad<D_F32, 8>(a, parts, s) : pick_grad<D_F32, 1>(a, parts, s);
-        else e = wide ? pick_grad<D_BF16, 8>(a, parts, s) : pick_grad<D_BF16, 1>(a, parts, s);
+        const hipError_t e = a.in_dtype == D_F32 ? pick_grad<D_F32>(a, parts, s) : pick_grad<D_BF16>(a, parts, s);
         if (e != hipSuccess) return e;
     }
     if ((a.dweight || a.dbias) && !lone)
