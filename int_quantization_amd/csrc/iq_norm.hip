@@ -123,13 +123,14 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-// Sums of two values over the NW waves of a workgroup, in wave order.  `red`
+// Sums of two values over the NW waves of a workgroup or of a group of its
+// threads (t: the thread's number there), in wave order.  `red`
 // may be written again once every thread has passed a later barrier.
-template <int NW> __device__ __forceinline__ void block_sum2(float& a, float& b, float (&red)[NW][2]) {
+template <int NW> __device__ __forceinline__ void block_sum2(float& a, float& b, float (&red)[NW][2], int t = threadIdx.x) {
     a = wave_sum(a);
     b = wave_sum(b);
     if constexpr (NW > 1) {
-        if ((threadIdx.x & 63) == 0) { red[threadIdx.x >> 6][0] = a; red[threadIdx.x >> 6][1] = b; }
+        if ((t & 63) == 0) { red[t >> 6][0] = a; red[t >> 6][1] = b; }
         __syncthreads();
         a = red[0][0];
         b = red[0][1];
@@ -248,16 +249,19 @@ __global__ __launch_bounds__(NT) void k_norm_long(NormArgs a) {
     }
 }
 
-// Backward: workgroup p of the grid takes rows p, p + gridDim.x, ... and a
-// thread the same columns of every one of them, so the sums over rows stay
-// in registers until the workgroup's last row and one partial row per
-// workgroup reaches memory; a lone workgroup writes the gradients.
-template <int IN, int NT, int HOLD>
-__global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
+// Backward: G groups of NT threads take a row each, and a thread the same
+// columns of every row of its group, so the sums over rows stay in registers
+// until the last one.  The groups' sums are added in LDS in their order, and
+// one partial row per workgroup reaches memory; a lone workgroup writes the
+// gradients.  (Narrow rows need the groups: 60000 x 1001 FP32 takes 373 us
+// with one row at a time to a workgroup.)
+template <int IN, int NT, int HOLD, int G>
+__global__ __launch_bounds__(NT * G) void k_norm_grad(NormGradArgs a) {
     constexpr int NW = NT / 64;
-    constexpr bool AHEAD = NT < 1024;     // 1024 threads have no registers for the next row
-    __shared__ float red[2][NW][2];
-    const int t = threadIdx.x;
+    constexpr bool AHEAD = NT * HOLD < 2048;     // 1024 threads of two vectors have no registers for the next row
+    __shared__ float red[2][G][NW][2];
+    __shared__ float sums[G > 1 ? G - 1 : 1][G > 1 ? 2 * HOLD * 8 : 1][NT];
+    const int t = threadIdx.x % NT, g0 = threadIdx.x / NT;
     const int nv = (int)((a.cols + 7) / 8);
     auto have = [&](int64_t c) { return (int)min((int64_t)8, a.cols - 8 * c); };      // elements of vector c
     const float inv = 1.f / (float)a.cols;
@@ -280,26 +284,30 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
                 ng[k] = raw<IN>(a.dy, row * a.cols + (int64_t)(t + k * NT) * 8, have(t + k * NT));
             }
     };
-    if (AHEAD) fetch(blockIdx.x);
+    // every group makes the same number of turns, for their barriers are one
+    const int64_t stride = (int64_t)gridDim.x * G;
+    if (AHEAD && (int64_t)blockIdx.x * G + g0 < a.rows) fetch((int64_t)blockIdx.x * G + g0);
     int odd = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, odd ^= 1) {
+    for (int64_t at = (int64_t)blockIdx.x * G; at < a.rows; at += stride, odd ^= 1) {
+        const int64_t row = at + g0;
+        const bool live = row < a.rows;
         const int64_t yo = row * a.cols;
-        const float mean = AHEAD ? next_mean : a.mean[row], rstd = AHEAD ? next_rstd : a.rstd[row];
+        const float mean = AHEAD ? next_mean : live ? a.mean[row] : 0.f, rstd = AHEAD ? next_rstd : live ? a.rstd[row] : 0.f;
         float x[HOLD][8], g[HOLD][8], s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
             if constexpr (AHEAD) {
                 unpack<IN>(nx[k], x[k]);
                 unpack<IN>(ng[k], g[k]);
-            } else if (t + k * NT < nv) {
+            } else if (live && t + k * NT < nv) {
                 load8<IN>(a.x, row * a.ld + (int64_t)(t + k * NT) * 8, have(t + k * NT), x[k]);
                 load8<IN>(a.dy, yo + (int64_t)(t + k * NT) * 8, have(t + k * NT), g[k]);
             }
         }
-        if (AHEAD && row + gridDim.x < a.rows) fetch(row + gridDim.x);
+        if (AHEAD && row + stride < a.rows) fetch(row + stride);
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
-            if (t + k * NT < nv) {
+            if (live && t + k * NT < nv) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float n = (x[k][i] - mean) * rstd, e = g[k][i] * w[k][i];
@@ -312,12 +320,12 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
                 }
             }
         if (!a.dx) continue;
-        block_sum2<NW>(s1, s2, red[odd]);
+        block_sum2<NW>(s1, s2, red[odd][g0], t);
         s1 *= inv;
         s2 *= inv;
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
-            if (t + k * NT < nv) {
+            if (live && t + k * NT < nv) {
                 float d[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) d[i] = rstd * (g[k][i] - __builtin_fmaf(x[k][i], s2, s1));
@@ -325,6 +333,26 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormGradArgs a) {
             }
     }
     if (!a.dweight && !a.dbias) return;
+    if constexpr (G > 1) {
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (g0) {
+                    sums[g0 - 1][16 * k + i][t] = dw[k][i];
+                    sums[g0 - 1][16 * k + 8 + i][t] = db[k][i];
+                }
+        __syncthreads();
+        if (g0) return;
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                for (int g = 0; g < G - 1; ++g) {
+                    dw[k][i] += sums[g][16 * k + i][t];
+                    db[k][i] += sums[g][16 * k + 8 + i][t];
+                }
+    }
     float* pw = a.partial + (int64_t)blockIdx.x * 2 * a.cols;
 #pragma unroll
     for (int k = 0; k < HOLD; ++k)
@@ -440,12 +468,18 @@ template <int IN> hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
 // call for one row, 17 with the fold).
 constexpr int64_t kNormLone = 4;
 
+// Groups of a workgroup: 1024 threads, or half of them where a thread holds
+// two vectors (and 1024 with one group beyond).
+int norm_groups(int64_t nv) { return nv <= 64 ? 16 : nv <= 128 ? 8 : nv <= 256 ? 4 : nv <= 512 ? 2 : 1; }
+
 template <int IN> hipError_t pick_grad(const NormGradArgs& a, unsigned grid, hipStream_t s) {
     const int64_t nv = (a.cols + 7) / 8;
-    if (nv <= 256) k_norm_grad<IN, 256, 1><<<grid, 256, 0, s>>>(a);
-    else if (nv <= 512) k_norm_grad<IN, 512, 1><<<grid, 512, 0, s>>>(a);
-    else if (nv <= 1024) k_norm_grad<IN, 512, 2><<<grid, 512, 0, s>>>(a);
-    else if (nv <= kNormHeld) k_norm_grad<IN, 1024, 2><<<grid, 1024, 0, s>>>(a);
+    if (nv <= 64) k_norm_grad<IN, 64, 1, 16><<<grid, 1024, 0, s>>>(a);
+    else if (nv <= 128) k_norm_grad<IN, 128, 1, 8><<<grid, 1024, 0, s>>>(a);
+    else if (nv <= 256) k_norm_grad<IN, 256, 1, 4><<<grid, 1024, 0, s>>>(a);
+    else if (nv <= 512) k_norm_grad<IN, 512, 1, 2><<<grid, 1024, 0, s>>>(a);
+    else if (nv <= 1024) k_norm_grad<IN, 512, 2, 1><<<grid, 512, 0, s>>>(a);
+    else if (nv <= kNormHeld) k_norm_grad<IN, 1024, 2, 1><<<grid, 1024, 0, s>>>(a);
     else k_norm_grad_long<IN, 512><<<grid, 512, 0, s>>>(a);
     return hipGetLastError();
 }
@@ -458,8 +492,9 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_layer_norm_grad(const NormGradArgs& a, hipStream_t s) {
-    const bool lone = a.rows > 0 && a.rows <= kNormLone && (a.cols + 7) / 8 <= kNormHeld;
-    const int parts = lone ? 1 : (int)std::min<int64_t>(a.rows, kNormParts);
+    const int64_t nv = (a.cols + 7) / 8, groups = norm_groups(nv);
+    const bool lone = a.rows > 0 && a.rows <= std::max(kNormLone, groups) && nv <= kNormHeld;
+    const int parts = lone ? 1 : (int)std::min<int64_t>((a.rows + groups - 1) / groups, kNormParts);
     if (parts > 0) {
         const hipError_t e = a.in_dtype == D_F32 ? pick_grad<D_F32>(a, parts, s) : pick_grad<D_BF16>(a, parts, s);
         if (e != hipSuccess) return e;
