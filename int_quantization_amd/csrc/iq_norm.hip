@@ -14,7 +14,8 @@
 // much larger than the spread costs no digits.
 // Measured on 8192 x 8192 BF16: forward 48 us (5.6 TB/s), backward 76 (5.3) and
 // the fold of its 256 partial rows 5; with a workgroup to each row and no row
-// ahead 73 and 93.  One row of 4096: 2.9 us, all of it latency.
+// ahead 73 and 93.  8192 x 8191, whose rows start anywhere: 60 and 142, FP32
+// 101 (5.3 TB/s) and 157 (5.1).  One row of 4096: 2.9 us, all of it latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -465,11 +466,10 @@ template <int IN> hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
 }
 
 // Rows that one workgroup takes in less time than the fold's launch (13 us a
-// call for one row, 17 with the fold).
+// call for one row, 17 with the fold), or all at once.
 constexpr int64_t kNormLone = 4;
 
-// Groups of a workgroup: 1024 threads, or half of them where a thread holds
-// two vectors (and 1024 with one group beyond).
+// Rows that a workgroup of the backward pass takes at once, in 1024 threads.
 int norm_groups(int64_t nv) { return nv <= 64 ? 16 : nv <= 128 ? 8 : nv <= 256 ? 4 : nv <= 512 ? 2 : 1; }
 
 template <int IN> hipError_t pick_grad(const NormGradArgs& a, unsigned grid, hipStream_t s) {

@@ -266,6 +266,8 @@ __global__ __launch_bounds__(256, XR > 4 && FMT != F_BF16W ? 3 : 4) void k_packe
         const int unit = FMT == F_INT4 ? 2 : D;                       // whole batches, and whole 4-byte words of scales
         const int share = (s1 - s0 + 4 * unit - 1) / (4 * unit) * unit;
         const int first = s0 + wave * share, end = min(s1, first + share);      // past s1: no steps
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt(0): the last chunk's scales have been read
         if constexpr (SB > 0) {
             const uint32_t per_row = (uint32_t)(FMT == F_INT4 ? a.K / 128 * 2 : FMT == F_NVFP4 ? a.K / 16 : a.K / 32);
             const uint32_t most = (uint32_t)min(kRows, a.n0 - j0);
