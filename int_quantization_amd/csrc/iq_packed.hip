@@ -160,8 +160,10 @@ __global__ __launch_bounds__(256, XR > 4 && FMT != F_BF16W ? 3 : 4) void k_packe
     // wave's last k or the row's, tokens are given an offset beyond their
     // buffer and return zeros, and so are BF16 weights, which need not be
     // finite; codes there are finite and meet zeros, and past the last row
-    // their buffer ends.  A step past the matrix stands for its end, so that
-    // no offset exceeds a buffer.  The loop has no branch: the copies are
+    // their buffer ends.  A step past the matrix stands for its end, and its
+    // offset is part of the lane's: the range check takes a scalar offset off
+    // the buffer's size, which a row shorter than a step (K = 32 .. 96, a
+    // workgroup's only row) does not have.  The loop has no branch: the copies are
     // waited for by counting what was issued after them, and the compiler
     // would move loads into a branch that alone uses them.
     auto k_of = [&](int s, int q) { return s * kStep + (FMT == F_BF16W ? 32 * q + 8 * h : 32 * h); };
@@ -177,9 +179,8 @@ __global__ __launch_bounds__(256, XR > 4 && FMT != F_BF16W ? 3 : 4) void k_packe
                 for (int m = 0; m < M; ++m)
 #pragma unroll
                     for (int f = 0; f < FR; ++f) {
-                        const uint32_t off = FMT != F_BF16W || k_of(s + d, q) < limit ? coff[f] + 64 * q : kOutside;
-                        o.c[d][m][f].v[q] = FMT == F_BF16W ? __builtin_amdgcn_raw_buffer_load_b128(cbuf[m], off + (off == kOutside ? 0 : at), 0, 0)
-                                                           : __builtin_amdgcn_raw_buffer_load_b128(cbuf[m], off, at, 0);
+                        const uint32_t off = FMT != F_BF16W || k_of(s + d, q) < limit ? coff[f] + 64 * q + at : kOutside;
+                        o.c[d][m][f].v[q] = __builtin_amdgcn_raw_buffer_load_b128(cbuf[m], off, 0, 0);
                     }
         }
     };
