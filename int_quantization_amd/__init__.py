@@ -6,9 +6,13 @@ short calls).  torch provides device
 memory (torch.empty) and the current HIP stream; every step of quantization
 runs in the HIP kernels of libiq.so.  There is no CPU fallback: importing
 works anywhere, but any call raises if the library is missing.
+
+With `stream` a call runs on that stream, and what it allocates (results and
+workspace) belongs to it, as under `with torch.cuda.stream(stream)`.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -287,10 +291,23 @@ def desc_for(x, fmt: str, gran: str, cols: int | None = None, flags: int = 0) ->
     return IQDesc(FORMATS[fmt], GRANS[gran], dt, 0, rows, c, ld, flags, 0)
 
 
-def _stream(stream):
+_here = contextlib.nullcontext()
+
+
+def _place(stream):
+    """What a call allocates and launches inside belongs to `stream`, or to
+    torch's current stream where none is named.  Memory of another stream
+    could be taken back, or still be in use there, while the call runs."""
+    if stream is None:
+        return _here
     torch = _torch()
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
+def _stream():
+    return _torch().cuda.current_stream().cuda_stream
 
 
 def _ptr(t):
@@ -385,86 +402,89 @@ def quantize(x, fmt: str, gran: str, *, stats: bool = True, xhat_dtype=None, col
     `out` (a Quantized from a previous call of the same shape) is given.
     static_amax (a device float32 tensor of one element) selects static
     scaling: iq_quantize_static with that absmax instead of the measured one."""
-    torch = _torch()
-    d = desc_for(x, fmt, gran, cols, flags)
-    if out is None:
-        codes, scales, gscale = empty_outputs(d, x.device, fmt, gran)
-        sbuf = torch.empty((64,), dtype=torch.uint8, device=x.device) if stats else None
-        xh = None
-        if xhat_dtype is not None:
-            xh = torch.empty((d.rows, d.cols), dtype=xhat_dtype, device=x.device)
-        shifts = (torch.empty((d.rows, d.cols // 256), dtype=torch.uint8, device=x.device)
-                  if fmt == "int4zp" else None)
-        out = Quantized(codes, scales, gscale, xh, sbuf, fmt, gran, d.rows, d.cols, shifts)
-    else:
-        _check_out(out, d, fmt, gran, x.device)
-    if workspace is None:
-        ws = workspace_for(d, x.device)
-    else:
-        _check_buffer(workspace, iq_workspace_bytes(d), "workspace", x.device)
-        ws = workspace
-    xdt = IQ_F32
-    if out.xhat is not None:
-        xdt = IQ_F32 if out.xhat.dtype == torch.float32 else IQ_BF16
-    if fmt == "int4zp":
-        if static_amax is not None:
-            raise ValueError("static_amax needs a per-tensor format or NVFP4")
-        st = iq_quantize_zp(d, x.data_ptr(), _ptr(out.codes), _ptr(out.scales), _ptr(out.shifts),
-                            _ptr(out.stats_buf), _ptr(out.xhat), xdt, ws.data_ptr(), _stream(stream))
-        _check(st, "iq_quantize_zp")
-    elif static_amax is None:
-        st = iq_quantize(d, x.data_ptr(), _ptr(out.codes), _ptr(out.scales), _ptr(out.global_scale),
-                         _ptr(out.stats_buf), _ptr(out.xhat), xdt, ws.data_ptr(), _stream(stream))
-        _check(st, "iq_quantize")
-    else:
-        if static_amax.dtype != torch.float32 or static_amax.numel() != 1 or static_amax.device != x.device:
-            raise ValueError("static_amax must be one float32 on the input's device")
-        st = iq_quantize_static(d, x.data_ptr(), static_amax.data_ptr(), _ptr(out.codes), _ptr(out.scales),
-                                _ptr(out.global_scale), _ptr(out.stats_buf), _ptr(out.xhat), xdt,
-                                ws.data_ptr(), _stream(stream))
-        _check(st, "iq_quantize_static")
-    return out
+    with _place(stream):
+        torch = _torch()
+        d = desc_for(x, fmt, gran, cols, flags)
+        if out is None:
+            codes, scales, gscale = empty_outputs(d, x.device, fmt, gran)
+            sbuf = torch.empty((64,), dtype=torch.uint8, device=x.device) if stats else None
+            xh = None
+            if xhat_dtype is not None:
+                xh = torch.empty((d.rows, d.cols), dtype=xhat_dtype, device=x.device)
+            shifts = (torch.empty((d.rows, d.cols // 256), dtype=torch.uint8, device=x.device)
+                      if fmt == "int4zp" else None)
+            out = Quantized(codes, scales, gscale, xh, sbuf, fmt, gran, d.rows, d.cols, shifts)
+        else:
+            _check_out(out, d, fmt, gran, x.device)
+        if workspace is None:
+            ws = workspace_for(d, x.device)
+        else:
+            _check_buffer(workspace, iq_workspace_bytes(d), "workspace", x.device)
+            ws = workspace
+        xdt = IQ_F32
+        if out.xhat is not None:
+            xdt = IQ_F32 if out.xhat.dtype == torch.float32 else IQ_BF16
+        if fmt == "int4zp":
+            if static_amax is not None:
+                raise ValueError("static_amax needs a per-tensor format or NVFP4")
+            st = iq_quantize_zp(d, x.data_ptr(), _ptr(out.codes), _ptr(out.scales), _ptr(out.shifts),
+                                _ptr(out.stats_buf), _ptr(out.xhat), xdt, ws.data_ptr(), _stream())
+            _check(st, "iq_quantize_zp")
+        elif static_amax is None:
+            st = iq_quantize(d, x.data_ptr(), _ptr(out.codes), _ptr(out.scales), _ptr(out.global_scale),
+                             _ptr(out.stats_buf), _ptr(out.xhat), xdt, ws.data_ptr(), _stream())
+            _check(st, "iq_quantize")
+        else:
+            if static_amax.dtype != torch.float32 or static_amax.numel() != 1 or static_amax.device != x.device:
+                raise ValueError("static_amax must be one float32 on the input's device")
+            st = iq_quantize_static(d, x.data_ptr(), static_amax.data_ptr(), _ptr(out.codes), _ptr(out.scales),
+                                    _ptr(out.global_scale), _ptr(out.stats_buf), _ptr(out.xhat), xdt,
+                                    ws.data_ptr(), _stream())
+            _check(st, "iq_quantize_static")
+        return out
 
 
 def dequantize(q: Quantized, out_dtype=None, out=None, stream=None):
-    torch = _torch()
-    out_dtype = torch.float32 if out_dtype is None else out_dtype
-    d = make_desc(q.fmt, q.gran, q.rows, q.cols)
-    if out is None:
-        out = torch.empty((q.rows, q.cols), dtype=out_dtype, device=q.codes.device)
-    elif out.dtype not in (torch.float32, torch.bfloat16) or tuple(out.shape) != (q.rows, q.cols):
-        raise ValueError("out must be a float32 or bfloat16 [rows, cols] tensor")
-    else:
-        _check_buffer(out, q.rows * q.cols * out.element_size(), "out", q.codes.device)
-    _check_buffer(q.codes, iq_codes_bytes(d), "codes", q.codes.device, torch.uint8)
-    _check_buffer(q.scales, iq_scales_bytes(d), "scales", q.codes.device)
-    if q.fmt == "nvfp4":
-        _check_buffer(q.global_scale, 4, "global_scale", q.codes.device, torch.float32)
-    if q.fmt == "int4zp":
-        _check_buffer(q.shifts, iq_shifts_bytes(d), "shifts", q.codes.device, torch.uint8)
-    dt = IQ_F32 if out.dtype == torch.float32 else IQ_BF16
-    if q.fmt == "int4zp":
-        st = iq_dequantize_zp(d, q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.shifts), out.data_ptr(), dt,
-                              _stream(stream))
-        _check(st, "iq_dequantize_zp")
+    with _place(stream):
+        torch = _torch()
+        out_dtype = torch.float32 if out_dtype is None else out_dtype
+        d = make_desc(q.fmt, q.gran, q.rows, q.cols)
+        if out is None:
+            out = torch.empty((q.rows, q.cols), dtype=out_dtype, device=q.codes.device)
+        elif out.dtype not in (torch.float32, torch.bfloat16) or tuple(out.shape) != (q.rows, q.cols):
+            raise ValueError("out must be a float32 or bfloat16 [rows, cols] tensor")
+        else:
+            _check_buffer(out, q.rows * q.cols * out.element_size(), "out", q.codes.device)
+        _check_buffer(q.codes, iq_codes_bytes(d), "codes", q.codes.device, torch.uint8)
+        _check_buffer(q.scales, iq_scales_bytes(d), "scales", q.codes.device)
+        if q.fmt == "nvfp4":
+            _check_buffer(q.global_scale, 4, "global_scale", q.codes.device, torch.float32)
+        if q.fmt == "int4zp":
+            _check_buffer(q.shifts, iq_shifts_bytes(d), "shifts", q.codes.device, torch.uint8)
+        dt = IQ_F32 if out.dtype == torch.float32 else IQ_BF16
+        if q.fmt == "int4zp":
+            st = iq_dequantize_zp(d, q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.shifts), out.data_ptr(), dt,
+                                  _stream())
+            _check(st, "iq_dequantize_zp")
+            return out
+        st = iq_dequantize(d, q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.global_scale), out.data_ptr(), dt,
+                           _stream())
+        _check(st, "iq_dequantize")
         return out
-    st = iq_dequantize(d, q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.global_scale), out.data_ptr(), dt,
-                       _stream(stream))
-    _check(st, "iq_dequantize")
-    return out
 
 
 def amax(x, workspace=None, stream=None):
-    torch = _torch()
-    d = desc_for(x, "e4m3", "tensor")
-    out = torch.empty((1,), dtype=torch.float32, device=x.device)
-    if workspace is None:
-        ws = workspace_for(d, x.device)
-    else:
-        _check_buffer(workspace, iq_workspace_bytes(d), "workspace", x.device)
-        ws = workspace
-    _check(iq_amax(d, x.data_ptr(), out.data_ptr(), ws.data_ptr(), _stream(stream)), "iq_amax")
-    return out
+    with _place(stream):
+        torch = _torch()
+        d = desc_for(x, "e4m3", "tensor")
+        out = torch.empty((1,), dtype=torch.float32, device=x.device)
+        if workspace is None:
+            ws = workspace_for(d, x.device)
+        else:
+            _check_buffer(workspace, iq_workspace_bytes(d), "workspace", x.device)
+            ws = workspace
+        _check(iq_amax(d, x.data_ptr(), out.data_ptr(), ws.data_ptr(), _stream()), "iq_amax")
+        return out
 
 
 def _gemm_out(out, n0: int, n1: int, device):
@@ -482,65 +502,68 @@ def zp_gemm(q: "Quantized", x, out=None, stream=None):
     """Puzzle 12's z[j, k] = sum_l sc (w - sh) y[l, k] for asymmetric INT4
     weights q (from quantize(..., "int4zp", "block")) and token-major BF16
     activations x [n1, K]; returns z float32 [N0, n1]."""
-    torch = _torch()
-    if q.fmt != "int4zp":
-        raise ValueError("zp_gemm needs asymmetric INT4 weights")
-    if x.dim() != 2 or x.shape[1] != q.cols or x.dtype != torch.bfloat16 or not x.is_contiguous():
-        raise ValueError("x must be a contiguous BF16 [n1, K] tensor")
-    n1 = x.shape[0]
-    out = _gemm_out(out, q.rows, n1, x.device)
-    d = make_desc("int4zp", "block", q.rows, q.cols)
-    _check_buffer(q.codes, iq_codes_bytes(d), "codes", x.device, torch.uint8)
-    _check_buffer(q.scales, iq_scales_bytes(d), "scales", x.device, torch.float32)
-    _check_buffer(q.shifts, iq_shifts_bytes(d), "shifts", x.device, torch.uint8)
-    st = iq_zp_gemm(d, q.codes.data_ptr(), q.scales.data_ptr(), q.shifts.data_ptr(), x.data_ptr(), IQ_BF16, n1,
-                    out.data_ptr(), _stream(stream))
-    _check(st, "iq_zp_gemm")
-    return out
+    with _place(stream):
+        torch = _torch()
+        if q.fmt != "int4zp":
+            raise ValueError("zp_gemm needs asymmetric INT4 weights")
+        if x.dim() != 2 or x.shape[1] != q.cols or x.dtype != torch.bfloat16 or not x.is_contiguous():
+            raise ValueError("x must be a contiguous BF16 [n1, K] tensor")
+        n1 = x.shape[0]
+        out = _gemm_out(out, q.rows, n1, x.device)
+        d = make_desc("int4zp", "block", q.rows, q.cols)
+        _check_buffer(q.codes, iq_codes_bytes(d), "codes", x.device, torch.uint8)
+        _check_buffer(q.scales, iq_scales_bytes(d), "scales", x.device, torch.float32)
+        _check_buffer(q.shifts, iq_shifts_bytes(d), "shifts", x.device, torch.uint8)
+        st = iq_zp_gemm(d, q.codes.data_ptr(), q.scales.data_ptr(), q.shifts.data_ptr(), x.data_ptr(), IQ_BF16, n1,
+                        out.data_ptr(), _stream())
+        _check(st, "iq_zp_gemm")
+        return out
 
 
 def mx_gemm(qw: "Quantized", qa: "Quantized", out=None, stream=None):
     """FP4 GEMM z[j, t] = sum_k xw[j, k] xa[t, k] of two MXFP4 operands (from
     quantize(..., "mxfp4", "block")), weights qw [N0, K] and activations
     qa [n1, K]; returns z float32 [N0, n1]."""
-    torch = _torch()
-    if qw.fmt != "mxfp4" or qa.fmt != "mxfp4":
-        raise ValueError("mx_gemm needs two MXFP4 operands")
-    if qa.cols != qw.cols:
-        raise ValueError("operands disagree on K")
-    n1 = qa.rows
-    out = _gemm_out(out, qw.rows, n1, qw.codes.device)
-    d = make_desc("mxfp4", "block", qw.rows, qw.cols)
-    da = make_desc("mxfp4", "block", qa.rows, qa.cols)
-    dev = qw.codes.device
-    _check_buffer(qw.codes, iq_codes_bytes(d), "weight codes", dev, torch.uint8)
-    _check_buffer(qw.scales, iq_scales_bytes(d), "weight scales", dev, torch.uint8)
-    _check_buffer(qa.codes, iq_codes_bytes(da), "activation codes", dev, torch.uint8)
-    _check_buffer(qa.scales, iq_scales_bytes(da), "activation scales", dev, torch.uint8)
-    st = iq_mx_gemm(d, qw.codes.data_ptr(), qw.scales.data_ptr(), qa.codes.data_ptr(), qa.scales.data_ptr(), n1,
-                    out.data_ptr(), _stream(stream))
-    _check(st, "iq_mx_gemm")
-    return out
+    with _place(stream):
+        torch = _torch()
+        if qw.fmt != "mxfp4" or qa.fmt != "mxfp4":
+            raise ValueError("mx_gemm needs two MXFP4 operands")
+        if qa.cols != qw.cols:
+            raise ValueError("operands disagree on K")
+        n1 = qa.rows
+        out = _gemm_out(out, qw.rows, n1, qw.codes.device)
+        d = make_desc("mxfp4", "block", qw.rows, qw.cols)
+        da = make_desc("mxfp4", "block", qa.rows, qa.cols)
+        dev = qw.codes.device
+        _check_buffer(qw.codes, iq_codes_bytes(d), "weight codes", dev, torch.uint8)
+        _check_buffer(qw.scales, iq_scales_bytes(d), "weight scales", dev, torch.uint8)
+        _check_buffer(qa.codes, iq_codes_bytes(da), "activation codes", dev, torch.uint8)
+        _check_buffer(qa.scales, iq_scales_bytes(da), "activation scales", dev, torch.uint8)
+        st = iq_mx_gemm(d, qw.codes.data_ptr(), qw.scales.data_ptr(), qa.codes.data_ptr(), qa.scales.data_ptr(), n1,
+                        out.data_ptr(), _stream())
+        _check(st, "iq_mx_gemm")
+        return out
 
 
 def mxw_gemm(qw: "Quantized", x, out=None, stream=None):
     """MXFP4 weights qw [N0, K] (from quantize(..., "mxfp4", "block")) against
     token-major BF16 activations x [n1, K]: z[j, t] = sum_k xw[j, k] x[t, k];
     returns z float32 [N0, n1]."""
-    torch = _torch()
-    if qw.fmt != "mxfp4":
-        raise ValueError("mxw_gemm needs MXFP4 weights")
-    if x.dim() != 2 or x.shape[1] != qw.cols or x.dtype != torch.bfloat16 or not x.is_contiguous():
-        raise ValueError("x must be a contiguous BF16 [n1, K] tensor")
-    n1 = x.shape[0]
-    out = _gemm_out(out, qw.rows, n1, x.device)
-    d = make_desc("mxfp4", "block", qw.rows, qw.cols)
-    _check_buffer(qw.codes, iq_codes_bytes(d), "weight codes", x.device, torch.uint8)
-    _check_buffer(qw.scales, iq_scales_bytes(d), "weight scales", x.device, torch.uint8)
-    st = iq_mxw_gemm(d, qw.codes.data_ptr(), qw.scales.data_ptr(), x.data_ptr(), IQ_BF16, n1, out.data_ptr(),
-                     _stream(stream))
-    _check(st, "iq_mxw_gemm")
-    return out
+    with _place(stream):
+        torch = _torch()
+        if qw.fmt != "mxfp4":
+            raise ValueError("mxw_gemm needs MXFP4 weights")
+        if x.dim() != 2 or x.shape[1] != qw.cols or x.dtype != torch.bfloat16 or not x.is_contiguous():
+            raise ValueError("x must be a contiguous BF16 [n1, K] tensor")
+        n1 = x.shape[0]
+        out = _gemm_out(out, qw.rows, n1, x.device)
+        d = make_desc("mxfp4", "block", qw.rows, qw.cols)
+        _check_buffer(qw.codes, iq_codes_bytes(d), "weight codes", x.device, torch.uint8)
+        _check_buffer(qw.scales, iq_scales_bytes(d), "weight scales", x.device, torch.uint8)
+        st = iq_mxw_gemm(d, qw.codes.data_ptr(), qw.scales.data_ptr(), x.data_ptr(), IQ_BF16, n1, out.data_ptr(),
+                         _stream())
+        _check(st, "iq_mxw_gemm")
+        return out
 
 
 # ---- the feed-forward half of a layer ---------------------------------------
@@ -587,12 +610,10 @@ def _dtype_of(t, what: str) -> int:
     return code
 
 
-def _stream_for(x, stream):
+def _stream_for(x):
     """The stream of a call on x, which has to be in GPU memory."""
     if not x.is_cuda:
         raise ValueError(f"x is on {x.device}, not on a GPU")
-    if stream is not None:
-        return stream.cuda_stream
     torch = _torch()
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())     # current_stream() without its object
 
@@ -652,16 +673,17 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
         done = (_fast_calls or _bind_fast()).layer_norm(x, weight, bias, eps)
         if done is not None:
             return done
-    d = _norm_desc(x)
-    rows, cols = d.rows, d.cols
-    pt = _norm_params(x, cols, weight, bias)
-    y = _torch().empty_like(x) if out is None and x.is_contiguous() else _result(out, (rows, cols), x.dtype, x)
-    mean, rstd = x.new_empty((2, rows), dtype=_torch().float32).unbind(0)
-    st = iq_layer_norm(d, x.data_ptr(), _ptr(weight), _ptr(bias), pt, eps, y.data_ptr(), mean.data_ptr(),
-                       rstd.data_ptr(), _stream_for(x, stream))
-    if st:
-        _check(st, "iq_layer_norm")
-    return y, mean, rstd
+    with _place(stream):
+        d = _norm_desc(x)
+        rows, cols = d.rows, d.cols
+        pt = _norm_params(x, cols, weight, bias)
+        y = _torch().empty_like(x) if out is None and x.is_contiguous() else _result(out, (rows, cols), x.dtype, x)
+        mean, rstd = x.new_empty((2, rows), dtype=_torch().float32).unbind(0)
+        st = iq_layer_norm(d, x.data_ptr(), _ptr(weight), _ptr(bias), pt, eps, y.data_ptr(), mean.data_ptr(),
+                           rstd.data_ptr(), _stream_for(x))
+        if st:
+            _check(st, "iq_layer_norm")
+        return y, mean, rstd
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, workspace=None, stream=None):
@@ -671,24 +693,25 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, workspac
         done = (_fast_calls or _bind_fast()).layer_norm_backward(dy, x, weight, mean, rstd)
         if done is not None:
             return done
-    f32 = _torch().float32
-    d = _norm_desc(x)
-    rows, cols = d.rows, d.cols
-    pt = _norm_params(x, cols, weight, None)
-    _check_dense(dy, (rows, cols), x.dtype, x, "dy")
-    _check_dense(mean, (rows,), f32, x, "mean")
-    _check_dense(rstd, (rows,), f32, x, "rstd")
-    pdt = weight.dtype if weight is not None else f32 if param_dtype is None else param_dtype
-    dx = _torch().empty_like(dy)
-    dweight, dbias = x.new_empty((2, cols), dtype=pdt).unbind(0)
-    if weight is None:
-        pt = _dtype_of(dweight, "param_dtype")
-    ws = _scratch(workspace, iq_layer_norm_workspace_bytes(d), x)
-    st = iq_layer_norm_backward(d, x.data_ptr(), dy.data_ptr(), _ptr(weight), pt, mean.data_ptr(), rstd.data_ptr(),
-                                dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr(), _stream_for(x, stream))
-    if st:
-        _check(st, "iq_layer_norm_backward")
-    return dx, dweight, dbias
+    with _place(stream):
+        f32 = _torch().float32
+        d = _norm_desc(x)
+        rows, cols = d.rows, d.cols
+        pt = _norm_params(x, cols, weight, None)
+        _check_dense(dy, (rows, cols), x.dtype, x, "dy")
+        _check_dense(mean, (rows,), f32, x, "mean")
+        _check_dense(rstd, (rows,), f32, x, "rstd")
+        pdt = weight.dtype if weight is not None else f32 if param_dtype is None else param_dtype
+        dx = _torch().empty_like(dy)
+        dweight, dbias = x.new_empty((2, cols), dtype=pdt).unbind(0)
+        if weight is None:
+            pt = _dtype_of(dweight, "param_dtype")
+        ws = _scratch(workspace, iq_layer_norm_workspace_bytes(d), x)
+        st = iq_layer_norm_backward(d, x.data_ptr(), dy.data_ptr(), _ptr(weight), pt, mean.data_ptr(), rstd.data_ptr(),
+                                    dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr(), _stream_for(x))
+        if st:
+            _check(st, "iq_layer_norm_backward")
+        return dx, dweight, dbias
 
 
 def _gated_desc(x, w_gate, w_up, act: str):
@@ -714,14 +737,15 @@ def gated(x, w_gate, w_up, act: str = "silu", *, save: bool = False, out=None, s
         done = (_fast_calls or _bind_fast()).gated(x, w_gate, w_up, ACTS[act], save)
         if done is not None:
             return done
-    d = _gated_desc(x, w_gate, w_up, act)
-    h = _result(out, (d.tokens, d.features), x.dtype, x)
-    saved = x.new_empty((2, d.tokens, d.features), dtype=_torch().float32) if save else None
-    st = iq_gated_forward(d, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(), _ptr(saved),
-                          _stream_for(x, stream))
-    if st:
-        _check(st, "iq_gated_forward")
-    return (h, saved) if save else h
+    with _place(stream):
+        d = _gated_desc(x, w_gate, w_up, act)
+        h = _result(out, (d.tokens, d.features), x.dtype, x)
+        saved = x.new_empty((2, d.tokens, d.features), dtype=_torch().float32) if save else None
+        st = iq_gated_forward(d, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(), _ptr(saved),
+                              _stream_for(x))
+        if st:
+            _check(st, "iq_gated_forward")
+        return (h, saved) if save else h
 
 
 def gated_backward(dh, x, w_gate, w_up, saved, act: str = "silu", *, workspace=None, stream=None):
@@ -731,18 +755,19 @@ def gated_backward(dh, x, w_gate, w_up, saved, act: str = "silu", *, workspace=N
         done = (_fast_calls or _bind_fast()).gated_backward(dh, x, w_gate, w_up, saved, ACTS[act])
         if done is not None:
             return done
-    d = _gated_desc(x, w_gate, w_up, act)
-    tokens, cols, features = d.tokens, d.cols, d.features
-    _check_dense(dh, (tokens, features), x.dtype, x, "dh")
-    _check_dense(saved, (2, tokens, features), _torch().float32, x, "saved")
-    dx = x.new_empty((tokens, cols))
-    dwg, dwu = x.new_empty((2, features, cols)).unbind(0)
-    ws = _scratch(workspace, iq_gated_workspace_bytes(d), x)
-    st = iq_gated_backward(d, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), saved.data_ptr(),
-                           dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), ws.data_ptr(), _stream_for(x, stream))
-    if st:
-        _check(st, "iq_gated_backward")
-    return dx, dwg, dwu
+    with _place(stream):
+        d = _gated_desc(x, w_gate, w_up, act)
+        tokens, cols, features = d.tokens, d.cols, d.features
+        _check_dense(dh, (tokens, features), x.dtype, x, "dh")
+        _check_dense(saved, (2, tokens, features), _torch().float32, x, "saved")
+        dx = x.new_empty((tokens, cols))
+        dwg, dwu = x.new_empty((2, features, cols)).unbind(0)
+        ws = _scratch(workspace, iq_gated_workspace_bytes(d), x)
+        st = iq_gated_backward(d, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), saved.data_ptr(),
+                               dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), ws.data_ptr(), _stream_for(x))
+        if st:
+            _check(st, "iq_gated_backward")
+        return dx, dwg, dwu
 
 
 # format -> codes and elements per scale, bytes per scale
@@ -786,15 +811,16 @@ def packed_gemv(q: "Quantized", x, out_dtype=None, out=None, stream=None):
         done = (_fast_calls or _bind_fast()).packed_gemv(x, FORMATS[q.fmt], rows, cols, f32, q.codes, q.scales, q.global_scale)
         if done is not None:
             return done
-    _packed_x(x, cols)
-    codes, scales, gscale = _packed_weights(q, x)
-    n1 = x.shape[0]
-    z = _result(out, (n1, rows), x.dtype if out_dtype is None else out_dtype, x)
-    st = iq_packed_gemv(make_desc(q.fmt, "block", rows, cols), codes, scales, gscale, x.data_ptr(), IQ_BF16, n1,
-                        z.data_ptr(), _dtype_of(z, "out"), _stream_for(x, stream))
-    if st:
-        _check(st, "iq_packed_gemv")
-    return z
+    with _place(stream):
+        _packed_x(x, cols)
+        codes, scales, gscale = _packed_weights(q, x)
+        n1 = x.shape[0]
+        z = _result(out, (n1, rows), x.dtype if out_dtype is None else out_dtype, x)
+        st = iq_packed_gemv(make_desc(q.fmt, "block", rows, cols), codes, scales, gscale, x.data_ptr(), IQ_BF16, n1,
+                            z.data_ptr(), _dtype_of(z, "out"), _stream_for(x))
+        if st:
+            _check(st, "iq_packed_gemv")
+        return z
 
 
 def packed_gated(q_gate: "Quantized", q_up: "Quantized", x, act: str = "silu", out_dtype=None, out=None, stream=None):
@@ -812,12 +838,13 @@ def packed_gated(q_gate: "Quantized", q_up: "Quantized", x, act: str = "silu", o
                                                      q_gate.global_scale, q_up.codes, q_up.scales, q_up.global_scale)
         if done is not None:
             return done
-    _packed_x(x, cols)
-    gate, up = _packed_weights(q_gate, x, "gate weights"), _packed_weights(q_up, x, "up weights")
-    n1 = x.shape[0]
-    h = _result(out, (n1, rows), x.dtype if out_dtype is None else out_dtype, x)
-    st = iq_packed_gated(make_desc(q_gate.fmt, "block", rows, cols), ACTS[act], *gate, *up, x.data_ptr(), IQ_BF16, n1,
-                         h.data_ptr(), _dtype_of(h, "out"), _stream_for(x, stream))
-    if st:
-        _check(st, "iq_packed_gated")
-    return h
+    with _place(stream):
+        _packed_x(x, cols)
+        gate, up = _packed_weights(q_gate, x, "gate weights"), _packed_weights(q_up, x, "up weights")
+        n1 = x.shape[0]
+        h = _result(out, (n1, rows), x.dtype if out_dtype is None else out_dtype, x)
+        st = iq_packed_gated(make_desc(q_gate.fmt, "block", rows, cols), ACTS[act], *gate, *up, x.data_ptr(), IQ_BF16, n1,
+                             h.data_ptr(), _dtype_of(h, "out"), _stream_for(x))
+        if st:
+            _check(st, "iq_packed_gated")
+        return h

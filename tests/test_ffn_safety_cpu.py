@@ -3,8 +3,11 @@ their operands, buffers that another stream may take, results cut from a graph."
 import os
 import re
 import subprocess
+from functools import partial
 
 import pytest
+import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 
 @pytest.fixture(scope="module")
@@ -65,3 +68,89 @@ def test_packed_code_offsets_stay_in_their_rows(cols):
                     at = row * row_bytes + 16 * h + 64 * min(step, steps)
                     if at < size:
                         assert at + 16 <= size
+
+
+# ---- buffers of a named stream -----------------------------------------------------------
+class Allocations(TorchDispatchMode):
+    """Notes for every tensor made whether `place` was entered."""
+
+    def __init__(self, place):
+        super().__init__()
+        self.place, self.seen = place, []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        if func.overloadpacket.__name__ in ("empty", "empty_like", "new_empty", "empty_strided", "zeros", "full"):
+            self.seen.append(self.place.inside)
+        return func(*args, **(kwargs or {}))
+
+
+class Place:
+    """Stands for torch.cuda.stream: the streams named, and whether one is current."""
+
+    def __init__(self):
+        self.named, self.inside = [], False
+
+    def __call__(self, stream):
+        self.named.append(stream)
+        return self
+
+    def __enter__(self):
+        self.inside = True
+
+    def __exit__(self, *error):
+        self.inside = False
+
+
+class FakeStream:
+    cuda_stream, device = 0, torch.device("cpu")
+
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def packed(iq, fmt, rows=32, cols=256):
+    d = iq.make_desc(fmt, "block", rows, cols)
+    codes, scales, g = iq.empty_outputs(d, "cpu", fmt, "block")
+    shifts = torch.zeros(rows, cols // 256, dtype=torch.uint8) if fmt == "int4zp" else None
+    return iq.Quantized(codes, scales, g, None, None, fmt, "block", rows, cols, shifts)
+
+
+X, W, STAT = torch.zeros(4, 256, dtype=BF), torch.zeros(32, 256, dtype=BF), torch.zeros(4)
+DH, SAVED = torch.zeros(4, 32, dtype=BF), torch.zeros(2, 4, 32)
+CALLS = {                          # each makes its operands and returns the call
+    "quantize": lambda iq: partial(iq.quantize, X, "nvfp4", "block", xhat_dtype=F32),
+    "quantize static": lambda iq: partial(iq.quantize, X, "nvfp4", "block", static_amax=STAT[:1]),
+    "quantize int4zp": lambda iq: partial(iq.quantize, X, "int4zp", "block"),
+    "dequantize": lambda iq: partial(iq.dequantize, packed(iq, "nvfp4")),
+    "dequantize int4zp": lambda iq: partial(iq.dequantize, packed(iq, "int4zp")),
+    "amax": lambda iq: partial(iq.amax, X),
+    "zp_gemm": lambda iq: partial(iq.zp_gemm, packed(iq, "int4zp"), X),
+    "mx_gemm": lambda iq: partial(iq.mx_gemm, packed(iq, "mxfp4"), packed(iq, "mxfp4", 4)),
+    "mxw_gemm": lambda iq: partial(iq.mxw_gemm, packed(iq, "mxfp4"), X),
+    "layer_norm": lambda iq: partial(iq.layer_norm, X),
+    "layer_norm_backward": lambda iq: partial(iq.layer_norm_backward, X, X, None, STAT, STAT),
+    "gated": lambda iq: partial(iq.gated, X, W, W, save=True),
+    "gated_backward": lambda iq: partial(iq.gated_backward, DH, X, W, W, SAVED),
+    "packed_gemv": lambda iq: partial(iq.packed_gemv, packed(iq, "int4"), X),
+    "packed_gated": lambda iq: partial(iq.packed_gated, packed(iq, "mxfp4"), packed(iq, "mxfp4"), X),
+}
+LAUNCHES = ("iq_quantize", "iq_quantize_static", "iq_quantize_zp", "iq_dequantize", "iq_dequantize_zp", "iq_amax", "iq_zp_gemm",
+            "iq_mx_gemm", "iq_mxw_gemm", "iq_layer_norm", "iq_layer_norm_backward", "iq_gated_forward", "iq_gated_backward",
+            "iq_packed_gemv", "iq_packed_gated")
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_named_streams_call_allocates_under_that_stream(iq, monkeypatch, name):
+    """Results and workspace taken from another stream's memory could be handed out again there while the call runs."""
+    place, launched, call = Place(), [], CALLS[name](iq)
+    monkeypatch.setattr(torch.cuda, "stream", place)
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    for of in ("_stream", "_stream_for"):
+        monkeypatch.setattr(iq, of, lambda *a: 0, raising=False)
+    for launch in LAUNCHES:
+        monkeypatch.setattr(iq, launch, lambda *a: launched.append(place.inside) or iq.IQ_OK)
+    stream = FakeStream()
+    with Allocations(place) as made:
+        call(stream=stream)
+    assert launched == [True] and place.named == [stream]
+    assert made.seen and all(made.seen)

@@ -21,3 +21,45 @@ def test_packed_lone_short_rows(iq, fmt, rows):  # noqa: F811
             fo.assert_within(iq.packed_gemv(q, x, F32), *want, f"{cols} columns, {n1} tokens")
             h = iq.packed_gated(q, q, torch.zeros_like(x), "silu", BF)
             assert not h.any()
+
+
+# ---- a named stream -----------------------------------------------------------------------
+def test_calls_on_a_named_stream_keep_their_buffers(iq):  # noqa: F811
+    """Every call on a stream of its own that is still busy, while the current stream takes blocks of the sizes of the calls'
+    results and workspaces and overwrites them: the same bits as without."""
+    g = gen(60)
+    x, wg, wu = rand(g, 300, 256), rand(g, 512, 256, scale=0.06), rand(g, 512, 256, scale=0.06)
+    dh, dy, few = rand(g, 300, 512, scale=0.1), rand(g, 300, 256), x[:7].contiguous()
+    y, mean, rstd = iq.layer_norm(x)
+    h, saved = iq.gated(x, wg, wu, save=True)
+    q, zp = iq.quantize(wg, "nvfp4", "block", stats=False), iq.quantize(wg, "int4zp", "block", stats=False)
+    mx, mxa = iq.quantize(wg, "mxfp4", "block", stats=False), iq.quantize(x, "mxfp4", "block", stats=False)
+
+    def outputs(t):
+        if isinstance(t, iq.Quantized):
+            return [u for u in (t.codes, t.scales, t.global_scale, t.xhat, t.shifts) if u is not None]
+        return [t] if torch.is_tensor(t) else list(t)
+
+    calls = [lambda s: iq.layer_norm(x, stream=s), lambda s: iq.layer_norm_backward(dy, x, None, mean, rstd, stream=s),
+             lambda s: iq.gated(x, wg, wu, save=True, stream=s), lambda s: iq.gated_backward(dh, x, wg, wu, saved, stream=s),
+             lambda s: iq.packed_gemv(q, few, F32, stream=s), lambda s: iq.packed_gated(q, q, few, stream=s),
+             lambda s: iq.quantize(x, "nvfp4", "block", xhat_dtype=F32, stream=s), lambda s: iq.quantize(x, "int8", "tensor", stream=s),
+             lambda s: iq.quantize(x, "int4zp", "block", stream=s), lambda s: iq.amax(x, stream=s), lambda s: iq.dequantize(q, stream=s),
+             lambda s: iq.zp_gemm(zp, few, stream=s), lambda s: iq.mx_gemm(mx, mxa, stream=s), lambda s: iq.mxw_gemm(mx, few, stream=s)]
+    side = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, generator=g, device="cuda")
+    sizes = [n for n in (256, 512, 1024, 4096, 65536, 153600, 307200, 614400, 921600, 1228800) for _ in range(4)]
+    for k, call in enumerate(calls):
+        print("call", k, flush=True)
+        want = [t.clone() for t in outputs(call(None))]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            keep = [busy @ busy for _ in range(4)]         # a few milliseconds before the call's kernels
+        got = outputs(call(side))
+        for _ in range(3):
+            blocks = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in sizes]
+            del blocks
+        side.synchronize()
+        assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want)), k
+        torch.cuda.synchronize()
+        del keep
