@@ -294,20 +294,27 @@ def desc_for(x, fmt: str, gran: str, cols: int | None = None, flags: int = 0) ->
 _here = contextlib.nullcontext()
 
 
-def _place(stream):
-    """What a call allocates and launches inside belongs to `stream`, or to
-    torch's current stream where none is named.  Memory of another stream
-    could be taken back, or still be in use there, while the call runs."""
-    if stream is None:
-        return _here
+def _place(stream, x):
+    """What a call on x allocates and launches inside belongs to `stream`, or
+    to the current stream of x's device where none is named.  Memory of another
+    stream could be taken back, or still be in use there, while the call runs."""
     torch = _torch()
+    if stream is None:
+        if not x.is_cuda or x.get_device() == torch._C._cuda_getDevice():
+            return _here
+        return torch.cuda.device(x.device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, x.device)
+    if stream.device != x.device:
+        raise ValueError(f"x is on {x.device}, the stream on {stream.device}")
     return torch.cuda.stream(stream)
 
 
-def _stream():
-    return _torch().cuda.current_stream().cuda_stream
+def _stream_for(x):
+    """The stream that a call on x runs on, inside `_place`; x has to be in GPU memory."""
+    if not x.is_cuda:
+        raise ValueError(f"x is on {x.device}, not on a GPU")
+    return _torch()._C._cuda_getCurrentRawStream(x.get_device())     # current_stream() without its object
 
 
 def _ptr(t):
@@ -402,7 +409,7 @@ def quantize(x, fmt: str, gran: str, *, stats: bool = True, xhat_dtype=None, col
     `out` (a Quantized from a previous call of the same shape) is given.
     static_amax (a device float32 tensor of one element) selects static
     scaling: iq_quantize_static with that absmax instead of the measured one."""
-    with _place(stream):
+    with _place(stream, x):
         torch = _torch()
         d = desc_for(x, fmt, gran, cols, flags)
         if out is None:
@@ -428,24 +435,24 @@ def quantize(x, fmt: str, gran: str, *, stats: bool = True, xhat_dtype=None, col
             if static_amax is not None:
                 raise ValueError("static_amax needs a per-tensor format or NVFP4")
             st = iq_quantize_zp(d, x.data_ptr(), _ptr(out.codes), _ptr(out.scales), _ptr(out.shifts),
-                                _ptr(out.stats_buf), _ptr(out.xhat), xdt, ws.data_ptr(), _stream())
+                                _ptr(out.stats_buf), _ptr(out.xhat), xdt, ws.data_ptr(), _stream_for(x))
             _check(st, "iq_quantize_zp")
         elif static_amax is None:
             st = iq_quantize(d, x.data_ptr(), _ptr(out.codes), _ptr(out.scales), _ptr(out.global_scale),
-                             _ptr(out.stats_buf), _ptr(out.xhat), xdt, ws.data_ptr(), _stream())
+                             _ptr(out.stats_buf), _ptr(out.xhat), xdt, ws.data_ptr(), _stream_for(x))
             _check(st, "iq_quantize")
         else:
             if static_amax.dtype != torch.float32 or static_amax.numel() != 1 or static_amax.device != x.device:
                 raise ValueError("static_amax must be one float32 on the input's device")
             st = iq_quantize_static(d, x.data_ptr(), static_amax.data_ptr(), _ptr(out.codes), _ptr(out.scales),
                                     _ptr(out.global_scale), _ptr(out.stats_buf), _ptr(out.xhat), xdt,
-                                    ws.data_ptr(), _stream())
+                                    ws.data_ptr(), _stream_for(x))
             _check(st, "iq_quantize_static")
         return out
 
 
 def dequantize(q: Quantized, out_dtype=None, out=None, stream=None):
-    with _place(stream):
+    with _place(stream, q.codes):
         torch = _torch()
         out_dtype = torch.float32 if out_dtype is None else out_dtype
         d = make_desc(q.fmt, q.gran, q.rows, q.cols)
@@ -464,17 +471,17 @@ def dequantize(q: Quantized, out_dtype=None, out=None, stream=None):
         dt = IQ_F32 if out.dtype == torch.float32 else IQ_BF16
         if q.fmt == "int4zp":
             st = iq_dequantize_zp(d, q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.shifts), out.data_ptr(), dt,
-                                  _stream())
+                                  _stream_for(q.codes))
             _check(st, "iq_dequantize_zp")
             return out
         st = iq_dequantize(d, q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.global_scale), out.data_ptr(), dt,
-                           _stream())
+                           _stream_for(q.codes))
         _check(st, "iq_dequantize")
         return out
 
 
 def amax(x, workspace=None, stream=None):
-    with _place(stream):
+    with _place(stream, x):
         torch = _torch()
         d = desc_for(x, "e4m3", "tensor")
         out = torch.empty((1,), dtype=torch.float32, device=x.device)
@@ -483,7 +490,7 @@ def amax(x, workspace=None, stream=None):
         else:
             _check_buffer(workspace, iq_workspace_bytes(d), "workspace", x.device)
             ws = workspace
-        _check(iq_amax(d, x.data_ptr(), out.data_ptr(), ws.data_ptr(), _stream()), "iq_amax")
+        _check(iq_amax(d, x.data_ptr(), out.data_ptr(), ws.data_ptr(), _stream_for(x)), "iq_amax")
         return out
 
 
@@ -502,7 +509,7 @@ def zp_gemm(q: "Quantized", x, out=None, stream=None):
     """Puzzle 12's z[j, k] = sum_l sc (w - sh) y[l, k] for asymmetric INT4
     weights q (from quantize(..., "int4zp", "block")) and token-major BF16
     activations x [n1, K]; returns z float32 [N0, n1]."""
-    with _place(stream):
+    with _place(stream, x):
         torch = _torch()
         if q.fmt != "int4zp":
             raise ValueError("zp_gemm needs asymmetric INT4 weights")
@@ -515,7 +522,7 @@ def zp_gemm(q: "Quantized", x, out=None, stream=None):
         _check_buffer(q.scales, iq_scales_bytes(d), "scales", x.device, torch.float32)
         _check_buffer(q.shifts, iq_shifts_bytes(d), "shifts", x.device, torch.uint8)
         st = iq_zp_gemm(d, q.codes.data_ptr(), q.scales.data_ptr(), q.shifts.data_ptr(), x.data_ptr(), IQ_BF16, n1,
-                        out.data_ptr(), _stream())
+                        out.data_ptr(), _stream_for(x))
         _check(st, "iq_zp_gemm")
         return out
 
@@ -524,7 +531,7 @@ def mx_gemm(qw: "Quantized", qa: "Quantized", out=None, stream=None):
     """FP4 GEMM z[j, t] = sum_k xw[j, k] xa[t, k] of two MXFP4 operands (from
     quantize(..., "mxfp4", "block")), weights qw [N0, K] and activations
     qa [n1, K]; returns z float32 [N0, n1]."""
-    with _place(stream):
+    with _place(stream, qw.codes):
         torch = _torch()
         if qw.fmt != "mxfp4" or qa.fmt != "mxfp4":
             raise ValueError("mx_gemm needs two MXFP4 operands")
@@ -540,7 +547,7 @@ def mx_gemm(qw: "Quantized", qa: "Quantized", out=None, stream=None):
         _check_buffer(qa.codes, iq_codes_bytes(da), "activation codes", dev, torch.uint8)
         _check_buffer(qa.scales, iq_scales_bytes(da), "activation scales", dev, torch.uint8)
         st = iq_mx_gemm(d, qw.codes.data_ptr(), qw.scales.data_ptr(), qa.codes.data_ptr(), qa.scales.data_ptr(), n1,
-                        out.data_ptr(), _stream())
+                        out.data_ptr(), _stream_for(qw.codes))
         _check(st, "iq_mx_gemm")
         return out
 
@@ -549,7 +556,7 @@ def mxw_gemm(qw: "Quantized", x, out=None, stream=None):
     """MXFP4 weights qw [N0, K] (from quantize(..., "mxfp4", "block")) against
     token-major BF16 activations x [n1, K]: z[j, t] = sum_k xw[j, k] x[t, k];
     returns z float32 [N0, n1]."""
-    with _place(stream):
+    with _place(stream, x):
         torch = _torch()
         if qw.fmt != "mxfp4":
             raise ValueError("mxw_gemm needs MXFP4 weights")
@@ -561,7 +568,7 @@ def mxw_gemm(qw: "Quantized", x, out=None, stream=None):
         _check_buffer(qw.codes, iq_codes_bytes(d), "weight codes", x.device, torch.uint8)
         _check_buffer(qw.scales, iq_scales_bytes(d), "weight scales", x.device, torch.uint8)
         st = iq_mxw_gemm(d, qw.codes.data_ptr(), qw.scales.data_ptr(), x.data_ptr(), IQ_BF16, n1, out.data_ptr(),
-                         _stream())
+                         _stream_for(x))
         _check(st, "iq_mxw_gemm")
         return out
 
@@ -608,14 +615,6 @@ def _dtype_of(t, what: str) -> int:
     if code is None:
         raise TypeError(f"{what} must be float32 or bfloat16")
     return code
-
-
-def _stream_for(x):
-    """The stream of a call on x, which has to be in GPU memory."""
-    if not x.is_cuda:
-        raise ValueError(f"x is on {x.device}, not on a GPU")
-    torch = _torch()
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())     # current_stream() without its object
 
 
 def _result(out, shape: tuple, dtype, x, what: str = "out"):
@@ -673,7 +672,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
         done = (_fast_calls or _bind_fast()).layer_norm(x, weight, bias, eps)
         if done is not None:
             return done
-    with _place(stream):
+    with _place(stream, x):
         d = _norm_desc(x)
         rows, cols = d.rows, d.cols
         pt = _norm_params(x, cols, weight, bias)
@@ -693,7 +692,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, workspac
         done = (_fast_calls or _bind_fast()).layer_norm_backward(dy, x, weight, mean, rstd)
         if done is not None:
             return done
-    with _place(stream):
+    with _place(stream, x):
         f32 = _torch().float32
         d = _norm_desc(x)
         rows, cols = d.rows, d.cols
@@ -737,7 +736,7 @@ def gated(x, w_gate, w_up, act: str = "silu", *, save: bool = False, out=None, s
         done = (_fast_calls or _bind_fast()).gated(x, w_gate, w_up, ACTS[act], save)
         if done is not None:
             return done
-    with _place(stream):
+    with _place(stream, x):
         d = _gated_desc(x, w_gate, w_up, act)
         h = _result(out, (d.tokens, d.features), x.dtype, x)
         saved = x.new_empty((2, d.tokens, d.features), dtype=_torch().float32) if save else None
@@ -755,7 +754,7 @@ def gated_backward(dh, x, w_gate, w_up, saved, act: str = "silu", *, workspace=N
         done = (_fast_calls or _bind_fast()).gated_backward(dh, x, w_gate, w_up, saved, ACTS[act])
         if done is not None:
             return done
-    with _place(stream):
+    with _place(stream, x):
         d = _gated_desc(x, w_gate, w_up, act)
         tokens, cols, features = d.tokens, d.cols, d.features
         _check_dense(dh, (tokens, features), x.dtype, x, "dh")
@@ -811,7 +810,7 @@ def packed_gemv(q: "Quantized", x, out_dtype=None, out=None, stream=None):
         done = (_fast_calls or _bind_fast()).packed_gemv(x, FORMATS[q.fmt], rows, cols, f32, q.codes, q.scales, q.global_scale)
         if done is not None:
             return done
-    with _place(stream):
+    with _place(stream, x):
         _packed_x(x, cols)
         codes, scales, gscale = _packed_weights(q, x)
         n1 = x.shape[0]
@@ -838,7 +837,7 @@ def packed_gated(q_gate: "Quantized", q_up: "Quantized", x, act: str = "silu", o
                                                      q_gate.global_scale, q_up.codes, q_up.scales, q_up.global_scale)
         if done is not None:
             return done
-    with _place(stream):
+    with _place(stream, x):
         _packed_x(x, cols)
         gate, up = _packed_weights(q_gate, x, "gate weights"), _packed_weights(q_up, x, "up weights")
         n1 = x.shape[0]

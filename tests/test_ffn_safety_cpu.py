@@ -4,6 +4,7 @@ import os
 import re
 import subprocess
 from functools import partial
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -154,3 +155,26 @@ def test_a_named_streams_call_allocates_under_that_stream(iq, monkeypatch, name)
         call(stream=stream)
     assert launched == [True] and place.named == [stream]
     assert made.seen and all(made.seen)
+
+
+# ---- tensors elsewhere than on the current device ---------------------------------------------
+def test_calls_run_on_their_tensors_device(iq, monkeypatch):
+    """A launch on another device's stream would run where the tensor's memory is not."""
+    entered = []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 100 + device, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: entered.append(d) or Place())
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    here, there = (SimpleNamespace(is_cuda=True, device=torch.device("cuda", k), get_device=lambda k=k: k) for k in (0, 1))
+    with iq._place(None, here):
+        assert not entered and iq._stream_for(here) == 100
+    with iq._place(None, there):
+        assert entered == [there.device] and iq._stream_for(there) == 101
+    with pytest.raises(ValueError, match="the stream on"):
+        iq._place(FakeStream(), there)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_host_memory_is_refused(iq, name):
+    with pytest.raises(ValueError, match="not on a GPU"):
+        CALLS[name](iq)()
