@@ -733,7 +733,7 @@ def gated(x, w_gate, w_up, act: str = "silu", *, save: bool = False, out=None, s
     cols] and weights [features, cols]; with save=True returns h and what
     gated_backward needs."""
     if out is None and stream is None and act in ACTS:
-        done = (_fast_calls or _bind_fast()).gated(x, w_gate, w_up, ACTS[act], save)
+        done = (_fast_calls or _bind_fast()).gated(x, w_gate, w_up, ACTS[act], bool(save))
         if done is not None:
             return done
     with _place(stream, x):

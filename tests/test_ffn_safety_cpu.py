@@ -178,3 +178,12 @@ def test_calls_run_on_their_tensors_device(iq, monkeypatch):
 def test_host_memory_is_refused(iq, name):
     with pytest.raises(ValueError, match="not on a GPU"):
         CALLS[name](iq)()
+
+
+# ---- arguments of the short calls ----------------------------------------------------------
+@pytest.mark.parametrize("save", [1, "yes", 0, ""])
+def test_save_is_taken_for_its_truth(iq, monkeypatch, save):
+    """The short calls compare with True itself, so 1 would return h alone where the caller unpacks two results."""
+    given = []
+    monkeypatch.setattr(iq, "_fast_calls", SimpleNamespace(gated=lambda *a: given.append(a[4]) or "done"))
+    assert iq.gated(X, W, W, save=save) == "done" and given == [bool(save)]

@@ -63,3 +63,9 @@ def test_calls_on_a_named_stream_keep_their_buffers(iq):  # noqa: F811
         assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want)), k
         torch.cuda.synchronize()
         del keep
+
+
+def test_gated_save_by_truth(iq):  # noqa: F811
+    x, w = torch.zeros(3, 64, dtype=BF, device="cuda"), torch.zeros(8, 64, dtype=BF, device="cuda")
+    h, saved = iq.gated(x, w, w, save=1)
+    assert h.shape == (3, 8) and saved.shape == (2, 3, 8) and torch.is_tensor(iq.gated(x, w, w, save=0))
