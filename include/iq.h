@@ -325,7 +325,8 @@ iq_status iq_mxw_gemm(const iq_desc* d, const void* codes, const void* scales, c
  *   param_dtype  iq_dtype of weight and bias
  *   weight, bias [cols]; NULL stands for ones / zeros
  *   mean, rstd   float32 [rows]; NULL where they are not wanted
- * Any cols >= 1 up to 2^26 (more: IQ_EUNSUPPORTED) and any alignment that the
+ * Any cols up to 2^26 (more: IQ_EUNSUPPORTED; of none, mean is 0 and rstd
+ * 1 / sqrt(eps), and x and y may be NULL) and any alignment that the
  * element types need are accepted; BF16 rows that start on 16-byte words are
  * faster, in the backward pass nearly twice.  Statistics are held in FP32.  A NaN or an
  * infinity makes its whole row NaN.  eps must be finite and >= 0.

@@ -85,8 +85,8 @@ iq_status iq_layer_norm(const iq_desc* d, const void* x, const void* weight, con
     if (st != IQ_OK) return st;
     if (!known_dtype(param_dtype)) return IQ_EINVAL;
     if (!(eps >= 0.f) || eps > 3.402823466e+38f) return IQ_EINVAL;
-    if (d->rows == 0 || d->cols == 0) return IQ_OK;
-    if (!x || !y) return IQ_EINVAL;
+    if (d->rows == 0 || (d->cols == 0 && !mean && !rstd)) return IQ_OK;
+    if (d->cols > 0 && (!x || !y)) return IQ_EINVAL;
     const uintptr_t ex = (uintptr_t)size_of(d->in_dtype), ep = (uintptr_t)size_of(param_dtype);
     if (!aligned(x, ex) || !aligned(y, ex) || !aligned(weight, ep) || !aligned(bias, ep) || !aligned(mean, 4) ||
         !aligned(rstd, 4))

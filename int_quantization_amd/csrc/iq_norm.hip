@@ -153,7 +153,7 @@ __global__ __launch_bounds__(NT) void k_norm(NormArgs a) {
     __shared__ float red[2][2][NW][2];
     const int t = threadIdx.x, nv = (int)((a.cols + 7) / 8);
     auto have = [&](int64_t c) { return (int)min((int64_t)8, a.cols - 8 * c); };      // elements of vector c
-    const float inv = 1.f / (float)a.cols;
+    const float inv = a.cols ? 1.f / (float)a.cols : 0.f;               // rows without elements have statistics too
     Raw<IN> next[HOLD] = {};
     float w[HOLD][8], b[HOLD][8];
     auto fetch = [&](int64_t row) {

@@ -187,3 +187,12 @@ def test_save_is_taken_for_its_truth(iq, monkeypatch, save):
     given = []
     monkeypatch.setattr(iq, "_fast_calls", SimpleNamespace(gated=lambda *a: given.append(a[4]) or "done"))
     assert iq.gated(X, W, W, save=save) == "done" and given == [bool(save)]
+
+
+# ---- rows without elements --------------------------------------------------------------
+def test_layer_norm_without_columns_does_not_end_before_its_statistics(iq):
+    """Returning early left mean and rstd as the allocator gave them; what is checked late shows that the call goes on."""
+    d, fake = iq.IQDesc(0, 0, iq.IQ_BF16, 0, 5, 0, 0, 0, 0), 0x10000
+    assert iq.iq_layer_norm(d, None, None, None, 1, 1e-5, None, fake + 2, fake, None) == iq.IQ_EALIGN
+    assert iq.iq_layer_norm(d, None, None, None, 1, 1e-5, None, fake, fake + 2, None) == iq.IQ_EALIGN
+    assert iq.iq_layer_norm(d, None, None, None, 1, 1e-5, None, None, None, None) == iq.IQ_OK

@@ -69,3 +69,20 @@ def test_gated_save_by_truth(iq):  # noqa: F811
     x, w = torch.zeros(3, 64, dtype=BF, device="cuda"), torch.zeros(8, 64, dtype=BF, device="cuda")
     h, saved = iq.gated(x, w, w, save=1)
     assert h.shape == (3, 8) and saved.shape == (2, 3, 8) and torch.is_tensor(iq.gated(x, w, w, save=0))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [1, 5, 3000])
+def test_layer_norm_rows_without_elements(iq, dtype, rows):  # noqa: F811
+    """Sums of nothing: mean 0 and rstd 1 / sqrt(eps), on both ways through the binding."""
+    x = torch.empty((rows, 0), dtype=dtype, device="cuda")
+    for stream in (None, torch.cuda.current_stream()):
+        for _ in range(3):
+            old = [torch.full((rows,), float("nan"), device="cuda") for _ in range(8)]
+            old += [torch.full((2, rows), float("nan"), device="cuda") for _ in range(8)]
+            del old                                    # what the allocator hands out next
+            y, mean, rstd = iq.layer_norm(x, eps=0.25, stream=stream)
+            assert y.shape == x.shape and torch.equal(mean, torch.zeros(rows, device="cuda"))
+            assert torch.equal(rstd, torch.full((rows,), 2.0, device="cuda"))
+        dx, dw, db = iq.layer_norm_backward(x, x, None, mean, rstd, stream=stream)
+        assert dx.shape == x.shape and dw.shape == db.shape == (0,)
