@@ -9,6 +9,9 @@ works anywhere, but any call raises if the library is missing.
 
 With `stream` a call runs on that stream, and what it allocates (results and
 workspace) belongs to it, as under `with torch.cuda.stream(stream)`.
+
+The feed-forward operators record no graph: gradients come from the *_backward
+functions, and tensors that require gradients are refused outside no_grad().
 """
 from __future__ import annotations
 
@@ -617,6 +620,13 @@ def _dtype_of(t, what: str) -> int:
     return code
 
 
+def _refuse_grad(*tensors):
+    """No graph is recorded, so a tensor that asks for a gradient would never get it."""
+    if _torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise RuntimeError("no gradient passes through this call: use tensors without requires_grad or torch.no_grad(), "
+                           "and layer_norm_backward or gated_backward for the gradients")
+
+
 def _result(out, shape: tuple, dtype, x, what: str = "out"):
     """A new tensor on x's device, or the caller's after checks."""
     if out is None:
@@ -673,6 +683,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
         if done is not None:
             return done
     with _place(stream, x):
+        _refuse_grad(x, weight, bias, out)
         d = _norm_desc(x)
         rows, cols = d.rows, d.cols
         pt = _norm_params(x, cols, weight, bias)
@@ -693,6 +704,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, workspac
         if done is not None:
             return done
     with _place(stream, x):
+        _refuse_grad(dy, x, weight, mean, rstd)
         f32 = _torch().float32
         d = _norm_desc(x)
         rows, cols = d.rows, d.cols
@@ -737,6 +749,7 @@ def gated(x, w_gate, w_up, act: str = "silu", *, save: bool = False, out=None, s
         if done is not None:
             return done
     with _place(stream, x):
+        _refuse_grad(x, w_gate, w_up, out)
         d = _gated_desc(x, w_gate, w_up, act)
         h = _result(out, (d.tokens, d.features), x.dtype, x)
         saved = x.new_empty((2, d.tokens, d.features), dtype=_torch().float32) if save else None
@@ -755,6 +768,7 @@ def gated_backward(dh, x, w_gate, w_up, saved, act: str = "silu", *, workspace=N
         if done is not None:
             return done
     with _place(stream, x):
+        _refuse_grad(dh, x, w_gate, w_up, saved)
         d = _gated_desc(x, w_gate, w_up, act)
         tokens, cols, features = d.tokens, d.cols, d.features
         _check_dense(dh, (tokens, features), x.dtype, x, "dh")
@@ -811,6 +825,7 @@ def packed_gemv(q: "Quantized", x, out_dtype=None, out=None, stream=None):
         if done is not None:
             return done
     with _place(stream, x):
+        _refuse_grad(x, out)
         _packed_x(x, cols)
         codes, scales, gscale = _packed_weights(q, x)
         n1 = x.shape[0]
@@ -838,6 +853,7 @@ def packed_gated(q_gate: "Quantized", q_up: "Quantized", x, act: str = "silu", o
         if done is not None:
             return done
     with _place(stream, x):
+        _refuse_grad(x, out)
         _packed_x(x, cols)
         gate, up = _packed_weights(q_gate, x, "gate weights"), _packed_weights(q_up, x, "up weights")
         n1 = x.shape[0]

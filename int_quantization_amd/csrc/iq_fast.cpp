@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -42,9 +43,12 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 struct Other {};          // not the common case
 
+// A tensor that no graph follows; of others the binding in Python says that their gradients would be lost.
 const at::Tensor& tensor(PyObject* o) {
     if (!THPVariable_CheckExact(o)) throw Other();
-    return THPVariable_Unpack(o);
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.requires_grad() && c10::GradMode::is_enabled()) throw Other();
+    return t;
 }
 int64_t whole(PyObject* o) {
     const long long v = PyLong_AsLongLong(o);

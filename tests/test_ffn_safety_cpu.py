@@ -196,3 +196,26 @@ def test_layer_norm_without_columns_does_not_end_before_its_statistics(iq):
     assert iq.iq_layer_norm(d, None, None, None, 1, 1e-5, None, fake + 2, fake, None) == iq.IQ_EALIGN
     assert iq.iq_layer_norm(d, None, None, None, 1, 1e-5, None, fake, fake + 2, None) == iq.IQ_EALIGN
     assert iq.iq_layer_norm(d, None, None, None, 1, 1e-5, None, None, None, None) == iq.IQ_OK
+
+
+# ---- tensors that a graph follows ------------------------------------------------------------
+GRAD = {                           # every tensor that may ask for a gradient, one at a time
+    "layer_norm": (lambda iq, x, w, b: iq.layer_norm(x, w, b), (X, W[0], W[0])),
+    "layer_norm_backward": (lambda iq, *a: iq.layer_norm_backward(*a), (X, X, W[0], STAT, STAT)),
+    "gated": (lambda iq, *a: iq.gated(*a), (X, W, W)),
+    "gated_backward": (lambda iq, *a: iq.gated_backward(*a), (DH, X, W, W, SAVED)),
+    "packed_gemv": (lambda iq, x: iq.packed_gemv(packed(iq, "int4"), x), (X,)),
+    "packed_gated": (lambda iq, x: iq.packed_gated(packed(iq, "int4"), packed(iq, "int4"), x), (X,)),
+}
+
+
+@pytest.mark.parametrize("name", GRAD)
+def test_tensors_that_require_gradients_are_refused(iq, name):
+    """The results would be cut from the graph without a word."""
+    call, operands = GRAD[name]
+    for k in range(len(operands)):
+        given = [t.clone().requires_grad_(i == k) for i, t in enumerate(operands)]
+        with pytest.raises(RuntimeError, match="no gradient passes"):
+            call(iq, *given)
+        with torch.no_grad(), pytest.raises(ValueError, match="not on a GPU"):
+            call(iq, *given)

@@ -86,3 +86,23 @@ def test_layer_norm_rows_without_elements(iq, dtype, rows):  # noqa: F811
             assert torch.equal(rstd, torch.full((rows,), 2.0, device="cuda"))
         dx, dw, db = iq.layer_norm_backward(x, x, None, mean, rstd, stream=stream)
         assert dx.shape == x.shape and dw.shape == db.shape == (0,)
+
+
+def test_tensors_that_require_gradients_on_the_gpu(iq):  # noqa: F811
+    """Refused on the short path too, and taken under no_grad()."""
+    g = gen(70)
+    x, w, p = rand(g, 5, 128), rand(g, 32, 128), rand(g, 128, offset=1.0)
+    q = iq.quantize(w, "int4", "block", stats=False)
+    y, mean, rstd = iq.layer_norm(x, p)
+    h, saved = iq.gated(x, w, w, save=True)
+    z = iq.packed_gemv(q, x)
+    calls = [(lambda x, w, p: iq.layer_norm(x, p), (y, mean, rstd)), (lambda x, w, p: (iq.gated(x, w, w),), (h,)),
+             (lambda x, w, p: iq.layer_norm_backward(y, x, p, mean, rstd), iq.layer_norm_backward(y, x, p, mean, rstd)),
+             (lambda x, w, p: iq.gated_backward(h, x, w, w, saved), iq.gated_backward(h, x, w, w, saved)),
+             (lambda x, w, p: (iq.packed_gemv(q, x),), (z,))]
+    leaf = [t.clone().requires_grad_() for t in (x, w, p)]
+    for call, want in calls:
+        with pytest.raises(RuntimeError, match="no gradient passes"):
+            call(*leaf)
+        for got in (call(x, w, p), torch.no_grad()(call)(*leaf)):
+            assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, want))
