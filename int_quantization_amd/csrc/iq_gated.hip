@@ -174,6 +174,8 @@ template <bool KC, int T> struct Copy {
 // to depend on them; they have no output register, and the step's wait and
 // barrier stand between them and the reads.  Lane l's 16 bytes go to byte
 // `to` + 16 l of LDS.
+// m0 is the compiler's reserved register and cannot be named as overwritten:
+// every copy sets it anew, and nothing else in the kernel may use it.
 __device__ __forceinline__ void copy_1k(uint32_t off, u4v buf, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(buf) : "memory");
 }

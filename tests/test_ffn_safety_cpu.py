@@ -71,6 +71,21 @@ def test_packed_code_offsets_stay_in_their_rows(cols):
                         assert at + 16 <= size
 
 
+# ---- the register of the copies written out ----------------------------------------------
+def test_copies_set_m0_and_nothing_else_uses_it(tmp_path):
+    """The tiles' copies write m0, which the compiler reserves and does not let them name: a use of its own would not see
+    the change, and a copy that relied on an earlier one's value could be moved from behind it."""
+    copies = 0
+    for name, code in kernels("iq_gated.hip", "k_gemm", tmp_path).items():
+        used = [i for i, c in enumerate(code) if re.search(r"\bm0\b", c)]
+        sets = [i for i in used if re.match(r"s_mov_b32 m0, |s_add_u32 m0, ", code[i])]
+        loads = [i for i, c in enumerate(code) if c.startswith("buffer_load") and c.endswith(" lds")]
+        assert used == sets, name
+        assert [i + 2 for i in sets] == loads, name        # one instruction between: the wait state
+        copies += len(loads)
+    assert copies > 300
+
+
 # ---- buffers of a named stream -----------------------------------------------------------
 class Allocations(TorchDispatchMode):
     """Notes for every tensor made whether `place` was entered."""
