@@ -418,7 +418,9 @@ size_t iq_gated_workspace_bytes(const iq_gated_desc* d);
  * INT4 without the group scale, as 4 a + b with a in [-2, 1], b in [0, 3])
  * and are summed in FP32: before z's own rounding |z - exact| <=
  * (2 K + 8) 2^-24 sum_k |x| m, where m is |w|, for INT4 |w| plus six group
- * scales.  MXFP4 scale bytes of 255 and NVFP4 ones of 0x7F or 0xFF are NaN
+ * scales.  MXFP4 weights of 2^128 and more (the largest codes under scale
+ * bytes 253 and 254) are infinite, as iq_dequantize gives them.  MXFP4 scale
+ * bytes of 255 and NVFP4 ones of 0x7F or 0xFF are NaN
  * and make their row's outputs NaN.  An infinity in a token makes that
  * token's outputs infinite where the weight is not zero, or NaN for INT4,
  * whose two parts may pull either way.

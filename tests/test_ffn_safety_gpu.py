@@ -106,3 +106,43 @@ def test_tensors_that_require_gradients_on_the_gpu(iq):  # noqa: F811
             call(*leaf)
         for got in (call(x, w, p), torch.no_grad()(call)(*leaf)):
             assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, want))
+
+
+# ---- packed weights: both ends of the MXFP4 scales ------------------------------------------
+def mx_weights(iq, rows, cols, low, high, seed):  # noqa: F811
+    q = any_weights(iq, rows, cols, "mxfp4", seed)
+    q.scales.random_(low, high + 1, generator=gen(seed))
+    return q
+
+
+@pytest.mark.parametrize("n1", [1, 5, 16, 33])
+@pytest.mark.parametrize("low,high,exponent", [(0, 0, 100), (1, 1, 100), (0, 3, 100), (0, 40, 90), (140, 200, -60), (200, 252, -100),
+                                               (252, 252, -120)])
+def test_packed_mx_scales_of_every_size(iq, n1, low, high, exponent):  # noqa: F811
+    """Scale bytes 0 and 1, whose weights are subnormal BF16, to 252, the last whose weights BF16 holds all of, with
+    activations that bring the products back to ordinary numbers."""
+    for rows, cols in ((40, 96), (33, 1184), (4133, 256)):
+        q = mx_weights(iq, rows, cols, low, high, low + n1)
+        x = (rand(gen(high), n1, cols, dtype=F32) * 2.0 ** exponent).to(BF)
+        g, e = fo.packed(x, values(q))
+        fo.assert_within(iq.packed_gemv(q, x, F32), g, e, f"{rows} rows")
+        if high < 64:                                  # products near 1, where act has something to say
+            fo.assert_within(iq.packed_gated(q, q, x, "silu", F32), *fo.gate(g, g, e, e, "silu"), f"gated, {rows} rows")
+
+
+@pytest.mark.parametrize("n1", [1, 20])
+@pytest.mark.parametrize("byte", [253, 254])
+def test_packed_mx_weights_past_bf16_are_infinite(iq, n1, byte):  # noqa: F811
+    """Of scale bytes 253 and 254 the largest codes' weights are 2^128 and more, infinite as iq_dequantize gives them."""
+    q = mx_weights(iq, 48, 256, byte, byte, byte)
+    q.codes[0] = 0x11                                  # the smallest code alone: all finite
+    q.codes[1, :] = 0x99
+    x = torch.full((n1, 256), 2.0 ** -130, dtype=BF, device="cuda")
+    w, m = values(q)
+    past = w.abs() >= 2.0 ** 128
+    assert torch.equal(torch.isinf(iq.dequantize(q)), past) and torch.equal(torch.isinf(iq.dequantize(q, BF)), past)
+    w = torch.where(past, w.sign() * float("inf"), w)
+    z = iq.packed_gemv(q, x, F32)
+    want, e = fo.packed(x, (w, torch.where(past, torch.zeros_like(m), m)))
+    fo.assert_within(z, want, e, "z")
+    assert torch.isfinite(z[:, :2]).all() and not torch.isfinite(z[:, 2:]).any()
