@@ -69,7 +69,8 @@ template <int ACT> __device__ __forceinline__ void act_slope(float g, float& a, 
     } else {
         const float p = logistic(2.f * kTanhC * (g + kTanhA * g * g * g));
         a = g * p;
-        da = p + a * (1.f - p) * 2.f * kTanhC * (1.f + 3.f * kTanhA * g * g);
+        // beyond 100 p is 0 or 1 and the product 0, also where g g would be infinite
+        da = p + a * (1.f - p) * 2.f * kTanhC * (1.f + 3.f * kTanhA * fminf(g * g, 1e4f));
     }
 }
 

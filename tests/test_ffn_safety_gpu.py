@@ -146,3 +146,23 @@ def test_packed_mx_weights_past_bf16_are_infinite(iq, n1, byte):  # noqa: F811
     want, e = fo.packed(x, (w, torch.where(past, torch.zeros_like(m), m)))
     fo.assert_within(z, want, e, "z")
     assert torch.isfinite(z[:, :2]).all() and not torch.isfinite(z[:, 2:]).any()
+
+
+# ---- activations far out and in their tails ---------------------------------------------------
+@pytest.mark.parametrize("act", fo.ACTS)
+def test_gated_very_far_arguments(iq, act):  # noqa: F811
+    """g of either sign from 1 to 2^119, whose square is infinite: no product of 0 and infinity, forward or backward."""
+    tokens, cols, features = 240, 64, 64
+    x = torch.zeros(tokens, cols, dtype=BF, device="cuda")
+    x[:120, 0] = torch.exp2(torch.arange(120, device="cuda").float()).to(BF)
+    x[120:, 0] = -x[:120, 0]
+    x[:, 1] = 1
+    wg, wu = torch.zeros(features, cols, dtype=BF, device="cuda"), torch.zeros(features, cols, dtype=BF, device="cuda")
+    wg[:, 0], wu[:, 1] = 1, 2
+    dh = torch.full((tokens, features), 2.0 ** -100, dtype=BF, device="cuda")
+    h, saved = iq.gated(x, wg, wu, act, save=True)
+    fo.assert_within(h, *fo.gated(x, wg, wu, act), "h")
+    want, bound = fo.gated_grad(dh, x, wg, wu, act)
+    for got, r, e, what in zip(iq.gated_backward(dh, x, wg, wu, saved, act), want, bound, ("dx", "dwg", "dwu")):
+        r = torch.where(r.abs() >= 2.0 ** 128, r.sign() * float("inf"), r)     # x act(x) of the farthest: more than FP32 holds
+        fo.assert_within(got, r, e, what)
