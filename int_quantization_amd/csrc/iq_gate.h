@@ -43,16 +43,20 @@ template <int N> __device__ __forceinline__ void wait_for_all_but() {
     asm volatile("" ::: "memory");
 }
 
-// 1 / (1 + e^-v), also for both infinities.
+// 1 / (1 + e^-v), also for both infinities.  The exponential is the hardware's
+// power of two: its argument, v times log2 e, is rounded once, which costs a
+// relative |v| 2^-24, as much as rounding v itself to FP32 did.
 __device__ __forceinline__ float logistic(float v) { return 1.f / (1.f + __expf(-v)); }
 
 constexpr float kTanhC = 0.7978845608028654f;    // sqrt(2 / pi)
 constexpr float kTanhA = 0.044715f;
 
-// act(g).  GELU's tanh form uses (1 + tanh z) / 2 = 1 / (1 + e^-2z).
+// act(g).  GELU's tanh form uses (1 + tanh z) / 2 = 1 / (1 + e^-2z), and the
+// exact one (1 + erf z) / 2 = erfc(-z) / 2: from g = -3 on 1 + erf has lost
+// digits, at -6 all.
 template <int ACT> __device__ __forceinline__ float act(float g) {
     if constexpr (ACT == A_SILU) return g * logistic(g);
-    if constexpr (ACT == A_GELU) return 0.5f * g * (1.f + erff(g * 0.7071067811865476f));
+    if constexpr (ACT == A_GELU) return 0.5f * g * erfcf(g * -0.7071067811865476f);
     return g * logistic(2.f * kTanhC * (g + kTanhA * g * g * g));
 }
 
@@ -63,7 +67,7 @@ template <int ACT> __device__ __forceinline__ void act_slope(float g, float& a, 
         a = g * p;
         da = p + a * (1.f - p);
     } else if constexpr (ACT == A_GELU) {
-        const float p = 0.5f * (1.f + erff(g * 0.7071067811865476f));
+        const float p = 0.5f * erfcf(g * -0.7071067811865476f);
         a = g * p;
         da = p + g * __expf(-0.5f * g * g) * 0.3989422804014327f;
     } else {

@@ -166,3 +166,48 @@ def test_gated_very_far_arguments(iq, act):  # noqa: F811
     for got, r, e, what in zip(iq.gated_backward(dh, x, wg, wu, saved, act), want, bound, ("dx", "dwg", "dwu")):
         r = torch.where(r.abs() >= 2.0 ** 128, r.sign() * float("inf"), r)     # x act(x) of the farthest: more than FP32 holds
         fo.assert_within(got, r, e, what)
+
+
+def tail_inputs():
+    """g from -9 to 9 in steps of 1/16 as BF16, in the first column of x; u is 1."""
+    g = torch.arange(-144, 145, device="cuda").div(16).to(BF)
+    x = torch.zeros(g.numel(), 128, dtype=BF, device="cuda")
+    x[:, 0], x[:, 1] = g, 1
+    return x, g
+
+
+def tail_error(g, act, value):
+    """What FP32 may be off by, relative: a function of g rounded a few times within takes the relative error of e^(-g^2 / 2)
+    for GELU and of e^-arg for the others, |exponent| roundings, and 16 more."""
+    g = g.double().abs()
+    exponent = g if act == "silu" else 0.5 * g * g if act == "gelu" else 1.6 * (g + 0.044715 * g ** 3)
+    return (16 + 4 * exponent) * fo.U * value.abs() + fo.TINY
+
+
+@pytest.mark.parametrize("act", fo.ACTS)
+def test_gated_tails_keep_their_digits(iq, act):  # noqa: F811
+    """The activations' left tails, 10^-6 and less, to the last digit of the output's type: nothing is taken off 1."""
+    x, g = tail_inputs()
+    a = fo.act_parts(g, act)[0]
+    if act == "gelu_tanh":                              # 1 + tanh loses the tail in 64 bits too: (1 + tanh z) / 2 = 1 / (1 + e^-2z)
+        a = g.double() * torch.sigmoid(2 * (2 / torch.pi) ** 0.5 * (g.double() + 0.044715 * g.double() ** 3))
+    w = torch.zeros(2, 8, 128, dtype=BF, device="cuda")
+    w[0, :, 0], w[1, :, 1] = 1, 1
+    h, saved = iq.gated(x, w[0], w[1], act, save=True)
+    fo.assert_within(h[:, 0], a, tail_error(g, act, a), "h of 289 tokens")
+    fo.assert_within(iq.gated(x[:40], w[0], w[1], act)[:, 0], a[:40], tail_error(g, act, a)[:40], "h of 40 tokens")
+    q = iq.Quantized(torch.zeros(8, 64, dtype=torch.uint8, device="cuda"), torch.full((8, 1), 0x3C00, dtype=torch.int16, device="cuda"),
+                     None, None, None, "int4", "block", 8, 128)
+    q.codes[:, 0] = 0x01                                # code 1 in column 0, scale 1
+    up = iq.Quantized(q.codes.clone(), q.scales, None, None, None, "int4", "block", 8, 128)
+    up.codes[:, 0] = 0x10
+    for at in range(0, 289, 64):
+        z = iq.packed_gated(q, up, x[at:at + 64].contiguous(), act, F32)
+        fo.assert_within(z[:, 0], a[at:at + 64], tail_error(g, act, a)[at:at + 64], "packed, FP32")
+    # du = dh act(g) through dw_up's first tokens: one token at a time has a weight gradient of its own
+    dh = torch.ones(1, 8, dtype=BF, device="cuda")
+    for t in (8, 40, 72, 100, 144, 180, 250):
+        kept = saved[:, t:t + 1].contiguous()
+        dwu = iq.gated_backward(dh, x[t:t + 1].contiguous(), w[0], w[1], kept, act)[2]
+        e = tail_error(g, act, a)[t] + fo.HALF[BF] * a[t].abs()          # du is rounded to BF16, and dw_up again
+        fo.assert_within(dwu[:1, 1], a[t:t + 1], e[None], f"dw_up at {t}")
