@@ -366,12 +366,18 @@ template <int FMT, int FR, bool GATED> hipError_t pick_tokens(const PackedK& k, 
     return run<FMT, FR, 16, GATED>(k, s);
 }
 
-// 32 rows of one matrix to a workgroup share its tokens; few rows are better
-// spread over more workgroups (1501 rows, 37 tokens: 8.8 us by 32, 7.6 by 16;
-// 14336 rows, 16 tokens: 11.4 by 32, 13.4 by 16).
+// 32 rows of one matrix to a workgroup share its tokens; while workgroups of 16
+// rows are too few to give every CU two, these end sooner.  K = 4096, INT4, by 16
+// and by 32 rows, in us: one token, 1024 rows 4.8 and 6.1, 4096 rows 5.0 and
+// 6.3, 6144 rows 6.2 and 6.5, 14336 rows 10.8 and 10.6; 16 tokens, 4096 rows 6.0
+// and 7.2, 6144 rows 7.6 and 7.3, 14336 rows 16.6 and 13.6; 64 tokens, 1024 rows
+// 5.9 and 7.1, 2048 rows 7.6 and 7.3, 4096 rows 12.2 and 10.3.  NVFP4 and MXFP4
+// cross near the same sizes.
+constexpr int64_t kFewWorkgroups = 384;
 template <int FMT, bool GATED> hipError_t pick(const PackedK& k, hipStream_t s) {
     if constexpr (GATED) return pick_tokens<FMT, 1, true>(k, s);
-    else return k.n0 < 4096 ? pick_tokens<FMT, 1, false>(k, s) : pick_tokens<FMT, 2, false>(k, s);
+    else if ((int64_t)((k.n0 + 15) / 16) * ((k.n1 + 15) / 16) < kFewWorkgroups) return pick_tokens<FMT, 1, false>(k, s);
+    else return pick_tokens<FMT, 2, false>(k, s);
 }
 
 template <int FMT> hipError_t pick(bool gated, const PackedK& k, hipStream_t s) {

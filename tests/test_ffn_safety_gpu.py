@@ -108,6 +108,17 @@ def test_tensors_that_require_gradients_on_the_gpu(iq):  # noqa: F811
             assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("fmt", ["int4", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("rows,tokens", [(6128, (1, 8, 16)), (6144, (1, 4, 5, 8, 9, 16)), (6161, (3, 7, 16, 17)), (3056, (17, 32)), (3089, (20, 33)),
+                                         (1537, (49, 64))])
+def test_packed_workgroups_around_the_choice_of_rows(iq, fmt, rows, tokens):  # noqa: F811
+    """16 or 32 rows to a workgroup, chosen by the number of workgroups, with every way of staging tokens."""
+    q = any_weights(iq, rows, 384 if fmt == "int4" else 352, fmt, rows)
+    for n1 in tokens:
+        x = rand(gen(n1), n1, q.cols)
+        fo.assert_within(iq.packed_gemv(q, x, F32), *fo.packed(x, values(q)), f"{n1} tokens")
+
+
 # ---- packed weights: both ends of the MXFP4 scales ------------------------------------------
 def mx_weights(iq, rows, cols, low, high, seed):  # noqa: F811
     q = any_weights(iq, rows, cols, "mxfp4", seed)
