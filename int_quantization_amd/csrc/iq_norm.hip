@@ -308,6 +308,12 @@ __global__ __launch_bounds__(NT * G) void k_norm_grad(NormGradArgs a) {
         if (AHEAD && row + stride < a.rows) fetch(row + stride);
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
+            if (const int n = have(t + k * NT); n < 8) {              // past the row's end: nothing off the mean
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[k][i] = i < n ? x[k][i] : mean;
+            }
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
             if (live && t + k * NT < nv) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -400,7 +406,7 @@ __global__ __launch_bounds__(NT) void k_norm_grad_long(NormGradArgs a) {
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float n = (x[i] - mean) * rstd, e = g[i] * w[i];
+                const float n = i < have(c) ? (x[i] - mean) * rstd : 0.f, e = g[i] * w[i];
                 s1 += e;
                 s2 = __builtin_fmaf(e, n, s2);
                 pdw[i] = __builtin_fmaf(g[i], n, first ? 0.f : pdw[i]);

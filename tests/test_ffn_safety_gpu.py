@@ -222,3 +222,20 @@ def test_gated_tails_keep_their_digits(iq, act):  # noqa: F811
         dwu = iq.gated_backward(dh, x[t:t + 1].contiguous(), w[0], w[1], kept, act)[2]
         e = tail_error(g, act, a)[t] + fo.HALF[BF] * a[t].abs()          # du is rounded to BF16, and dw_up again
         fo.assert_within(dwu[:1, 1], a[t:t + 1], e[None], f"dw_up at {t}")
+
+
+# ---- layer norm: what lies past a row's end -------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols", [7, 8, 9, 1001, 2049, 4099, 8191, 16389])
+def test_layer_norm_backward_takes_nothing_from_past_the_row(iq, dtype, cols):  # noqa: F811
+    """A row of equal large values has n = 0 throughout; the elements that fill its last vector up would have
+    n = -mean rstd, infinite here, and make the sum of a n NaN."""
+    g = gen(cols)
+    for rows in (1, 3, 300):
+        x, dy = rand(g, rows, cols, dtype=dtype), rand(g, rows, cols, dtype=dtype)
+        mean, rstd = x.float().mean(1), torch.ones(rows, device="cuda")
+        x[rows // 2], mean[rows // 2], rstd[rows // 2] = 2.0 ** 110, 2.0 ** 110, 2.0 ** 20
+        for w in (None, rand(g, cols, dtype=dtype, offset=1.0)):
+            want, bound = fo.norm_grad(dy, x, w, mean, rstd)
+            for got, r, e, what in zip(iq.layer_norm_backward(dy, x, w, mean, rstd), want, bound, ("dx", "dweight", "dbias")):
+                fo.assert_within(got, r, e, f"{what}, {rows} rows")
