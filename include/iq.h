@@ -423,7 +423,8 @@ size_t iq_gated_workspace_bytes(const iq_gated_desc* d);
  * bytes of 255 and NVFP4 ones of 0x7F or 0xFF are NaN
  * and make their row's outputs NaN.  An infinity in a token makes that
  * token's outputs infinite where the weight is not zero, or NaN for INT4,
- * whose two parts may pull either way.
+ * whose two parts may pull either way.  Sums are made before INT4's group scale
+ * and NVFP4's global scale, so activations beyond 2^100 may overflow there.
  * d->in_dtype and d->ld_in are ignored.  n1 == 0 or N0 == 0 is legal and
  * writes nothing, K == 0 writes zeros.  No workspace.
  */

@@ -21,14 +21,16 @@
 // lines.  Scales and up to 16 tokens are copied to LDS by the wave that needs
 // them, so that nothing but the sums is shared and no wave waits for another.
 //
-// Measured, one pass after another on weights not in any cache: INT4 28672 x
-// 8192, one token 26.5 us (4.6 TB/s); gated INT4 14336 x 4096, one token 15;
-// gated NVFP4 28672 x 8192, 8 tokens 58 (4.6 TB/s); NVFP4 14336 x 4096, 16
-// tokens 11; gated BF16 14336 x 4096, 16 tokens 48 (4.9 TB/s).  With a single
-// read of the codes and nothing else these take 21, 11, 44, 7 and 45: what is
-// left is the start of a workgroup and, for NVFP4, 70 vector instructions per
-// 2048 weights.  More steps in flight, 32 rows of both matrices to a workgroup
-// and starting each workgroup at another k made no difference or cost a little.
+// Measured on weights that come from memory: INT4 28672 x 8192, one token 28 us
+// (4.3 TB/s); gated NVFP4 28672 x 8192, 8 tokens 58 (4.6 TB/s); gated BF16
+// 14336 x 4096, 16 tokens 48 (4.9 TB/s).  With a single read of the codes and
+// nothing else these take 21, 44 and 45: what is left is the start of a
+// workgroup and, for NVFP4, 70 vector instructions per 2048 weights.  At 14336 x
+// 4096 the start weighs more: gated INT4, one token 17; NVFP4, 16 tokens 13.6.
+// 64 tokens take 31 there in every format, for each tile of 16 tokens converts
+// the codes again.  More steps in flight, 32 rows of
+// both matrices to a workgroup and starting each workgroup at another k made no
+// difference or cost a little.
 //
 // Every code becomes exact BF16:
 //   E2M1   one convert per pair, the E8M0 scale applied by the convert;
@@ -38,7 +40,9 @@
 //          signed number, b = its lower two: both are E2M1 codes of halves
 //          (b: 0, 1/2, 1, 3/2; a: sign and 0, 1/2, 1), so the FP4 convert
 //          serves here too and two MFMAs add the parts.  14 instructions per
-//          8 weights, where unsigned converts and subtractions take 23.
+//          8 weights, where unsigned converts and subtractions take 23.  The
+//          parts may have opposite signs, so an infinite activation, or one
+//          near 2^125 whose multiple overflows, gives NaN.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
