@@ -13,7 +13,8 @@
  * ---------------------------------------
  * - Pointers named x, codes, scales, global_scale, stats, xhat, workspace,
  *   amax_in and amax_out are DEVICE pointers (HIP device memory of the current
- *   device).  The descriptor is a HOST pointer.  The caller allocates and
+ *   device), and so are all other operands that are not said to be host
+ *   memory.  Descriptors are HOST pointers.  The caller allocates and
  *   owns every buffer; the library allocates nothing and never
  *   synchronizes.  Between calls it keeps only a cache of occupancy queries
  *   per kernel and device (host memory, guarded by a mutex), and the
@@ -441,6 +442,194 @@ iq_status iq_packed_gated(const iq_desc* d, int32_t act, const void* codes_gate,
                           const float* global_gate, const void* codes_up, const void* scales_up,
                           const float* global_up, const void* x, int32_t x_dtype, int64_t n1, void* h,
                           int32_t h_dtype, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The attention half of a transformer layer around an 8-bit cache: rotary
+ * positions, a paged cache of keys and values in INT8 or E4M3 with a scale for
+ * each block of 32 tokens and head, and attention over it.
+ * ------------------------------------------------------------------------- */
+
+typedef enum {
+    IQ_ROTARY_HALF = 0,       /* pair i: elements i and i + rot / 2 */
+    IQ_ROTARY_INTERLEAVED = 1 /* pair i: elements 2 i and 2 i + 1 */
+} iq_rotary_layout;
+
+typedef enum {
+    IQ_ROTARY_PLAIN = 0,
+    IQ_ROTARY_LINEAR = 1, /* every angle over factor */
+    IQ_ROTARY_BASE = 2,   /* base * factor^(rot / (rot - 2)): the slowest pair's angle over factor, the fastest's kept */
+    IQ_ROTARY_PARTS = 3   /* pairs by their turns r over `context` positions: over factor up to `low`, kept from `high`
+                             on, in between a mean of both with weight (r - low) / (high - low) for the kept angle */
+} iq_rotary_scaling;
+
+/*
+ * The table that rotations read: turns per position of each of rot / 2 pairs,
+ *   table[i] = base^(-2 i / rot) / (2 pi), scaled.
+ * A HOST function: `table` is host memory, and the other calls take a copy of
+ * it in device memory.  rot even and >= 0; base > 0, factor > 0 and, for
+ * IQ_ROTARY_PARTS, context > 0 and high > low, all finite (IQ_EINVAL).
+ */
+iq_status iq_rotary_table(int32_t rot, double base, int32_t scaling, double factor, double context, double low,
+                          double high, double* table);
+
+/* Strides count elements; the elements of a head are contiguous. */
+typedef struct {
+    int32_t dtype;                      /* iq_dtype of x and y */
+    int32_t layout;                     /* iq_rotary_layout */
+    int64_t tokens, heads, dim;
+    int64_t ld_token, ld_head;          /* of x */
+    int64_t ld_token_out, ld_head_out;  /* of y */
+    int32_t rot;                        /* leading elements of a head that turn: even, 0 to dim */
+    float amplitude;                    /* factor of what turns */
+    uint32_t flags;                     /* 0 */
+    uint32_t reserved;
+} iq_rotary_desc;
+
+/*
+ * Rotary positions.  With the angle f = 2 pi positions[t] table[i] of token t
+ * and pair i (a, b), A = amplitude:
+ *   a' = A (a cos f - b sin f),  b' = A (b cos f + a sin f)
+ * and elements from rot on as they are.  Angles are reduced in 64 bits, so
+ * far positions keep their digits; products are FP32, rounded once.
+ *   x, y       [tokens, heads, dim] of dtype, of any alignment that the type
+ *              needs; faster where bases are 16-byte aligned, strides and dim
+ *              multiples of 16 bytes, and rot of 32 (half) or 16 bytes.
+ *              y may be x where both have the same strides; otherwise they
+ *              must not overlap.  x may repeat itself (strides of 0), y not.
+ *   positions  int32 [tokens], of either sign
+ *   table      double [rot / 2], as iq_rotary_table writes it (device memory)
+ * heads up to 4096, dim up to 1024, heads * dim up to 2^20, tokens below 2^24
+ * (IQ_EUNSUPPORTED).
+ */
+iq_status iq_rotary(const iq_rotary_desc* d, const void* x, const int32_t* positions, const double* table, void* y,
+                    hipStream_t stream);
+
+/* Its backward pass: the transposed rotation, from dy (as x) to dx (as y):
+ *   da = A (da' cos f + db' sin f),  db = A (db' cos f - da' sin f). */
+iq_status iq_rotary_backward(const iq_rotary_desc* d, const void* dy, const int32_t* positions, const double* table,
+                             void* dx, hipStream_t stream);
+
+/*
+ * The cache.  Memory is `pages` pages of `page` tokens for each of `heads`
+ * key and value heads; the page table says which pages hold a sequence.
+ *   codes   uint8 [pages, heads, page / 32, 2, 32 * dim], 16-byte aligned: for
+ *           every block of 32 tokens the keys' codes (0), then the values' (1).
+ *           Keys lie as [dim / 16, 32 tokens, 16], values as [dim, 32 places],
+ *           token t of the block at place
+ *             16 * bit 2 of t + 8 * bit 4 + 4 * bit 3 + (t mod 4),
+ *           the orders in which the matrix cores take both
+ *   scales  float32 [pages, heads, page / 32, 2], 8-byte aligned: key and value scale of each block;
+ *           a value is its code's value (INT8, E4M3) times the scale
+ *   page_table  int32 [batch, width]: token t of sequence b lies in page
+ *           page_table[b][t / page].  Entries outside [0, pages) stand for absent pages:
+ *           nothing is written there, and their tokens are not seen
+ *   lengths int32 [batch]: tokens of each sequence, those of this call among them
+ *   starts  int32 [batch + 1], ascending: the call's tokens of sequence b are rows starts[b] to
+ *           starts[b + 1] - 1 of its dense operands, and the last of the sequence's
+ *           lengths[b].  NULL: one token for each sequence (tokens == batch).
+ *           Rows from starts[batch] on, and rows before a sequence's first
+ *           token, are no sequence's: what they would write is left as it was
+ *           (iq_cache_attention writes zeros for the latter)
+ * These arrays are device memory and are read when the kernel runs; whatever
+ * they hold, nothing outside the operands is read or written.
+ */
+typedef struct {
+    int32_t fmt;          /* IQ_INT8 or IQ_FP8_E4M3 */
+    int32_t heads;        /* key and value heads, 1 to 1024 */
+    int32_t dim;          /* elements of a head: 64, 96, 128, 192 or 256 */
+    int32_t page;         /* tokens of a page: a power of two, 32 to 4096 */
+    int64_t pages;        /* pages of the memory, up to 2^31 - 1 */
+    int64_t batch, width; /* of the page table: up to 2^20; width * page up to 2^30 */
+    uint32_t flags;       /* 0 */
+    uint32_t reserved;
+} iq_cache_desc;
+
+/* Bytes of the cache's memory (0 on an invalid descriptor); only fmt, heads, dim, page and pages are used. */
+size_t iq_cache_codes_bytes(const iq_cache_desc* d);
+size_t iq_cache_scales_bytes(const iq_cache_desc* d);
+
+typedef struct {
+    int32_t dtype;                  /* iq_dtype of k, v, q and q_out */
+    int32_t layout;                 /* iq_rotary_layout */
+    int64_t tokens;                 /* rows of k, v and q: below 2^24 */
+    int64_t q_heads;                /* heads of q: up to 4096; 0 without q */
+    int64_t ld_k_token, ld_k_head;  /* strides in elements */
+    int64_t ld_v_token, ld_v_head;
+    int64_t ld_q_token, ld_q_head;
+    int32_t rot;                    /* elements of a key's and query's head that turn: even, 0 to dim */
+    float amplitude;
+    uint32_t flags;                 /* 0 */
+    uint32_t reserved;
+} iq_append_desc;
+
+/*
+ * Appends the call's tokens: keys are turned by their position in the sequence
+ * (as iq_rotary, FP32, not rounded in between), keys and values quantized into
+ * their pages, and queries, if there are any, turned by the same positions.
+ *   k, v    [tokens, heads, dim] of dtype;  q [tokens, q_heads, dim] or NULL
+ *   q_out   dense [tokens, q_heads, dim] of dtype
+ *   table   double [rot / 2] (device memory; may be NULL where rot is 0)
+ * A block whose first token comes with this call gets s = alpha / 127 or
+ * alpha / 448 in FP32, alpha being the largest finite magnitude of its new
+ * elements; codes are x / s rounded to nearest even.  A block that holds
+ * tokens already keeps its scale if that is at least the new tokens' alpha /
+ * 127 or 448; otherwise the scale doubles until it is, and the codes there are
+ * divided by the same power of two and rounded to nearest even (E4M3 codes
+ * lose nothing by it above E4M3's subnormal range; INT8 codes are off by less than
+ * one new step however often it happens).  A scale of 0, all elements being 0, counts
+ * as none.  The cache holds finite values only: NaN is stored as 0, an infinity as the largest
+ * code of its sign.  Codes of tokens that are not the sequence's are left as they were.
+ * Sequences of one call must not share the pages that they append to; pages shared and only
+ * read are fine.  (tokens / 32 + 2 batch) * heads * 2 + tokens up to 2^23 (IQ_EUNSUPPORTED).
+ */
+iq_status iq_cache_append(const iq_cache_desc* d, const iq_append_desc* a, const void* k, const void* v,
+                          const int32_t* page_table, const int32_t* lengths, const int32_t* starts,
+                          const double* table, const void* q, void* q_out, void* codes, float* scales,
+                          hipStream_t stream);
+
+/*
+ * Reads back: rows starts[b] to starts[b + 1] - 1 of k and v receive the last
+ * tokens of sequence b, as iq_cache_append takes them (keys turned), each the code's value times its
+ * scale, rounded once to out_dtype.  k and v dense [tokens, heads, dim], 16-byte aligned;
+ * either may be NULL.  Tokens of absent pages are zeros.  Limits as for iq_cache_append.
+ */
+iq_status iq_cache_read(const iq_cache_desc* d, const void* codes, const float* scales, const int32_t* page_table,
+                        const int32_t* lengths, const int32_t* starts, int64_t tokens, void* k, void* v,
+                        int32_t out_dtype, hipStream_t stream);
+
+typedef struct {
+    int32_t dtype;              /* of q and o: IQ_BF16 */
+    int32_t causal;             /* 1: a query sees tokens up to its own; 0: all of its sequence */
+    int64_t tokens, q_heads;    /* q_heads a multiple of the cache's heads: query head h reads head
+                                   h / (q_heads / heads) */
+    int64_t ld_token, ld_head;  /* strides of q, in elements */
+    int64_t window;             /* 0, or with causal 1 the number of tokens that a query sees, its own the last */
+    float scale;                /* of the scores, finite and >= 0 */
+    uint32_t flags;             /* 0 */
+} iq_attention_desc;
+
+/*
+ * Attention of the call's tokens over the cache, their own keys and values
+ * (appended before) among it:
+ *   o = sum over seen t of softmax_t(scale q . k_t) v_t
+ * for prompts, for pieces of prompts behind what the cache holds, and for
+ * single tokens; the lengths of one call may differ as they like.
+ *   q   [tokens, q_heads, dim] BF16, 16-byte aligned, strides multiples of 8 elements (IQ_EALIGN)
+ *   o   dense [tokens, q_heads, dim] BF16, 16-byte aligned.  A query that sees nothing gets zeros
+ *   workspace  iq_cache_attention_workspace_bytes(d, a) bytes, 256-byte aligned, of any content
+ * Codes enter the matrix cores exactly, as FP16, and so do queries, scaled by a power of
+ * two for each row (elements below 2^-28 of their row's largest lose digits); probabilities are
+ * rounded to FP16 (half a step: 2^-11), sums, maxima and the running output are FP32.  Tokens that a query does
+ * not see add nothing, whatever their codes and scales hold; a NaN or an infinity in a query makes that
+ * query's output NaN.  Scales are expected to be finite and >= 0; NaN codes of E4M3 (which iq_cache_append never writes)
+ * in tokens that a sequence holds may make any of that sequence's outputs of their head NaN.
+ * The order of all sums is fixed by shapes, lengths and starts: calls repeat their bits.
+ * tokens * q_heads up to 2^28 (IQ_EUNSUPPORTED).
+ */
+iq_status iq_cache_attention(const iq_cache_desc* d, const iq_attention_desc* a, const void* codes, const float* scales,
+                             const int32_t* page_table, const int32_t* lengths, const int32_t* starts, const void* q,
+                             void* o, void* workspace, hipStream_t stream);
+size_t iq_cache_attention_workspace_bytes(const iq_cache_desc* d, const iq_attention_desc* a);
 
 const char* iq_status_str(iq_status s);
 int iq_abi_version(void);

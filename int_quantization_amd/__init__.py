@@ -10,8 +10,9 @@ works anywhere, but any call raises if the library is missing.
 With `stream` a call runs on that stream, and what it allocates (results and
 workspace) belongs to it, as under `with torch.cuda.stream(stream)`.
 
-The feed-forward operators record no graph: gradients come from the *_backward
-functions, and tensors that require gradients are refused outside no_grad().
+The feed-forward and attention operators record no graph: gradients come from
+the *_backward functions, and tensors that require gradients are refused
+outside no_grad().
 """
 from __future__ import annotations
 
@@ -30,6 +31,11 @@ IQ_F32, IQ_BF16 = 0, 1
 IQ_OK, IQ_EINVAL, IQ_EALIGN, IQ_EUNSUPPORTED, IQ_EHIP = 0, 1, 2, 3, 4
 # iq_desc.flags: scale-rule variants (MXFP4 exponent rounding, NVFP4 block-scale rounding)
 IQ_FLAG_MX_ROUND_NEAREST, IQ_FLAG_MX_ROUND_UP, IQ_FLAG_NV_SCALE_RNE = 0x1, 0x2, 0x4
+# iq_rotary_layout and iq_rotary_scaling values
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
+# formats of the cache
+CACHE_FORMATS = {"int8": 0, "e4m3": 1}
 # iq_act values
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 FOUR_BIT = ("mxfp4", "nvfp4", "int4", "int4zp")
@@ -45,6 +51,32 @@ class IQGatedDesc(ctypes.Structure):
     _fields_ = [("act", ctypes.c_int32), ("dtype", ctypes.c_int32), ("tokens", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("features", ctypes.c_int64), ("ld_x", ctypes.c_int64),
                 ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class IQRotaryDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("tokens", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("ld_token", ctypes.c_int64), ("ld_head", ctypes.c_int64), ("ld_token_out", ctypes.c_int64),
+                ("ld_head_out", ctypes.c_int64), ("rot", ctypes.c_int32), ("amplitude", ctypes.c_float), ("flags", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class IQCacheDesc(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("pages", ctypes.c_int64), ("batch", ctypes.c_int64), ("width", ctypes.c_int64), ("flags", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class IQAppendDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int64),
+                ("ld_k_token", ctypes.c_int64), ("ld_k_head", ctypes.c_int64), ("ld_v_token", ctypes.c_int64),
+                ("ld_v_head", ctypes.c_int64), ("ld_q_token", ctypes.c_int64), ("ld_q_head", ctypes.c_int64), ("rot", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class IQAttentionDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int64),
+                ("ld_token", ctypes.c_int64), ("ld_head", ctypes.c_int64), ("window", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
 
 
 class IQStats(ctypes.Structure):
@@ -112,6 +144,23 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.iq_packed_gemv.argtypes = [D, P, P, P, P, I, N, P, I, P]
     L.iq_packed_gated.restype = ctypes.c_int
     L.iq_packed_gated.argtypes = [D, I, P, P, P, P, P, P, P, I, N, P, I, P]
+    R, C, T = ctypes.POINTER(IQRotaryDesc), ctypes.POINTER(IQCacheDesc), ctypes.c_double
+    L.iq_rotary_table.restype = ctypes.c_int
+    L.iq_rotary_table.argtypes = [I, T, I, T, T, T, T, P]
+    L.iq_rotary.restype = ctypes.c_int
+    L.iq_rotary.argtypes = [R, P, P, P, P, P]
+    L.iq_rotary_backward.restype = ctypes.c_int
+    L.iq_rotary_backward.argtypes = [R, P, P, P, P, P]
+    L.iq_cache_codes_bytes.restype, L.iq_cache_codes_bytes.argtypes = S, [C]
+    L.iq_cache_scales_bytes.restype, L.iq_cache_scales_bytes.argtypes = S, [C]
+    L.iq_cache_append.restype = ctypes.c_int
+    L.iq_cache_append.argtypes = [C, ctypes.POINTER(IQAppendDesc), P, P, P, P, P, P, P, P, P, P, P]
+    L.iq_cache_read.restype = ctypes.c_int
+    L.iq_cache_read.argtypes = [C, P, P, P, P, P, N, P, P, I, P]
+    L.iq_cache_attention.restype = ctypes.c_int
+    L.iq_cache_attention.argtypes = [C, ctypes.POINTER(IQAttentionDesc), P, P, P, P, P, P, P, P, P]
+    L.iq_cache_attention_workspace_bytes.restype = S
+    L.iq_cache_attention_workspace_bytes.argtypes = [C, ctypes.POINTER(IQAttentionDesc)]
     L.iq_status_str.restype, L.iq_status_str.argtypes = ctypes.c_char_p, [ctypes.c_int]
     L.iq_abi_version.restype, L.iq_abi_version.argtypes = ctypes.c_int, []
     _lib = L
@@ -258,6 +307,50 @@ def iq_packed_gated(d: IQDesc, act: int, codes_gate: int, scales_gate: int, glob
                     stream: int | None) -> int:
     return (_lib or load_library()).iq_packed_gated(ctypes.byref(d), act, codes_gate, scales_gate, global_gate, codes_up,
                                           scales_up, global_up, x, x_dtype, n1, h, h_dtype, stream)
+
+
+def iq_rotary_table(rot: int, base: float, scaling: int, factor: float, context: float, low: float, high: float,
+                    table: int | None) -> int:
+    """`table` is a HOST address."""
+    return load_library().iq_rotary_table(rot, base, scaling, factor, context, low, high, table)
+
+
+def iq_rotary(d: IQRotaryDesc, x: int, positions: int, table: int | None, y: int, stream: int | None) -> int:
+    return (_lib or load_library()).iq_rotary(ctypes.byref(d), x, positions, table, y, stream)
+
+
+def iq_rotary_backward(d: IQRotaryDesc, dy: int, positions: int, table: int | None, dx: int, stream: int | None) -> int:
+    return (_lib or load_library()).iq_rotary_backward(ctypes.byref(d), dy, positions, table, dx, stream)
+
+
+def iq_cache_codes_bytes(d: IQCacheDesc) -> int:
+    return load_library().iq_cache_codes_bytes(ctypes.byref(d))
+
+
+def iq_cache_scales_bytes(d: IQCacheDesc) -> int:
+    return load_library().iq_cache_scales_bytes(ctypes.byref(d))
+
+
+def iq_cache_append(d: IQCacheDesc, a: IQAppendDesc, k: int, v: int, page_table: int, lengths: int, starts: int | None,
+                    table: int | None, q: int | None, q_out: int | None, codes: int, scales: int, stream: int | None) -> int:
+    return (_lib or load_library()).iq_cache_append(ctypes.byref(d), ctypes.byref(a), k, v, page_table, lengths, starts, table, q,
+                                                    q_out, codes, scales, stream)
+
+
+def iq_cache_read(d: IQCacheDesc, codes: int, scales: int, page_table: int, lengths: int, starts: int | None, tokens: int,
+                  k: int | None, v: int | None, out_dtype: int, stream: int | None) -> int:
+    return (_lib or load_library()).iq_cache_read(ctypes.byref(d), codes, scales, page_table, lengths, starts, tokens, k, v,
+                                                  out_dtype, stream)
+
+
+def iq_cache_attention(d: IQCacheDesc, a: IQAttentionDesc, codes: int, scales: int, page_table: int, lengths: int,
+                       starts: int | None, q: int, o: int, workspace: int, stream: int | None) -> int:
+    return (_lib or load_library()).iq_cache_attention(ctypes.byref(d), ctypes.byref(a), codes, scales, page_table, lengths, starts,
+                                                       q, o, workspace, stream)
+
+
+def iq_cache_attention_workspace_bytes(d: IQCacheDesc, a: IQAttentionDesc) -> int:
+    return (_lib or load_library()).iq_cache_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(a))
 
 
 # ---- torch-facing helpers (allocation with torch.empty + the calls above) ---
@@ -624,7 +717,7 @@ def _refuse_grad(*tensors):
     """No graph is recorded, so a tensor that asks for a gradient would never get it."""
     if _torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
         raise RuntimeError("no gradient passes through this call: use tensors without requires_grad or torch.no_grad(), "
-                           "and layer_norm_backward or gated_backward for the gradients")
+                           "and layer_norm_backward, gated_backward or rotary_backward for the gradients")
 
 
 def _result(out, shape: tuple, dtype, x, what: str = "out"):
@@ -863,3 +956,187 @@ def packed_gated(q_gate: "Quantized", q_up: "Quantized", x, act: str = "silu", o
         if st:
             _check(st, "iq_packed_gated")
         return h
+
+
+# ---- the attention half of a layer ------------------------------------------
+def rotary_table(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, context: float = 0.0,
+                 low: float = 1.0, high: float = 32.0, device="cuda"):
+    """Turns per position of the rot / 2 pairs, float64 [rot / 2] on `device`; made
+    once and kept by the caller.  scaling: "plain", "linear" (angles over
+    factor), "base" (a larger base) or "parts" (slow pairs over factor, those
+    with `high` turns and more over `context` positions kept)."""
+    torch = _torch()
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}")
+    host = torch.empty((max(rot, 0) // 2,), dtype=torch.float64)
+    _check(iq_rotary_table(rot, base, ROTARY_SCALINGS[scaling], factor, context, low, high, host.data_ptr() if rot > 0 else None),
+           "iq_rotary_table")
+    return host.to(device)
+
+
+def _heads_of(x, what: str) -> None:
+    """x is [tokens, heads, dim], the elements of a head contiguous."""
+    if x.dim() != 3 or not (x.is_contiguous() or x.shape[2] == 1 or x.stride(2) == 1):
+        raise ValueError(f"{what} must be [tokens, heads, dim] with unit stride in a head")
+
+
+def _rotary(call, what: str, x, positions, table, interleaved: bool, amplitude: float, out, stream):
+    with _place(stream, x):
+        torch = _torch()
+        _refuse_grad(x, out)
+        _heads_of(x, "x")
+        dtype = _dtype_of(x, "x")
+        tokens, heads, dim = x.shape
+        _check_dense(positions, (tokens,), torch.int32, x, "positions")
+        if table.dim() != 1 or 2 * table.shape[0] > dim:
+            raise ValueError(f"table must be [rot / 2] for at most {dim} elements")
+        _check_dense(table, tuple(table.shape), torch.float64, x, "table")
+        if out is None:
+            out = x.new_empty((tokens, heads, dim))
+        else:
+            _heads_of(out, "out")
+            if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+                raise ValueError("out must be of x's shape, type and device")
+        d = IQRotaryDesc(dtype, int(bool(interleaved)), tokens, heads, dim, x.stride(0), x.stride(1), out.stride(0), out.stride(1),
+                         2 * table.shape[0], amplitude, 0, 0)
+        _check(call(d, x.data_ptr(), positions.data_ptr(), table.data_ptr(), out.data_ptr(), _stream_for(x)), what)
+        return out
+
+
+def rotary(x, positions, table, *, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
+    """The first 2 * len(table) elements of every head of x [tokens, heads, dim]
+    (float32 or bfloat16, any strides with contiguous heads) turned by their
+    positions' (int32 [tokens]) angles; pairs are halves apart or, interleaved,
+    neighbours.  out may be x itself."""
+    return _rotary(iq_rotary, "iq_rotary", x, positions, table, interleaved, amplitude, out, stream)
+
+
+def rotary_backward(dy, positions, table, *, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
+    """The gradient of rotary's x from that of its result: the transposed rotation."""
+    return _rotary(iq_rotary_backward, "iq_rotary_backward", dy, positions, table, interleaved, amplitude, out, stream)
+
+
+@dataclass
+class KVCache:
+    """Pages of keys and values in 8 bits: codes uint8 [pages, heads, page / 32,
+    2, 32 * dim] and scales float32 [pages, heads, page / 32, 2], laid out as
+    include/iq.h says."""
+    codes: object
+    scales: object
+    fmt: str
+    heads: int
+    dim: int
+    page: int
+
+
+def make_cache(pages: int, heads: int, dim: int, fmt: str = "e4m3", page: int = 64, device="cuda") -> KVCache:
+    """Memory for `pages` pages of `page` tokens; its content is of no matter."""
+    torch = _torch()
+    if fmt not in CACHE_FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(CACHE_FORMATS)}")
+    if not iq_cache_codes_bytes(IQCacheDesc(CACHE_FORMATS[fmt], heads, dim, page, 1, 0, 0, 0, 0)) or pages < 0:
+        raise ValueError("heads, dim (64, 96, 128, 192 or 256) or page (a power of two, 32 to 4096) is not supported")
+    return KVCache(torch.empty((pages, heads, page // 32, 2, 32 * dim), dtype=torch.uint8, device=device),
+                   torch.empty((pages, heads, page // 32, 2), dtype=torch.float32, device=device), fmt, heads, dim, page)
+
+
+def _cache_desc(cache: "KVCache", page_table, lengths, starts, tokens: int, x) -> IQCacheDesc:
+    """Checks of a cache and of what says where its sequences lie."""
+    torch = _torch()
+    if cache.fmt not in CACHE_FORMATS:
+        raise ValueError(f"the cache's fmt must be one of {sorted(CACHE_FORMATS)}")
+    if page_table.dim() != 2 or lengths.dim() != 1:
+        raise ValueError("page_table must be [batch, width] and lengths [batch]")
+    batch, width = page_table.shape
+    i32, pages, blocks = torch.int32, cache.codes.shape[0], cache.page // 32
+    _check_dense(cache.codes, (pages, cache.heads, blocks, 2, 32 * cache.dim), torch.uint8, x, "the cache's codes")
+    _check_dense(cache.scales, (pages, cache.heads, blocks, 2), torch.float32, x, "the cache's scales")
+    _check_dense(page_table, (batch, width), i32, x, "page_table")
+    _check_dense(lengths, (batch,), i32, x, "lengths")
+    if starts is not None:
+        _check_dense(starts, (batch + 1,), i32, x, "starts")
+    elif tokens != batch:
+        raise ValueError(f"without starts every sequence has one token: {tokens} tokens, {batch} sequences")
+    return IQCacheDesc(CACHE_FORMATS[cache.fmt], cache.heads, cache.dim, cache.page, pages, batch, width, 0, 0)
+
+
+def cache_append(cache: "KVCache", k, v, page_table, lengths, starts=None, *, q=None, rotary=None, interleaved: bool = False,
+                 amplitude: float = 1.0, stream=None):
+    """Appends k and v [tokens, heads, dim] to their sequences' pages, keys
+    turned by their positions if `rotary` (a rotary_table) is given.
+    page_table int32 [batch, width]; lengths int32 [batch], the new tokens
+    among them; starts int32 [batch + 1], the rows where each sequence's new
+    tokens begin (None: one token each).  Returns q [tokens, q_heads, dim]
+    turned as well, or None without q."""
+    with _place(stream, k):
+        _refuse_grad(k, v, q)
+        dtype = _dtype_of(k, "k")
+        for x, what, heads in ((k, "k", cache.heads), (v, "v", cache.heads), (q, "q", None)):
+            if x is None:
+                continue
+            _heads_of(x, what)
+            if x.shape[0] != k.shape[0] or x.shape[2] != cache.dim or (heads is not None and x.shape[1] != heads):
+                raise ValueError(f"{what} must be [tokens, heads, {cache.dim}] for the cache's heads")
+            if x.dtype != k.dtype or x.device != k.device:
+                raise TypeError("q, k and v must be of one type and on one device")
+        tokens = k.shape[0]
+        d = _cache_desc(cache, page_table, lengths, starts, tokens, k)
+        rot = 0
+        if rotary is not None:
+            if rotary.dim() != 1 or 2 * rotary.shape[0] > cache.dim:
+                raise ValueError(f"rotary must be [rot / 2] for at most {cache.dim} elements")
+            _check_dense(rotary, tuple(rotary.shape), _torch().float64, k, "rotary")
+            rot = 2 * rotary.shape[0]
+        q_out, q_heads, q_strides = None, 0, (0, 0)
+        if q is not None:
+            q_out, q_heads, q_strides = q.new_empty(tuple(q.shape)), q.shape[1], (q.stride(0), q.stride(1))
+        a = IQAppendDesc(dtype, int(bool(interleaved)), tokens, q_heads, k.stride(0), k.stride(1), v.stride(0), v.stride(1), *q_strides,
+                         rot, amplitude, 0, 0)
+        _check(iq_cache_append(d, a, k.data_ptr(), v.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), _ptr(starts), _ptr(rotary),
+                               _ptr(q), _ptr(q_out), cache.codes.data_ptr(), cache.scales.data_ptr(), _stream_for(k)),
+               "iq_cache_append")
+        return q_out
+
+
+def cache_read(cache: "KVCache", page_table, lengths, starts, tokens: int, out_dtype=None, *, out=None, stream=None):
+    """Keys and values [tokens, heads, dim] (bfloat16 by default, or float32) of
+    the last starts[b + 1] - starts[b] tokens of every sequence, at rows
+    starts[b] on (starts None: the last token of each); `out` a pair of tensors."""
+    with _place(stream, cache.codes):
+        codes = cache.codes
+        d = _cache_desc(cache, page_table, lengths, starts, tokens, codes)
+        dtype = _torch().bfloat16 if out_dtype is None else out_dtype
+        if out is not None:
+            dtype = out[0].dtype
+        shape = (tokens, cache.heads, cache.dim)
+        k, v = (_result(None if out is None else o, shape, dtype, codes, what) for o, what in zip(out or (None, None), ("out[0]", "out[1]")))
+        _check(iq_cache_read(d, codes.data_ptr(), cache.scales.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), _ptr(starts), tokens,
+                             k.data_ptr(), v.data_ptr(), _dtype_of(k, "out_dtype"), _stream_for(codes)), "iq_cache_read")
+        return k, v
+
+
+def cache_attention(cache: "KVCache", q, page_table, lengths, starts=None, *, scale: float | None = None, causal: bool = True,
+                    window: int = 0, out=None, workspace=None, stream=None):
+    """Attention of q [tokens, q_heads, dim] (bfloat16) over what the cache
+    holds of each row's sequence, the rows' own tokens (the last of lengths[b])
+    among it: softmax(scale q k) v over tokens up to the row's own, or with
+    `window` the last so many, or with causal=False all.  scale: dim ** -0.5
+    by default.  Returns [tokens, q_heads, dim]; rows from starts[batch] on
+    are not written."""
+    with _place(stream, q):
+        torch = _torch()
+        _refuse_grad(q, out)
+        _heads_of(q, "q")
+        if q.dtype != torch.bfloat16:
+            raise TypeError("q must be bfloat16")
+        tokens, heads, dim = q.shape
+        if dim != cache.dim or heads == 0 or heads % cache.heads:
+            raise ValueError(f"q must be [tokens, a multiple of {cache.heads} heads, {cache.dim}]")
+        d = _cache_desc(cache, page_table, lengths, starts, tokens, q)
+        o = _result(out, (tokens, heads, dim), q.dtype, q)
+        a = IQAttentionDesc(IQ_BF16, int(bool(causal)), tokens, heads, q.stride(0), q.stride(1), window,
+                            dim ** -0.5 if scale is None else scale, 0)
+        ws = _scratch(workspace, iq_cache_attention_workspace_bytes(d, a), q)
+        _check(iq_cache_attention(d, a, cache.codes.data_ptr(), cache.scales.data_ptr(), page_table.data_ptr(), lengths.data_ptr(),
+                                  _ptr(starts), q.data_ptr(), o.data_ptr(), ws.data_ptr(), _stream_for(q)), "iq_cache_attention")
+        return o

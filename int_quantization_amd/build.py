@@ -9,7 +9,8 @@ from concurrent.futures import ThreadPoolExecutor
 _HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(_HERE)
 SOURCES = [os.path.join(_HERE, "csrc", name) for name in
-           ("iq_kernels.hip", "iq_api.cpp", "iq_norm.hip", "iq_packed.hip", "iq_gated.hip", "iq_ffn_api.cpp")]
+           ("iq_kernels.hip", "iq_api.cpp", "iq_norm.hip", "iq_packed.hip", "iq_gated.hip", "iq_ffn_api.cpp", "iq_cache.hip", "iq_attend.hip",
+            "iq_attn_api.cpp")]
 OUT = os.path.join(_HERE, "libiq.so")
 BENCH_SOURCES = [os.path.join(_HERE, "csrc", "bench_copy.hip")]
 BENCH_OUT = os.path.join(_HERE, "libiq_bench.so")
