@@ -139,8 +139,8 @@ def attention(q, k, v, first, length, scale, causal=True, window=0):
 
     A score is a sum of dim exact products in FP32, off by (dim + 4) U sum |q k|, and rounded once more; its exponent is
     rounded as often as the running maximum changes, at sizes up to |score| + |maximum| + 15 ln 2.  A probability is rounded
-    to FP16 (2^-11; below 2^-29 of the largest it is off by 2^-40 of it), its scale and exponential add 4 U, and every sum,
-    rescaling and join of N tokens N U."""
+    to FP16 (2^-11; held times 2^9 of a maximum that is at most the row's, so small ones are off by half of 2^-24 over 2^9 =
+    2^-34 of the largest), its scale and exponential add 4 U, and every sum, rescaling and join of N tokens N U."""
     q, k, v = q.double(), k.double(), v.double()
     n, heads, dim = q.shape
     group, keys = heads // k.shape[1], k.shape[0]
@@ -168,7 +168,7 @@ def attention(q, k, v, first, length, scale, causal=True, window=0):
         delta = torch.where(seen, size, torch.zeros_like(s)).amax(1) * (dim + 4) * U + 8 * U * far if keys else torch.zeros(n, dtype=torch.float64)
         each = 2.0 ** -11 + 2 * delta + (2 * keys + 64) * U
         o[:, h] = p @ vh
-        e[:, h] = (p @ vh.abs()) * (2 * each)[:, None] + vh.abs().amax(0, keepdim=True) * keys * 2.0 ** -40 + TINY if keys else TINY
+        e[:, h] = (p @ vh.abs()) * (2 * each)[:, None] + vh.abs().amax(0, keepdim=True) * keys * 2.0 ** -34 + TINY if keys else TINY
         bad = torch.isnan(q[:, h]).any(1) | torch.isinf(q[:, h]).any(1)
         o[:, h][bad & some] = math.nan
     o[~some], e[~some] = 0, 0
