@@ -1,13 +1,15 @@
 // Attention over the paged 8-bit cache.
 //
-// A wave takes 32 columns: neighbouring (token, query head) pairs of one key
-// head, so that the heads that share a key head read its codes once.  For
+// A wave takes 16 or 32 columns: neighbouring (token, query head) pairs of one
+// key head, so that the heads that share a key head read its codes once.  For
 // every block of 32 tokens it forms the scores S^T = K Q^T and the running
-// output O^T += V^T P^T on the matrix cores (32 x 32 x 16, FP16).  In both
-// results a lane holds one column, so maxima, sums and scales are its own, and
-// the tokens that a lane holds of S^T are those that it feeds to the second
-// product: the order of the cache's values makes them match.
+// output O^T += V^T P^T on the matrix cores (FP16, 32 x 32 x 16 or 16 x 16 x
+// 32).  In both results a lane holds one column, so maxima, sums and scales
+// are its own, and the tokens that a lane holds of S^T are those that it feeds
+// to the second product: the order of the cache's values makes them match.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "iq_attn_launch.h"
 #include "iq_cache.h"
@@ -84,68 +86,184 @@ __device__ __forceinline__ View view_of(const AttendArgs& a, const Tile& t) {
     return v;
 }
 
+// How the lanes of a wave share a block and C columns.  Lane group g = lane / C
+// holds column lane % C.
+//   C = 32: scores r = 0 .. 15 are tokens 8 (r / 4) + 4 g + r % 4; fragment f of
+//     keys and queries holds elements 32 (f / 2) + 16 g + 8 (f % 2) + 0 .. 7;
+//     output tile i, register r is element 32 i + 8 (r / 4) + 4 g + r % 4.
+//   C = 16: scores r = 0 .. 7 are tokens 16 (g % 2) + 8 (r / 4) + 4 (g / 2) + r % 4 (the rows of the two
+//     score tiles are taken in the order that makes them 8 neighbouring places of the values);
+//     fragment f holds elements 64 (f / 2) + 16 g + 8 (f % 2) + 0 .. 7, the last of an odd number 64 (f / 2) + 8 g + 0 .. 7;
+//     output tile i, register r is element 16 i + 4 g + r.
+template <int D, int C> struct Shape {
+    static constexpr int kGroups = 64 / C, kScores = C / 2, kFragments = C == 32 ? D / 16 : D / 32, kSteps = C == 32 ? 2 : 1;
+    static constexpr int kTiles = D / C, kPerTile = C * C / 64;      // output tiles and their registers
+    using Tile = __attribute__((ext_vector_type(kPerTile))) float;
+
+    static __device__ __forceinline__ int token(int g, int r) {
+        return C == 32 ? 8 * (r >> 2) + 4 * g + (r & 3) : 16 * (g & 1) + 8 * (r >> 2) + 4 * (g >> 1) + (r & 3);
+    }
+    static __device__ __forceinline__ int element(int g, int f) {
+        if (C == 32) return 32 * (f >> 1) + 16 * g + 8 * (f & 1);
+        return f + 1 == kFragments && kFragments % 2 ? 64 * (f >> 1) + 8 * g : 64 * (f >> 1) + 16 * g + 8 * (f & 1);
+    }
+    static __device__ __forceinline__ int output(int g, int i, int r) {
+        return C == 32 ? 32 * i + 8 * (r >> 2) + 4 * g + (r & 3) : 16 * i + 4 * g + r;
+    }
+    static __device__ __forceinline__ float over_groups(float v, bool sum) {
+#pragma unroll
+        for (int d = C; d < 64; d <<= 1) {
+            const float u = __shfl_xor(v, d);
+            v = sum ? v + u : fmaxf(v, u);
+        }
+        return v;
+    }
+};
+
+// The codes of a block that a lane feeds to the matrix cores.
+template <int D, int FMT, int C> struct Codes {
+    using S = Shape<D, C>;
+    static constexpr int kKeys = C == 32 ? D / 32 : 2 * (D / 64), kRest = C == 16 && D % 64 ? 2 : 0, kValues = C == 32 ? D / 32 : D / 16;
+    using Value = typename std::conditional<C == 32, uint4, uint2>::type;
+    uint4 k[kKeys];
+    uint2 rest[kRest + 1];
+    Value v[kValues];
+
+    __device__ __forceinline__ void fetch_keys(const uint8_t* block, int lane) {
+        const uint4* p = reinterpret_cast<const uint4*>(block);
+        const int g = lane / C;
+        if constexpr (C == 32) {
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) k[j] = p[(2 * j + g) * 32 + (lane & 31)];
+        } else {
+            const int row = lane & 15, token = 16 * ((row >> 2) & 1) + 4 * (row >> 3) + (row & 3);
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) k[j] = p[(4 * (j >> 1) + g) * 32 + 8 * (j & 1) + token];
+            if constexpr (kRest) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    rest[t] = reinterpret_cast<const uint2*>(p + (D / 64 * 4 + (g >> 1)) * 32 + 8 * t + token)[g & 1];
+            }
+        }
+    }
+    __device__ __forceinline__ void fetch_values(const uint8_t* block, int lane) {
+        const Value* p = reinterpret_cast<const Value*>(block + kBlock * D);
+#pragma unroll
+        for (int j = 0; j < kValues; ++j) v[j] = p[(C * j + (lane & (C - 1))) * S::kGroups + lane / C];
+    }
+    // Values of tokens from `keep` on (of the block), which may be anything, as zeros.
+    __device__ __forceinline__ void keep_values(int g, int keep) {
+#pragma unroll
+        for (int j = 0; j < kValues; ++j) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v[j]);
+#pragma unroll
+            for (int i = 0; i < S::kScores / 4; ++i) {
+                const int n = keep - S::token(g, 4 * i);       // bytes of this word that are the sequence's
+                w[i] &= n <= 0 ? 0u : n >= 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+            }
+        }
+    }
+    // Scores of the lane's tokens: codes times FP16 queries.
+    __device__ __forceinline__ void scores(const half8* q, float* s) const {
+        if constexpr (C == 32) {
+            float16v x = 0.f;
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) {
+                x = __builtin_amdgcn_mfma_f32_32x32x16_f16(expand8<FMT>(k[j].x, k[j].y), q[2 * j], x, 0, 0, 0);
+                x = __builtin_amdgcn_mfma_f32_32x32x16_f16(expand8<FMT>(k[j].z, k[j].w), q[2 * j + 1], x, 0, 0, 0);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = x[r];
+        } else {
+            float4v x[2] = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) {
+                x[j & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(expand8<FMT>(k[j].x, k[j].y), q[j >> 1 << 1], x[j & 1], 0, 0, 0);
+                x[j & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(expand8<FMT>(k[j].z, k[j].w), q[(j >> 1 << 1) + 1], x[j & 1], 0, 0, 0);
+            }
+            if constexpr (kRest) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    x[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(expand8<FMT>(rest[t].x, rest[t].y), q[S::kFragments - 1], x[t], 0, 0, 0);
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) s[r] = x[r >> 2][r & 3];
+        }
+    }
+    __device__ __forceinline__ void add_values(const half8* p, typename S::Tile* o) const {
+#pragma unroll
+        for (int j = 0; j < kValues; ++j) {
+            if constexpr (C == 32) {
+                o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(expand8<FMT>(v[j].x, v[j].y), p[0], o[j], 0, 0, 0);
+                o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(expand8<FMT>(v[j].z, v[j].w), p[1], o[j], 0, 0, 0);
+            } else {
+                o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(expand8<FMT>(v[j].x, v[j].y), p[0], o[j], 0, 0, 0);
+            }
+        }
+    }
+};
+
 // Queries of a column as the matrix cores take them: FP16 times a power of two
 // that brings the row's largest into [2^14, 2^15), and the factor that makes
 // scores exponents of 2.
-template <int J> __device__ __forceinline__ float load_query(const AttendArgs& a, const uint16_t* row, int h, half8* q) {
-    uint4 raw[2 * J];
+template <int D, int C> __device__ __forceinline__ float load_query(float scale, const uint16_t* row, int g, half8* q) {
+    using S = Shape<D, C>;
+    uint4 raw[S::kFragments];
     uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        raw[2 * j] = *reinterpret_cast<const uint4*>(row + 32 * j + 16 * h);
-        raw[2 * j + 1] = *reinterpret_cast<const uint4*>(row + 32 * j + 16 * h + 8);
-    }
+    for (int f = 0; f < S::kFragments; ++f) raw[f] = *reinterpret_cast<const uint4*>(row + S::element(g, f));
 #pragma unroll
-    for (int j = 0; j < 2 * J; ++j)
+    for (int f = 0; f < S::kFragments; ++f)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t w = reinterpret_cast<const uint32_t*>(&raw[j])[e];
+            const uint32_t w = reinterpret_cast<const uint32_t*>(&raw[f])[e];
             top = max(top, max((w << 16) & 0x7FFFFFFFu, w & 0x7FFF0000u));
         }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+#pragma unroll
+    for (int d = C; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
     int e = (int)(top >> 23);                          // 0 for zeros and subnormals, 255 for infinities and NaN
     e = e == 255 ? 0 : max(e, 1) - 127 - 14;
 #pragma unroll
-    for (int j = 0; j < 2 * J; ++j)
+    for (int f = 0; f < S::kFragments; ++f)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const uint32_t w = reinterpret_cast<const uint32_t*>(&raw[j])[k >> 1];
-            q[j][k] = (_Float16)ldexpf(__uint_as_float(k & 1 ? w & 0xFFFF0000u : w << 16), -e);
+            const uint32_t w = reinterpret_cast<const uint32_t*>(&raw[f])[k >> 1];
+            q[f][k] = (_Float16)ldexpf(__uint_as_float(k & 1 ? w & 0xFFFF0000u : w << 16), -e);
         }
-    return ldexpf(a.scale * 1.44269504f, e);
+    return ldexpf(scale * 1.44269504f, e);
 }
 
 // Running state of a column: maximum, sum of this lane's tokens, output.
-template <int J> struct State {
-    float16v o[J];
+template <int D, int C> struct State {
+    using S = Shape<D, C>;
+    typename S::Tile o[S::kTiles];
     float m, l;
     int lift;                    // values' scales are held over 2^lift, the largest so far
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int j = 0; j < J; ++j) o[j] = 0.f;
+        for (int j = 0; j < S::kTiles; ++j) o[j] = 0.f;
         m = -INFINITY;
         l = 0.f;
         lift = -126;
     }
     __device__ __forceinline__ void scale(float by) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) o[j] *= by;
+        for (int j = 0; j < S::kTiles; ++j) o[j] *= by;
     }
-    // From scores (codes times FP16 queries) to probabilities: pv[step][e] is
-    // that of the e-th of the 8 tokens of matrix product `step`.  seen: bit r for score r.
-    __device__ __forceinline__ void probabilities(const float16v& s, float fk, float scale_v, uint32_t seen, bool masked, half8* pv) {
+    // From scores to probabilities p, in the second product's order.  seen: bit r for score r.
+    __device__ __forceinline__ void probabilities(const float* s, float fk, float scale_v, uint32_t seen, bool masked, half8* p) {
         float top = -INFINITY;
         if (!masked) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[r]);
+            for (int r = 0; r < S::kScores; ++r) top = fmaxf(top, s[r]);
         } else {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) top = (seen >> r) & 1 ? fmaxf(top, s[r]) : top;
+            for (int r = 0; r < S::kScores; ++r) top = (seen >> r) & 1 ? fmaxf(top, s[r]) : top;
         }
         top = top == -INFINITY ? top : top * fk;
         if (__any(top > m + kSlack)) {
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = S::over_groups(top, false);
             const float now = fmaxf(m, top), alpha = now == m ? 1.f : exp2_fast(m - now);
             m = now;
             l *= alpha;
@@ -161,35 +279,25 @@ template <int J> struct State {
         const float off = kLift + __builtin_amdgcn_logf(fraction) - m;
         float sum = 0.f;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
+        for (int r = 0; r < S::kScores; ++r) {
             float e = exp2_fast(__builtin_fmaf(s[r], fk, off));
             if (masked) e = (seen >> r) & 1 ? e : 0.f;
             sum += e;
-            pv[r >> 3][r & 7] = (_Float16)e;
+            p[r >> 3][r & 7] = (_Float16)e;
         }
         l = __builtin_fmaf(sum, 1.f / fraction, l);
     }
 };
 
-// Bits of the scores of lane half h whose tokens lie in [from, to); the block's token 0 is t0.
-__device__ __forceinline__ uint32_t seen_bits(int t0, int h, int from, int to) {
+// Bits of the scores of lane group g whose tokens lie in [from, to); the block's token 0 is t0.
+template <int D, int C> __device__ __forceinline__ uint32_t seen_bits(int t0, int g, int from, int to) {
     uint32_t seen = 0;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int token = t0 + 8 * (r >> 2) + 4 * h + (r & 3);
+    for (int r = 0; r < Shape<D, C>::kScores; ++r) {
+        const int token = t0 + Shape<D, C>::token(g, r);
         seen |= (token >= from && token < to ? 1u : 0u) << r;
     }
     return seen;
-}
-
-// Codes of 16 values of lane half h with those from token `keys` on, which may be anything, as zeros.
-__device__ __forceinline__ void keep_values(uint4* v, int t0, int h, int keys) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = keys - t0 - (8 * i + 4 * h);     // bytes of this word that are the sequence's
-        w[i] &= n <= 0 ? 0u : n >= 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
-    }
 }
 
 // Values that a wave's lanes share, in scalar registers.
@@ -224,35 +332,46 @@ __device__ __forceinline__ Place place_at(const CacheArgs& c, int seq, int b, in
     return p;
 }
 
-// ---- few columns: the work is the cache's codes ------------------------------------------
-// All (tile, key head, block) triples in order are shared out evenly among a
-// fixed number of workgroups, so sequences of any lengths keep every CU busy.
-// A row that more than one workgroup has a share of is joined by a second launch.
-//
-// A workgroup's four waves take its blocks in turn, each with the next block's
-// codes in flight, and join their outputs through LDS.
-constexpr int kLeastShare = 8;   // blocks of a workgroup, at least
+// ---- sharing the work out ----------------------------------------------------------------
+// A row is a tile of columns of one sequence and key head; its units are the
+// blocks that some column sees (one where there are none: someone writes its
+// zeros).  The units of all rows, key head by key head, are shared out evenly among
+// the workgroups that the GPU holds at once, so sequences of any lengths keep
+// every CU busy.  A row that more than one workgroup has a share of is joined by another launch.
 
-__host__ __device__ inline int64_t part_floats(int dim) { return (int64_t)kColumns * (dim + 2); }
+// Sequences of few columns are k_few's, the others k_many's.
+constexpr int kFewColumns = 64;
+enum { kAny = 0, kFew = 1, kMany = 2 };        // which of them a kernel takes: all where the other is not launched
 
-struct Plan {
-    int64_t slots;
-    int workers;
-    int64_t parts;               // where the parts begin in the workspace, in floats
-};
-// The workspace begins with the share and the running sums of blocks of all
-// slots, int64 [2 + slots]; parts follow, two for every workgroup: of the row
-// that its share begins in (0), and of the one that it ends in (1).
-
-__device__ __forceinline__ int units_of(const AttendArgs& a, const Plan& plan, int64_t slot) {
-    Tile t;
-    if (slot >= plan.slots || !tile_of(a, slot, &t)) return 0;
-    return max(view_of(a, t).blocks, 1);               // a row that sees nothing is written by someone
+__device__ __forceinline__ bool takes(const AttendArgs& a, int kind, const Span& s) {
+    const bool few = (int64_t)s.n * a.group <= kFewColumns;
+    return s.n > 0 && (kind == kAny || (kind == kFew) == few);
 }
 
-// The share of a workgroup: sum over slots, then the slot that unit `at` lies in.
-struct Shares {
-    int64_t total, per;
+// A row's parts: the normalized output of its columns, their maxima and sums.
+__host__ __device__ inline int64_t part_floats(int dim, int columns) { return (int64_t)columns * (dim + 2); }
+
+// The row that a workgroup's share ends in, if it began there and does not end
+// there: the join's work.  columns is 0 if there is none.
+struct Open {
+    int64_t begin;               // unit that the row begins with
+    int64_t per;                 // units of a share
+    int seq, f0, columns, head;
+    int last, unused;            // workgroup that has the row's end
+};
+
+struct Plan {
+    int kind, workers;
+    int slots;                   // of k_many: tiles' slots
+    int64_t opens, parts;        // where the Opens and the parts begin in the workspace, in bytes: an Open and two
+                                 // parts for every workgroup, of the row that its share begins in (0) and ends in (1)
+};
+
+struct Share {
+    int64_t at, end, per;        // units
+    int64_t entry;               // that `at` lies in
+    int64_t entry_begin;         // unit that the entry begins with, counting its head's
+    int head;
 };
 
 __device__ __forceinline__ int64_t wave_sum(int64_t v) {
@@ -261,31 +380,27 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
     return v;
 }
 
-template <int D, int FMT> __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_few(AttendArgs a, Plan plan) {
-    constexpr int J = D / 32;                          // pieces of 32 elements
-    __shared__ float other[2][kWaves * kColumns];      // maxima and sums of the waves
-    __shared__ float pass[2 * (D / 2) * 64];           // outputs on their way to another wave
-    __shared__ int64_t sums[kWaves + 1];
-    __shared__ int64_t found[2];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
-    int64_t* header = static_cast<int64_t*>(a.workspace);
-
-    // the workgroup's share of all units
-    int64_t mine = 0;
-    for (int64_t s = threadIdx.x; s < plan.slots; s += kThreads) mine += units_of(a, plan, s);
+// The share of workgroup `worker`; units(e) are those of entry e of `entries` for one head.
+template <typename F>
+__device__ __forceinline__ Share share_of(int worker, int workers, int heads, int64_t entries, int least, const F& units) {
+    __shared__ int64_t sums[kWaves], found[2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int64_t first = threadIdx.x < entries ? units(threadIdx.x) : 0, mine = first;
+    for (int64_t e = threadIdx.x + kThreads; e < entries; e += kThreads) mine += units(e);
     mine = wave_sum(mine);
     if (lane == 0) sums[wave] = mine;
     __syncthreads();
-    const int64_t total = (sums[0] + sums[1] + sums[2] + sums[3]) * a.c.heads;
-    int64_t per = (total + plan.workers - 1) / plan.workers;
-    per = per < kLeastShare ? kLeastShare : per;
-    int64_t at = blockIdx.x * per;
-    const int64_t end = min(at + per, total);
-    if (blockIdx.x == 0 && threadIdx.x == 0) header[0] = per;
-    if (at >= total) return;
-    int64_t before = 0;                                // units of the slots before the current 256, one head
-    for (int64_t base = 0; base < plan.slots; base += kThreads) {
-        const int v = units_of(a, plan, base + threadIdx.x);
+    const int64_t one_head = sums[0] + sums[1] + sums[2] + sums[3], total = one_head * heads;
+    Share s;
+    s.per = max((total + workers - 1) / workers, (int64_t)least);
+    s.at = worker * s.per;
+    s.end = min(s.at + s.per, total);
+    if (s.at >= total) return s;
+    s.head = (int)(s.at / one_head);
+    const int64_t into = s.at - s.head * one_head;
+    int64_t before = 0;                                // units of the entries before the current 256
+    for (int64_t base = 0; base < entries; base += kThreads) {
+        const int64_t e = base + threadIdx.x, v = base == 0 ? first : e < entries ? units(e) : 0;
         int64_t upto = v;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -297,233 +412,582 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 
         __syncthreads();
         for (int w = 0; w < wave; ++w) upto += sums[w];
         upto += before;
-        if (blockIdx.x == 0 && base + threadIdx.x < plan.slots) header[1 + base + threadIdx.x] = upto - v;
-        if (at >= (upto - v) * a.c.heads && at < upto * a.c.heads) {
-            found[0] = base + threadIdx.x;
+        if (into >= upto - v && into < upto) {
+            found[0] = e;
             found[1] = upto - v;
         }
         before += sums[0] + sums[1] + sums[2] + sums[3];
-        if (blockIdx.x != 0 && at < before * a.c.heads) break;
+        if (into < before) break;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) header[1 + plan.slots] = before;
     __syncthreads();
-    int64_t slot = found[0];
-    const int64_t into = at - found[1] * a.c.heads;
-    bool opening = true;                               // the share's first row
-    int head = -1, skip = 0;
+    s.entry = found[0];
+    s.entry_begin = s.head * one_head + found[1];
+    return s;
+}
 
-    while (at < end) {
-        Tile t;
-        if (!tile_of(a, slot, &t)) {
-            ++slot;
-            continue;
-        }
-        t = one(t);
-        const View v = view_of(a, t);
-        const int units = max(v.blocks, 1);
-        if (opening) {
-            head = one((int)(into / units));
-            skip = one((int)(into - (int64_t)head * units));
-        } else {
-            if (++head == a.c.heads) {
-                head = -1;
-                ++slot;
+// Columns of a lane's column `col`, of a tile that begins with flattened column f0.
+struct Column {
+    int row, head;               // of q and o; head among those of the key head
+    int from, to;                // tokens that it sees
+};
+__device__ __forceinline__ Column column_of(const AttendArgs& a, const Tile& t, const View& v, int col) {
+    const int f = t.f0 + min(col, t.columns - 1), i = f / a.group;
+    return {t.s.row + i, f - i * a.group, seen_from(a, v.first + i, v.keys), seen_to(a, v.first + i, v.keys)};
+}
+
+// ---- few columns: the work is the cache's codes ------------------------------------------
+// A workgroup's four waves take a row's blocks in turn, each with the next
+// block's codes in flight, and join their outputs through LDS.
+constexpr int kLeastShare = 8;   // blocks of a workgroup, at least
+
+// Waves of a SIMD, and so workgroups of a CU.
+constexpr int few_waves(int dim, int columns) { return columns == 16 ? (dim <= 128 ? 4 : 2) : dim <= 128 ? 2 : 1; }
+
+__device__ __forceinline__ Tile tile_at(const AttendArgs& a, int unit, int seq, const Span& s, int k) {
+    const int64_t left = (int64_t)s.n * a.group - (int64_t)k * unit;
+    return {seq, k * unit, (int)min(left, (int64_t)unit), s};
+}
+
+template <int C> __device__ __forceinline__ int64_t units_of(const AttendArgs& a, const Plan& plan, int seq) {
+    const Span s = span_of(a.c, seq);
+    if (!takes(a, plan.kind, s)) return 0;
+    const int tiles = (int)(((int64_t)s.n * a.group + C - 1) / C);
+    if (s.n == 1) return (int64_t)tiles * max(view_of(a, tile_at(a, C, seq, s, 0)).blocks, 1);      // tiles of one token see the same
+    int64_t sum = 0;
+    for (int k = 0; k < tiles; ++k) sum += max(view_of(a, tile_at(a, C, seq, s, k)).blocks, 1);
+    return sum;
+}
+
+template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThreads, few_waves(D, C)) void k_few(AttendArgs a, Plan plan) {
+    using S = Shape<D, C>;
+    constexpr int R = D * C / 64;                      // registers of the output
+    __shared__ float other[2][kWaves * C];             // maxima and sums of the waves
+    __shared__ float pass[2 * R * 64];                 // outputs on their way to another wave
+    const int lane = threadIdx.x & 63, wave = one(threadIdx.x >> 6), col = lane & (C - 1), g = lane / C;
+    Share share;
+    int seq, tile = 0;
+    Span span;
+    if constexpr (DIRECT) {                            // a workgroup for each row
+        const int per = a.c.starts ? kFewColumns / C : (a.group + C - 1) / C;
+        seq = blockIdx.x / per;
+        tile = blockIdx.x % per;
+        span = span_of(a.c, seq);
+        if (!takes(a, plan.kind, span) || (int64_t)tile * C >= (int64_t)span.n * a.group) return;
+        share.head = blockIdx.y;
+    } else {
+        Open* open = reinterpret_cast<Open*>(static_cast<char*>(a.workspace) + plan.opens);
+        share = share_of(blockIdx.x, plan.workers, a.c.heads, a.c.batch, kLeastShare, [&](int64_t e) { return units_of<C>(a, plan, (int)e); });
+        if (threadIdx.x == 0) open[blockIdx.x].columns = 0;
+        if (share.at >= share.end) return;
+        seq = one((int)share.entry);
+        share.head = one(share.head);
+        span = span_of(a.c, seq);
+    }
+    int64_t row_begin = DIRECT ? 0 : share.entry_begin;                // unit that the row begins with
+    bool opening = true;                               // the share's first row
+
+    while (true) {
+        if (!DIRECT) {
+            if (share.at >= share.end) break;
+            if ((int64_t)tile * C >= (int64_t)span.n * a.group || !takes(a, plan.kind, span)) {     // the next sequence, or head
+                if (++seq == a.c.batch) {
+                    seq = 0;
+                    if (++share.head >= a.c.heads) break;              // the arrays changed meanwhile
+                }
+                tile = 0;
+                span = span_of(a.c, seq);
                 continue;
             }
-            skip = 0;
         }
-        const int take = one((int)min((int64_t)(units - skip), end - at));
+        const Tile t = one(tile_at(a, C, seq, span, tile));
+        const View v = view_of(a, t);
+        const int units = max(v.blocks, 1), head = share.head;
+        if (!DIRECT && opening && share.at >= row_begin + units) {     // the share begins in a later row of its sequence
+            row_begin += units;
+            ++tile;
+            continue;
+        }
+        const int skip = DIRECT ? 0 : one((int)min(max(share.at - row_begin, (int64_t)0), (int64_t)units));
+        const int take = DIRECT ? units : one((int)min((int64_t)(units - skip), share.end - share.at));
         const bool whole = take == units;
         const int b0 = v.block + min(skip, v.blocks), b1 = v.block + min(skip + take, v.blocks);
 
-        // what this column sees: tokens [from, to)
-        const int f = t.f0 + min(col, t.columns - 1), i = f / a.group, g = f - i * a.group;
-        const int from = seen_from(a, v.first + i, v.keys), to = seen_to(a, v.first + i, v.keys);
-        half8 q[2 * J];
-        const float factor = load_query<J>(
-            a, static_cast<const uint16_t*>(a.q) + (t.s.row + i) * a.ld_token + ((int64_t)head * a.group + g) * a.ld_head, h, q);
-
-        State<J> st;
-        st.clear();
-        // Codes of the wave's next block: keys are fetched once the scores of this one are formed, values after its output.
-        // Past the last block the last one is fetched again; absent pages stand for a page that nothing is seen of.
-        uint4 kc[J], vc[J];
+        Codes<D, FMT, C> codes;
+        Place now = {};
+        const auto block_codes = [&](const Place& p) { return a.c.codes + p.at * (2 * kBlock * (int64_t)D); };
         if (b0 + wave < b1) {
-            Place now = place_at(a.c, t.seq, b0 + wave, head), next = now;
-            const auto fetch_keys = [&](int64_t at) {
-                const uint4* codes = reinterpret_cast<const uint4*>(a.c.codes + at * (2 * kBlock * (int64_t)D));
-#pragma unroll
-                for (int j = 0; j < J; ++j) kc[j] = codes[(2 * j + h) * 32 + col];
-            };
-            const auto fetch_values = [&](int64_t at) {
-                const uint4* codes = reinterpret_cast<const uint4*>(a.c.codes + at * (2 * kBlock * (int64_t)D)) + 2 * D;
-#pragma unroll
-                for (int j = 0; j < J; ++j) vc[j] = codes[(32 * j + col) * 2 + h];
-            };
-            fetch_keys(now.at);
-            fetch_values(now.at);
-            for (int b = b0 + wave; b < b1; b += kWaves) {
-                next = place_at(a.c, t.seq, min(b + kWaves, b1 - 1), head);
-                float16v s = 0.f;
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    s = __builtin_amdgcn_mfma_f32_32x32x16_f16(expand8<FMT>(kc[j].x, kc[j].y), q[2 * j], s, 0, 0, 0);
-                    s = __builtin_amdgcn_mfma_f32_32x32x16_f16(expand8<FMT>(kc[j].z, kc[j].w), q[2 * j + 1], s, 0, 0, 0);
-                }
-                fetch_keys(next.at);
-                const int t0 = b * kBlock;
-                half8 pv[2];
-                const bool masked = now.absent || t0 + kBlock > v.each_to || t0 < v.each_from;
-                uint32_t seen = 0xFFFFu;
-                if (masked) seen = seen_bits(t0, h, from, now.absent ? 0 : to);
-                st.probabilities(s, factor * now.scale_k, now.scale_v, seen, masked, pv);
-                if (now.absent || t0 + kBlock > v.keys) {
-#pragma unroll
-                    for (int j = 0; j < J; ++j) keep_values(&vc[j], t0, h, now.absent ? 0 : v.keys);
-                }
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    st.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(expand8<FMT>(vc[j].x, vc[j].y), pv[0], st.o[j], 0, 0, 0);
-                    st.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(expand8<FMT>(vc[j].z, vc[j].w), pv[1], st.o[j], 0, 0, 0);
-                }
-                fetch_values(next.at);
-                now = next;
-            }
+            now = place_at(a.c, t.seq, b0 + wave, head);
+            codes.fetch_keys(block_codes(now), lane);
+            codes.fetch_values(block_codes(now), lane);
         }
-        float l = st.l + __shfl_xor(st.l, 32);
+        const Column c = column_of(a, t, v, col);
+        half8 q[S::kFragments];
+        const float factor = load_query<D, C>(
+            a.scale, static_cast<const uint16_t*>(a.q) + c.row * a.ld_token + ((int64_t)head * a.group + c.head) * a.ld_head, g, q);
+        State<D, C> st;
+        st.clear();
+        // Keys of the wave's next block are fetched once the scores of this one are formed, values after its output.
+        // Past the last block the last one is fetched again; absent pages stand for a page that nothing is seen of.
+        for (int b = b0 + wave; b < b1; b += kWaves) {
+            const Place next = place_at(a.c, t.seq, min(b + kWaves, b1 - 1), head);
+            float s[S::kScores];
+            codes.scores(q, s);
+            codes.fetch_keys(block_codes(next), lane);
+            const int t0 = b * kBlock;
+            half8 p[S::kSteps];
+            const bool masked = now.absent || t0 + kBlock > v.each_to || t0 < v.each_from;
+            uint32_t seen = 0xFFFFu;
+            if (masked) seen = seen_bits<D, C>(t0, g, c.from, now.absent ? 0 : c.to);
+            st.probabilities(s, factor * now.scale_k, now.scale_v, seen, masked, p);
+            if (now.absent || t0 + kBlock > v.keys) codes.keep_values(g, now.absent ? 0 : v.keys - t0);
+            codes.add_values(p, st.o);
+            codes.fetch_values(block_codes(next), lane);
+            now = next;
+        }
+        const float l = S::over_groups(st.l, true);
 
         // join the four waves: each output over the sum of all, weighted by its maximum
-        other[0][wave * kColumns + col] = st.m;
-        other[1][wave * kColumns + col] = l;
+        other[0][wave * C + col] = st.m;
+        other[1][wave * C + col] = l;
         __syncthreads();
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, other[0][w * kColumns + col]);
+        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, other[0][w * C + col]);
         const auto weight = [&](float m) { return m == top ? 1.f : exp2_fast(m - top); };
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) sum += other[1][w * kColumns + col] * weight(other[0][w * kColumns + col]);
+        for (int w = 0; w < kWaves; ++w) sum += other[1][w * C + col] * weight(other[0][w * C + col]);
         // sums are positive unless nothing was seen; NaN passes through
-        const float share = l == 0.f ? 0.f : weight(st.m) / sum;
+        const float part_share = l == 0.f ? 0.f : weight(st.m) / sum;
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+        for (int j = 0; j < S::kTiles; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) st.o[j][r] = l == 0.f ? 0.f : ldexpf(st.o[j][r] * share, st.lift);
+            for (int r = 0; r < S::kPerTile; ++r) st.o[j][r] = l == 0.f ? 0.f : ldexpf(st.o[j][r] * part_share, st.lift);
 #pragma unroll
         for (int round = kWaves / 2; round; round >>= 1) {
-            float* mail = pass + (wave & (round - 1)) * (D / 2) * 64;
+            float* mail = pass + (wave & (round - 1)) * R * 64;
             if (wave >= round && wave < 2 * round) {
 #pragma unroll
-                for (int j = 0; j < J; ++j)
+                for (int j = 0; j < S::kTiles; ++j)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) mail[(j * 16 + r) * 64 + lane] = st.o[j][r];
+                    for (int r = 0; r < S::kPerTile; ++r) mail[(j * S::kPerTile + r) * 64 + lane] = st.o[j][r];
             }
             __syncthreads();
             if (wave < round) {
 #pragma unroll
-                for (int j = 0; j < J; ++j)
+                for (int j = 0; j < S::kTiles; ++j)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) st.o[j][r] += mail[(j * 16 + r) * 64 + lane];
+                    for (int r = 0; r < S::kPerTile; ++r) st.o[j][r] += mail[(j * S::kPerTile + r) * 64 + lane];
             }
-            __syncthreads();
+            if (!DIRECT || round > 1) __syncthreads();
         }
         if (wave == 0 && col < t.columns) {
-            if (whole) {
-                uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)(t.s.row + i) * a.q_heads + (int64_t)head * a.group + g) * D;
+            uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)c.row * a.q_heads + (int64_t)head * a.group + c.head) * D;
+            float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan.parts) +
+                          (blockIdx.x * 2 + (opening ? 0 : 1)) * part_floats(D, C);
 #pragma unroll
-                for (int j = 0; j < J; ++j)
+            for (int j = 0; j < S::kTiles; ++j)
 #pragma unroll
-                    for (int r = 0; r < 16; r += 4) {
+                for (int r = 0; r < S::kPerTile; r += 4) {
+                    const int d = S::output(g, j, r);
+                    if (DIRECT || whole) {
                         union { __bf16 b[4]; uint2 w; } u;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) u.b[e] = (__bf16)st.o[j][r + e];
-                        *reinterpret_cast<uint2*>(out + 32 * j + 2 * r + 4 * h) = u.w;
+                        *reinterpret_cast<uint2*>(out + d) = u.w;
+                    } else {
+                        *reinterpret_cast<float4v*>(part + col * D + d) = (float4v){st.o[j][r], st.o[j][r + 1], st.o[j][r + 2], st.o[j][r + 3]};
                     }
-            } else {
-                float* part = static_cast<float*>(a.workspace) + plan.parts + (blockIdx.x * 2 + (opening ? 0 : 1)) * part_floats(D);
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; r += 4)
-                        *reinterpret_cast<float4v*>(part + col * D + 32 * j + 2 * r + 4 * h) =
-                            (float4v){st.o[j][r], st.o[j][r + 1], st.o[j][r + 2], st.o[j][r + 3]};
-                if (h == 0) {
-                    part[kColumns * D + col] = top;
-                    part[kColumns * (D + 1) + col] = sum;
                 }
+            if (!DIRECT && !whole && g == 0) {
+                part[C * D + col] = top;
+                part[C * (D + 1) + col] = sum;
             }
         }
-        at += take;
+        if constexpr (DIRECT) {
+            break;
+        } else {
+            if (!whole && skip == 0 && threadIdx.x == 0) {             // the row begins here and goes on
+                Open* open = reinterpret_cast<Open*>(static_cast<char*>(a.workspace) + plan.opens);
+                open[blockIdx.x] = {row_begin, share.per, t.seq, t.f0, t.columns, head, (int)((row_begin + units - 1) / share.per), 0};
+            }
+            share.at += take;
+            row_begin += units;
+            ++tile;
+            opening = false;
+        }
+    }
+}
+
+// Joins the parts of the row that workgroup blockIdx.x began and others went
+// on with, one column a workgroup: parts' weights in LDS first, then D / 4 threads for each of
+// several parts at a time.
+template <int D, int C> __global__ __launch_bounds__(kThreads) void k_join(AttendArgs a, Plan plan) {
+    constexpr int Q = D / 4, P = kThreads / Q;         // threads of a part, parts at a time
+    __shared__ float weights[kThreads], reduced[2][kWaves];
+    __shared__ float4v sums[P][Q];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = blockIdx.y;
+    const Open open = reinterpret_cast<const Open*>(static_cast<const char*>(a.workspace) + plan.opens)[blockIdx.x];
+    if (col >= open.columns) return;
+    const float* parts = reinterpret_cast<const float*>(static_cast<const char*>(a.workspace) + plan.parts);
+    const int many = open.last - (int)blockIdx.x + 1;
+    const auto part_of = [&](int k) {
+        const int64_t w = blockIdx.x + k;
+        return parts + (w * 2 + (w * open.per < open.begin ? 1 : 0)) * part_floats(D, C);
+    };
+    const int p = threadIdx.x / Q, x = threadIdx.x % Q;
+    float top = -INFINITY, total = 0.f;
+    float4v sum = 0.f;
+    for (int base = 0; base < many; base += kThreads) {                // one round up to 256 parts
+        const int n = min(many - base, kThreads);
+        float m = -INFINITY, l = 0.f;
+        if (threadIdx.x < n) {
+            const float* q = part_of(base + threadIdx.x);
+            m = q[C * D + col];
+            l = q[C * (D + 1) + col];
+        }
+        float now = m;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) now = fmaxf(now, __shfl_xor(now, d));
+        if (lane == 0) reduced[0][wave] = now;
+        __syncthreads();
+        now = fmaxf(top, fmaxf(fmaxf(reduced[0][0], reduced[0][1]), fmaxf(reduced[0][2], reduced[0][3])));
+        const float weight = l == 0.f ? 0.f : (m == now ? 1.f : exp2_fast(m - now)) * l;       // 0: nothing seen there
+        weights[threadIdx.x] = weight;
+        float added = weight;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) added += __shfl_xor(added, d);
+        if (lane == 0) reduced[1][wave] = added;
+        __syncthreads();
+        const float alpha = now == top ? 1.f : exp2_fast(top - now);
+        top = now;
+        total = total * alpha + (reduced[1][0] + reduced[1][1] + reduced[1][2] + reduced[1][3]);
+        sum *= alpha;
+        if (p < P) {
+#pragma unroll 8
+            for (int k = p; k < n; k += P) {
+                const float w = weights[k];
+                const float4v o = *reinterpret_cast<const float4v*>(part_of(base + k) + col * D + 4 * x);
+                sum += w == 0.f ? (float4v)0.f : o * w;
+            }
+        }
+        __syncthreads();
+    }
+    if (p < P) sums[p][x] = sum;
+    __syncthreads();
+    if (p != 0) return;
+#pragma unroll
+    for (int k = 1; k < P; ++k) sum += sums[k][x];
+    const int f = open.f0 + col, i = f / a.group, gh = f - i * a.group, row = span_of(a.c, open.seq).row + i;
+    uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)row * a.q_heads + (int64_t)open.head * a.group + gh) * D;
+    union { __bf16 b[4]; uint2 w; } u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u.b[e] = (__bf16)(total == 0.f ? 0.f : sum[e] / total);
+    *reinterpret_cast<uint2*>(out + 4 * x) = u.w;
+}
+
+// ---- many columns: the work is products ----------------------------------------------------
+// A workgroup takes 4 * 32 * T columns.  Its waves turn two blocks' codes into
+// FP16 once, in LDS and in the order in which the matrix cores take them, with the
+// next two's codes in flight; every fragment read from there serves T products.
+constexpr int kLeastManyShare = 16;      // blocks of a workgroup, at least
+
+constexpr int many_tiles(int dim) { return dim <= 192 ? 2 : 1; }       // T: what the registers of a wave hold
+constexpr int many_columns(int dim) { return kWaves * 32 * many_tiles(dim); }
+
+template <int D, int FMT> __global__ __launch_bounds__(kThreads, 1) void k_many(AttendArgs a, Plan plan) {
+    using S = Shape<D, 32>;
+    constexpr int T = many_tiles(D), C = many_columns(D), J = D / 32, F = D / 16, N = (2 * J + kWaves - 1) / kWaves;
+    __shared__ half8 stage[2][2][2][F][64];            // [buffer][block][keys, values][fragment][lane]
+    const int lane = threadIdx.x & 63, wave = one(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
+    Open* open = reinterpret_cast<Open*>(static_cast<char*>(a.workspace) + plan.opens);
+    // workgroups of one XCD, every eighth, take neighbouring shares: of few key heads, whose codes then stay in its L2
+    const int worker = (blockIdx.x % 8) * (plan.workers / 8) + blockIdx.x / 8;
+    Share share = share_of(worker, plan.workers, a.c.heads, plan.slots, kLeastManyShare, [&](int64_t e) -> int64_t {
+        Tile t;
+        if (!tile_of(a, C, e, &t) || !takes(a, plan.kind, t.s)) return 0;
+        return max(view_of(a, t).blocks, 1);
+    });
+    if (threadIdx.x == 0) open[worker].columns = 0;
+    if (share.at >= share.end) return;
+    int64_t slot = share.entry, row_begin = share.entry_begin;         // a slot is one row
+    int head = one(share.head);
+    bool opening = true;
+
+    while (share.at < share.end) {
+        Tile t;
+        if (slot >= plan.slots) {
+            slot = 0;
+            if (++head >= a.c.heads) break;            // starts out of order: rows were not all found again
+        }
+        const bool some = tile_of(a, C, slot, &t);
+        t = one(t);
+        if (!some || !takes(a, plan.kind, t.s)) {      // on to the next sequence's first slot
+            slot = t.seq + 1 < a.c.batch ? max(slot + 1, (int64_t)max(a.c.starts[t.seq + 1], 0) * a.group / C + t.seq + 1) : (int64_t)plan.slots;
+            continue;
+        }
+        const View v = view_of(a, t);
+        const int units = max(v.blocks, 1), skip = one((int)min(max(share.at - row_begin, (int64_t)0), (int64_t)units));
+        const int take = one((int)min((int64_t)(units - skip), share.end - share.at));
+        const bool whole = take == units;
+        const int b0 = v.block + min(skip, v.blocks), b1 = v.block + min(skip + take, v.blocks);
+
+        // the wave's columns
+        const int c0 = wave * 32 * T;
+        Tile mine = t;
+        mine.f0 += c0;
+        mine.columns = min(t.columns - c0, 32 * T);
+        View w = {};
+        if (mine.columns > 0) w = view_of(a, mine);
+        Column c[T];
+        half8 q[T][F];
+        float factor[T];
+        State<D, 32> st[T];
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            c[k] = column_of(a, t, v, c0 + 32 * k + col);
+            factor[k] = load_query<D, 32>(
+                a.scale, static_cast<const uint16_t*>(a.q) + c[k].row * a.ld_token + ((int64_t)head * a.group + c[k].head) * a.ld_head, h, q[k]);
+            st[k].clear();
+        }
+
+        uint4 kc[N], vc[N];
+        Place now[2], next[2];
+        const auto places = [&](int b, Place* p) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) p[k] = place_at(a.c, t.seq, min(b + k, b1 - 1), head);
+        };
+        const auto fetch = [&](const Place* p) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int it = wave + kWaves * n, k = it >= J, j = it - k * J;
+                if (2 * J % kWaves == 0 || it < 2 * J) {
+                    const uint4* codes = reinterpret_cast<const uint4*>(a.c.codes + p[k].at * (2 * kBlock * (int64_t)D));
+                    kc[n] = codes[(2 * j + h) * 32 + col];
+                    vc[n] = codes[2 * D + (32 * j + col) * 2 + h];
+                }
+            }
+        };
+        const auto fill = [&](int buffer, int b, const Place* p) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int it = wave + kWaves * n, k = it >= J, j = it - k * J;
+                if (2 * J % kWaves == 0 || it < 2 * J) {
+                    stage[buffer][k][0][2 * j][lane] = expand8<FMT>(kc[n].x, kc[n].y);
+                    stage[buffer][k][0][2 * j + 1][lane] = expand8<FMT>(kc[n].z, kc[n].w);
+                    const int keep = p[k].absent ? 0 : v.keys - (b + k) * kBlock;
+                    if (keep < kBlock) {               // what is no token's may be anything: zeros
+                        uint32_t* x = reinterpret_cast<uint32_t*>(&vc[n]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int m = keep - S::token(h, 4 * i);
+                            x[i] &= m <= 0 ? 0u : m >= 4 ? 0xFFFFFFFFu : (1u << (8 * m)) - 1u;
+                        }
+                    }
+                    stage[buffer][k][1][2 * j][lane] = expand8<FMT>(vc[n].x, vc[n].y);
+                    stage[buffer][k][1][2 * j + 1][lane] = expand8<FMT>(vc[n].z, vc[n].w);
+                }
+            }
+        };
+        if (b0 < b1) {
+            places(b0, now);
+            fetch(now);
+            fill(0, b0, now);
+            places(b0 + 2, next);
+            fetch(next);
+            __syncthreads();
+            int buffer = 0;
+            for (int b = b0; b < b1; b += 2) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int t0 = (b + k) * kBlock;
+                    if (b + k >= b1 || t0 >= w.all_to || t0 + kBlock <= w.all_from) continue;
+                    float16v x[T];
+#pragma unroll
+                    for (int u = 0; u < T; ++u) x[u] = 0.f;
+#pragma unroll
+                    for (int f = 0; f < F; ++f) {
+                        const half8 y = stage[buffer][k][0][f][lane];
+#pragma unroll
+                        for (int u = 0; u < T; ++u) x[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y, q[u][f], x[u], 0, 0, 0);
+                    }
+                    const bool masked = now[k].absent || t0 + kBlock > w.each_to || t0 < w.each_from;
+                    half8 p[T][2];
+#pragma unroll
+                    for (int u = 0; u < T; ++u) {
+                        uint32_t seen = 0xFFFFu;
+                        if (masked) seen = seen_bits<D, 32>(t0, h, c[u].from, now[k].absent ? 0 : c[u].to);
+                        float s[16];
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) s[r] = x[u][r];
+                        st[u].probabilities(s, factor[u] * now[k].scale_k, now[k].scale_v, seen, masked, p[u]);
+                    }
+#pragma unroll
+                    for (int f = 0; f < F; ++f) {
+                        const half8 y = stage[buffer][k][1][f][lane];
+#pragma unroll
+                        for (int u = 0; u < T; ++u)
+                            st[u].o[f >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y, p[u][f & 1], st[u].o[f >> 1], 0, 0, 0);
+                    }
+                }
+                if (b + 2 < b1) {
+                    fill(buffer ^ 1, b + 2, next);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) now[k] = next[k];
+                    places(b + 4, next);
+                    fetch(next);
+                }
+                __syncthreads();
+                buffer ^= 1;
+            }
+        }
+
+#pragma unroll
+        for (int u = 0; u < T; ++u) {
+            const float l = S::over_groups(st[u].l, true);
+            const int column = c0 + 32 * u + col;
+            if (column >= t.columns) continue;
+            const float over = l == 0.f ? 0.f : 1.f / l;               // nothing seen: zeros
+            uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)c[u].row * a.q_heads + (int64_t)head * a.group + c[u].head) * D;
+            float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan.parts) + (worker * 2 + (opening ? 0 : 1)) * part_floats(D, C);
+#pragma unroll
+            for (int j = 0; j < S::kTiles; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4) {
+                    const int d = S::output(h, j, r);
+                    float x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = l == 0.f ? 0.f : ldexpf(st[u].o[j][r + e] * over, st[u].lift);
+                    if (whole) {
+                        union { __bf16 b[4]; uint2 w; } y;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y.b[e] = (__bf16)x[e];
+                        *reinterpret_cast<uint2*>(out + d) = y.w;
+                    } else {
+                        *reinterpret_cast<float4v*>(part + column * D + d) = (float4v){x[0], x[1], x[2], x[3]};
+                    }
+                }
+            if (!whole && h == 0) {
+                part[C * D + column] = st[u].m;
+                part[C * (D + 1) + column] = l;
+            }
+        }
+        if (!whole && skip == 0 && threadIdx.x == 0)   // the row begins here and goes on
+            open[worker] = {row_begin, share.per, t.seq, t.f0, t.columns, head, (int)((row_begin + units - 1) / share.per), 0};
+        share.at += take;
+        row_begin += units;
+        ++slot;
         opening = false;
     }
 }
 
-// Joins the parts of rows that several workgroups had a share of: a wave for
-// each column, its lanes the parts for the weights and the elements for the sums.
-template <int D> __global__ __launch_bounds__(kThreads) void k_join(AttendArgs a, Plan plan) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, head = blockIdx.y, col = blockIdx.z * kWaves + wave;
-    const int64_t* header = static_cast<const int64_t*>(a.workspace);
-    const int64_t per = header[0], slot = blockIdx.x, units = header[2 + slot] - header[1 + slot];
-    if (units == 0) return;
-    const int64_t u0 = header[1 + slot] * a.c.heads + head * units, u1 = u0 + units;
-    const int64_t w0 = u0 / per, w1 = (u1 - 1) / per;
-    if (w0 == w1) return;                              // one workgroup had it all and wrote it
-    Tile t;
-    if (!tile_of(a, slot, &t) || col >= t.columns) return;
-    const float* parts = static_cast<const float*>(a.workspace) + plan.parts;
-    const auto part_of = [&](int64_t w) { return parts + (w * 2 + (w * per < u0 ? 1 : 0)) * part_floats(D); };
-    float top = -INFINITY;
-    for (int64_t w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, part_of(w)[kColumns * D + col]);
-#pragma unroll
-    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-    constexpr int E = (D + 63) / 64;
-    float total = 0.f, sum[E] = {};
-    for (int64_t base = w0; base <= w1; base += 64) {
-        const int n = (int)min((int64_t)64, w1 + 1 - base);
-        float mine = 0.f;
-        if (lane < n) {
-            const float* p = part_of(base + lane);
-            const float m = p[kColumns * D + col], l = p[kColumns * (D + 1) + col];
-            mine = l == 0.f ? 0.f : (m == top ? 1.f : exp2_fast(m - top)) * l;        // 0: nothing seen there
-        }
-        for (int k = 0; k < n; ++k) {
-            const float w = __shfl(mine, k);
-            total += w;
-            const float* p = part_of(base + k) + col * D;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (D % 64 == 0 || e * 64 + lane < D) sum[e] += w * p[e * 64 + lane];
-        }
+// Joins the parts of a row of many columns: D / 4 threads for each of several columns.
+template <int D> __global__ __launch_bounds__(kThreads) void k_join_many(AttendArgs a, Plan plan) {
+    constexpr int Q = D / 4, P = kThreads / Q, C = many_columns(D);
+    const Open open = reinterpret_cast<const Open*>(static_cast<const char*>(a.workspace) + plan.opens)[blockIdx.x];
+    const int x = threadIdx.x % Q, lane_column = threadIdx.x / Q, col = blockIdx.y * P + lane_column;
+    if (lane_column >= P || col >= open.columns) return;
+    const float* parts = reinterpret_cast<const float*>(static_cast<const char*>(a.workspace) + plan.parts);
+    const int many = open.last - (int)blockIdx.x + 1;
+    const auto part_of = [&](int k) {
+        const int64_t w = blockIdx.x + k;
+        return parts + (w * 2 + (w * open.per < open.begin ? 1 : 0)) * part_floats(D, C);
+    };
+    float top = -INFINITY, total = 0.f;
+    for (int k = 0; k < many; ++k) top = fmaxf(top, part_of(k)[C * D + col]);
+    float4v sum = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < many; ++k) {
+        const float* p = part_of(k);
+        const float m = p[C * D + col], l = p[C * (D + 1) + col];
+        const float w = l == 0.f ? 0.f : (m == top ? 1.f : exp2_fast(m - top)) * l;            // 0: nothing seen there
+        const float4v o = *reinterpret_cast<const float4v*>(p + col * D + 4 * x);
+        total += w;
+        sum += w == 0.f ? (float4v)0.f : o * w;
     }
-    const int f = t.f0 + col, i = f / a.group, g = f - i * a.group;
-    uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)(t.s.row + i) * a.q_heads + (int64_t)head * a.group + g) * D;
+    const int f = open.f0 + col, i = f / a.group, gh = f - i * a.group, row = span_of(a.c, open.seq).row + i;
+    uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)row * a.q_heads + (int64_t)open.head * a.group + gh) * D;
+    union { __bf16 b[4]; uint2 w; } u;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (D % 64 == 0 || e * 64 + lane < D)
-            out[e * 64 + lane] = __builtin_bit_cast(uint16_t, (__bf16)(total == 0.f ? 0.f : sum[e] / total));
+    for (int e = 0; e < 4; ++e) u.b[e] = (__bf16)(total == 0.f ? 0.f : sum[e] / total);
+    *reinterpret_cast<uint2*>(out + 4 * x) = u.w;
 }
 
-Plan plan_of(const AttendArgs& a) {
-    Plan p;
-    p.slots = tile_slots(a);
-    p.workers = a.c.dim <= 128 ? 512 : 256;            // what the GPU holds at once: two or one on a CU
-    p.parts = ((p.slots + 2) * 2 + 63) / 64 * 64;
+// ---- launches ----------------------------------------------------------------------------
+// 16 columns to a wave where that holds a sequence's columns: half the work
+// on them, and room for twice as many waves.
+int few_columns(const AttendArgs& a) {
+    const int64_t columns = a.c.starts ? (int64_t)a.c.tokens * a.group / (a.c.batch > 0 ? a.c.batch : 1) : a.group;
+    return columns <= 16 ? 16 : 32;
+}
+
+// A row of this many blocks is not worth sharing: its workgroup takes it whole,
+// without a search for its share and without the join's launch.
+constexpr int64_t kDirectBlocks = 32;
+bool direct(const AttendArgs& a) { return ((int64_t)a.c.width << a.c.shift) <= kDirectBlocks; }
+
+struct Plans {
+    Plan few, many;
+    size_t bytes;
+};
+
+Plans plans_of(const AttendArgs& a) {
+    Plans p = {};
+    const int64_t rows = (int64_t)a.c.tokens * a.group;
+    int64_t at = 0;
+    const auto room = [&](int64_t bytes) { const int64_t here = at; at += (bytes + 255) / 256 * 256; return here; };
+    // which kernels some sequence may be for; of one sequence the host knows nothing better than that it has all rows
+    const bool many = a.c.starts && rows > kFewColumns, few = !many || a.c.batch > 1;
+    if (few) {
+        const int columns = few_columns(a);
+        p.few.kind = many ? kFew : kAny;
+        p.few.workers = 256 * few_waves(a.c.dim, columns);             // what the GPU holds at once
+        if (!direct(a)) {
+            p.few.opens = room(p.few.workers * (int64_t)sizeof(Open));
+            p.few.parts = room(p.few.workers * 2 * part_floats(a.c.dim, columns) * (int64_t)sizeof(float));
+        }
+    }
+    if (many) {
+        p.many.kind = few ? kMany : kAny;
+        p.many.workers = 256;                          // one on a CU
+        p.many.slots = (int)tile_slots(a, many_columns(a.c.dim));
+        p.many.opens = room(p.many.workers * (int64_t)sizeof(Open));
+        p.many.parts = room(p.many.workers * 2 * part_floats(a.c.dim, many_columns(a.c.dim)) * (int64_t)sizeof(float));
+    }
+    p.bytes = (size_t)at;
     return p;
 }
 
-template <int D> hipError_t launch(const AttendArgs& a, hipStream_t stream) {
-    const Plan p = plan_of(a);
-    if (a.c.fmt) k_few<D, 1><<<p.workers, kThreads, 0, stream>>>(a, p);
-    else k_few<D, 0><<<p.workers, kThreads, 0, stream>>>(a, p);
-    k_join<D><<<dim3((unsigned)p.slots, (unsigned)a.c.heads, kColumns / kWaves), kThreads, 0, stream>>>(a, p);
+template <int D, int FMT, int C> void launch_few(const AttendArgs& a, const Plan& p, hipStream_t stream) {
+    if (direct(a)) {
+        const int64_t rows = (int64_t)a.c.batch * (a.c.starts ? kFewColumns / C : (a.group + C - 1) / C);
+        k_few<D, FMT, C, true><<<dim3((unsigned)rows, (unsigned)a.c.heads), kThreads, 0, stream>>>(a, p);
+        return;
+    }
+    k_few<D, FMT, C, false><<<p.workers, kThreads, 0, stream>>>(a, p);
+    k_join<D, C><<<dim3(p.workers, a.c.starts || a.group > C ? C : a.group), kThreads, 0, stream>>>(a, p);
+}
+
+template <int D, int FMT> hipError_t launch(const AttendArgs& a, hipStream_t stream) {
+    const Plans p = plans_of(a);
+    if (p.few.workers) {
+        if (few_columns(a) == 16) launch_few<D, FMT, 16>(a, p.few, stream);
+        else launch_few<D, FMT, 32>(a, p.few, stream);
+    }
+    if (p.many.workers) {
+        constexpr int P = kThreads / (D / 4);
+        k_many<D, FMT><<<p.many.workers, kThreads, 0, stream>>>(a, p.many);
+        k_join_many<D><<<dim3(p.many.workers, (many_columns(D) + P - 1) / P), kThreads, 0, stream>>>(a, p.many);
+    }
     return hipGetLastError();
+}
+
+template <int D> hipError_t launch(const AttendArgs& a, hipStream_t stream) {
+    return a.c.fmt ? launch<D, 1>(a, stream) : launch<D, 0>(a, stream);
 }
 
 }  // namespace
 
-size_t attend_workspace_bytes(const AttendArgs& a) {
-    const Plan p = plan_of(a);
-    return (size_t)(p.parts + p.workers * 2 * part_floats(a.c.dim)) * sizeof(float);
-}
+size_t attend_workspace_bytes(const AttendArgs& a) { return plans_of(a).bytes; }
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     switch (a.c.dim) {

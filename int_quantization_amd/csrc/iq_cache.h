@@ -95,14 +95,12 @@ template <int FMT> __device__ __forceinline__ uint32_t code_of(float y) {
     else return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, y, 0, false) & 0xFFu;
 }
 
-// ---- attention: 32 columns ----------------------------------------------------------
+// ---- attention: tiles of columns ------------------------------------------------------
 // The columns of a sequence and key head are its (token, query head of that
-// head) pairs in order.  Sequence s has the slots from floor(starts[s] * group
-// / 32) + s on, never fewer than the tiles of 32 columns that it needs.
-constexpr int kColumns = 32;
-
-__host__ __device__ inline int64_t tile_slots(const AttendArgs& a) {
-    return a.c.starts ? (int64_t)a.c.tokens * a.group / kColumns + a.c.batch : (int64_t)a.c.batch * ((a.group + kColumns - 1) / kColumns);
+// head) pairs in order.  With tiles of `unit` columns sequence s has the slots from floor(starts[s] * group
+// / unit) + s on, never fewer than the tiles that it needs.
+__host__ __device__ inline int64_t tile_slots(const AttendArgs& a, int unit) {
+    return a.c.starts ? (int64_t)a.c.tokens * a.group / unit + a.c.batch : (int64_t)a.c.batch * ((a.group + unit - 1) / unit);
 }
 
 struct Tile {
@@ -110,20 +108,20 @@ struct Tile {
     Span s;
 };
 
-__host__ __device__ inline bool tile_of(const AttendArgs& a, int64_t slot, Tile* t) {
-    const int per = (a.group + kColumns - 1) / kColumns;
+__host__ __device__ inline bool tile_of(const AttendArgs& a, int unit, int64_t slot, Tile* t) {
+    const int per = (a.group + unit - 1) / unit;
     int64_t index;
     if (a.c.starts) {
-        t->seq = sequence_of(a.c, slot, a.group, kColumns, 1);
-        index = slot - ((int64_t)max(a.c.starts[t->seq], 0) * a.group / kColumns + t->seq);
+        t->seq = sequence_of(a.c, slot, a.group, unit, 1);
+        index = slot - ((int64_t)max(a.c.starts[t->seq], 0) * a.group / unit + t->seq);
     } else {
         t->seq = (int)(slot / per);
         index = slot % per;
     }
     t->s = span_of(a.c, t->seq);
-    const int64_t left = (int64_t)t->s.n * a.group - index * kColumns;
-    t->f0 = (int)(index * kColumns);
-    t->columns = (int)(left < kColumns ? left : kColumns);
+    const int64_t left = (int64_t)t->s.n * a.group - index * unit;
+    t->f0 = (int)(index * unit);
+    t->columns = (int)(left < unit ? left : unit);
     return index >= 0 && left > 0;
 }
 

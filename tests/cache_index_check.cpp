@@ -71,13 +71,14 @@ static void run(bool sound, bool with_starts) {
     AttendArgs a = {};
     a.c = c;
     a.group = (int)pick(0, 2) ? (int)pick(1, 9) : (int)pick(10, 70);
+    const int unit = 1 << pick(3, 8);
     std::vector<int> answered((size_t)c.tokens * a.group);
-    for (int64_t slot = 0; slot < tile_slots(a); ++slot) {
+    for (int64_t slot = 0; slot < tile_slots(a, unit); ++slot) {
         Tile t;
-        const bool some = tile_of(a, slot, &t);
+        const bool some = tile_of(a, unit, slot, &t);
         EXPECT(t.seq >= 0 && t.seq < c.batch);
         if (!some) continue;
-        EXPECT(t.columns >= 1 && t.columns <= kColumns && t.f0 >= 0);
+        EXPECT(t.columns >= 1 && t.columns <= unit && t.f0 >= 0);
         for (int col = 0; col < t.columns; ++col) {
             const int64_t row = t.s.row + (t.f0 + col) / a.group;
             EXPECT(row >= 0 && row < c.tokens);
