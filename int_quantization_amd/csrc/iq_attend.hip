@@ -52,8 +52,8 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // from 2^-23 on and steps of 2^-33 below.  The factor leaves with the division by their sum.
 constexpr float kSlack = 6.f, kLift = 9.f;
 
-// The block's values scale enters the exponent, as a fraction of the largest
-// so far, 2^lift; a fraction below 2^-60 counts as 2^-60, where values are 2^-50 of
+// The block's values scale enters the exponent, as a fraction of the power of
+// two above the largest so far; a fraction below 2^-60 counts as 2^-60, where values are 2^-50 of
 // what the row holds already.
 constexpr float kLeastFraction = 0x1p-60f;
 
@@ -230,7 +230,8 @@ template <int D, int C> __device__ __forceinline__ float load_query(float scale,
             const uint32_t w = reinterpret_cast<const uint32_t*>(&raw[f])[k >> 1];
             q[f][k] = (_Float16)ldexpf(__uint_as_float(k & 1 ? w & 0xFFFF0000u : w << 16), -e);
         }
-    return ldexpf(scale * 1.44269504f, e);
+    // a query that is not finite answers NaN, whatever it sees
+    return top >= 0x7F800000u ? __builtin_nanf("") : ldexpf(scale * 1.44269504f, e);
 }
 
 // Running state of a column: maximum, sum of this lane's tokens, output.
@@ -238,67 +239,64 @@ template <int D, int C> struct State {
     using S = Shape<D, C>;
     typename S::Tile o[S::kTiles];
     float m, l;
-    int lift;                    // values' scales are held over 2^lift, the largest so far
+    int size;                    // values' scales are held over this power of two (its bits), above the largest so far
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int j = 0; j < S::kTiles; ++j) o[j] = 0.f;
         m = -INFINITY;
         l = 0.f;
-        lift = -126;
+        size = 1 << 23;
     }
-    __device__ __forceinline__ void scale(float by) {
+    // The largest of the lane's scores, as an exponent of 2.
+    static __device__ __forceinline__ float top_of(const float* s, float fk) {
+        float top = s[0];
+#pragma unroll
+        for (int r = 1; r < S::kScores; ++r) top = fmaxf(top, s[r]);
+        return top * fk;
+    }
+    // Whether the maximum or the size is behind the block's.  Scales compare as integers; those that are not finite and positive are not looked at.
+    __device__ __forceinline__ bool behind(float top, int scale_v) const { return __any(top > m + kSlack) || (scale_v > size && scale_v < 0x7F800000); }
+    // Brings both up to the block's.  Rare.
+    __device__ __forceinline__ void catch_up(float top, int scale_v) {
+        top = S::over_groups(top, false);
+        const float now = fmaxf(m, top), alpha = now == m ? 1.f : exp2_fast(m - now);
+        m = now;
+        l *= alpha;
+        const int up = scale_v > size && scale_v < 0x7F800000 ? min((scale_v >> 23) + 1, 253) << 23 : size;
+        const float by = alpha * __uint_as_float(size) * __uint_as_float((254 << 23) - up);
+        size = up;
 #pragma unroll
         for (int j = 0; j < S::kTiles; ++j) o[j] *= by;
     }
-    // From scores to probabilities p, in the second product's order.  seen: bit r for score r.
-    __device__ __forceinline__ void probabilities(const float* s, float fk, float scale_v, uint32_t seen, bool masked, half8* p) {
-        float top = -INFINITY;
-        if (!masked) {
-#pragma unroll
-            for (int r = 0; r < S::kScores; ++r) top = fmaxf(top, s[r]);
-        } else {
-#pragma unroll
-            for (int r = 0; r < S::kScores; ++r) top = (seen >> r) & 1 ? fmaxf(top, s[r]) : top;
-        }
-        top = top == -INFINITY ? top : top * fk;
-        if (__any(top > m + kSlack)) {
-            top = S::over_groups(top, false);
-            const float now = fmaxf(m, top), alpha = now == m ? 1.f : exp2_fast(m - now);
-            m = now;
-            l *= alpha;
-            scale(alpha);
-        }
-        if (scale_v > ldexpf(1.f, lift)) {             // the same for the whole wave
-            int e;
-            frexpf(scale_v, &e);
-            scale(ldexpf(1.f, max(lift - e, -200)));
-            lift = e;
-        }
-        const float fraction = fmaxf(ldexpf(scale_v, -lift), kLeastFraction);
-        const float off = kLift + __builtin_amdgcn_logf(fraction) - m;
+    // From scores to probabilities p, in the second product's order.
+    __device__ __forceinline__ void probabilities(const float* s, float fk, float scale_v, half8* p) {
+        const float fraction = fmaxf(scale_v * __uint_as_float((254 << 23) - size), kLeastFraction);
+        const float off = kLift + __builtin_amdgcn_logf(fraction) - fmaxf(m, -1e37f);      // m is -inf until a token is seen
         float sum = 0.f;
 #pragma unroll
         for (int r = 0; r < S::kScores; ++r) {
-            float e = exp2_fast(__builtin_fmaf(s[r], fk, off));
-            if (masked) e = (seen >> r) & 1 ? e : 0.f;
+            const float e = exp2_fast(__builtin_fmaf(s[r], fk, off));
             sum += e;
             p[r >> 3][r & 7] = (_Float16)e;
         }
-        l = __builtin_fmaf(sum, 1.f / fraction, l);
+        l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(fraction), l);
     }
+    // The output's registers over a sum of probabilities; a power of two at a time, since sizes may be anything.
+    __device__ __forceinline__ float value(float x, float by) const { return x * by * __uint_as_float(size); }
 };
 
-// Bits of the scores of lane group g whose tokens lie in [from, to); the block's token 0 is t0.
-template <int D, int C> __device__ __forceinline__ uint32_t seen_bits(int t0, int g, int from, int to) {
-    uint32_t seen = 0;
+// Scores of lane group g whose tokens lie outside [from, to) become -inf; the block's token 0 is t0.
+template <int D, int C> __device__ __forceinline__ void hide(float* s, int t0, int g, int from, int to) {
 #pragma unroll
     for (int r = 0; r < Shape<D, C>::kScores; ++r) {
         const int token = t0 + Shape<D, C>::token(g, r);
-        seen |= (token >= from && token < to ? 1u : 0u) << r;
+        s[r] = token >= from && token < to ? s[r] : -INFINITY;
     }
-    return seen;
 }
+
+// The factor of a block's scores: positive, so that hidden ones stay -inf.
+__device__ __forceinline__ float positive(float fk) { return fk < 1e-30f ? 1e-30f : fk; }
 
 // Values that a wave's lanes share, in scalar registers.
 __device__ __forceinline__ int one(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -327,8 +325,9 @@ __device__ __forceinline__ Place place_at(const CacheArgs& c, int seq, int b, in
     const int64_t page = scalar_load(c.page_table, (int64_t)seq * c.width + (b >> c.shift));
     p.absent = page < 0 || page >= c.pages;
     p.at = p.absent ? 0 : ((page * c.heads + head) << c.shift) | (b & ((1 << c.shift) - 1));
-    p.scale_k = scalar_load(c.scales, p.at * 2);
-    p.scale_v = scalar_load(c.scales, p.at * 2 + 1);
+    const float k = scalar_load(c.scales, p.at * 2), v = scalar_load(c.scales, p.at * 2 + 1);
+    p.scale_k = p.absent ? 1.f : k;
+    p.scale_v = p.absent ? 0.f : v;
     return p;
 }
 
@@ -441,7 +440,9 @@ __device__ __forceinline__ Column column_of(const AttendArgs& a, const Tile& t, 
 constexpr int kLeastShare = 8;   // blocks of a workgroup, at least
 
 // Waves of a SIMD, and so workgroups of a CU.
-constexpr int few_waves(int dim, int columns) { return columns == 16 ? (dim <= 128 ? 4 : 2) : dim <= 128 ? 2 : 1; }
+constexpr int few_waves(int dim, int columns) {
+    return columns == 16 ? (dim <= 64 ? 5 : dim <= 128 ? 4 : dim <= 192 ? 3 : 2) : dim <= 64 ? 4 : dim <= 96 ? 3 : dim <= 128 ? 2 : 1;
+}
 
 __device__ __forceinline__ Tile tile_at(const AttendArgs& a, int unit, int seq, const Span& s, int k) {
     const int64_t left = (int64_t)s.n * a.group - (int64_t)k * unit;
@@ -530,15 +531,16 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
         // Past the last block the last one is fetched again; absent pages stand for a page that nothing is seen of.
         for (int b = b0 + wave; b < b1; b += kWaves) {
             const Place next = place_at(a.c, t.seq, min(b + kWaves, b1 - 1), head);
+            const int t0 = b * kBlock;
+            const float fk = positive(factor * now.scale_k);
             float s[S::kScores];
             codes.scores(q, s);
             codes.fetch_keys(block_codes(next), lane);
-            const int t0 = b * kBlock;
+            if (now.absent || t0 + kBlock > v.each_to || t0 < v.each_from) hide<D, C>(s, t0, g, c.from, now.absent ? 0 : c.to);
+            const float top = st.top_of(s, fk);
+            if (st.behind(top, __float_as_int(now.scale_v))) st.catch_up(top, __float_as_int(now.scale_v));
             half8 p[S::kSteps];
-            const bool masked = now.absent || t0 + kBlock > v.each_to || t0 < v.each_from;
-            uint32_t seen = 0xFFFFu;
-            if (masked) seen = seen_bits<D, C>(t0, g, c.from, now.absent ? 0 : c.to);
-            st.probabilities(s, factor * now.scale_k, now.scale_v, seen, masked, p);
+            st.probabilities(s, fk, now.scale_v, p);
             if (now.absent || t0 + kBlock > v.keys) codes.keep_values(g, now.absent ? 0 : v.keys - t0);
             codes.add_values(p, st.o);
             codes.fetch_values(block_codes(next), lane);
@@ -561,7 +563,7 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
 #pragma unroll
         for (int j = 0; j < S::kTiles; ++j)
 #pragma unroll
-            for (int r = 0; r < S::kPerTile; ++r) st.o[j][r] = l == 0.f ? 0.f : ldexpf(st.o[j][r] * part_share, st.lift);
+            for (int r = 0; r < S::kPerTile; ++r) st.o[j][r] = l == 0.f ? 0.f : st.value(st.o[j][r], part_share);
 #pragma unroll
         for (int round = kWaves / 2; round; round >>= 1) {
             float* mail = pass + (wave & (round - 1)) * R * 64;
@@ -686,18 +688,19 @@ template <int D, int C> __global__ __launch_bounds__(kThreads) void k_join(Atten
 }
 
 // ---- many columns: the work is products ----------------------------------------------------
-// A workgroup takes 4 * 32 * T columns.  Its waves turn two blocks' codes into
-// FP16 once, in LDS and in the order in which the matrix cores take them, with the
-// next two's codes in flight; every fragment read from there serves T products.
+// A workgroup takes 128 columns, 32 to a wave.  Its waves turn a block's codes
+// into FP16 once, in LDS and in the order in which the matrix cores take them, while they
+// work on the block before and the codes of the next are in flight.
+constexpr int kManyColumns = kWaves * 32;
 constexpr int kLeastManyShare = 16;      // blocks of a workgroup, at least
 
-constexpr int many_tiles(int dim) { return dim <= 192 ? 2 : 1; }       // T: what the registers of a wave hold
-constexpr int many_columns(int dim) { return kWaves * 32 * many_tiles(dim); }
+// Waves of a SIMD, and so workgroups of a CU.
+constexpr int many_waves(int dim) { return dim <= 96 ? 3 : dim <= 192 ? 2 : 1; }
 
-template <int D, int FMT> __global__ __launch_bounds__(kThreads, 1) void k_many(AttendArgs a, Plan plan) {
+template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) void k_many(AttendArgs a, Plan plan) {
     using S = Shape<D, 32>;
-    constexpr int T = many_tiles(D), C = many_columns(D), J = D / 32, F = D / 16, N = (2 * J + kWaves - 1) / kWaves;
-    __shared__ half8 stage[2][2][2][F][64];            // [buffer][block][keys, values][fragment][lane]
+    constexpr int C = kManyColumns, J = D / 32, F = D / 16, N = (J + kWaves - 1) / kWaves;
+    __shared__ half8 stage[2][2][F][64];               // [buffer][keys, values][fragment][lane]
     const int lane = threadIdx.x & 63, wave = one(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
     Open* open = reinterpret_cast<Open*>(static_cast<char*>(a.workspace) + plan.opens);
     // workgroups of one XCD, every eighth, take neighbouring shares: of few key heads, whose codes then stay in its L2
@@ -731,123 +734,104 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, 1) void k_many(
         const bool whole = take == units;
         const int b0 = v.block + min(skip, v.blocks), b1 = v.block + min(skip + take, v.blocks);
 
-        // the wave's columns
-        const int c0 = wave * 32 * T;
+        // the wave's columns, and what they see
+        const int c0 = wave * 32;
         Tile mine = t;
         mine.f0 += c0;
-        mine.columns = min(t.columns - c0, 32 * T);
+        mine.columns = min(t.columns - c0, 32);
         View w = {};
         if (mine.columns > 0) w = view_of(a, mine);
-        Column c[T];
-        half8 q[T][F];
-        float factor[T];
-        State<D, 32> st[T];
-#pragma unroll
-        for (int k = 0; k < T; ++k) {
-            c[k] = column_of(a, t, v, c0 + 32 * k + col);
-            factor[k] = load_query<D, 32>(
-                a.scale, static_cast<const uint16_t*>(a.q) + c[k].row * a.ld_token + ((int64_t)head * a.group + c[k].head) * a.ld_head, h, q[k]);
-            st[k].clear();
-        }
+        const int each_from = one(w.each_from), each_to = one(w.each_to), keys = one(v.keys);
+        const Column c = column_of(a, t, v, c0 + col);
 
         uint4 kc[N], vc[N];
-        Place now[2], next[2];
-        const auto places = [&](int b, Place* p) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) p[k] = place_at(a.c, t.seq, min(b + k, b1 - 1), head);
-        };
-        const auto fetch = [&](const Place* p) {
+        const auto fetch = [&](const Place& p) {
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                const int it = wave + kWaves * n, k = it >= J, j = it - k * J;
-                if (2 * J % kWaves == 0 || it < 2 * J) {
-                    const uint4* codes = reinterpret_cast<const uint4*>(a.c.codes + p[k].at * (2 * kBlock * (int64_t)D));
+                const int j = wave + kWaves * n;
+                if (J % kWaves == 0 || j < J) {
+                    const uint4* codes = reinterpret_cast<const uint4*>(a.c.codes + p.at * (2 * kBlock * (int64_t)D));
                     kc[n] = codes[(2 * j + h) * 32 + col];
                     vc[n] = codes[2 * D + (32 * j + col) * 2 + h];
                 }
             }
         };
-        const auto fill = [&](int buffer, int b, const Place* p) {
+        const auto fill = [&](int buffer, int b, const Place& p) {
+            const int keep = p.absent ? 0 : keys - b * kBlock;
+            if (keep < kBlock) {                       // what is no token's may be anything: zeros
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int m = keep - S::token(h, 4 * i);
+                        reinterpret_cast<uint32_t*>(&vc[n])[i] &= m <= 0 ? 0u : m >= 4 ? 0xFFFFFFFFu : (1u << (8 * m)) - 1u;
+                    }
+            }
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                const int it = wave + kWaves * n, k = it >= J, j = it - k * J;
-                if (2 * J % kWaves == 0 || it < 2 * J) {
-                    stage[buffer][k][0][2 * j][lane] = expand8<FMT>(kc[n].x, kc[n].y);
-                    stage[buffer][k][0][2 * j + 1][lane] = expand8<FMT>(kc[n].z, kc[n].w);
-                    const int keep = p[k].absent ? 0 : v.keys - (b + k) * kBlock;
-                    if (keep < kBlock) {               // what is no token's may be anything: zeros
-                        uint32_t* x = reinterpret_cast<uint32_t*>(&vc[n]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int m = keep - S::token(h, 4 * i);
-                            x[i] &= m <= 0 ? 0u : m >= 4 ? 0xFFFFFFFFu : (1u << (8 * m)) - 1u;
-                        }
-                    }
-                    stage[buffer][k][1][2 * j][lane] = expand8<FMT>(vc[n].x, vc[n].y);
-                    stage[buffer][k][1][2 * j + 1][lane] = expand8<FMT>(vc[n].z, vc[n].w);
+                const int j = wave + kWaves * n;
+                if (J % kWaves == 0 || j < J) {
+                    stage[buffer][0][2 * j][lane] = expand8<FMT>(kc[n].x, kc[n].y);
+                    stage[buffer][0][2 * j + 1][lane] = expand8<FMT>(kc[n].z, kc[n].w);
+                    stage[buffer][1][2 * j][lane] = expand8<FMT>(vc[n].x, vc[n].y);
+                    stage[buffer][1][2 * j + 1][lane] = expand8<FMT>(vc[n].z, vc[n].w);
                 }
             }
         };
+        Place now = {}, next = {};
         if (b0 < b1) {
-            places(b0, now);
+            now = place_at(a.c, t.seq, b0, head);
             fetch(now);
+        }
+        half8 q[F];
+        const float factor = load_query<D, 32>(
+            a.scale, static_cast<const uint16_t*>(a.q) + c.row * a.ld_token + ((int64_t)head * a.group + c.head) * a.ld_head, h, q);
+        State<D, 32> st;
+        st.clear();
+        if (b0 < b1) {
             fill(0, b0, now);
-            places(b0 + 2, next);
+            next = place_at(a.c, t.seq, min(b0 + 1, b1 - 1), head);
             fetch(next);
             __syncthreads();
             int buffer = 0;
-            for (int b = b0; b < b1; b += 2) {
+            for (int b = b0; b < b1; ++b) {
+                const Place later = place_at(a.c, t.seq, min(b + 2, b1 - 1), head);
+                fill(buffer ^ 1, b + 1, next);         // past the last block nobody reads it
+                fetch(later);
+                const int t0 = b * kBlock;
+                const float fk = positive(factor * now.scale_k);
+                half8 y[F];                            // all of a product's fragments at once: the others' reads hide behind the first's
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int t0 = (b + k) * kBlock;
-                    if (b + k >= b1 || t0 >= w.all_to || t0 + kBlock <= w.all_from) continue;
-                    float16v x[T];
+                for (int f = 0; f < F; ++f) y[f] = stage[buffer][0][f][lane];
+                __builtin_amdgcn_sched_barrier(0);
+                float16v x = 0.f;
 #pragma unroll
-                    for (int u = 0; u < T; ++u) x[u] = 0.f;
+                for (int f = 0; f < F; ++f) x = __builtin_amdgcn_mfma_f32_32x32x16_f16(y[f], q[f], x, 0, 0, 0);
 #pragma unroll
-                    for (int f = 0; f < F; ++f) {
-                        const half8 y = stage[buffer][k][0][f][lane];
+                for (int f = 0; f < F; ++f) y[f] = stage[buffer][1][f][lane];
+                __builtin_amdgcn_sched_barrier(0);
+                float s[16];
 #pragma unroll
-                        for (int u = 0; u < T; ++u) x[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y, q[u][f], x[u], 0, 0, 0);
-                    }
-                    const bool masked = now[k].absent || t0 + kBlock > w.each_to || t0 < w.each_from;
-                    half8 p[T][2];
+                for (int r = 0; r < 16; ++r) s[r] = x[r];
+                if (now.absent || t0 + kBlock > each_to || t0 < each_from) hide<D, 32>(s, t0, h, c.from, now.absent ? 0 : c.to);
+                const float top = st.top_of(s, fk);
+                if (st.behind(top, __float_as_int(now.scale_v))) st.catch_up(top, __float_as_int(now.scale_v));
+                half8 p[2];
+                st.probabilities(s, fk, now.scale_v, p);
 #pragma unroll
-                    for (int u = 0; u < T; ++u) {
-                        uint32_t seen = 0xFFFFu;
-                        if (masked) seen = seen_bits<D, 32>(t0, h, c[u].from, now[k].absent ? 0 : c[u].to);
-                        float s[16];
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) s[r] = x[u][r];
-                        st[u].probabilities(s, factor[u] * now[k].scale_k, now[k].scale_v, seen, masked, p[u]);
-                    }
-#pragma unroll
-                    for (int f = 0; f < F; ++f) {
-                        const half8 y = stage[buffer][k][1][f][lane];
-#pragma unroll
-                        for (int u = 0; u < T; ++u)
-                            st[u].o[f >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y, p[u][f & 1], st[u].o[f >> 1], 0, 0, 0);
-                    }
-                }
-                if (b + 2 < b1) {
-                    fill(buffer ^ 1, b + 2, next);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) now[k] = next[k];
-                    places(b + 4, next);
-                    fetch(next);
-                }
+                for (int f = 0; f < F; ++f) st.o[f >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y[f], p[f & 1], st.o[f >> 1], 0, 0, 0);
+                now = next;
+                next = later;
                 __syncthreads();
                 buffer ^= 1;
             }
         }
 
-#pragma unroll
-        for (int u = 0; u < T; ++u) {
-            const float l = S::over_groups(st[u].l, true);
-            const int column = c0 + 32 * u + col;
-            if (column >= t.columns) continue;
+        const float l = S::over_groups(st.l, true);
+        const int column = c0 + col;
+        if (column < t.columns) {
             const float over = l == 0.f ? 0.f : 1.f / l;               // nothing seen: zeros
-            uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)c[u].row * a.q_heads + (int64_t)head * a.group + c[u].head) * D;
+            uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)c.row * a.q_heads + (int64_t)head * a.group + c.head) * D;
             float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan.parts) + (worker * 2 + (opening ? 0 : 1)) * part_floats(D, C);
 #pragma unroll
             for (int j = 0; j < S::kTiles; ++j)
@@ -856,7 +840,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, 1) void k_many(
                     const int d = S::output(h, j, r);
                     float x[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = l == 0.f ? 0.f : ldexpf(st[u].o[j][r + e] * over, st[u].lift);
+                    for (int e = 0; e < 4; ++e) x[e] = l == 0.f ? 0.f : st.value(st.o[j][r + e], over);
                     if (whole) {
                         union { __bf16 b[4]; uint2 w; } y;
 #pragma unroll
@@ -867,7 +851,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, 1) void k_many(
                     }
                 }
             if (!whole && h == 0) {
-                part[C * D + column] = st[u].m;
+                part[C * D + column] = st.m;
                 part[C * (D + 1) + column] = l;
             }
         }
@@ -882,7 +866,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, 1) void k_many(
 
 // Joins the parts of a row of many columns: D / 4 threads for each of several columns.
 template <int D> __global__ __launch_bounds__(kThreads) void k_join_many(AttendArgs a, Plan plan) {
-    constexpr int Q = D / 4, P = kThreads / Q, C = many_columns(D);
+    constexpr int Q = D / 4, P = kThreads / Q, C = kManyColumns;
     const Open open = reinterpret_cast<const Open*>(static_cast<const char*>(a.workspace) + plan.opens)[blockIdx.x];
     const int x = threadIdx.x % Q, lane_column = threadIdx.x / Q, col = blockIdx.y * P + lane_column;
     if (lane_column >= P || col >= open.columns) return;
@@ -948,10 +932,10 @@ Plans plans_of(const AttendArgs& a) {
     }
     if (many) {
         p.many.kind = few ? kMany : kAny;
-        p.many.workers = 256;                          // one on a CU
-        p.many.slots = (int)tile_slots(a, many_columns(a.c.dim));
+        p.many.workers = 256 * many_waves(a.c.dim);    // what the GPU holds at once
+        p.many.slots = (int)tile_slots(a, kManyColumns);
         p.many.opens = room(p.many.workers * (int64_t)sizeof(Open));
-        p.many.parts = room(p.many.workers * 2 * part_floats(a.c.dim, many_columns(a.c.dim)) * (int64_t)sizeof(float));
+        p.many.parts = room(p.many.workers * 2 * part_floats(a.c.dim, kManyColumns) * (int64_t)sizeof(float));
     }
     p.bytes = (size_t)at;
     return p;
@@ -976,7 +960,7 @@ template <int D, int FMT> hipError_t launch(const AttendArgs& a, hipStream_t str
     if (p.many.workers) {
         constexpr int P = kThreads / (D / 4);
         k_many<D, FMT><<<p.many.workers, kThreads, 0, stream>>>(a, p.many);
-        k_join_many<D><<<dim3(p.many.workers, (many_columns(D) + P - 1) / P), kThreads, 0, stream>>>(a, p.many);
+        k_join_many<D><<<dim3(p.many.workers, (kManyColumns + P - 1) / P), kThreads, 0, stream>>>(a, p.many);
     }
     return hipGetLastError();
 }
