@@ -269,19 +269,24 @@ template <int D, int C> struct State {
 #pragma unroll
         for (int j = 0; j < S::kTiles; ++j) o[j] *= by;
     }
-    // From scores to probabilities p, in the second product's order.
-    __device__ __forceinline__ void probabilities(const float* s, float fk, float scale_v, half8* p) {
+    // What turns a block's scores into probabilities: factor and offset of the exponents, and the running sum.
+    struct Exponent {
+        float factor, offset, fraction, sum;
+    };
+    __device__ __forceinline__ Exponent exponent(float fk, float scale_v) const {
         const float fraction = fmaxf(scale_v * __uint_as_float((254 << 23) - size), kLeastFraction);
-        const float off = kLift + __builtin_amdgcn_logf(fraction) - fmaxf(m, -1e37f);      // m is -inf until a token is seen
-        float sum = 0.f;
-#pragma unroll
-        for (int r = 0; r < S::kScores; ++r) {
-            const float e = exp2_fast(__builtin_fmaf(s[r], fk, off));
-            sum += e;
-            p[r >> 3][r & 7] = (_Float16)e;
-        }
-        l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(fraction), l);
+        return {fk, kLift + __builtin_amdgcn_logf(fraction) - fmaxf(m, -1e37f), fraction, 0.f};        // m is -inf until a token is seen
     }
+    // Probabilities r and r + 1, in the second product's order.  Their sum is of what they are before FP16, which loses
+    // those of a block whose values are small beside others'.
+    __device__ __forceinline__ void probabilities(const float* s, int r, Exponent& x, half8* p) const {
+        const float e0 = exp2_fast(__builtin_fmaf(s[r], x.factor, x.offset)), e1 = exp2_fast(__builtin_fmaf(s[r + 1], x.factor, x.offset));
+        x.sum += e0;
+        x.sum += e1;
+        p[r >> 3][r & 7] = (_Float16)e0;
+        p[r >> 3][(r & 7) + 1] = (_Float16)e1;
+    }
+    __device__ __forceinline__ void add(const Exponent& x) { l = __builtin_fmaf(x.sum, __builtin_amdgcn_rcpf(x.fraction), l); }
     // The output's registers over a sum of probabilities; a power of two at a time, since sizes may be anything.
     __device__ __forceinline__ float value(float x, float by) const { return x * by * __uint_as_float(size); }
 };
@@ -312,23 +317,30 @@ __device__ __forceinline__ Tile one(const Tile& t) {
 // of which nothing is to be used.
 struct Place {
     int64_t at;
-    float scale_k, scale_v;
+    float raw_k, raw_v;
     bool absent;
+    __device__ __forceinline__ float scale_k() const { return absent ? 1.f : raw_k; }
+    __device__ __forceinline__ float scale_v() const { return absent ? 0.f : raw_v; }
 };
 template <typename T> using scalar_t = const __attribute__((address_space(4))) T*;
 template <typename T> __device__ __forceinline__ T scalar_load(const T* p, int64_t i) {
     return ((scalar_t<T>)(uintptr_t)p)[i];
 }
-__device__ __forceinline__ Place place_at(const CacheArgs& c, int seq, int b, int head) {
+// The page that holds block b, as the table says.
+__device__ __forceinline__ int page_of(const CacheArgs& c, int seq, int b) {
+    return scalar_load(c.page_table, (int64_t)seq * c.width + (one(b) >> c.shift));
+}
+__device__ __forceinline__ Place place_in(const CacheArgs& c, int page, int b, int head) {
     Place p;
-    b = one(b);
-    const int64_t page = scalar_load(c.page_table, (int64_t)seq * c.width + (b >> c.shift));
-    p.absent = page < 0 || page >= c.pages;
-    p.at = p.absent ? 0 : ((page * c.heads + head) << c.shift) | (b & ((1 << c.shift) - 1));
-    const float k = scalar_load(c.scales, p.at * 2), v = scalar_load(c.scales, p.at * 2 + 1);
-    p.scale_k = p.absent ? 1.f : k;
-    p.scale_v = p.absent ? 0.f : v;
+    p.absent = (uint32_t)page >= (uint32_t)c.pages;
+    p.at = p.absent ? 0 : (((int64_t)page * c.heads + head) << c.shift) | (b & ((1 << c.shift) - 1));
+    p.raw_k = scalar_load(c.scales, p.at * 2);
+    p.raw_v = scalar_load(c.scales, p.at * 2 + 1);
     return p;
+}
+__device__ __forceinline__ Place place_at(const CacheArgs& c, int seq, int b, int head) {
+    b = one(b);
+    return place_in(c, page_of(c, seq, b), b, head);
 }
 
 // ---- sharing the work out ----------------------------------------------------------------
@@ -532,15 +544,18 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
         for (int b = b0 + wave; b < b1; b += kWaves) {
             const Place next = place_at(a.c, t.seq, min(b + kWaves, b1 - 1), head);
             const int t0 = b * kBlock;
-            const float fk = positive(factor * now.scale_k);
+            const float fk = positive(factor * now.scale_k());
             float s[S::kScores];
             codes.scores(q, s);
             codes.fetch_keys(block_codes(next), lane);
             if (now.absent || t0 + kBlock > v.each_to || t0 < v.each_from) hide<D, C>(s, t0, g, c.from, now.absent ? 0 : c.to);
             const float top = st.top_of(s, fk);
-            if (st.behind(top, __float_as_int(now.scale_v))) st.catch_up(top, __float_as_int(now.scale_v));
+            if (st.behind(top, __float_as_int(now.scale_v()))) st.catch_up(top, __float_as_int(now.scale_v()));
             half8 p[S::kSteps];
-            st.probabilities(s, fk, now.scale_v, p);
+            typename State<D, C>::Exponent ex = st.exponent(fk, now.scale_v());
+#pragma unroll
+            for (int r = 0; r < S::kScores; r += 2) st.probabilities(s, r, ex, p);
+            st.add(ex);
             if (now.absent || t0 + kBlock > v.keys) codes.keep_values(g, now.absent ? 0 : v.keys - t0);
             codes.add_values(p, st.o);
             codes.fetch_values(block_codes(next), lane);
@@ -689,45 +704,55 @@ template <int D, int C> __global__ __launch_bounds__(kThreads) void k_join(Atten
 
 // ---- many columns: the work is products ----------------------------------------------------
 // A workgroup takes 128 columns, 32 to a wave.  Its waves turn a block's codes
-// into FP16 once, in LDS and in the order in which the matrix cores take them, while they
-// work on the block before and the codes of the next are in flight.
+// into FP16 once, in LDS and in the order in which the matrix cores take them.
 constexpr int kManyColumns = kWaves * 32;
 constexpr int kLeastManyShare = 16;      // blocks of a workgroup, at least
 
 // Waves of a SIMD, and so workgroups of a CU.
-constexpr int many_waves(int dim) { return dim <= 96 ? 3 : dim <= 192 ? 2 : 1; }
+constexpr int many_waves(int dim) { return dim <= 64 ? 3 : dim <= 192 ? 2 : 1; }
 
 template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) void k_many(AttendArgs a, Plan plan) {
     using S = Shape<D, 32>;
-    constexpr int C = kManyColumns, J = D / 32, F = D / 16, N = (J + kWaves - 1) / kWaves;
+    constexpr int C = kManyColumns, J = D / 32, F = D / 16, N = (J + kWaves - 1) / kWaves, kAhead = 5;
     __shared__ half8 stage[2][2][F][64];               // [buffer][keys, values][fragment][lane]
     const int lane = threadIdx.x & 63, wave = one(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
     Open* open = reinterpret_cast<Open*>(static_cast<char*>(a.workspace) + plan.opens);
     // workgroups of one XCD, every eighth, take neighbouring shares: of few key heads, whose codes then stay in its L2
     const int worker = (blockIdx.x % 8) * (plan.workers / 8) + blockIdx.x / 8;
+    // Slots in an order that takes one from the front and one from the back by turns: a prompt's first rows see few
+    // tokens and its last ones many, and a share of either alone would hold many rows or few.
+    const auto row_at = [&](int64_t e, Tile* t) {
+        const int64_t slot = e & 1 ? plan.slots - 1 - (e >> 1) : e >> 1;
+        return tile_of(a, C, slot, t) && takes(a, plan.kind, t->s);
+    };
     Share share = share_of(worker, plan.workers, a.c.heads, plan.slots, kLeastManyShare, [&](int64_t e) -> int64_t {
         Tile t;
-        if (!tile_of(a, C, e, &t) || !takes(a, plan.kind, t.s)) return 0;
-        return max(view_of(a, t).blocks, 1);
+        return row_at(e, &t) ? max(view_of(a, t).blocks, 1) : 0;
     });
     if (threadIdx.x == 0) open[worker].columns = 0;
     if (share.at >= share.end) return;
-    int64_t slot = share.entry, row_begin = share.entry_begin;         // a slot is one row
+    int64_t entry = share.entry, row_begin = share.entry_begin;        // an entry is one row
     int head = one(share.head);
     bool opening = true;
 
     while (share.at < share.end) {
-        Tile t;
-        if (slot >= plan.slots) {
-            slot = 0;
-            if (++head >= a.c.heads) break;            // starts out of order: rows were not all found again
+        // the next entry that is a row, 64 at a time: sequences of few columns have entries that are none
+        uint64_t rows = 0;
+        while (entry < plan.slots) {
+            Tile u;
+            rows = __ballot(entry + lane < plan.slots && row_at(entry + lane, &u));
+            if (rows) break;
+            entry += 64;
         }
-        const bool some = tile_of(a, C, slot, &t);
-        t = one(t);
-        if (!some || !takes(a, plan.kind, t.s)) {      // on to the next sequence's first slot
-            slot = t.seq + 1 < a.c.batch ? max(slot + 1, (int64_t)max(a.c.starts[t.seq + 1], 0) * a.group / C + t.seq + 1) : (int64_t)plan.slots;
+        if (!rows) {
+            entry = 0;
+            if (++head >= a.c.heads) break;            // the arrays changed meanwhile
             continue;
         }
+        entry += __builtin_ctzll(rows);
+        Tile t;
+        row_at(entry, &t);
+        t = one(t);
         const View v = view_of(a, t);
         const int units = max(v.blocks, 1), skip = one((int)min(max(share.at - row_begin, (int64_t)0), (int64_t)units));
         const int take = one((int)min((int64_t)(units - skip), share.end - share.at));
@@ -756,27 +781,29 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
                 }
             }
         };
-        const auto fill = [&](int buffer, int b, const Place& p) {
+        // Codes that are no token's may be anything: zeros.
+        const auto keep_tail = [&](int b, const Place& p) {
             const int keep = p.absent ? 0 : keys - b * kBlock;
-            if (keep < kBlock) {                       // what is no token's may be anything: zeros
 #pragma unroll
-                for (int n = 0; n < N; ++n)
+            for (int n = 0; n < N; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int m = keep - S::token(h, 4 * i);
-                        reinterpret_cast<uint32_t*>(&vc[n])[i] &= m <= 0 ? 0u : m >= 4 ? 0xFFFFFFFFu : (1u << (8 * m)) - 1u;
-                    }
-            }
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const int j = wave + kWaves * n;
-                if (J % kWaves == 0 || j < J) {
-                    stage[buffer][0][2 * j][lane] = expand8<FMT>(kc[n].x, kc[n].y);
-                    stage[buffer][0][2 * j + 1][lane] = expand8<FMT>(kc[n].z, kc[n].w);
-                    stage[buffer][1][2 * j][lane] = expand8<FMT>(vc[n].x, vc[n].y);
-                    stage[buffer][1][2 * j + 1][lane] = expand8<FMT>(vc[n].z, vc[n].w);
+                for (int i = 0; i < 4; ++i) {
+                    const int m = keep - S::token(h, 4 * i);
+                    reinterpret_cast<uint32_t*>(&vc[n])[i] &= m <= 0 ? 0u : m >= 4 ? 0xFFFFFFFFu : (1u << (8 * m)) - 1u;
                 }
+        };
+        // Eight codes of the wave's part: a quarter of each of its N pieces.
+        const auto turn = [&](int buffer, int u) {
+            const int n = u >> 2, j = wave + kWaves * n, e = u & 1;
+            if (J % kWaves == 0 || j < J) {
+                const uint4& w = u & 2 ? vc[n] : kc[n];
+                stage[buffer][(u >> 1) & 1][2 * j + e][lane] = e ? expand8<FMT>(w.z, w.w) : expand8<FMT>(w.x, w.y);
             }
+        };
+        const auto fill = [&](int buffer, int b, const Place& p) {
+            if (p.absent || keys < (b + 1) * kBlock) keep_tail(b, p);
+#pragma unroll
+            for (int u = 0; u < 4 * N; ++u) turn(buffer, u);
         };
         Place now = {}, next = {};
         if (b0 < b1) {
@@ -792,36 +819,54 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
             fill(0, b0, now);
             next = place_at(a.c, t.seq, min(b0 + 1, b1 - 1), head);
             fetch(next);
+            int page = page_of(a.c, t.seq, min(b0 + 2, b1 - 1));
             __syncthreads();
             int buffer = 0;
             for (int b = b0; b < b1; ++b) {
-                const Place later = place_at(a.c, t.seq, min(b + 2, b1 - 1), head);
-                fill(buffer ^ 1, b + 1, next);         // past the last block nobody reads it
-                fetch(later);
                 const int t0 = b * kBlock;
-                const float fk = positive(factor * now.scale_k);
-                half8 y[F];                            // all of a product's fragments at once: the others' reads hide behind the first's
+                const float fk = positive(factor * now.scale_k());
+                half8 y[2 * F];                        // fragments of keys, then of values
+                const auto read = [&](int i) { y[i] = stage[buffer][i >= F][i >= F ? i - F : i][lane]; };
 #pragma unroll
-                for (int f = 0; f < F; ++f) y[f] = stage[buffer][0][f][lane];
-                __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < kAhead; ++i) read(i);
+                if (next.absent || keys < (b + 2) * kBlock) keep_tail(b + 1, next);
+                __builtin_amdgcn_s_setprio(1);
                 float16v x = 0.f;
 #pragma unroll
-                for (int f = 0; f < F; ++f) x = __builtin_amdgcn_mfma_f32_32x32x16_f16(y[f], q[f], x, 0, 0, 0);
+                for (int i = 0; i < F; ++i) {
+                    if (i + kAhead < 2 * F) read(i + kAhead);
+                    x = __builtin_amdgcn_mfma_f32_32x32x16_f16(y[i], q[i], x, 0, 0, 0);
 #pragma unroll
-                for (int f = 0; f < F; ++f) y[f] = stage[buffer][1][f][lane];
-                __builtin_amdgcn_sched_barrier(0);
+                    for (int u = 4 * N * i / F; u < 4 * N * (i + 1) / F; ++u) turn(buffer ^ 1, u);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                __builtin_amdgcn_s_setprio(0);
+                int ahead = min(b + 2, b1 - 1);
+                asm volatile("" : "+s"(ahead));
+                const Place last = place_in(a.c, page, ahead, head);
+                fetch(last);
+                page = page_of(a.c, t.seq, min(ahead + 1, b1 - 1));
                 float s[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = x[r];
                 if (now.absent || t0 + kBlock > each_to || t0 < each_from) hide<D, 32>(s, t0, h, c.from, now.absent ? 0 : c.to);
                 const float top = st.top_of(s, fk);
-                if (st.behind(top, __float_as_int(now.scale_v))) st.catch_up(top, __float_as_int(now.scale_v));
+                if (st.behind(top, __float_as_int(now.scale_v()))) st.catch_up(top, __float_as_int(now.scale_v()));
                 half8 p[2];
-                st.probabilities(s, fk, now.scale_v, p);
+                typename State<D, 32>::Exponent ex = st.exponent(fk, now.scale_v());
 #pragma unroll
-                for (int f = 0; f < F; ++f) st.o[f >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y[f], p[f & 1], st.o[f >> 1], 0, 0, 0);
+                for (int r = 0; r < 16; r += 2) st.probabilities(s, r, ex, p);
+                st.add(ex);
+                __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                for (int i = 0; i < F; ++i) {
+                    if (i + F + kAhead < 2 * F) read(i + F + kAhead);
+                    st.o[i >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y[F + i], p[i & 1], st.o[i >> 1], 0, 0, 0);
+                    if (i + F + kAhead < 2 * F) __builtin_amdgcn_sched_barrier(0);
+                }
+                __builtin_amdgcn_s_setprio(0);
                 now = next;
-                next = later;
+                next = last;
                 __syncthreads();
                 buffer ^= 1;
             }
@@ -859,7 +904,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
             open[worker] = {row_begin, share.per, t.seq, t.f0, t.columns, head, (int)((row_begin + units - 1) / share.per), 0};
         share.at += take;
         row_begin += units;
-        ++slot;
+        ++entry;
         opening = false;
     }
 }
