@@ -636,15 +636,14 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
 }
 
 // Joins the parts of the row that workgroup blockIdx.x began and others went
-// on with, one column a workgroup: parts' weights in LDS first, then D / 4 threads for each of
+// on with, a column at a time: parts' weights in LDS first, then D / 4 threads for each of
 // several parts at a time.
 template <int D, int C> __global__ __launch_bounds__(kThreads) void k_join(AttendArgs a, Plan plan) {
     constexpr int Q = D / 4, P = kThreads / Q;         // threads of a part, parts at a time
     __shared__ float weights[kThreads], reduced[2][kWaves];
     __shared__ float4v sums[P][Q];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = blockIdx.y;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const Open open = reinterpret_cast<const Open*>(static_cast<const char*>(a.workspace) + plan.opens)[blockIdx.x];
-    if (col >= open.columns) return;
     const float* parts = reinterpret_cast<const float*>(static_cast<const char*>(a.workspace) + plan.parts);
     const int many = open.last - (int)blockIdx.x + 1;
     const auto part_of = [&](int k) {
@@ -652,54 +651,58 @@ template <int D, int C> __global__ __launch_bounds__(kThreads) void k_join(Atten
         return parts + (w * 2 + (w * open.per < open.begin ? 1 : 0)) * part_floats(D, C);
     };
     const int p = threadIdx.x / Q, x = threadIdx.x % Q;
-    float top = -INFINITY, total = 0.f;
-    float4v sum = 0.f;
-    for (int base = 0; base < many; base += kThreads) {                // one round up to 256 parts
-        const int n = min(many - base, kThreads);
-        float m = -INFINITY, l = 0.f;
-        if (threadIdx.x < n) {
-            const float* q = part_of(base + threadIdx.x);
-            m = q[C * D + col];
-            l = q[C * (D + 1) + col];
-        }
-        float now = m;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) now = fmaxf(now, __shfl_xor(now, d));
-        if (lane == 0) reduced[0][wave] = now;
-        __syncthreads();
-        now = fmaxf(top, fmaxf(fmaxf(reduced[0][0], reduced[0][1]), fmaxf(reduced[0][2], reduced[0][3])));
-        const float weight = l == 0.f ? 0.f : (m == now ? 1.f : exp2_fast(m - now)) * l;       // 0: nothing seen there
-        weights[threadIdx.x] = weight;
-        float added = weight;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) added += __shfl_xor(added, d);
-        if (lane == 0) reduced[1][wave] = added;
-        __syncthreads();
-        const float alpha = now == top ? 1.f : exp2_fast(top - now);
-        top = now;
-        total = total * alpha + (reduced[1][0] + reduced[1][1] + reduced[1][2] + reduced[1][3]);
-        sum *= alpha;
-        if (p < P) {
-#pragma unroll 8
-            for (int k = p; k < n; k += P) {
-                const float w = weights[k];
-                const float4v o = *reinterpret_cast<const float4v*>(part_of(base + k) + col * D + 4 * x);
-                sum += w == 0.f ? (float4v)0.f : o * w;
+    for (int col = blockIdx.y; col < open.columns; col += gridDim.y) {
+        float top = -INFINITY, total = 0.f;
+        float4v sum = 0.f;
+        for (int base = 0; base < many; base += kThreads) {                // one round up to 256 parts
+            const int n = min(many - base, kThreads);
+            float m = -INFINITY, l = 0.f;
+            if (threadIdx.x < n) {
+                const float* q = part_of(base + threadIdx.x);
+                m = q[C * D + col];
+                l = q[C * (D + 1) + col];
             }
+            float now = m;
+#pragma unroll
+            for (int d = 32; d; d >>= 1) now = fmaxf(now, __shfl_xor(now, d));
+            if (lane == 0) reduced[0][wave] = now;
+            __syncthreads();
+            now = fmaxf(top, fmaxf(fmaxf(reduced[0][0], reduced[0][1]), fmaxf(reduced[0][2], reduced[0][3])));
+            const float weight = l == 0.f ? 0.f : (m == now ? 1.f : exp2_fast(m - now)) * l;       // 0: nothing seen there
+            weights[threadIdx.x] = weight;
+            float added = weight;
+#pragma unroll
+            for (int d = 32; d; d >>= 1) added += __shfl_xor(added, d);
+            if (lane == 0) reduced[1][wave] = added;
+            __syncthreads();
+            const float alpha = now == top ? 1.f : exp2_fast(top - now);
+            top = now;
+            total = total * alpha + (reduced[1][0] + reduced[1][1] + reduced[1][2] + reduced[1][3]);
+            sum *= alpha;
+            if (p < P) {
+#pragma unroll 8
+                for (int k = p; k < n; k += P) {
+                    const float w = weights[k];
+                    const float4v o = *reinterpret_cast<const float4v*>(part_of(base + k) + col * D + 4 * x);
+                    sum += w == 0.f ? (float4v)0.f : o * w;
+                }
+            }
+            __syncthreads();
+        }
+        if (p < P) sums[p][x] = sum;
+        __syncthreads();
+        if (p == 0) {
+#pragma unroll
+            for (int k = 1; k < P; ++k) sum += sums[k][x];
+            const int f = open.f0 + col, i = f / a.group, gh = f - i * a.group, row = span_of(a.c, open.seq).row + i;
+            uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)row * a.q_heads + (int64_t)open.head * a.group + gh) * D;
+            union { __bf16 b[4]; uint2 w; } u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u.b[e] = (__bf16)(total == 0.f ? 0.f : sum[e] / total);
+            *reinterpret_cast<uint2*>(out + 4 * x) = u.w;
         }
         __syncthreads();
     }
-    if (p < P) sums[p][x] = sum;
-    __syncthreads();
-    if (p != 0) return;
-#pragma unroll
-    for (int k = 1; k < P; ++k) sum += sums[k][x];
-    const int f = open.f0 + col, i = f / a.group, gh = f - i * a.group, row = span_of(a.c, open.seq).row + i;
-    uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)row * a.q_heads + (int64_t)open.head * a.group + gh) * D;
-    union { __bf16 b[4]; uint2 w; } u;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) u.b[e] = (__bf16)(total == 0.f ? 0.f : sum[e] / total);
-    *reinterpret_cast<uint2*>(out + 4 * x) = u.w;
 }
 
 // ---- many columns: the work is products ----------------------------------------------------
@@ -714,6 +717,7 @@ constexpr int many_waves(int dim) { return dim <= 64 ? 3 : dim <= 192 ? 2 : 1; }
 template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) void k_many(AttendArgs a, Plan plan) {
     using S = Shape<D, 32>;
     constexpr int C = kManyColumns, J = D / 32, F = D / 16, N = (J + kWaves - 1) / kWaves, kAhead = 5;
+    __shared__ Tile tiles[64];
     __shared__ half8 stage[2][2][F][64];               // [buffer][keys, values][fragment][lane]
     const int lane = threadIdx.x & 63, wave = one(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
     Open* open = reinterpret_cast<Open*>(static_cast<char*>(a.workspace) + plan.opens);
@@ -732,27 +736,34 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
     if (threadIdx.x == 0) open[worker].columns = 0;
     if (share.at >= share.end) return;
     int64_t entry = share.entry, row_begin = share.entry_begin;        // an entry is one row
+    int64_t known = entry - 64;                        // 64 entries from here on are in `tiles`
+    uint64_t rows = 0;
     int head = one(share.head);
     bool opening = true;
 
     while (share.at < share.end) {
-        // the next entry that is a row, 64 at a time: sequences of few columns have entries that are none
-        uint64_t rows = 0;
-        while (entry < plan.slots) {
+        // the next entry that is a row: of 64 at a time, looked up together; sequences of few columns have entries that are none
+        if (entry >= known + 64) {
+            known = entry;
             Tile u;
-            rows = __ballot(entry + lane < plan.slots && row_at(entry + lane, &u));
-            if (rows) break;
-            entry += 64;
+            const bool some = known + lane < plan.slots && row_at(known + lane, &u);
+            rows = __ballot(some);
+            __syncthreads();                           // the row before is done with what it read
+            if (wave == 0 && some) tiles[lane] = u;
+            __syncthreads();
         }
-        if (!rows) {
-            entry = 0;
-            if (++head >= a.c.heads) break;            // the arrays changed meanwhile
+        const uint64_t left = rows >> (entry - known);
+        if (!left) {
+            entry = known + 64;
+            if (entry >= plan.slots) {
+                entry = 0;
+                known = -64;
+                if (++head >= a.c.heads) break;        // the arrays changed meanwhile
+            }
             continue;
         }
-        entry += __builtin_ctzll(rows);
-        Tile t;
-        row_at(entry, &t);
-        t = one(t);
+        entry += __builtin_ctzll(left);
+        const Tile t = one(tiles[entry - known]);
         const View v = view_of(a, t);
         const int units = max(v.blocks, 1), skip = one((int)min(max(share.at - row_begin, (int64_t)0), (int64_t)units));
         const int take = one((int)min((int64_t)(units - skip), share.end - share.at));
@@ -993,7 +1004,7 @@ template <int D, int FMT, int C> void launch_few(const AttendArgs& a, const Plan
         return;
     }
     k_few<D, FMT, C, false><<<p.workers, kThreads, 0, stream>>>(a, p);
-    k_join<D, C><<<dim3(p.workers, a.c.starts || a.group > C ? C : a.group), kThreads, 0, stream>>>(a, p);
+    k_join<D, C><<<dim3(p.workers, a.c.starts || a.group > 8 ? 8 : a.group), kThreads, 0, stream>>>(a, p);
 }
 
 template <int D, int FMT> hipError_t launch(const AttendArgs& a, hipStream_t stream) {
