@@ -102,13 +102,74 @@ template <typename T, bool INTER, bool VEC> __global__ __launch_bounds__(kThread
 }
 
 // ---- append -----------------------------------------------------------------------
-template <typename T, int FMT> __global__ __launch_bounds__(kThreads) void k_append(AppendArgs a, int64_t slots, bool vec_q) {
-    extern __shared__ __align__(16) float lds[];
-    __shared__ float2 cs[128];
+// 16 elements of a head that a thread holds, two runs of 8: those of `item` of a row, of which there are dim / 16.  Halves
+// apart, an item of what turns holds 8 pairs; otherwise 16 neighbours.
+__device__ __forceinline__ int second_run(int item, int rot, bool interleaved, int* first) {
+    const int at = item * 16;
+    if (at >= rot || interleaved) {
+        *first = at;
+        return at + 8;
+    }
+    *first = at >> 1;
+    return (at >> 1) + (rot >> 1);
+}
+
+template <typename T> __device__ __forceinline__ void load8(const T* from, float* v) {
+#pragma unroll
+    for (int u = 0; u < 8 / Vec<T>::N; ++u) {
+        const Vec<T> w = reinterpret_cast<const Vec<T>*>(from)[u];
+#pragma unroll
+        for (int e = 0; e < Vec<T>::N; ++e) v[u * Vec<T>::N + e] = to_float(w.e[e]);
+    }
+}
+
+template <int FMT> __device__ __forceinline__ uint32_t code4(const float* v, float scale) {
+    if constexpr (FMT == 0) {
+        return code_of<0>(v[0] / scale) | code_of<0>(v[1] / scale) << 8 | code_of<0>(v[2] / scale) << 16 | code_of<0>(v[3] / scale) << 24;
+    } else {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[e] = v[e] / scale;
+            y[e] = y[e] == y[e] ? fminf(fmaxf(y[e], -448.f), 448.f) : 0.f;
+        }
+        const int low = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], low, true);
+    }
+}
+
+// Code of each byte over 2^up, rounded.
+template <int FMT> __device__ __forceinline__ uint32_t moved4(uint32_t w, int up) {
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = ldexpf(code_value<FMT>((w >> (8 * e)) & 0xFFu), -up);
+    return code4<FMT>(v, 1.f);
+}
+
+// Bytes of a word of values that are tokens [lo, hi); the word's first byte is token t.
+__device__ __forceinline__ uint32_t bytes_between(int t, int lo, int hi) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) m |= t + b >= lo && t + b < hi ? 0xFFu << (8 * b) : 0u;
+    return m;
+}
+
+// A block's new keys or values.  Every thread holds NI items of 16 elements in registers (heads of up to 128 elements have one for each): keys are turned there
+// (cosines and sines from LDS, made once for all heads of the workgroup), the largest magnitude is found, and codes are
+// written.  Values change places through LDS, where a row of 32 codes has 36 bytes so that rows meet in fewer banks.
+//   VEC: rows that start on 16 bytes, rot a multiple of 16.
+// The bytes of q, k, v and the codes bound it: 8192 tokens of 32 + 2 * 8 heads of 128 (184 MB)
+// take 43 us, 4.3 TB/s.
+constexpr int kPitch = 36;
+
+template <typename T, int FMT, bool VEC, int NI> __global__ __launch_bounds__(kThreads, NI == 1 ? 6 : 4) void k_append(AppendArgs a, int64_t slots, int per, bool vec_q) {
+    __shared__ __align__(16) uint8_t turned[256 * kPitch];
     __shared__ float most[kThreads / 64];
+    extern __shared__ float2 cs[];                     // [new tokens of the block][pairs]
     const CacheArgs& c = a.c;
     const int dim = c.dim, pairs = a.rot >> 1, tid = threadIdx.x;
-    const int64_t cache_work = slots * c.heads * 2;
+    const int groups = (c.heads + per - 1) / per;      // of the key heads, `per` to a workgroup
+    const int64_t cache_work = slots * (groups + c.heads);
     if ((int64_t)blockIdx.x >= cache_work) {           // a token's queries
         const int row = (int)(blockIdx.x - cache_work);
         int seq = row;
@@ -129,102 +190,161 @@ template <typename T, int FMT> __global__ __launch_bounds__(kThreads) void k_app
         }
         return;
     }
-    const int which = blockIdx.x & 1, head = (int)((blockIdx.x >> 1) % c.heads);
+    const int work = (int)(blockIdx.x % (groups + c.heads));
+    const bool which = work >= groups;                 // values
     int seq, block;
     Span s;
-    if (!slot_block(c, (blockIdx.x >> 1) / c.heads, &seq, &s, &block)) return;
-    const int64_t at = block_at(c, seq, block, head);
-    if (at < 0) return;
-    uint8_t* codes = c.codes + at * (2 * kBlock * (int64_t)dim) + which * (kBlock * dim);
-    float* scale_at = c.scales + at * 2 + which;
+    if (!slot_block(c, blockIdx.x / (groups + c.heads), &seq, &s, &block)) return;
+    const int64_t place = block_at(c, seq, block, 0);
+    if (place < 0) return;
     const int first = s.length - s.n;                  // position of the call's first token; may be negative
     const int lo = max(first - block * kBlock, 0), hi = min(s.length - block * kBlock, kBlock);      // new tokens of the block
-    const float had = lo > 0 ? *scale_at : 0.f;
-
-    // new rows to LDS
-    const int pitch = dim + 1;
-    const T* from = static_cast<const T*>(which ? a.v : a.k) + (int64_t)head * (which ? a.ld_v_head : a.ld_k_head);
-    const int64_t ld = which ? a.ld_v_token : a.ld_k_token;
-    const int row0 = s.row + (block * kBlock - first);   // row of the block's token 0
-    for (int i = tid; i < (hi - lo) * dim; i += kThreads) {
-        const int r = lo + i / dim, e = i % dim;
-        lds[r * pitch + e] = to_float(from[(row0 + r) * ld + e]);
-    }
-    __syncthreads();
-    if (!which && pairs > 0) {
+    const int row0 = s.row + (block * kBlock - first); // row of the block's token 0
+    const int chunks = dim / 16, items = (hi - lo) * chunks;
+    const bool turns = !which && pairs > 0;
+    if (turns) {
         for (int i = tid; i < (hi - lo) * pairs; i += kThreads) {
-            const int r = lo + i / pairs, p = i % pairs;
-            const float2 t = turn(block * kBlock + r, a.table[p], a.amplitude, 1.f);
-            float* pa = lds + r * pitch + (a.interleaved ? 2 * p : p);
-            float* pb = a.interleaved ? pa + 1 : pa + pairs;
-            const float x = *pa, y = *pb;
-            *pa = x * t.x - y * t.y;
-            *pb = y * t.x + x * t.y;
+            const int r = i / pairs, p = i - r * pairs;
+            cs[i] = turn(block * kBlock + lo + r, a.table[p], a.amplitude, 1.f);
         }
         __syncthreads();
     }
-    float amax = 0.f;
-    for (int i = tid; i < (hi - lo) * dim; i += kThreads) {
-        const float v = fabsf(lds[(lo + i / dim) * pitch + i % dim]);
-        amax = v <= 3.402823466e+38f ? fmaxf(amax, v) : amax;      // neither NaN nor infinite
-    }
+    for (int head = which ? work - groups : work * per; head < (which ? work - groups + 1 : min((work + 1) * per, c.heads)); ++head) {
+        int id = tid;                                  // known anew for every head: what hangs on it alone would be kept for all
+        asm volatile("" : "+v"(id));
+        const int64_t at = place + ((int64_t)head << c.shift);
+        uint8_t* codes = c.codes + at * (2 * kBlock * (int64_t)dim) + (which ? kBlock * dim : 0);
+        float* scale_at = c.scales + at * 2 + which;
+        const float had = lo > 0 ? *scale_at : 0.f;
+        const T* from = static_cast<const T*>(which ? a.v : a.k) + (int64_t)head * (which ? a.ld_v_head : a.ld_k_head);
+        const int64_t ld = which ? a.ld_v_token : a.ld_k_token;
+        float v[NI][16], amax = 0.f;
 #pragma unroll
-    for (int d = 32; d; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
-    if ((tid & 63) == 0) most[tid >> 6] = amax;
-    __syncthreads();
-    amax = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+        for (int n = 0; n < NI; ++n) {
+            const int i = id + n * kThreads, r = i / chunks, chunk = i - r * chunks;
+            if (i >= items) continue;
+            const T* row = from + (row0 + lo + r) * ld;
+            int x0;
+            const int x1 = second_run(chunk, which ? 0 : a.rot, a.interleaved, &x0);
+            if constexpr (VEC) {
+                load8(row + x0, v[n]);
+                load8(row + x1, v[n] + 8);
+            } else if (!turns || a.rot % 16 == 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[n][e] = to_float(row[x0 + e]), v[n][8 + e] = to_float(row[x1 + e]);
+            }
+            if (turns) {
+                const float2* w = cs + r * pairs;
+                if (!VEC && a.rot % 16) {              // an element and its partner at a time
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int d = chunk * 16 + e;
+                        const bool b = a.interleaved ? d & 1 : d >= pairs;
+                        const int p = a.interleaved ? d >> 1 : b ? d - pairs : d, other = a.interleaved ? d ^ 1 : b ? p : d + pairs;
+                        const float x = to_float(row[d]);
+                        v[n][e] = x;
+                        if (d < a.rot) {
+                            const float y = to_float(row[other]);
+                            v[n][e] = b ? x * w[p].x + y * w[p].y : x * w[p].x - y * w[p].y;
+                        }
+                    }
+                } else if (chunk * 16 < a.rot) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 t = w[chunk * 8 + e];
+                        if (a.interleaved) {
+                            const float x = v[n][2 * e], y = v[n][2 * e + 1];
+                            v[n][2 * e] = x * t.x - y * t.y;
+                            v[n][2 * e + 1] = y * t.x + x * t.y;
+                        } else {
+                            const float x = v[n][e], y = v[n][8 + e];
+                            v[n][e] = x * t.x - y * t.y;
+                            v[n][8 + e] = y * t.x + x * t.y;
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) amax = fabsf(v[n][e]) <= 3.402823466e+38f ? fmaxf(amax, fabsf(v[n][e])) : amax;   // neither NaN nor infinite
+        }
+#pragma unroll
+        for (int d = 32; d; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
+        __syncthreads();                               // the head before is done with the LDS
+        if ((tid & 63) == 0) most[tid >> 6] = amax;
+        __syncthreads();
+        amax = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
 
-    float scale = amax / kLargest<FMT>;
-    int up = 0;                                        // doublings of the scale that the block had
-    if (had > 0.f) {
-        if (scale > had) {
-            int en, eh;
-            const float mn = frexpf(scale, &en), mh = frexpf(had, &eh);
-            up = en - eh + (mn > mh);
+        float scale = amax / kLargest<FMT>;
+        int up = 0;                                    // doublings of the scale that the block had
+        if (had > 0.f) {
+            if (scale > had) {
+                int en, eh;
+                const float mn = frexpf(scale, &en), mh = frexpf(had, &eh);
+                up = en - eh + (mn > mh);
+            }
+            scale = ldexpf(had, up);
         }
-        scale = ldexpf(had, up);
-    }
-    const auto code = [&](float v) { return scale > 0.f ? code_of<FMT>(v / scale) : 0u; };
-    const auto moved = [&](uint32_t byte) { return code_of<FMT>(ldexpf(code_value<FMT>(byte & 0xFFu), -up)); };
-    uint4* out = reinterpret_cast<uint4*>(codes);
-    for (int i = tid; i < 2 * dim; i += kThreads) {    // 16 bytes each
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (!which) {                                  // key: 16 elements of token t
-            const int t = i & 31, e = (i >> 5) * 16;
-            if (t >= hi || (t < lo && up == 0)) continue;
-            if (t >= lo) {
+        if (!which && lo > 0 && up > 0) {              // keys that were there
+            for (int i = id; i < lo * chunks; i += kThreads) {
+                uint4* p = reinterpret_cast<uint4*>(codes + (i / lo) * 512 + (i % lo) * 16);
+                const uint4 w = *p;
+                *p = make_uint4(moved4<FMT>(w.x, up), moved4<FMT>(w.y, up), moved4<FMT>(w.z, up), moved4<FMT>(w.w, up));
+            }
+        }
 #pragma unroll
-                for (int j = 0; j < 16; ++j) w[j >> 2] |= code(lds[t * pitch + e + j]) << (8 * (j & 3));
+        for (int n = 0; n < NI; ++n) {
+            const int i = id + n * kThreads, r = i / chunks, chunk = i - r * chunks;
+            if (i >= items) continue;
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (scale > 0.f) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = code4<FMT>(v[n] + 4 * e, scale);
+                    __builtin_amdgcn_sched_barrier(0); // sixteen divisions side by side would take all registers
+                }
+            }
+            int x0;
+            const int x1 = second_run(chunk, which || (!VEC && a.rot % 16) ? 0 : a.rot, a.interleaved, &x0);
+            if (!which) {
+                *reinterpret_cast<uint2*>(codes + (x0 >> 4) * 512 + (lo + r) * 16 + (x0 & 15)) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint2*>(codes + (x1 >> 4) * 512 + (lo + r) * 16 + (x1 & 15)) = make_uint2(w[2], w[3]);
             } else {
-                const uint4 old = out[i];
-                const uint32_t o[4] = {old.x, old.y, old.z, old.w};
+                uint8_t* to = turned + chunk * 16 * kPitch + place_of(lo + r);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) w[j >> 2] |= moved(o[j >> 2] >> (8 * (j & 3))) << (8 * (j & 3));
-            }
-        } else {                                       // value: 16 tokens of element e
-            const int e = i >> 1, h = i & 1;
-            uint4 old = make_uint4(0, 0, 0, 0);
-            if (lo > 0 || hi < kBlock) old = out[i];
-            const uint32_t o[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int t = token_of(h, j);
-                uint32_t byte = (o[j >> 2] >> (8 * (j & 3))) & 0xFFu;
-                if (t >= lo && t < hi) byte = code(lds[t * pitch + e]);
-                else if (t < lo && up) byte = moved(byte);
-                w[j >> 2] |= byte << (8 * (j & 3));
+                for (int e = 0; e < 16; ++e) to[e * kPitch] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
             }
         }
-        out[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (which) {
+            __syncthreads();
+            for (int i = id; i < 2 * dim; i += kThreads) {            // 16 tokens of element i / 2
+                const int h = i & 1;
+                const uint32_t* fresh = reinterpret_cast<const uint32_t*>(turned + (i >> 1) * kPitch + h * 16);
+                uint4* p = reinterpret_cast<uint4*>(codes) + i;
+                uint32_t w[4] = {fresh[0], fresh[1], fresh[2], fresh[3]};
+                if (lo > 0 || hi < kBlock) {           // values that were there, and what is no token's
+                    const uint4 old = *p;
+                    const uint32_t o[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = token_of(h, 4 * e);
+                        const uint32_t now = bytes_between(t, lo, hi), then = bytes_between(t, 0, lo);
+                        const uint32_t before = up > 0 && then ? moved4<FMT>(o[e], up) : o[e];
+                        w[e] = (w[e] & now) | (before & then) | (o[e] & ~(now | then));
+                    }
+                }
+                *p = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        if (tid == 0) *scale_at = scale;
     }
-    if (tid == 0) *scale_at = scale;
 }
 
 // ---- read -------------------------------------------------------------------------
+// Keys and values of a block back to rows, 16 elements of a token to a thread; values change places in LDS.
 template <typename T, int FMT> __global__ __launch_bounds__(kThreads) void k_read(ReadArgs a) {
-    __shared__ uint8_t values[256 * 33];
+    __shared__ __align__(16) uint8_t turned[256 * kPitch];
     const CacheArgs& c = a.c;
-    const int dim = c.dim, tid = threadIdx.x;
+    const int dim = c.dim, tid = threadIdx.x, chunks = dim / 16;
     const int which = blockIdx.x & 1, head = (int)((blockIdx.x >> 1) % c.heads);
     T* to = static_cast<T*>(which ? a.v : a.k);
     if (!to) return;
@@ -235,17 +355,44 @@ template <typename T, int FMT> __global__ __launch_bounds__(kThreads) void k_rea
     const int lo = max(first - block * kBlock, 0), hi = min(s.length - block * kBlock, kBlock);
     const int row0 = s.row + (block * kBlock - first);
     const int64_t at = block_at(c, seq, block, head);
-    const uint8_t* codes = c.codes + at * (2 * kBlock * (int64_t)dim) + which * (kBlock * dim);
+    const uint4* codes = reinterpret_cast<const uint4*>(c.codes + at * (2 * kBlock * (int64_t)dim) + which * (kBlock * dim));
     const float scale = at < 0 ? 0.f : c.scales[at * 2 + which];
     if (which && at >= 0) {
-        for (int i = tid; i < kBlock * dim; i += kThreads) values[(i >> 5) * 33 + (i & 31)] = codes[i];
+        for (int i = tid; i < 2 * dim; i += kThreads) {
+            const uint4 w = codes[i];
+            uint32_t* p = reinterpret_cast<uint32_t*>(turned + (i >> 1) * kPitch + (i & 1) * 16);
+            p[0] = w.x, p[1] = w.y, p[2] = w.z, p[3] = w.w;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    for (int i = tid; i < (hi - lo) * dim; i += kThreads) {
-        const int t = lo + i / dim, e = i % dim;
-        uint32_t byte = 0;
-        if (at >= 0) byte = which ? values[e * 33 + place_of(t)] : codes[(e >> 4) * 512 + t * 16 + (e & 15)];
-        to[((int64_t)(row0 + t) * c.heads + head) * dim + e] = from_float<T>(at < 0 ? 0.f : code_value<FMT>(byte) * scale);
+    for (int i = tid; i < (hi - lo) * chunks; i += kThreads) {
+        const int r = i / chunks, chunk = i - r * chunks, t = lo + r;
+        float v[16];
+        if (at < 0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        } else {
+            uint32_t w[4];
+            if (which) {
+                const uint8_t* p = turned + chunk * 16 * kPitch + place_of(t);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = p[4 * e * kPitch] | p[(4 * e + 1) * kPitch] << 8 | p[(4 * e + 2) * kPitch] << 16 | (uint32_t)p[(4 * e + 3) * kPitch] << 24;
+            } else {
+                const uint4 u = codes[chunk * 32 + t];
+                w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = code_value<FMT>((w[e >> 2] >> (8 * (e & 3))) & 0xFFu) * scale;
+        }
+        T* out = to + ((int64_t)(row0 + t) * c.heads + head) * dim + chunk * 16;
+#pragma unroll
+        for (int u = 0; u < 16 / Vec<T>::N; ++u) {
+            Vec<T> y;
+#pragma unroll
+            for (int e = 0; e < Vec<T>::N; ++e) y.e[e] = from_float<T>(v[u * Vec<T>::N + e]);
+            reinterpret_cast<Vec<T>*>(out)[u] = y;
+        }
     }
 }
 
@@ -284,17 +431,34 @@ hipError_t launch_cache_append(const AppendArgs& a, hipStream_t stream) {
     const CacheArgs& c = a.c;
     const int64_t slots = append_slots(c.tokens, c.batch, c.starts != nullptr);
     const int v = a.dtype ? 8 : 4;
-    const bool vec = whole_units(c.dim, a.rot, a.interleaved, v) && aligned16(a.q) && aligned16(a.q_out) && multiple(a.ld_q_token, v) &&
-                     multiple(a.ld_q_head, v);
-    const dim3 grid((unsigned)(slots * c.heads * 2 + (a.q ? c.tokens : 0)));
-    const size_t lds = (size_t)kBlock * (c.dim + 1) * sizeof(float);
+    const bool vec_q = whole_units(c.dim, a.rot, a.interleaved, v) && aligned16(a.q) && aligned16(a.q_out) && multiple(a.ld_q_token, v) &&
+                       multiple(a.ld_q_head, v);
+    const auto whole = [&](const void* p, int64_t token, int64_t head) { return aligned16(p) && multiple(token, v) && multiple(head, v); };
+    const bool vec = a.rot % 16 == 0 && whole(a.k, a.ld_k_token, a.ld_k_head) && whole(a.v, a.ld_v_token, a.ld_v_head);
+    // key heads of a workgroup share its cosines and sines: up to 8 where there are workgroups enough without
+    int per = (int)(slots * c.heads / 512);
+    per = per < 1 ? 1 : per > 8 ? 8 : per;
+    const int groups = (c.heads + per - 1) / per;
+    const dim3 grid((unsigned)(slots * (groups + c.heads) + (a.q ? c.tokens : 0)));
+    const size_t lds = (size_t)(a.rot / 2) * kBlock * sizeof(float2);
+#define IQ_APPEND(T, FMT)                                                                                    \
+    do {                                                                                                     \
+        if (c.dim <= 128) {                                                                                  \
+            if (vec) k_append<T, FMT, true, 1><<<grid, kThreads, lds, stream>>>(a, slots, per, vec_q);       \
+            else k_append<T, FMT, false, 1><<<grid, kThreads, lds, stream>>>(a, slots, per, vec_q);          \
+        } else {                                                                                             \
+            if (vec) k_append<T, FMT, true, 2><<<grid, kThreads, lds, stream>>>(a, slots, per, vec_q);       \
+            else k_append<T, FMT, false, 2><<<grid, kThreads, lds, stream>>>(a, slots, per, vec_q);          \
+        }                                                                                                    \
+    } while (0)
     if (a.dtype) {
-        if (c.fmt) k_append<uint16_t, 1><<<grid, kThreads, lds, stream>>>(a, slots, vec);
-        else k_append<uint16_t, 0><<<grid, kThreads, lds, stream>>>(a, slots, vec);
+        if (c.fmt) IQ_APPEND(uint16_t, 1);
+        else IQ_APPEND(uint16_t, 0);
     } else {
-        if (c.fmt) k_append<float, 1><<<grid, kThreads, lds, stream>>>(a, slots, vec);
-        else k_append<float, 0><<<grid, kThreads, lds, stream>>>(a, slots, vec);
+        if (c.fmt) IQ_APPEND(float, 1);
+        else IQ_APPEND(float, 0);
     }
+#undef IQ_APPEND
     return hipGetLastError();
 }
 
