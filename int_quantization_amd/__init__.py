@@ -690,7 +690,8 @@ def _bind_fast():
         module = importlib.import_module(__name__ + "._fast")
         module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "iq_layer_norm", "iq_layer_norm_backward", "iq_layer_norm_workspace_bytes", "iq_gated_forward",
-            "iq_gated_backward", "iq_gated_workspace_bytes", "iq_packed_gemv", "iq_packed_gated")))
+            "iq_gated_backward", "iq_gated_workspace_bytes", "iq_packed_gemv", "iq_packed_gated", "iq_rotary", "iq_rotary_backward",
+            "iq_cache_append", "iq_cache_read", "iq_cache_attention", "iq_cache_attention_workspace_bytes")))
         _fast_calls = module
     return _fast_calls
 
@@ -981,6 +982,10 @@ def _heads_of(x, what: str) -> None:
 
 
 def _rotary(call, what: str, x, positions, table, interleaved: bool, amplitude: float, out, stream):
+    if out is None and stream is None:
+        done = (_fast_calls or _bind_fast()).rotary(x, positions, table, bool(interleaved), float(amplitude), call is iq_rotary_backward)
+        if done is not None:
+            return done
     with _place(stream, x):
         torch = _torch()
         _refuse_grad(x, out)
@@ -1068,6 +1073,11 @@ def cache_append(cache: "KVCache", k, v, page_table, lengths, starts=None, *, q=
     among them; starts int32 [batch + 1], the rows where each sequence's new
     tokens begin (None: one token each).  Returns q [tokens, q_heads, dim]
     turned as well, or None without q."""
+    if stream is None and cache.fmt in CACHE_FORMATS:
+        done = (_fast_calls or _bind_fast()).cache_append(cache.codes, cache.scales, CACHE_FORMATS[cache.fmt], cache.heads, cache.dim, cache.page,
+                                                          page_table, lengths, starts, k, v, q, rotary, bool(interleaved), float(amplitude))
+        if done is not None:
+            return done
     with _place(stream, k):
         _refuse_grad(k, v, q)
         dtype = _dtype_of(k, "k")
@@ -1102,6 +1112,12 @@ def cache_read(cache: "KVCache", page_table, lengths, starts, tokens: int, out_d
     """Keys and values [tokens, heads, dim] (bfloat16 by default, or float32) of
     the last starts[b + 1] - starts[b] tokens of every sequence, at rows
     starts[b] on (starts None: the last token of each); `out` a pair of tensors."""
+    f32 = _packed_f32(out_dtype)
+    if out is None and stream is None and f32 is not None and cache.fmt in CACHE_FORMATS:
+        done = (_fast_calls or _bind_fast()).cache_read(cache.codes, cache.scales, CACHE_FORMATS[cache.fmt], cache.heads, cache.dim, cache.page,
+                                                        page_table, lengths, starts, tokens, f32)
+        if done is not None:
+            return done
     with _place(stream, cache.codes):
         codes = cache.codes
         d = _cache_desc(cache, page_table, lengths, starts, tokens, codes)
@@ -1123,6 +1139,12 @@ def cache_attention(cache: "KVCache", q, page_table, lengths, starts=None, *, sc
     `window` the last so many, or with causal=False all.  scale: dim ** -0.5
     by default.  Returns [tokens, q_heads, dim]; rows from starts[batch] on
     are not written."""
+    if out is None and workspace is None and stream is None and cache.fmt in CACHE_FORMATS:
+        done = (_fast_calls or _bind_fast()).cache_attention(cache.codes, cache.scales, CACHE_FORMATS[cache.fmt], cache.heads, cache.dim, cache.page,
+                                                             page_table, lengths, starts, q, cache.dim ** -0.5 if scale is None else float(scale),
+                                                             bool(causal), window)
+        if done is not None:
+            return done
     with _place(stream, q):
         torch = _torch()
         _refuse_grad(q, out)

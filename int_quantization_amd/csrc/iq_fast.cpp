@@ -27,14 +27,22 @@ decltype(&iq_gated_backward) f_gated_backward;
 decltype(&iq_gated_workspace_bytes) f_gated_workspace_bytes;
 decltype(&iq_packed_gemv) f_packed_gemv;
 decltype(&iq_packed_gated) f_packed_gated;
+decltype(&iq_rotary) f_rotary;
+decltype(&iq_rotary_backward) f_rotary_backward;
+decltype(&iq_cache_append) f_cache_append;
+decltype(&iq_cache_read) f_cache_read;
+decltype(&iq_cache_attention) f_cache_attention;
+decltype(&iq_cache_attention_workspace_bytes) f_cache_attention_workspace_bytes;
 
 // bind(address, ...): the entry points in the order above.
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void** to[] = {(void**)&f_layer_norm, (void**)&f_layer_norm_backward, (void**)&f_layer_norm_workspace_bytes,
                    (void**)&f_gated_forward, (void**)&f_gated_backward, (void**)&f_gated_workspace_bytes,
-                   (void**)&f_packed_gemv, (void**)&f_packed_gated};
-    if (n != 8) return PyErr_Format(PyExc_TypeError, "eight addresses");
-    for (int i = 0; i < 8; ++i) {
+                   (void**)&f_packed_gemv, (void**)&f_packed_gated, (void**)&f_rotary, (void**)&f_rotary_backward,
+                   (void**)&f_cache_append, (void**)&f_cache_read, (void**)&f_cache_attention, (void**)&f_cache_attention_workspace_bytes};
+    constexpr int many = sizeof(to) / sizeof(*to);
+    if (n != many) return PyErr_Format(PyExc_TypeError, "%d addresses", many);
+    for (int i = 0; i < many; ++i) {
         *to[i] = PyLong_AsVoidPtr(args[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -231,10 +239,119 @@ PyObject* packed_gated(PyObject* const* a) {
     return THPVariable_Wrap(h);
 }
 
+double number(PyObject* o) { return PyFloat_Check(o) ? PyFloat_AS_DOUBLE(o) : throw Other(); }
+
+// x [tokens, heads, dim] on the current device, the elements of a head contiguous.
+void check_rows(const at::Tensor& x) {
+    need(x.is_cuda() && x.dim() == 3 && x.get_device() == c10::hip::current_device() && (x.stride(2) == 1 || x.size(2) == 1));
+}
+// A table of rotations, at most dim / 2 pairs.
+const double* turns(PyObject* o, const at::Tensor& x, int64_t dim, int32_t* rot) {
+    const at::Tensor& t = tensor(o);
+    need(t.dim() == 1 && 2 * t.size(0) <= dim);
+    check(t, x, at::kDouble, {t.size(0)});
+    *rot = (int32_t)(2 * t.size(0));
+    return t.data_ptr<double>();
+}
+
+// rotary(x, positions, table, interleaved, amplitude, backward)
+PyObject* rotary(PyObject* const* a) {
+    const at::Tensor &x = tensor(a[0]), &at = tensor(a[1]);
+    check_rows(x);
+    check(at, x, at::kInt, {x.size(0)});
+    int32_t rot = 0;
+    const double* table = turns(a[2], x, x.size(2), &rot);
+    at::Tensor y = make(x, {x.size(0), x.size(1), x.size(2)}, x.scalar_type());
+    const iq_rotary_desc d = {dtype(x), a[3] == Py_True, x.size(0), x.size(1), x.size(2), x.stride(0), x.stride(1), y.stride(0), y.stride(1),
+                              rot, (float)number(a[4]), 0, 0};
+    need((a[5] == Py_True ? f_rotary_backward : f_rotary)(&d, x.data_ptr(), at.data_ptr<int32_t>(), table, y.data_ptr(), stream(x)) == IQ_OK);
+    return THPVariable_Wrap(y);
+}
+
+// A cache and its sequences at a[0 .. 8]: codes, scales, format, heads, dim, page, page_table, lengths, starts (or None).
+struct Cache {
+    iq_cache_desc d;
+    void* codes;
+    float* scales;
+    const int32_t *page_table, *lengths, *starts;
+};
+Cache cache_of(PyObject* const* a, const at::Tensor& x, int64_t tokens) {
+    const at::Tensor &codes = tensor(a[0]), &scales = tensor(a[1]), &table = tensor(a[6]), &lengths = tensor(a[7]);
+    const int64_t fmt = whole(a[2]), heads = whole(a[3]), dim = whole(a[4]), page = whole(a[5]);
+    need(heads > 0 && heads <= 1024 && dim > 0 && dim <= 256 && page > 0 && page <= 4096 && codes.dim() == 5 && table.dim() == 2);
+    const int64_t pages = codes.size(0), batch = table.size(0), width = table.size(1), blocks = page / 32;
+    check(codes, x, at::kByte, {pages, heads, blocks, 2, 32 * dim});
+    check(scales, x, at::kFloat, {pages, heads, blocks, 2});
+    check(table, x, at::kInt, {batch, width});
+    check(lengths, x, at::kInt, {batch});
+    Cache c = {{(int32_t)fmt, (int32_t)heads, (int32_t)dim, (int32_t)page, pages, batch, width, 0, 0}, codes.data_ptr(), scales.data_ptr<float>(),
+               table.data_ptr<int32_t>(), lengths.data_ptr<int32_t>(), nullptr};
+    if (a[8] != Py_None) {
+        const at::Tensor& starts = tensor(a[8]);
+        check(starts, x, at::kInt, {batch + 1});
+        c.starts = starts.data_ptr<int32_t>();
+    } else {
+        need(tokens == batch);
+    }
+    return c;
+}
+
+// cache_append(cache and sequences, k, v, q or None, rotary or None, interleaved, amplitude)
+PyObject* cache_append(PyObject* const* a) {
+    const at::Tensor &k = tensor(a[9]), &v = tensor(a[10]);
+    check_rows(k);
+    check_rows(v);
+    const int64_t tokens = k.size(0);
+    const Cache c = cache_of(a, k, tokens);
+    need(k.size(1) == c.d.heads && k.size(2) == c.d.dim && v.sizes() == k.sizes() && v.scalar_type() == k.scalar_type());
+    iq_append_desc d = {dtype(k), a[13] == Py_True, tokens, 0, k.stride(0), k.stride(1), v.stride(0), v.stride(1), 0, 0, 0, (float)number(a[14]), 0, 0};
+    const double* table = a[12] == Py_None ? nullptr : turns(a[12], k, c.d.dim, &d.rot);
+    need(a[11] != Py_None);                            // without queries there is no result that tells the calls apart
+    const at::Tensor& q = tensor(a[11]);
+    check_rows(q);
+    need(q.size(0) == tokens && q.size(2) == c.d.dim && q.scalar_type() == k.scalar_type());
+    d.q_heads = q.size(1);
+    d.ld_q_token = q.stride(0);
+    d.ld_q_head = q.stride(1);
+    at::Tensor out = make(q, {tokens, q.size(1), q.size(2)}, q.scalar_type());
+    need(f_cache_append(&c.d, &d, k.data_ptr(), v.data_ptr(), c.page_table, c.lengths, c.starts, table, q.data_ptr(), out.data_ptr(), c.codes,
+                        c.scales, stream(k)) == IQ_OK);
+    return THPVariable_Wrap(out);
+}
+
+// cache_read(cache and sequences, tokens, out_f32)
+PyObject* cache_read(PyObject* const* a) {
+    const at::Tensor& codes = tensor(a[0]);
+    need(codes.is_cuda() && codes.get_device() == c10::hip::current_device());
+    const int64_t tokens = whole(a[9]);
+    need(tokens >= 0 && tokens < (1 << 24));
+    const Cache c = cache_of(a, codes, tokens);
+    const at::ScalarType type = a[10] == Py_True ? at::kFloat : at::kBFloat16;
+    at::Tensor k = make(codes, {tokens, c.d.heads, c.d.dim}, type), v = make(codes, {tokens, c.d.heads, c.d.dim}, type);
+    need(f_cache_read(&c.d, c.codes, c.scales, c.page_table, c.lengths, c.starts, tokens, k.data_ptr(), v.data_ptr(), a[10] == Py_True ? IQ_F32 : IQ_BF16,
+                      stream(codes)) == IQ_OK);
+    return wrap({k, v});
+}
+
+// cache_attention(cache and sequences, q, scale, causal, window)
+PyObject* cache_attention(PyObject* const* a) {
+    const at::Tensor& q = tensor(a[9]);
+    check_rows(q);
+    const Cache c = cache_of(a, q, q.size(0));
+    need(q.scalar_type() == at::kBFloat16 && q.size(2) == c.d.dim);
+    const iq_attention_desc d = {IQ_BF16, a[11] == Py_True, q.size(0), q.size(1), q.stride(0), q.stride(1), whole(a[12]), (float)number(a[10]), 0};
+    const size_t bytes = f_cache_attention_workspace_bytes(&c.d, &d);
+    need(bytes > 0);
+    at::Tensor o = make(q, {q.size(0), q.size(1), q.size(2)}, at::kBFloat16), ws = make(q, {(int64_t)bytes}, at::kByte);
+    need(f_cache_attention(&c.d, &d, c.codes, c.scales, c.page_table, c.lengths, c.starts, q.data_ptr(), o.data_ptr(), ws.data_ptr(), stream(q)) == IQ_OK);
+    return THPVariable_Wrap(o);
+}
+
 #define IQ_METHOD(name) {#name, (PyCFunction)(void (*)())guarded<name>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {{"bind", (PyCFunction)(void (*)())bind, METH_FASTCALL, nullptr},
                          IQ_METHOD(layer_norm), IQ_METHOD(layer_norm_backward), IQ_METHOD(gated), IQ_METHOD(gated_backward),
-                         IQ_METHOD(packed_gemv), IQ_METHOD(packed_gated), {nullptr, nullptr, 0, nullptr}};
+                         IQ_METHOD(packed_gemv), IQ_METHOD(packed_gated), IQ_METHOD(rotary), IQ_METHOD(cache_append),
+                         IQ_METHOD(cache_read), IQ_METHOD(cache_attention), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
