@@ -61,28 +61,22 @@ constexpr float kLeastFraction = 0x1p-60f;
 // the last bound them all.
 struct View {
     int keys;                    // tokens that the table has entries for
-    int64_t first;               // position of token 0 of the call; may be negative
-    int all_from, all_to;        // some column sees some of these
+    int first;                   // position of token 0 of the call; may be negative
     int each_from, each_to;      // every column sees all of these
-    int block, blocks;           // blocks that hold some
+    int block, blocks;           // blocks that hold some that some column sees
 };
 
-__device__ __forceinline__ int seen_to(const AttendArgs& a, int64_t p, int keys) {
-    return p < 0 ? 0 : a.causal ? (int)min((int64_t)keys, p + 1) : keys;
-}
-__device__ __forceinline__ int seen_from(const AttendArgs& a, int64_t p, int keys) {
-    return (int)min(max((int64_t)0, p + 1 - a.window), (int64_t)keys);
-}
+__device__ __forceinline__ int seen_to(const AttendArgs& a, int p, int keys) { return p < 0 ? 0 : a.causal ? min(keys - 1, p) + 1 : keys; }
+__device__ __forceinline__ int seen_from(const AttendArgs& a, int p, int keys) { return min(max(0, p - (a.window - 1)), keys); }
 
 __device__ __forceinline__ View view_of(const AttendArgs& a, const Tile& t) {
     View v;
-    v.keys = a.c.pages > 0 ? (int)min((int64_t)t.s.length, ((int64_t)a.c.width << a.c.shift) * kBlock) : 0;
-    v.first = (int64_t)t.s.length - t.s.n;
-    const int64_t lo = v.first + t.f0 / a.group, hi = v.first + (t.f0 + t.columns - 1) / a.group;
-    v.all_to = seen_to(a, hi, v.keys); v.all_from = seen_from(a, lo, v.keys);
+    v.keys = a.c.pages > 0 ? min(t.s.length, (a.c.width << a.c.shift) * kBlock) : 0;
+    v.first = t.s.length - t.s.n;
+    const int lo = v.first + t.f0 / a.group, hi = v.first + (t.f0 + t.columns - 1) / a.group;
     v.each_to = seen_to(a, lo, v.keys); v.each_from = seen_from(a, hi, v.keys);
-    v.block = v.all_from / kBlock;
-    v.blocks = max((v.all_to + kBlock - 1) / kBlock - v.block, 0);
+    v.block = seen_from(a, lo, v.keys) / kBlock;
+    v.blocks = max((seen_to(a, hi, v.keys) + kBlock - 1) / kBlock - v.block, 0);
     return v;
 }
 
@@ -367,7 +361,7 @@ __host__ __device__ inline int64_t part_floats(int dim, int columns) { return (i
 struct Open {
     int64_t begin;               // unit that the row begins with
     int64_t per;                 // units of a share
-    int seq, f0, columns, head;
+    int row, f0, columns, head;  // row: of q and o, of the sequence's first token
     int last, unused;            // workgroup that has the row's end
 };
 
@@ -625,7 +619,7 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
         } else {
             if (!whole && skip == 0 && threadIdx.x == 0) {             // the row begins here and goes on
                 Open* open = reinterpret_cast<Open*>(static_cast<char*>(a.workspace) + plan.opens);
-                open[blockIdx.x] = {row_begin, share.per, t.seq, t.f0, t.columns, head, (int)((row_begin + units - 1) / share.per), 0};
+                open[blockIdx.x] = {row_begin, share.per, t.s.row, t.f0, t.columns, head, (int)((row_begin + units - 1) / share.per), 0};
             }
             share.at += take;
             row_begin += units;
@@ -694,7 +688,7 @@ template <int D, int C> __global__ __launch_bounds__(kThreads) void k_join(Atten
         if (p == 0) {
 #pragma unroll
             for (int k = 1; k < P; ++k) sum += sums[k][x];
-            const int f = open.f0 + col, i = f / a.group, gh = f - i * a.group, row = span_of(a.c, open.seq).row + i;
+            const int f = open.f0 + col, i = f / a.group, gh = f - i * a.group, row = open.row + i;
             uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)row * a.q_heads + (int64_t)open.head * a.group + gh) * D;
             union { __bf16 b[4]; uint2 w; } u;
 #pragma unroll
@@ -912,7 +906,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
             }
         }
         if (!whole && skip == 0 && threadIdx.x == 0)   // the row begins here and goes on
-            open[worker] = {row_begin, share.per, t.seq, t.f0, t.columns, head, (int)((row_begin + units - 1) / share.per), 0};
+            open[worker] = {row_begin, share.per, t.s.row, t.f0, t.columns, head, (int)((row_begin + units - 1) / share.per), 0};
         share.at += take;
         row_begin += units;
         ++entry;
@@ -944,7 +938,7 @@ template <int D> __global__ __launch_bounds__(kThreads) void k_join_many(AttendA
         total += w;
         sum += w == 0.f ? (float4v)0.f : o * w;
     }
-    const int f = open.f0 + col, i = f / a.group, gh = f - i * a.group, row = span_of(a.c, open.seq).row + i;
+    const int f = open.f0 + col, i = f / a.group, gh = f - i * a.group, row = open.row + i;
     uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)row * a.q_heads + (int64_t)open.head * a.group + gh) * D;
     union { __bf16 b[4]; uint2 w; } u;
 #pragma unroll

@@ -136,8 +136,7 @@ iqk::AttendArgs attend_args(const iq_cache_desc* d, const iq_attention_desc* a, 
     k.c = cache_args(d, nullptr, nullptr, nullptr, nullptr, starts, a->tokens);
     k.q_heads = (int)a->q_heads; k.group = (int)(a->q_heads / d->heads);
     k.causal = a->causal; k.ld_token = a->ld_token; k.ld_head = a->ld_head;
-    k.window = a->window > 0 ? a->window : (int64_t)1 << 40;
-    if (k.window > ((int64_t)1 << 40)) k.window = (int64_t)1 << 40;
+    k.window = a->window > 0 && a->window < (1 << 30) ? (int)a->window : 1 << 30;
     k.scale = a->scale;
     return k;
 }

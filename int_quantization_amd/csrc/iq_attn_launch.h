@@ -57,7 +57,7 @@ struct AttendArgs {
     int q_heads, group;          // group: query heads of a key head
     int causal;
     int64_t ld_token, ld_head;
-    int64_t window;              // at least 1; as good as none where it is larger than every length
+    int window;                  // 1 to 2^30; the latter is as good as none, since no table has entries for more
     float scale;
     const void* q;
     void* o;
