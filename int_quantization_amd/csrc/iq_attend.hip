@@ -447,7 +447,7 @@ constexpr int kLeastShare = 8;   // blocks of a workgroup, at least
 
 // Waves of a SIMD, and so workgroups of a CU.
 constexpr int few_waves(int dim, int columns) {
-    return columns == 16 ? (dim <= 64 ? 5 : dim <= 128 ? 4 : dim <= 192 ? 3 : 2) : dim <= 64 ? 4 : dim <= 96 ? 3 : dim <= 128 ? 2 : 1;
+    return columns == 16 ? (dim <= 64 ? 3 : 2) : dim <= 64 ? 4 : dim <= 96 ? 3 : dim <= 128 ? 2 : 1;
 }
 
 __device__ __forceinline__ Tile tile_at(const AttendArgs& a, int unit, int seq, const Span& s, int k) {
@@ -710,7 +710,7 @@ constexpr int many_waves(int dim) { return dim <= 64 ? 3 : dim <= 192 ? 2 : 1; }
 
 template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) void k_many(AttendArgs a, Plan plan) {
     using S = Shape<D, 32>;
-    constexpr int C = kManyColumns, J = D / 32, F = D / 16, N = (J + kWaves - 1) / kWaves, kAhead = 5;
+    constexpr int C = kManyColumns, J = D / 32, F = D / 16, N = (J + kWaves - 1) / kWaves, kAhead = D <= 128 ? 5 : 3;
     __shared__ Tile tiles[64];
     __shared__ half8 stage[2][2][F][64];               // [buffer][keys, values][fragment][lane]
     const int lane = threadIdx.x & 63, wave = one(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
