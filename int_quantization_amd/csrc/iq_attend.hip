@@ -388,16 +388,23 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
 // The share of workgroup `worker`; units(e) are those of entry e of `entries` for one head.
 template <typename F>
 __device__ __forceinline__ Share share_of(int worker, int workers, int heads, int64_t entries, int least, const F& units) {
-    __shared__ int64_t sums[kWaves], found[2];
+    __shared__ int64_t sums[kWaves], counts[kWaves], found[2];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t first = threadIdx.x < entries ? units(threadIdx.x) : 0, mine = first;
-    for (int64_t e = threadIdx.x + kThreads; e < entries; e += kThreads) mine += units(e);
+    int64_t first = threadIdx.x < entries ? units(threadIdx.x) : 0, mine = first, some = first > 0;
+    for (int64_t e = threadIdx.x + kThreads; e < entries; e += kThreads) {
+        const int64_t u = units(e);
+        mine += u;
+        some += u > 0;
+    }
     mine = wave_sum(mine);
-    if (lane == 0) sums[wave] = mine;
+    some = wave_sum(some);
+    if (lane == 0) sums[wave] = mine, counts[wave] = some;
     __syncthreads();
     const int64_t one_head = sums[0] + sums[1] + sums[2] + sums[3], total = one_head * heads;
+    const int64_t rows = max(counts[0] + counts[1] + counts[2] + counts[3], (int64_t)1);
     Share s;
-    s.per = max((total + workers - 1) / workers, (int64_t)least);
+    // `least` spares short rows the join; rows shorter than that take a workgroup each, since a row costs several blocks' time to begin with
+    s.per = max(max((total + workers - 1) / workers, min((int64_t)least, one_head / rows)), (int64_t)1);
     s.at = worker * s.per;
     s.end = min(s.at + s.per, total);
     if (s.at >= total) return s;
