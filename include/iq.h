@@ -567,7 +567,7 @@ typedef struct {
  * (as iq_rotary, FP32, not rounded in between), keys and values quantized into
  * their pages, and queries, if there are any, turned by the same positions.
  *   k, v    [tokens, heads, dim] of dtype;  q [tokens, q_heads, dim] or NULL
- *   q_out   dense [tokens, q_heads, dim] of dtype
+ *   q_out   dense [tokens, q_heads, dim] of dtype; may be q where that is dense, otherwise they must not overlap
  *   table   double [rot / 2] (device memory; may be NULL where rot is 0)
  * A block whose first token comes with this call gets s = alpha / 127 or
  * alpha / 448 in FP32, alpha being the largest finite magnitude of its new
@@ -590,7 +590,7 @@ iq_status iq_cache_append(const iq_cache_desc* d, const iq_append_desc* a, const
 /*
  * Reads back: rows starts[b] to starts[b + 1] - 1 of k and v receive the last
  * tokens of sequence b, as iq_cache_append takes them (keys turned), each the code's value times its
- * scale, rounded once to out_dtype.  k and v dense [tokens, heads, dim], 16-byte aligned;
+ * scale, rounded once to out_dtype.  k and v dense [tokens, heads, dim], 16-byte aligned, apart;
  * either may be NULL.  Tokens of absent pages are zeros.  Limits as for iq_cache_append.
  */
 iq_status iq_cache_read(const iq_cache_desc* d, const void* codes, const float* scales, const int32_t* page_table,
@@ -615,7 +615,8 @@ typedef struct {
  * for prompts, for pieces of prompts behind what the cache holds, and for
  * single tokens; the lengths of one call may differ as they like.
  *   q   [tokens, q_heads, dim] BF16, 16-byte aligned, strides multiples of 8 elements (IQ_EALIGN)
- *   o   dense [tokens, q_heads, dim] BF16, 16-byte aligned.  A query that sees nothing gets zeros
+ *   o   dense [tokens, q_heads, dim] BF16, 16-byte aligned; may be q where that is dense, otherwise they must not
+ *       overlap.  A query that sees nothing gets zeros
  *   workspace  iq_cache_attention_workspace_bytes(d, a) bytes, 256-byte aligned, of any content
  * Codes enter the matrix cores exactly, as FP16, and so do queries, scaled by a power of
  * two for each row (elements below 2^-28 of their row's largest lose digits); probabilities are

@@ -963,8 +963,13 @@ int few_columns(const AttendArgs& a) {
 
 // A row of this many blocks is not worth sharing: its workgroup takes it whole,
 // without a search for its share and without the join's launch.
-constexpr int64_t kDirectBlocks = 32;
-bool direct(const AttendArgs& a) { return ((int64_t)a.c.width << a.c.shift) <= kDirectBlocks; }
+constexpr int64_t kDirectBlocks = 32, kDirectRows = 1 << 20;
+int64_t direct_rows(const AttendArgs& a, int columns) {
+    return (int64_t)a.c.batch * (a.c.starts ? kFewColumns / columns : (a.group + columns - 1) / columns);
+}
+bool direct(const AttendArgs& a) {
+    return ((int64_t)a.c.width << a.c.shift) <= kDirectBlocks && direct_rows(a, few_columns(a)) * a.c.heads <= kDirectRows;
+}
 
 struct Plans {
     Plan few, many;
@@ -1000,8 +1005,7 @@ Plans plans_of(const AttendArgs& a) {
 
 template <int D, int FMT, int C> void launch_few(const AttendArgs& a, const Plan& p, hipStream_t stream) {
     if (direct(a)) {
-        const int64_t rows = (int64_t)a.c.batch * (a.c.starts ? kFewColumns / C : (a.group + C - 1) / C);
-        k_few<D, FMT, C, true><<<dim3((unsigned)rows, (unsigned)a.c.heads), kThreads, 0, stream>>>(a, p);
+        k_few<D, FMT, C, true><<<dim3((unsigned)direct_rows(a, C), (unsigned)a.c.heads), kThreads, 0, stream>>>(a, p);
         return;
     }
     k_few<D, FMT, C, false><<<p.workers, kThreads, 0, stream>>>(a, p);

@@ -39,6 +39,9 @@ bool apart(int64_t n, int64_t m, int64_t dim, int64_t ld_n, int64_t ld_m) {
     return (ld_m >= dim && ld_n >= (m - 1) * ld_m + dim) || (ld_n >= dim && ld_m >= (n - 1) * ld_n + dim);
 }
 
+// Whether rows [n, m, dim] with these strides lie as a dense result's do.
+bool dense(int64_t n, int64_t m, int64_t dim, int64_t ld_n, int64_t ld_m) { return (n <= 1 || ld_n == m * dim) && (m <= 1 || ld_m == dim); }
+
 iq_status check_rotary(const iq_rotary_desc* d) {
     if (!d) return IQ_EINVAL;
     if (!known_dtype(d->dtype) || !known_layout(d->layout)) return IQ_EINVAL;
@@ -201,6 +204,7 @@ iq_status iq_cache_append(const iq_cache_desc* d, const iq_append_desc* a, const
     if (block_work(d, a->tokens, starts) + a->tokens > kMostWork) return IQ_EUNSUPPORTED;
     if (a->tokens == 0 || d->batch == 0) return IQ_OK;
     if (!k || !v || (a->rot > 0 && !table) || (a->q_heads > 0 && (!q || !q_out))) return IQ_EINVAL;
+    if (a->q_heads > 0 && q == q_out && !dense(a->tokens, a->q_heads, d->dim, a->ld_q_token, a->ld_q_head)) return IQ_EINVAL;
     if ((st = check_arrays(d, codes, scales, page_table, lengths, starts)) != IQ_OK) return st;
     const uintptr_t e = (uintptr_t)size_of(a->dtype);
     if (!aligned(k, e) || !aligned(v, e) || !aligned(q, e) || !aligned(q_out, e) || !aligned(table, 8)) return IQ_EALIGN;
@@ -223,6 +227,7 @@ iq_status iq_cache_read(const iq_cache_desc* d, const void* codes, const float* 
     if (tokens == 0 || d->batch == 0 || (!k && !v)) return IQ_OK;
     if ((st = check_arrays(d, codes, scales, page_table, lengths, starts)) != IQ_OK) return st;
     if (!aligned(k, 16) || !aligned(v, 16)) return IQ_EALIGN;
+    if (k == v) return IQ_EINVAL;
     iqk::ReadArgs g;
     g.c = cache_args(d, codes, scales, page_table, lengths, starts, tokens);
     g.dtype = out_dtype; g.k = k; g.v = v;
@@ -251,6 +256,7 @@ iq_status iq_cache_attention(const iq_cache_desc* d, const iq_attention_desc* a,
     if (st != IQ_OK) return st;
     if (a->tokens == 0 || d->batch == 0) return IQ_OK;
     if (!q || !o || !workspace) return IQ_EINVAL;
+    if (q == o && !dense(a->tokens, a->q_heads, d->dim, a->ld_token, a->ld_head)) return IQ_EINVAL;
     if ((st = check_arrays(d, codes, scales, page_table, lengths, starts)) != IQ_OK) return st;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(workspace, 256)) return IQ_EALIGN;
     iqk::AttendArgs k = attend_args(d, a, starts);

@@ -314,3 +314,13 @@ def test_binding_refusals(iq):
             read(**kw)
     with pytest.raises(RuntimeError, match="no gradient passes"):
         append(k=x.float().requires_grad_(), v=x.float(), q=None)
+
+
+def test_results_that_lie_on_operands(iq):
+    """q_out and o may be q where that is dense; k and v of a read are apart."""
+    E, d, p = iq.IQ_EINVAL, cache_desc(iq), FAKE
+    for strides in ((512, 64), (256, 128), (64, 192), (0, 64)):
+        a = append_desc(iq, strides=(128, 64, 128, 64, *strides))
+        assert iq.iq_cache_append(d, a, p, p, p, p, p, p, p, p, p, p, None) == E, strides
+        assert iq.iq_cache_attention(d, attention_desc(iq, strides=strides), p, p, p, p, p, p, p, p, None) == E, strides
+    assert iq.iq_cache_read(d, p, p, p, p, p, 3, p, p, 1, None) == E

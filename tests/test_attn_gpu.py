@@ -520,3 +520,112 @@ def test_tensors_that_require_gradients(iq):
             call(leaf)
         want, got = call(q), torch.no_grad()(call)(leaf)
         assert torch.equal(got, want) and not got.requires_grad
+
+
+# ---- calls of many kinds of sequences ---------------------------------------------------------
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim,heads,group", [(64, 2, 8), (96, 3, 2), (128, 1, 6), (192, 2, 3), (256, 1, 4)])
+def test_attention_mixed(iq, fmt, dim, heads, group):
+    """Prompts, pieces behind a long cache, single tokens and sequences without new tokens in one call: rows split among
+    workgroups and whole ones, of both kinds of kernels."""
+    cases = (([0, 3000, 500, 17, 900], [700, 1, 90, 1, 0]), ([2000, 0], [64 // group, 64 // group + 1]), ([1, 1, 4000], [1, 300, 33]))
+    for had, new in cases:
+        cache, q, table, lengths, starts = scene(iq, fmt, heads, group, dim, 64, had, new, dim)
+        for kw in (dict(), dict(causal=False), dict(window=333), dict(window=2500)):
+            a = ao.check_attention(iq, cache, q, table, lengths, starts, what=f"{had} {new} {kw}", **kw)
+            assert torch.equal(a, iq.cache_attention(cache, q, table, lengths, starts, **kw))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_many_short_sequences(iq, fmt):
+    """More sequences than a workgroup has threads, in a wide table: single tokens, and prompts of all short lengths."""
+    n = 600
+    for had, new in (([k % 37 for k in range(n)], [1] * n), ([0] * 90, [k % 45 for k in range(90)])):
+        cache, q, table, lengths, starts = scene(iq, fmt, 2, 4, 64, 32, had, new, 9)
+        wide = torch.full((len(had), 64), -1, dtype=I32, device="cuda")
+        wide[:, :table.shape[1]] = table
+        for t in (wide, table):
+            ao.check_attention(iq, cache, q, t, lengths, starts, what=f"{len(had)}, {t.shape[1]}")
+        if max(new) == 1:
+            ao.check_attention(iq, cache, q, wide, lengths, what="without starts")
+
+
+@pytest.mark.parametrize("width", [8, 200])
+def test_attention_writes_its_rows_only(iq, width):
+    """Rows behind the last sequence stay as they were, in all kernels; sequences whose table is too narrow see what it holds."""
+    for had, new in (([100, 30, 0], [1, 5, 0]), ([400, 90, 0], [150, 1, 40]), ([0], [130])):
+        cache, q, table, lengths, starts = scene(iq, "e4m3", 2, 4, 64, 64, had, new, 5)
+        n = sum(new)
+        t = torch.full((len(had), width), -1, dtype=I32, device="cuda")
+        t[:, :min(width, table.shape[1])] = table[:, :width]
+        long = torch.cat([q, rand(gen(3), 70, 8, 64)])
+        out = torch.full_like(long, 7.0)
+        got = iq.cache_attention(cache, long, t, lengths, starts, out=out)
+        assert got is out and (out[n:] == 7).all()
+        ao.check_attention(iq, cache, q, t, lengths, starts, got=out[:n], what=f"{had}")
+
+
+def test_attention_without_pages(iq):
+    """No pages, no table entries, no tokens, no sequences."""
+    q, one = rand(gen(1), 90, 8, 128), whole([90])
+    empty, some = iq.make_cache(0, 2, 128), iq.make_cache(3, 2, 128)
+    some.scales.fill_(math.nan)
+    for cache, table in ((empty, whole([[0, 1]])), (some, whole([[]]).view(1, 0)), (some, whole([[-1, 3]]))):
+        for rows, starts in ((90, whole([0, 90])), (3, whole([0, 3])), (1, None)):
+            out = torch.full_like(q[:rows], 7.0)
+            assert not iq.cache_attention(cache, q[:rows], table, one, starts, out=out).any()
+            k, v = iq.cache_read(cache, table, one, starts, rows)
+            assert not k.any() and not v.any()
+            iq.cache_append(cache, q[:rows, :2], q[:rows, 2:4], table, one, starts)
+    assert torch.isnan(some.scales).all()
+    assert iq.cache_attention(some, q[:0], whole([[0]]), whole([5]), whole([0, 0])).shape == (0, 8, 128)
+    none = whole([]).view(0, 4)
+    assert iq.cache_attention(some, q[:0], none, whole([])).shape == (0, 8, 128)
+    out = torch.full_like(q, 7.0)
+    assert (iq.cache_attention(some, q, none, whole([]), whole([0]), out=out) == 7).all()
+
+
+def test_results_in_place_of_queries(iq):
+    """Dense queries may be overwritten by their turned form and by their outputs, in all kernels."""
+    freqs = iq.rotary_table(128)
+    for had, new in (([5000, 90], [1, 1]), ([1000], [3]), ([3000, 5], [200, 1])):
+        cache, q, table, lengths, starts = scene(iq, "e4m3", 2, 4, 128, 64, had, new, 8)
+        want = iq.cache_attention(cache, q, table, lengths, starts)
+        here = q.clone()
+        assert iq.cache_attention(cache, here, table, lengths, starts, out=here) is here
+        assert torch.equal(here, want)
+        k = rand(gen(2), sum(new), 2, 128)
+        want = iq.cache_append(cache, k, k, table, lengths, starts, q=q, rotary=freqs)
+        d = iq._cache_desc(cache, table, lengths, starts, sum(new), q)
+        a = iq.IQAppendDesc(iq.IQ_BF16, 0, sum(new), 8, 256, 128, 256, 128, 1024, 128, 128, 1.0, 0, 0)
+        here = q.clone()
+        assert iq.iq_cache_append(d, a, k.data_ptr(), k.data_ptr(), table.data_ptr(), lengths.data_ptr(), starts.data_ptr(), freqs.data_ptr(),
+                                  here.data_ptr(), here.data_ptr(), cache.codes.data_ptr(), cache.scales.data_ptr(),
+                                  torch.cuda.current_stream().cuda_stream) == iq.IQ_OK
+        assert torch.equal(here, want)
+
+
+def test_captured_prompts(iq):
+    """A call with both kinds of sequences captured, in two graphs that share a workspace and are replayed by turns with other
+    lengths, between eager calls."""
+    cache, q, table, lengths, starts = scene(iq, "int8", 2, 4, 64, 64, [1500, 700, 40], [120, 1, 30], 21)
+    need = iq.iq_cache_attention_workspace_bytes(iq._cache_desc(cache, table, lengths, starts, 151, q),
+                                                 iq.IQAttentionDesc(iq.IQ_BF16, 1, 151, 8, 512, 64, 0, 0.125, 0))
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    x, at, outs, graphs = [q.clone(), q.clone()], [lengths.clone(), lengths.clone()], [], []
+    iq.cache_attention(cache, q, table, lengths, starts, workspace=ws)
+    torch.cuda.synchronize()
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(iq.cache_attention(cache, x[i], table, at[i], starts, workspace=ws))
+    full = lengths.tolist()
+    for t in range(12):
+        i = t % 2
+        x[i].copy_(rand(gen(100 + t), 151, 8, 64))
+        at[i].copy_(whole([n - (17 * t) % 30 for n in full]))
+        graphs[i].replay()
+        got = outs[i].clone()
+        want = iq.cache_attention(cache, x[i], table, at[i], starts)
+        assert torch.equal(got, want), t
+        torch.cuda.synchronize()
