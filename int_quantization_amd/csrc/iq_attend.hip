@@ -345,13 +345,7 @@ __device__ __forceinline__ Place place_at(const CacheArgs& c, int seq, int b, in
 // every CU busy.  A row that more than one workgroup has a share of is joined by another launch.
 
 // Sequences of few columns are k_few's, the others k_many's.
-constexpr int kFewColumns = 64;
 enum { kAny = 0, kFew = 1, kMany = 2 };        // which of them a kernel takes: all where the other is not launched
-
-__device__ __forceinline__ bool takes(const AttendArgs& a, int kind, const Span& s) {
-    const bool few = (int64_t)s.n * a.group <= kFewColumns;
-    return s.n > 0 && (kind == kAny || (kind == kFew) == few);
-}
 
 // A row's parts: the normalized output of its columns, their maxima and sums.
 __host__ __device__ inline int64_t part_floats(int dim, int columns) { return (int64_t)columns * (dim + 2); }
@@ -367,10 +361,16 @@ struct Open {
 
 struct Plan {
     int kind, workers;
+    int few;                     // columns that are few
     int slots;                   // of k_many: tiles' slots
     int64_t opens, parts;        // where the Opens and the parts begin in the workspace, in bytes: an Open and two
                                  // parts for every workgroup, of the row that its share begins in (0) and ends in (1)
 };
+
+__device__ __forceinline__ bool takes(const AttendArgs& a, const Plan& plan, const Span& s) {
+    const bool few = (int64_t)s.n * a.group <= plan.few;
+    return s.n > 0 && (plan.kind == kAny || (plan.kind == kFew) == few);
+}
 
 struct Share {
     int64_t at, end, per;        // units
@@ -464,7 +464,7 @@ __device__ __forceinline__ Tile tile_at(const AttendArgs& a, int unit, int seq, 
 
 template <int C> __device__ __forceinline__ int64_t units_of(const AttendArgs& a, const Plan& plan, int seq) {
     const Span s = span_of(a.c, seq);
-    if (!takes(a, plan.kind, s)) return 0;
+    if (!takes(a, plan, s)) return 0;
     const int tiles = (int)(((int64_t)s.n * a.group + C - 1) / C);
     if (s.n == 1) return (int64_t)tiles * max(view_of(a, tile_at(a, C, seq, s, 0)).blocks, 1);      // tiles of one token see the same
     int64_t sum = 0;
@@ -482,11 +482,10 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
     int seq, tile = 0;
     Span span;
     if constexpr (DIRECT) {                            // a workgroup for each row
-        const int per = a.c.starts ? kFewColumns / C : (a.group + C - 1) / C;
-        seq = blockIdx.x / per;
-        tile = blockIdx.x % per;
+        seq = blockIdx.x % a.c.batch;                  // tiles that few sequences have come last: they leave no XCD without work
+        tile = blockIdx.x / a.c.batch;
         span = span_of(a.c, seq);
-        if (!takes(a, plan.kind, span) || (int64_t)tile * C >= (int64_t)span.n * a.group) return;
+        if (!takes(a, plan, span) || (int64_t)tile * C >= (int64_t)span.n * a.group) return;
         share.head = blockIdx.y;
     } else {
         Open* open = reinterpret_cast<Open*>(static_cast<char*>(a.workspace) + plan.opens);
@@ -503,7 +502,7 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
     while (true) {
         if (!DIRECT) {
             if (share.at >= share.end) break;
-            if ((int64_t)tile * C >= (int64_t)span.n * a.group || !takes(a, plan.kind, span)) {     // the next sequence, or head
+            if ((int64_t)tile * C >= (int64_t)span.n * a.group || !takes(a, plan, span)) {     // the next sequence, or head
                 if (++seq == a.c.batch) {
                     seq = 0;
                     if (++share.head >= a.c.heads) break;              // the arrays changed meanwhile
@@ -717,7 +716,7 @@ constexpr int many_waves(int dim) { return dim <= 64 ? 3 : dim <= 192 ? 2 : 1; }
 
 template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) void k_many(AttendArgs a, Plan plan) {
     using S = Shape<D, 32>;
-    constexpr int C = kManyColumns, J = D / 32, F = D / 16, N = (J + kWaves - 1) / kWaves, kAhead = D <= 128 ? 5 : 3;
+    constexpr int C = kManyColumns, J = D / 32, F = D / 16, N = (J + kWaves - 1) / kWaves, kAhead = 3;
     __shared__ Tile tiles[64];
     __shared__ half8 stage[2][2][F][64];               // [buffer][keys, values][fragment][lane]
     const int lane = threadIdx.x & 63, wave = one(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
@@ -728,7 +727,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
     // tokens and its last ones many, and a share of either alone would hold many rows or few.
     const auto row_at = [&](int64_t e, Tile* t) {
         const int64_t slot = e & 1 ? plan.slots - 1 - (e >> 1) : e >> 1;
-        return tile_of(a, C, slot, t) && takes(a, plan.kind, t->s);
+        return tile_of(a, C, slot, t) && takes(a, plan, t->s);
     };
     Share share = share_of(worker, plan.workers, a.c.heads, plan.slots, kLeastManyShare, [&](int64_t e) -> int64_t {
         Tile t;
@@ -934,9 +933,10 @@ template <int D> __global__ __launch_bounds__(kThreads) void k_join_many(AttendA
         return parts + (w * 2 + (w * open.per < open.begin ? 1 : 0)) * part_floats(D, C);
     };
     float top = -INFINITY, total = 0.f;
+#pragma unroll 8
     for (int k = 0; k < many; ++k) top = fmaxf(top, part_of(k)[C * D + col]);
     float4v sum = 0.f;
-#pragma unroll 2
+#pragma unroll 8
     for (int k = 0; k < many; ++k) {
         const float* p = part_of(k);
         const float m = p[C * D + col], l = p[C * (D + 1) + col];
@@ -954,6 +954,13 @@ template <int D> __global__ __launch_bounds__(kThreads) void k_join_many(AttendA
 }
 
 // ---- launches ----------------------------------------------------------------------------
+// Columns of a sequence that are few.
+constexpr int kFewColumns = 64, kFewColumnsShort = 128, kShortUnits = 8192;
+int few_limit(const AttendArgs& a) {
+    const int64_t units = ((int64_t)a.c.width << a.c.shift) * a.c.heads * a.c.batch;
+    return a.c.dim <= 128 && (int64_t)a.c.tokens * a.group <= (int64_t)kFewColumnsShort * a.c.batch && units <= kShortUnits ? kFewColumnsShort : kFewColumns;
+}
+
 // 16 columns to a wave where that holds a sequence's columns: half the work
 // on them, and room for twice as many waves.
 int few_columns(const AttendArgs& a) {
@@ -963,12 +970,14 @@ int few_columns(const AttendArgs& a) {
 
 // A row of this many blocks is not worth sharing: its workgroup takes it whole,
 // without a search for its share and without the join's launch.
-constexpr int64_t kDirectBlocks = 32, kDirectRows = 1 << 20;
+constexpr int64_t kDirectBlocks = 64, kDirectManyBlocks = 128, kDirectManyRows = 128, kDirectRows = 1 << 20;
 int64_t direct_rows(const AttendArgs& a, int columns) {
-    return (int64_t)a.c.batch * (a.c.starts ? kFewColumns / columns : (a.group + columns - 1) / columns);
+    return (int64_t)a.c.batch * (a.c.starts ? few_limit(a) / columns : (a.group + columns - 1) / columns);
 }
 bool direct(const AttendArgs& a) {
-    return ((int64_t)a.c.width << a.c.shift) <= kDirectBlocks && direct_rows(a, few_columns(a)) * a.c.heads <= kDirectRows;
+    const int64_t blocks = (int64_t)a.c.width << a.c.shift;
+    return blocks <= ((int64_t)a.c.batch * a.c.heads < kDirectManyRows ? kDirectBlocks : kDirectManyBlocks) &&
+           direct_rows(a, few_columns(a)) * a.c.heads <= kDirectRows;
 }
 
 struct Plans {
@@ -982,7 +991,9 @@ Plans plans_of(const AttendArgs& a) {
     int64_t at = 0;
     const auto room = [&](int64_t bytes) { const int64_t here = at; at += (bytes + 255) / 256 * 256; return here; };
     // which kernels some sequence may be for; of one sequence the host knows nothing better than that it has all rows
-    const bool many = a.c.starts && rows > kFewColumns, few = !many || a.c.batch > 1;
+    const int limit = few_limit(a);
+    const bool many = a.c.starts && rows > limit, few = !many || a.c.batch > 1;
+    p.few.few = p.many.few = limit;
     if (few) {
         const int columns = few_columns(a);
         p.few.kind = many ? kFew : kAny;

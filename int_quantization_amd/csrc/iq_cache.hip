@@ -162,7 +162,7 @@ __device__ __forceinline__ uint32_t bytes_between(int t, int lo, int hi) {
 // take 43 us, 4.3 TB/s.
 constexpr int kPitch = 36;
 
-template <typename T, int FMT, bool VEC, int NI> __global__ __launch_bounds__(kThreads, NI == 1 ? 6 : 4) void k_append(AppendArgs a, int64_t slots, int per, bool vec_q) {
+template <typename T, int FMT, bool VEC, int NI> __global__ __launch_bounds__(kThreads, 4) void k_append(AppendArgs a, int64_t slots, int per, bool vec_q) {
     __shared__ __align__(16) uint8_t turned[256 * kPitch];
     __shared__ float most[kThreads / 64];
     extern __shared__ float2 cs[];                     // [new tokens of the block][pairs]

@@ -537,6 +537,18 @@ def test_attention_mixed(iq, fmt, dim, heads, group):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim,heads,group", [(64, 2, 8), (96, 3, 3), (128, 1, 4), (192, 2, 4)])
+def test_attention_short_pieces(iq, fmt, dim, heads, group):
+    """Calls of short pieces only, up to and past 64 and 128 columns, behind short and long caches."""
+    for had in (0, 600, 5000):
+        for columns in ([128], [129], [65, 128, 40], [70] * 5, [128, 129, 1]):
+            new = [max(1, n // group) for n in columns]
+            cache, q, table, lengths, starts = scene(iq, fmt, heads, group, dim, 64, [had] * len(new), new, dim)
+            for kw in (dict(), dict(window=100)):
+                ao.check_attention(iq, cache, q, table, lengths, starts, what=f"{had} {new} {kw}", **kw)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_attention_many_short_sequences(iq, fmt):
     """More sequences than a workgroup has threads, in a wide table: single tokens, and prompts of all short lengths."""
     n = 600
