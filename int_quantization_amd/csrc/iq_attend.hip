@@ -403,7 +403,8 @@ __device__ __forceinline__ Share share_of(int worker, int workers, int heads, in
     const int64_t one_head = sums[0] + sums[1] + sums[2] + sums[3], total = one_head * heads;
     const int64_t rows = max(counts[0] + counts[1] + counts[2] + counts[3], (int64_t)1);
     Share s;
-    // `least` spares short rows the join; rows shorter than that take a workgroup each, since a row costs several blocks' time to begin with
+    // `least` spares short rows the join.  Rows shorter than that take a workgroup each, since a row costs several
+    // blocks' time to begin with: 5 prompts of 18 to 25 tokens take 24 us, 122 with 16 rows to a workgroup.
     s.per = max(max((total + workers - 1) / workers, min((int64_t)least, one_head / rows)), (int64_t)1);
     s.at = worker * s.per;
     s.end = min(s.at + s.per, total);
@@ -449,10 +450,19 @@ __device__ __forceinline__ Column column_of(const AttendArgs& a, const Tile& t, 
 
 // ---- few columns: the work is the cache's codes ------------------------------------------
 // A workgroup's four waves take a row's blocks in turn, each with the next
-// block's codes in flight, and join their outputs through LDS.
-constexpr int kLeastShare = 8;   // blocks of a workgroup, at least
+// block's codes in flight, and join their outputs through LDS.  Codes go from memory to registers in the order in which
+// the matrix cores take them, so LDS holds none, and waves wait for nothing but their own loads.
+// HBM bounds it: 64 sequences of 1024 to 16384 tokens (8 key heads of 128, 1.14 GB of codes) take 202 us, 5.6 TB/s
+// (a large read: 5.8 to 7.0); one of 131072 tokens (268 MB) 52 us, 5.2 TB/s, and 7 for the join.  Fetching two blocks
+// ahead is slower by 1% (its registers), and so are 32 columns where 16 are enough (`few_columns`).
 
-// Waves of a SIMD, and so workgroups of a CU.
+// Blocks of a workgroup, at least.  One sequence of 8000 tokens takes 19.4 us, 23.2 with 4 and 19.6 with 16; one of 2000
+// takes 17.3, and 18.6 with 16.
+constexpr int kLeastShare = 8;
+
+// Waves of a SIMD, and so workgroups of a CU: as many as registers allow, but for 16 columns of 96 elements and more,
+// where two take 212 us for the 64 sequences above and 61 for the long one, three 212 and 66, four 217 and 69: more
+// workgroups mean more parts to join, and two have enough codes in flight.
 constexpr int few_waves(int dim, int columns) {
     return columns == 16 ? (dim <= 64 ? 3 : 2) : dim <= 64 ? 4 : dim <= 96 ? 3 : dim <= 128 ? 2 : 1;
 }
@@ -707,16 +717,25 @@ template <int D, int C> __global__ __launch_bounds__(kThreads) void k_join(Atten
 
 // ---- many columns: the work is products ----------------------------------------------------
 // A workgroup takes 128 columns, 32 to a wave.  Its waves turn a block's codes
-// into FP16 once, in LDS and in the order in which the matrix cores take them.
+// into FP16 once, in LDS and in the order in which the matrix cores take them; two blocks are there, one read, one made.
+// The issue of instructions bounds it: for a block of 32 tokens a wave of 128 elements has 16 products (512 cycles) and
+// about 600 cycles of vector work (conversion, maxima, exponentials, rounding), and two waves of a SIMD overlap them to
+// about 1200 cycles for both kinds of both.  A prompt of 8192 tokens (32 heads of 128 on 8; 550 GFLOP) takes 585 to 690 us, 0.80 to
+// 0.94 PFLOP/s, and 20 for the join.  Priority for the wave in its products gains 5%; rows in the order of `row_at` 12%;
+// 64 columns a wave cost their output registers' copies (1506 us), three LDS buffers 690 to 723 against 698.
 constexpr int kManyColumns = kWaves * 32;
-constexpr int kLeastManyShare = 16;      // blocks of a workgroup, at least
 
-// Waves of a SIMD, and so workgroups of a CU.
+// Blocks of a workgroup, at least: prompts of 77 to 2047 tokens (12 heads of 64) take 71 us, 74 with 24.
+constexpr int kLeastManyShare = 16;
+
+// Waves of a SIMD, and so workgroups of a CU: as many as LDS and registers allow.  Prompts of 4096 tokens of 64 elements
+// take 129 us with 3 and 135 with 2; of 2048 tokens of 192 elements 112 with 2 and 136 with 1.
 constexpr int many_waves(int dim) { return dim <= 64 ? 3 : dim <= 192 ? 2 : 1; }
 
 template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) void k_many(AttendArgs a, Plan plan) {
     using S = Shape<D, 32>;
-    constexpr int C = kManyColumns, J = D / 32, F = D / 16, N = (J + kWaves - 1) / kWaves, kAhead = 3;
+    constexpr int C = kManyColumns, J = D / 32, F = D / 16, N = (J + kWaves - 1) / kWaves;
+    constexpr int kAhead = 3;                          // fragments read before their products (with 5: 1% slower)
     __shared__ Tile tiles[64];
     __shared__ half8 stage[2][2][F][64];               // [buffer][keys, values][fragment][lane]
     const int lane = threadIdx.x & 63, wave = one(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
@@ -920,7 +939,8 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
     }
 }
 
-// Joins the parts of a row of many columns: D / 4 threads for each of several columns.
+// Joins the parts of a row of many columns: D / 4 threads for each of several columns.  The parts' bytes bound it, written
+// and read once each: 14 to 20 us after prompts.  Eight parts are loaded together (one row of 63 parts: 121 to 108 us in all).
 template <int D> __global__ __launch_bounds__(kThreads) void k_join_many(AttendArgs a, Plan plan) {
     constexpr int Q = D / 4, P = kThreads / Q, C = kManyColumns;
     const Open open = reinterpret_cast<const Open*>(static_cast<const char*>(a.workspace) + plan.opens)[blockIdx.x];
@@ -954,22 +974,29 @@ template <int D> __global__ __launch_bounds__(kThreads) void k_join_many(AttendA
 }
 
 // ---- launches ----------------------------------------------------------------------------
-// Columns of a sequence that are few.
+// Columns of a sequence that are few: two tiles of k_few read the codes as often as one of k_many and start sooner.
+// 64: 12 tokens of 4 heads (48 columns) at 2000 tokens take 29 us, 39 in k_many; at 32000 48 and 113.
+// 128 where all sequences are pieces of that size and their blocks are few for the GPU, for k_many's waves then wait for
+// their codes alone: 24 tokens (96 columns) at 8000 tokens take 37 us, 60 in k_many; four such 61 and 66; past 8192 blocks
+// eight such take 95, and 80 in k_many, 32 of them 335 and 205.  Heads of 192 elements and more have one wave a SIMD in
+// k_few: 16 prompts of 20 to 30 tokens (256 elements) 31 us, and 25 in k_many.
 constexpr int kFewColumns = 64, kFewColumnsShort = 128, kShortUnits = 8192;
 int few_limit(const AttendArgs& a) {
     const int64_t units = ((int64_t)a.c.width << a.c.shift) * a.c.heads * a.c.batch;
     return a.c.dim <= 128 && (int64_t)a.c.tokens * a.group <= (int64_t)kFewColumnsShort * a.c.batch && units <= kShortUnits ? kFewColumnsShort : kFewColumns;
 }
 
-// 16 columns to a wave where that holds a sequence's columns: half the work
-// on them, and room for twice as many waves.
+// 16 columns to a wave where that holds a sequence's columns: half the work on them.  8 sequences of 4 tokens of 4 heads
+// at 8000 tokens take 44 us, 47 with 32 columns; with 8 tokens (32 columns) 64 in two tiles of 16, 53 in one of 32.
 int few_columns(const AttendArgs& a) {
     const int64_t columns = a.c.starts ? (int64_t)a.c.tokens * a.group / (a.c.batch > 0 ? a.c.batch : 1) : a.group;
     return columns <= 16 ? 16 : 32;
 }
 
-// A row of this many blocks is not worth sharing: its workgroup takes it whole,
-// without a search for its share and without the join's launch.
+// A row of this many blocks is not worth sharing: its workgroup takes it whole, without a search for its share and
+// without the join's launch.  One sequence of 2000 tokens takes 14.4 us, 17.6 shared; of 4000 tokens 23.0 and 18.2.  Where
+// rows fill half the CUs twice as many blocks are not worth it: 16 sequences of 4000 tokens 26.8 and 34.0, 64 of 100 to 4000 tokens 62
+// and 78, but 4 of 4000 24.1 and 21.9.  kDirectRows bounds the launch where most sequences have no tokens.
 constexpr int64_t kDirectBlocks = 64, kDirectManyBlocks = 128, kDirectManyRows = 128, kDirectRows = 1 << 20;
 int64_t direct_rows(const AttendArgs& a, int columns) {
     return (int64_t)a.c.batch * (a.c.starts ? few_limit(a) / columns : (a.group + columns - 1) / columns);
