@@ -1138,7 +1138,7 @@ def cache_attention(cache: "KVCache", q, page_table, lengths, starts=None, *, sc
     among it: softmax(scale q k) v over tokens up to the row's own, or with
     `window` the last so many, or with causal=False all.  scale: dim ** -0.5
     by default.  Returns [tokens, q_heads, dim]; rows from starts[batch] on
-    are not written."""
+    are not written.  out may be q itself where that is dense."""
     if out is None and workspace is None and stream is None and cache.fmt in CACHE_FORMATS:
         done = (_fast_calls or _bind_fast()).cache_attention(cache.codes, cache.scales, CACHE_FORMATS[cache.fmt], cache.heads, cache.dim, cache.page,
                                                              page_table, lengths, starts, q, cache.dim ** -0.5 if scale is None else float(scale),
