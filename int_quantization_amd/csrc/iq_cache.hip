@@ -37,14 +37,16 @@ __device__ __forceinline__ float2 turn(int position, double turns, float amplitu
 }
 
 // Turns the heads [head0, head1) of one token.  cs: cosine and sine of its pairs, in LDS.
-//   VEC: 16-byte units, where strides, bases and the ends of what turns are multiples of them.
+//   VEC: 16-byte units, where strides, bases and the ends of what turns are multiples of them.  Otherwise single
+//   elements, but for those from `edge` on, which are copied in such units (dim: none are).
 template <typename T, bool INTER, bool VEC>
 __device__ __forceinline__ void turn_token(const T* x, T* y, int64_t ldx, int64_t ldy, int head0, int head1, int dim, int rot,
-                                           const float2* cs, int thread, int threads) {
+                                           int edge, const float2* cs, int thread, int threads) {
     constexpr int V = VEC ? Vec<T>::N : 1;
     const int pairs = rot >> 1;
     const int turned = INTER ? (VEC ? rot / V : pairs) : pairs / V;     // units that hold pairs
-    const int rest = x == y ? 0 : (dim - rot) / V;                        // units to copy
+    const int single = (edge - rot) / V;                                  // units to copy: of V, then of 16 bytes
+    const int rest = x == y ? 0 : single + (dim - edge) / Vec<T>::N;
     const int units = turned + rest;
     if (units == 0) return;
     const float inv = 1.f / (float)units;
@@ -55,8 +57,8 @@ __device__ __forceinline__ void turn_token(const T* x, T* y, int64_t ldx, int64_
         const T* from = x + (head0 + head) * ldx;
         T* to = y + (head0 + head) * ldy;
         if (u >= turned) {
-            const int at = rot + (u - turned) * V;
-            if constexpr (VEC) *reinterpret_cast<Vec<T>*>(to + at) = *reinterpret_cast<const Vec<T>*>(from + at);
+            const int r = u - turned, at = r < single ? rot + r * V : edge + (r - single) * Vec<T>::N;
+            if (VEC || r >= single) *reinterpret_cast<Vec<T>*>(to + at) = *reinterpret_cast<const Vec<T>*>(from + at);
             else to[at] = from[at];
         } else if constexpr (INTER && VEC) {
             Vec<T> v = *reinterpret_cast<const Vec<T>*>(from + u * V);
@@ -94,14 +96,14 @@ __device__ __forceinline__ void turn_token(const T* x, T* y, int64_t ldx, int64_
 // launch and the 64-bit angles.
 constexpr int kMostPairs = 512;
 
-template <typename T, bool INTER, bool VEC> __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs a) {
+template <typename T, bool INTER, bool VEC> __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs a, int edge) {
     __shared__ float2 cs[kMostPairs];
     const int t = blockIdx.x;
     const int position = a.positions[t];
     for (int p = threadIdx.x; p < a.rot / 2; p += kThreads) cs[p] = turn(position, a.table[p], a.amplitude, a.way);
     __syncthreads();
     turn_token<T, INTER, VEC>(static_cast<const T*>(a.x) + t * a.ld_token, static_cast<T*>(a.y) + t * a.ld_token_out, a.ld_head,
-                              a.ld_head_out, 0, a.heads, a.dim, a.rot, cs, threadIdx.x, kThreads);
+                              a.ld_head_out, 0, a.heads, a.dim, a.rot, edge, cs, threadIdx.x, kThreads);
 }
 
 // ---- append -----------------------------------------------------------------------
@@ -186,11 +188,11 @@ template <typename T, int FMT, bool VEC, int NI> __global__ __launch_bounds__(kT
         const T* x = static_cast<const T*>(a.q) + row * a.ld_q_token;
         T* y = static_cast<T*>(a.q_out) + (int64_t)row * a.q_heads * dim;
         if (vec_q) {
-            if (a.interleaved) turn_token<T, true, true>(x, y, a.ld_q_head, dim, 0, a.q_heads, dim, a.rot, cs, tid, kThreads);
-            else turn_token<T, false, true>(x, y, a.ld_q_head, dim, 0, a.q_heads, dim, a.rot, cs, tid, kThreads);
+            if (a.interleaved) turn_token<T, true, true>(x, y, a.ld_q_head, dim, 0, a.q_heads, dim, a.rot, dim, cs, tid, kThreads);
+            else turn_token<T, false, true>(x, y, a.ld_q_head, dim, 0, a.q_heads, dim, a.rot, dim, cs, tid, kThreads);
         } else {
-            if (a.interleaved) turn_token<T, true, false>(x, y, a.ld_q_head, dim, 0, a.q_heads, dim, a.rot, cs, tid, kThreads);
-            else turn_token<T, false, false>(x, y, a.ld_q_head, dim, 0, a.q_heads, dim, a.rot, cs, tid, kThreads);
+            if (a.interleaved) turn_token<T, true, false>(x, y, a.ld_q_head, dim, 0, a.q_heads, dim, a.rot, dim, cs, tid, kThreads);
+            else turn_token<T, false, false>(x, y, a.ld_q_head, dim, 0, a.q_heads, dim, a.rot, dim, cs, tid, kThreads);
         }
         return;
     }
@@ -413,13 +415,17 @@ bool whole_units(int dim, int rot, bool interleaved, int v) {
 
 hipError_t launch_rotary(const RotaryArgs& a, hipStream_t stream) {
     const int v = a.dtype ? 8 : 4;
-    const bool vec = whole_units(a.dim, a.rot, a.interleaved, v) && aligned16(a.x) && aligned16(a.y) && multiple(a.ld_token, v) &&
-                     multiple(a.ld_head, v) && multiple(a.ld_token_out, v) && multiple(a.ld_head_out, v);
+    const bool rows = multiple(a.dim, v) && aligned16(a.x) && aligned16(a.y) && multiple(a.ld_token, v) && multiple(a.ld_head, v) &&
+                      multiple(a.ld_token_out, v) && multiple(a.ld_head_out, v);
+    const bool vec = rows && whole_units(a.dim, a.rot, a.interleaved, v);
+    // few elements that turn leave most to copy: 4 of 192 (3589 tokens of 35 heads BF16, 193 MB there and back)
+    // take 50 us, 108 element by element
+    const int edge = rows ? (a.rot + v - 1) / v * v : a.dim;
     const dim3 grid((unsigned)a.tokens);
 #define IQ_ROTARY(T, INTER)                                                          \
     do {                                                                             \
-        if (vec) k_rotary<T, INTER, true><<<grid, kThreads, 0, stream>>>(a);         \
-        else k_rotary<T, INTER, false><<<grid, kThreads, 0, stream>>>(a);            \
+        if (vec) k_rotary<T, INTER, true><<<grid, kThreads, 0, stream>>>(a, edge);   \
+        else k_rotary<T, INTER, false><<<grid, kThreads, 0, stream>>>(a, edge);      \
     } while (0)
     if (a.dtype) {
         if (a.interleaved) IQ_ROTARY(uint16_t, true);

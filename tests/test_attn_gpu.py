@@ -68,6 +68,21 @@ def test_rotary_sizes(iq, dtype, inter):
                 check_rotary(iq, x, at, iq.rotary_table(rot), inter, 1.25, what=f"{tokens} x {heads} x {dim}, {rot}")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotary_of_few_elements(iq, dtype, inter):
+    """Ends of what turns inside 16 bytes, whole rows and rows that start anywhere, into a new result and in place."""
+    g = gen(40)
+    for dim, rots in ((192, (0, 2, 4, 10, 186, 190)), (40, (2, 6, 34, 38)), (8, (2, 6, 8)), (44, (2, 4, 42))):
+        for rot in rots:
+            table, at = iq.rotary_table(rot), whole([3, 70000, -5, 0, 11])
+            wide = rand(g, 5, 3, dim + 3, dtype=dtype)
+            for x in (rand(g, 5, 3, dim, dtype=dtype), wide[..., :dim], wide[..., 3:]):
+                check_rotary(iq, x, at, table, inter, what=f"{dim} {rot}")
+                want, here = iq.rotary(x, at, table, interleaved=inter), x.clone(memory_format=torch.contiguous_format)
+                assert torch.equal(iq.rotary(here, at, table, interleaved=inter, out=here), want)
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_rotary_strides_and_in_place(iq, inter):
     g = gen(2)
