@@ -619,10 +619,10 @@ typedef struct {
  *       overlap.  A query that sees nothing gets zeros
  *   workspace  iq_cache_attention_workspace_bytes(d, a) bytes, 256-byte aligned, of any content
  * Codes enter the matrix cores exactly, as FP16, and so do queries, scaled by a power of
- * two for each row (elements below 2^-28 of their row's largest lose digits); probabilities are
- * rounded to FP16 (half a step: 2^-11, of those below 2^-23 of the largest 2^-34 of that); sums, maxima and the
- * running output are FP32.
- * Values whose block's scale is below 2^-60 of a scale before it count as of that size.  Tokens that a query does
+ * two for each row (elements below 2^-28 of their row's largest lose digits); probabilities times
+ * their block's values scale are rounded to FP16 (half a step: 2^-11; of those below 2^-23 of the largest such product that the
+ * query has seen 2^-34 of that); sums, maxima and the running output are FP32, and probabilities below 2^-126 may count as 0.
+ * Tokens that a query does
  * not see add nothing, whatever their codes and scales hold; a NaN or an infinity in a query makes that
  * query's output NaN.  Scales are expected to be finite and >= 0; NaN codes of E4M3 (which iq_cache_append never writes)
  * in tokens that a sequence holds may make any of that sequence's outputs of their head NaN.

@@ -48,14 +48,15 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 
 // Probabilities are relative to a running maximum m that follows the scores
 // once one is 2^kSlack past it, so a block rarely costs a rescaling of the
-// output.  They are held times 2^kLift: at most 2^15 in FP16, with all digits
-// from 2^-23 on and steps of 2^-33 below.  The factor leaves with the division by their sum.
+// output.  What the matrix cores take is a probability times its block's values scale, over the largest such product
+// 2^(m + z) so far, which is followed as m is: blocks that a column does not see, or sees with next to no probability, take
+// no digits from the others.  It is held times 2^kLift: at most 2^15 in FP16, with all digits from 2^-23 of the
+// largest product on and steps of 2^-33 of that below.
 constexpr float kSlack = 6.f, kLift = 9.f;
 
-// The block's values scale enters the exponent, as a fraction of the power of
-// two above the largest so far; a fraction below 2^-60 counts as 2^-60, where values are 2^-50 of
-// what the row holds already.
-constexpr float kLeastFraction = 0x1p-60f;
+// Log2 of a block's values scale over 2^z, at least: what FP16 leaves nothing of, and FP32 enough for the sum, so that
+// blocks of small values or none (scale 0) still count in it.
+constexpr float kLeastRatio = -60.f, kMostRatio = 1000.f;                 // at most: 2^z is 0 until a value other than 0 is seen
 
 // What a tile's columns see.  Columns are sorted by position, so the first and
 // the last bound them all.
@@ -228,19 +229,20 @@ template <int D, int C> __device__ __forceinline__ float load_query(float scale,
     return top >= 0x7F800000u ? __builtin_nanf("") : ldexpf(scale * 1.44269504f, e);
 }
 
-// Running state of a column: maximum, sum of this lane's tokens, output.
+// Log2 of a scale, subnormal ones too; -inf of 0.
+__device__ __forceinline__ float log2_of(float x) { return __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(x)) + (float)__builtin_amdgcn_frexp_expf(x); }
+
+// Running state of a column: maximum, sum of this lane's tokens' probabilities over 2^m, output over 2^(m + z - kLift).
 template <int D, int C> struct State {
     using S = Shape<D, C>;
     typename S::Tile o[S::kTiles];
-    float m, l;
-    int size;                    // values' scales are held over this power of two (its bits), above the largest so far
+    float m, l, z;
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int j = 0; j < S::kTiles; ++j) o[j] = 0.f;
-        m = -INFINITY;
+        m = z = -INFINITY;
         l = 0.f;
-        size = 1 << 23;
     }
     // The largest of the lane's scores, as an exponent of 2.
     static __device__ __forceinline__ float top_of(const float* s, float fk) {
@@ -249,29 +251,32 @@ template <int D, int C> struct State {
         for (int r = 1; r < S::kScores; ++r) top = fmaxf(top, s[r]);
         return top * fk;
     }
-    // Whether the maximum or the size is behind the block's.  Scales compare as integers; those that are not finite and positive are not looked at.
-    __device__ __forceinline__ bool behind(float top, int scale_v) const { return __any(top > m + kSlack) || (scale_v > size && scale_v < 0x7F800000); }
+    // Whether a maximum is behind the block's; scale_v is the log2 of the block's values scale.  Nothing seen, so far and here, is NaN: no.
+    __device__ __forceinline__ bool behind(float top, float scale_v) const {
+        const float past = top - m;
+        return __any(past > kSlack || past + scale_v > z + kSlack);
+    }
     // Brings both up to the block's.  Rare.
-    __device__ __forceinline__ void catch_up(float top, int scale_v) {
+    __device__ __forceinline__ void catch_up(float top, float scale_v) {
         top = S::over_groups(top, false);
-        const float now = fmaxf(m, top), alpha = now == m ? 1.f : exp2_fast(m - now);
+        const float now = fmaxf(m, top), fall = now == m ? 0.f : m - now, was = z + fall;
+        z = fmaxf(was, top - now + scale_v);
         m = now;
-        l *= alpha;
-        const int up = scale_v > size && scale_v < 0x7F800000 ? min((scale_v >> 23) + 1, 253) << 23 : size;
-        const float by = alpha * __uint_as_float(size) * __uint_as_float((254 << 23) - up);
-        size = up;
+        l *= exp2_fast(fall);
+        const float by = z == was ? 1.f : exp2_fast(was - z);
 #pragma unroll
         for (int j = 0; j < S::kTiles; ++j) o[j] *= by;
     }
-    // What turns a block's scores into probabilities: factor and offset of the exponents, and the running sum.
+    // What turns a block's scores into what the second product takes: factor and offset of the exponents, their running
+    // sum, and what makes a sum of probabilities over 2^m of it.
     struct Exponent {
-        float factor, offset, fraction, sum;
+        float factor, offset, weight, sum;
     };
     __device__ __forceinline__ Exponent exponent(float fk, float scale_v) const {
-        const float fraction = fmaxf(scale_v * __uint_as_float((254 << 23) - size), kLeastFraction);
-        return {fk, kLift + __builtin_amdgcn_logf(fraction) - fmaxf(m, -1e37f), fraction, 0.f};        // m is -inf until a token is seen
+        const float ratio = __builtin_amdgcn_fmed3f(scale_v - z, kLeastRatio, kMostRatio) + kLift;           // NaN, of 0 and 0: the least
+        return {fk, ratio - fmaxf(m, -1e37f), exp2_fast(-ratio), 0.f};             // m is -inf until a token is seen
     }
-    // Probabilities r and r + 1, in the second product's order.  Their sum is of what they are before FP16, which loses
+    // Elements r and r + 1, in the second product's order.  The sum is of what they are before FP16, which loses
     // those of a block whose values are small beside others'.
     __device__ __forceinline__ void probabilities(const float* s, int r, Exponent& x, half8* p) const {
         const float e0 = exp2_fast(__builtin_fmaf(s[r], x.factor, x.offset)), e1 = exp2_fast(__builtin_fmaf(s[r + 1], x.factor, x.offset));
@@ -280,9 +285,18 @@ template <int D, int C> struct State {
         p[r >> 3][r & 7] = (_Float16)e0;
         p[r >> 3][(r & 7) + 1] = (_Float16)e1;
     }
-    __device__ __forceinline__ void add(const Exponent& x) { l = __builtin_fmaf(x.sum, __builtin_amdgcn_rcpf(x.fraction), l); }
-    // The output's registers over a sum of probabilities; a power of two at a time, since sizes may be anything.
-    __device__ __forceinline__ float value(float x, float by) const { return x * by * __uint_as_float(size); }
+    __device__ __forceinline__ void add(const Exponent& x) { l = __builtin_fmaf(x.sum, x.weight, l); }
+    // What turns the output's registers into values over a sum of probabilities: a factor, and a power of two apart from
+    // it, since z may be anything (-inf where all values are 0, and the output with them).
+    struct Over {
+        float by;
+        int power;
+    };
+    __device__ __forceinline__ Over over(float by) const {
+        const float whole = __builtin_rintf(fmaxf(z, -1e4f));
+        return {by * exp2_fast(fmaxf(z, -1e4f) - whole), (int)(whole - kLift)};
+    }
+    static __device__ __forceinline__ float value(float x, const Over& to) { return __builtin_amdgcn_ldexpf(x * to.by, to.power); }
 };
 
 // Scores of lane group g whose tokens lie outside [from, to) become -inf; the block's token 0 is t0.
@@ -554,15 +568,15 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
         for (int b = b0 + wave; b < b1; b += kWaves) {
             const Place next = place_at(a.c, t.seq, min(b + kWaves, b1 - 1), head);
             const int t0 = b * kBlock;
-            const float fk = positive(factor * now.scale_k());
+            const float fk = positive(factor * now.scale_k()), scale_v = log2_of(now.scale_v());
             float s[S::kScores];
             codes.scores(q, s);
             codes.fetch_keys(block_codes(next), lane);
             if (now.absent || t0 + kBlock > v.each_to || t0 < v.each_from) hide<D, C>(s, t0, g, c.from, now.absent ? 0 : c.to);
             const float top = st.top_of(s, fk);
-            if (st.behind(top, __float_as_int(now.scale_v()))) st.catch_up(top, __float_as_int(now.scale_v()));
+            if (st.behind(top, scale_v)) st.catch_up(top, scale_v);
             half8 p[S::kSteps];
-            typename State<D, C>::Exponent ex = st.exponent(fk, now.scale_v());
+            typename State<D, C>::Exponent ex = st.exponent(fk, scale_v);
 #pragma unroll
             for (int r = 0; r < S::kScores; r += 2) st.probabilities(s, r, ex, p);
             st.add(ex);
@@ -584,7 +598,7 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) sum += other[1][w * C + col] * weight(other[0][w * C + col]);
         // sums are positive unless nothing was seen; NaN passes through
-        const float part_share = l == 0.f ? 0.f : weight(st.m) / sum;
+        const auto part_share = st.over(l == 0.f ? 0.f : weight(st.m) / sum);
 #pragma unroll
         for (int j = 0; j < S::kTiles; ++j)
 #pragma unroll
@@ -854,7 +868,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
             int buffer = 0;
             for (int b = b0; b < b1; ++b) {
                 const int t0 = b * kBlock;
-                const float fk = positive(factor * now.scale_k());
+                const float fk = positive(factor * now.scale_k()), scale_v = log2_of(now.scale_v());
                 half8 y[2 * F];                        // fragments of keys, then of values
                 const auto read = [&](int i) { y[i] = stage[buffer][i >= F][i >= F ? i - F : i][lane]; };
 #pragma unroll
@@ -881,9 +895,9 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
                 for (int r = 0; r < 16; ++r) s[r] = x[r];
                 if (now.absent || t0 + kBlock > each_to || t0 < each_from) hide<D, 32>(s, t0, h, c.from, now.absent ? 0 : c.to);
                 const float top = st.top_of(s, fk);
-                if (st.behind(top, __float_as_int(now.scale_v()))) st.catch_up(top, __float_as_int(now.scale_v()));
+                if (st.behind(top, scale_v)) st.catch_up(top, scale_v);
                 half8 p[2];
-                typename State<D, 32>::Exponent ex = st.exponent(fk, now.scale_v());
+                typename State<D, 32>::Exponent ex = st.exponent(fk, scale_v);
 #pragma unroll
                 for (int r = 0; r < 16; r += 2) st.probabilities(s, r, ex, p);
                 st.add(ex);
@@ -905,7 +919,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
         const float l = S::over_groups(st.l, true);
         const int column = c0 + col;
         if (column < t.columns) {
-            const float over = l == 0.f ? 0.f : 1.f / l;               // nothing seen: zeros
+            const auto over = st.over(l == 0.f ? 0.f : 1.f / l);       // nothing seen: zeros
             uint16_t* out = static_cast<uint16_t*>(a.o) + ((int64_t)c.row * a.q_heads + (int64_t)head * a.group + c.head) * D;
             float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan.parts) + (worker * 2 + (opening ? 0 : 1)) * part_floats(D, C);
 #pragma unroll

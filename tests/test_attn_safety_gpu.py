@@ -1,0 +1,118 @@
+"""The attention operators on the GPU where numbers lie far apart and where a query's answer must not hang on what it does not see.
+
+Errors are bounded by what each row sees alone.  U is half a step of FP32."""
+import math
+
+import pytest
+import torch
+
+import attn_oracle as ao
+from attn_oracle import TINY, U
+from test_attn_gpu import FORMATS, I32, gen, iq, model_of, scene  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def parts_of(model, row, count):
+    """Code values and scales [count, heads, dim] and [count, heads] of keys and of values, 64 bits, of a sequence's first
+    tokens; and which of them lie in pages that are there."""
+    codes = torch.zeros(2, count, model.heads, model.dim, dtype=torch.float64)
+    scales, there = torch.zeros(2, count, model.heads, dtype=torch.float64), torch.zeros(count, dtype=torch.bool)
+    for block in range(-(-count // 32)):
+        page, n = model.page_of(row, 32 * block), min(32, count - 32 * block)
+        if page is None:
+            continue
+        at = slice(32 * block, 32 * block + n)
+        there[at] = True
+        for head in range(model.heads):
+            for which in range(2):
+                inside = block % (model.page // 32)
+                codes[which, at, head] = ao.value_of(model.block(page, head, inside, which)[:n], model.fmt).double()
+                scales[which, at, head] = model.scales[page, head, inside, which].double()
+    return codes, scales, there
+
+
+def answer(q, codes, scales, there, first, length, scale, causal, window):
+    """Rows q [n, q_heads, dim] as attn_oracle.attention has them, and a bound before rounding that goes by seen tokens alone.
+
+    A score is a sum of dim exact products, off by (dim + 4) U of their magnitudes, and its exponent is formed from it, the
+    running maximum and offsets of up to 75, each rounded (8 U of those sizes in all): delta.  A probability times its values
+    scale is rounded to FP16: 2^-11 of it, or, held times 2^9 of the largest such product so far, 2^-25 - 9 = 2^-34 of that
+    where it is small; the codes that it meets are exact.  A weight of FP32 below its smallest normal number is 0, so that a
+    probability below 2^-126 may be.  Sums over N tokens with their rescalings: (2 N + 64) U."""
+    q = q.double()
+    n, heads, dim = q.shape
+    group, keys = heads // codes.shape[2], codes.shape[1]
+    position, key = first + torch.arange(n), torch.arange(keys)
+    seen = there[None, :] & (key[None, :] < length) & (position[:, None] >= 0)
+    if causal:
+        seen = seen & (key[None, :] <= position[:, None])
+    if window:
+        seen = seen & (key[None, :] > position[:, None] - window)
+    o, e = torch.zeros(n, heads, dim, dtype=torch.float64), torch.zeros(n, heads, dim, dtype=torch.float64)
+    some, zero = seen.any(1), torch.zeros((), dtype=torch.float64)
+    for h in range(heads):
+        (ck, cv), (sk, sv) = codes[:, :, h // group], scales[:, :, h // group]
+        s = torch.where(seen, (q[:, h] @ ck.t().contiguous()) * sk * scale, zero)
+        size = torch.where(seen, (q[:, h].abs() @ ck.abs().t().contiguous()) * sk * scale, zero).amax(1)
+        p = torch.softmax(s.masked_fill(~seen, -math.inf), 1)
+        z = torch.where(seen, p * sv, zero)
+        delta = size * (dim + 4) * U + 8 * U * (s.abs().amax(1) + 75)
+        each = 2.0 ** -11 + 2 * delta + (2 * seen.sum(1) + 64) * U
+        o[:, h] = z @ cv
+        e[:, h] = 2 * each[:, None] * (z @ cv.abs()) + 2.0 ** -34 * z.amax(1)[:, None] * (seen.double() @ cv.abs())
+        e[:, h] += TINY * (torch.where(seen, sv, zero) @ cv.abs()) + TINY
+    o[~some], e[~some] = 0, 0
+    return o, e
+
+
+def check(iq, cache, q, table, lengths, starts, *, causal=True, window=0, scale=None, rows=None, what="", **kw):  # noqa: F811
+    """Runs cache_attention and holds its rows (those where `rows` is true) to `answer`."""
+    got = iq.cache_attention(cache, q, table, lengths, starts, causal=causal, window=window, scale=scale, **kw)
+    model, scale = model_of(cache), cache.dim ** -0.5 if scale is None else scale
+    for b, length in enumerate(lengths.tolist()):
+        lo, hi = (int(starts[b]), int(starts[b + 1])) if starts is not None else (b, b + 1)
+        codes, scales, there = parts_of(model, table[b].tolist(), min(length, table.shape[1] * cache.page))
+        o, e = answer(q[lo:hi].cpu(), codes, scales, there, length - (hi - lo), length, scale, causal, window)
+        keep = slice(None) if rows is None else rows[lo:hi].cpu()
+        ao.assert_within(got[lo:hi].cpu()[keep], o[keep], e[keep], f"{what} sequence {b}")
+    return got
+
+
+def widened(table, width):
+    wide = torch.full((table.shape[0], width), -1, dtype=I32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
+# ---- values of very different sizes ---------------------------------------------------------
+KINDS = (([300], [1]), ([200, 77], [5, 3]), ([70], [150]), ([0, 190], [140, 33]))     # new tokens behind cached ones
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_values_scales_far_apart(iq, fmt, dim):  # noqa: F811
+    """Blocks whose value scales are 2^-60 to 2^60, some 0: each row is as exact as the largest product of a probability and a
+    scale that it sees allows, with a window, without, and in tables that share rows out."""
+    for k, (had, new) in enumerate(KINDS):
+        cache, q, table, lengths, starts = scene(iq, fmt, 1, 2, dim, 32, had, new, dim + k, garbage=False)
+        power = torch.randint(-60, 61, cache.scales[..., 1].shape, generator=gen(k), device="cuda")
+        cache.scales[..., 1] = torch.exp2(power) * (power % 7 != 0)
+        for t in (table, widened(table, 400)):
+            for kw in (dict(), dict(window=20), dict(window=100), dict(causal=False)):
+                check(iq, cache, q, t, lengths, starts, what=f"{had} {new} {t.shape[1]} {kw}", **kw)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("ratio", [-30, -50, -110])
+def test_values_behind_a_large_block(iq, fmt, ratio):  # noqa: F811
+    """One block of large values that a window has left, that is not yet seen, or that is seen with next to no probability."""
+    for had, new in KINDS:
+        for spot in (0, 2, 5):
+            cache, q, table, lengths, starts = scene(iq, fmt, 1, 3, 128, 32, had, new, 5, garbage=False)
+            cache.scales[..., 1] = 2.0 ** ratio
+            for b in range(len(had)):
+                if table[b, min(spot, table.shape[1] - 1)] >= 0:
+                    cache.scales[table[b, min(spot, table.shape[1] - 1)].long(), ..., 1] = 1.0
+            for kw in (dict(window=33), dict(window=70), dict(), dict(scale=3.0)):
+                check(iq, cache, q, table, lengths, starts, what=f"{had} {new} {spot} {kw}", **kw)
