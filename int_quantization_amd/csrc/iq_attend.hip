@@ -299,13 +299,17 @@ template <int D, int C> struct State {
     static __device__ __forceinline__ float value(float x, const Over& to) { return __builtin_amdgcn_ldexpf(x * to.by, to.power); }
 };
 
-// Scores of lane group g whose tokens lie outside [from, to) become -inf; the block's token 0 is t0.
-template <int D, int C> __device__ __forceinline__ void hide(float* s, int t0, int g, int from, int to) {
+// Scores of lane group g whose tokens lie outside [from, to) become -inf; the block's token 0 is t0.  Of a block that a
+// column sees nothing of it does not take the scales either, which may be anything, nor its own factor, which may be NaN.
+template <int D, int C> __device__ __forceinline__ void hide(float* s, float& fk, float& scale_v, int t0, int g, int from, int to) {
 #pragma unroll
     for (int r = 0; r < Shape<D, C>::kScores; ++r) {
         const int token = t0 + Shape<D, C>::token(g, r);
         s[r] = token >= from && token < to ? s[r] : -INFINITY;
     }
+    const bool none = max(from, t0) >= min(to, t0 + kBlock);
+    fk = none ? 1.f : fk;
+    scale_v = none ? -INFINITY : scale_v;
 }
 
 // The factor of a block's scores: positive, so that hidden ones stay -inf.
@@ -568,11 +572,11 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
         for (int b = b0 + wave; b < b1; b += kWaves) {
             const Place next = place_at(a.c, t.seq, min(b + kWaves, b1 - 1), head);
             const int t0 = b * kBlock;
-            const float fk = positive(factor * now.scale_k()), scale_v = log2_of(now.scale_v());
+            float fk = positive(factor * now.scale_k()), scale_v = log2_of(now.scale_v());
             float s[S::kScores];
             codes.scores(q, s);
             codes.fetch_keys(block_codes(next), lane);
-            if (now.absent || t0 + kBlock > v.each_to || t0 < v.each_from) hide<D, C>(s, t0, g, c.from, now.absent ? 0 : c.to);
+            if (now.absent || t0 + kBlock > v.each_to || t0 < v.each_from) hide<D, C>(s, fk, scale_v, t0, g, c.from, now.absent ? 0 : c.to);
             const float top = st.top_of(s, fk);
             if (st.behind(top, scale_v)) st.catch_up(top, scale_v);
             half8 p[S::kSteps];
@@ -868,7 +872,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
             int buffer = 0;
             for (int b = b0; b < b1; ++b) {
                 const int t0 = b * kBlock;
-                const float fk = positive(factor * now.scale_k()), scale_v = log2_of(now.scale_v());
+                float fk = positive(factor * now.scale_k()), scale_v = log2_of(now.scale_v());
                 half8 y[2 * F];                        // fragments of keys, then of values
                 const auto read = [&](int i) { y[i] = stage[buffer][i >= F][i >= F ? i - F : i][lane]; };
 #pragma unroll
@@ -893,7 +897,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
                 float s[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = x[r];
-                if (now.absent || t0 + kBlock > each_to || t0 < each_from) hide<D, 32>(s, t0, h, c.from, now.absent ? 0 : c.to);
+                if (now.absent || t0 + kBlock > each_to || t0 < each_from) hide<D, 32>(s, fk, scale_v, t0, h, c.from, now.absent ? 0 : c.to);
                 const float top = st.top_of(s, fk);
                 if (st.behind(top, scale_v)) st.catch_up(top, scale_v);
                 half8 p[2];

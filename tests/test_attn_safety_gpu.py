@@ -8,7 +8,7 @@ import torch
 
 import attn_oracle as ao
 from attn_oracle import TINY, U
-from test_attn_gpu import FORMATS, I32, gen, iq, model_of, scene  # noqa: F401
+from test_attn_gpu import FORMATS, I32, gen, iq, model_of, rand, scene  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +116,42 @@ def test_values_behind_a_large_block(iq, fmt, ratio):  # noqa: F811
                     cache.scales[table[b, min(spot, table.shape[1] - 1)].long(), ..., 1] = 1.0
             for kw in (dict(window=33), dict(window=70), dict(), dict(scale=3.0)):
                 check(iq, cache, q, table, lengths, starts, what=f"{had} {new} {spot} {kw}", **kw)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_scales_of_blocks_that_a_query_does_not_see(iq, fmt):  # noqa: F811
+    """Whatever the scales of a block hold: queries that do not see it, of the same call, answer without it."""
+    for had, new in KINDS[1:]:
+        for bad in (math.nan, math.inf, -math.inf, 3e38):
+            for window in (0, 12, 40):
+                cache, q, table, lengths, starts = scene(iq, fmt, 1, 2, 64, 32, had, new, 9, garbage=False)
+                rows = torch.ones(sum(new), dtype=torch.bool)
+                for b, (h, n) in enumerate(zip(had, new)):
+                    spot = (h + n // 2) // 32                       # the block that the sequence's middle new token lies in
+                    cache.scales[table[b, spot].long()] = bad
+                    at = torch.arange(h, h + n)
+                    least = (at - window + 1).clamp_min(0) if window else torch.zeros_like(at)
+                    rows[int(starts[b]):int(starts[b + 1])] = (at < 32 * spot) | (least >= 32 * spot + 32)
+                check(iq, cache, q, table, lengths, starts, window=window, rows=rows, what=f"{had} {new} {bad} {window}")
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_bad_queries_that_see_nothing(iq, bad):  # noqa: F811
+    """A query that is not finite answers NaN where it sees a token, and zeros where it sees none, whatever the others of its
+    tile see: rows before a sequence's first token, and rows of absent pages, in calls of few and of many columns."""
+    for new, length, table in ((5, 3, [[1, 2]]), (150, 60, [[1, 2]]), (7, 40, [[-1, 2]]), (160, 160, [[1, -1, 2, 3, 4]]), (150, 160, [[-1, -1, 2, 3, 9]])):
+        cache = iq.make_cache(6, 1, 64, "e4m3", 32)
+        ao.fill(cache, 4)
+        table, starts = torch.tensor(table, dtype=I32, device="cuda"), torch.tensor([0, new], dtype=I32, device="cuda")
+        lengths = torch.tensor([length], dtype=I32, device="cuda")
+        q = rand(gen(2), new, 3, 64)
+        want = iq.cache_attention(cache, q, table, lengths, starts, window=50)
+        hurt = torch.arange(new, device="cuda") % 3 == 1
+        q[hurt, 1, 7] = bad
+        position = torch.arange(length - new, length)
+        there = torch.tensor([0 <= p < len(table[0]) * 32 and 0 <= int(table[0, p // 32]) < 6 for p in range(max(length, 1))])
+        sees = torch.tensor([bool(there[max(0, p - 49):p + 1].any()) if p >= 0 else False for p in position.tolist()]).cuda()
+        got = iq.cache_attention(cache, q, table, lengths, starts, window=50)
+        assert torch.isnan(got[hurt & sees, 1]).all() and not got[~sees].any()
+        want[hurt & sees, 1] = got[hurt & sees, 1] = 0
+        assert torch.equal(got, want), (new, length)
