@@ -216,17 +216,23 @@ template <int D, int C> __device__ __forceinline__ float load_query(float scale,
         }
 #pragma unroll
     for (int d = C; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    // a query that is not finite answers NaN, whatever it sees: all its elements are
+    const uint32_t bad = top >= 0x7F800000u ? 0xFFFFFFFFu : 0u;
     int e = (int)(top >> 23);                          // 0 for zeros and subnormals, 255 for infinities and NaN
     e = e == 255 ? 0 : max(e, 1) - 127 - 14;
 #pragma unroll
-    for (int f = 0; f < S::kFragments; ++f)
+    for (int f = 0; f < S::kFragments; ++f) {
+        union { half8 v; uint32_t w[4]; } u;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const uint32_t w = reinterpret_cast<const uint32_t*>(&raw[f])[k >> 1];
-            q[f][k] = (_Float16)ldexpf(__uint_as_float(k & 1 ? w & 0xFFFF0000u : w << 16), -e);
+            u.v[k] = (_Float16)ldexpf(__uint_as_float(k & 1 ? w & 0xFFFF0000u : w << 16), -e);
         }
-    // a query that is not finite answers NaN, whatever it sees
-    return top >= 0x7F800000u ? __builtin_nanf("") : ldexpf(scale * 1.44269504f, e);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u.w[k] |= bad;
+        q[f] = u.v;
+    }
+    return ldexpf(scale * 1.44269504f, e);
 }
 
 // Log2 of a scale, subnormal ones too; -inf of 0.
@@ -299,21 +305,17 @@ template <int D, int C> struct State {
     static __device__ __forceinline__ float value(float x, const Over& to) { return __builtin_amdgcn_ldexpf(x * to.by, to.power); }
 };
 
-// Scores of lane group g whose tokens lie outside [from, to) become -inf; the block's token 0 is t0.  Of a block that a
-// column sees nothing of it does not take the scales either, which may be anything, nor its own factor, which may be NaN.
-template <int D, int C> __device__ __forceinline__ void hide(float* s, float& fk, float& scale_v, int t0, int g, int from, int to) {
+// Scores of lane group g whose tokens lie outside [from, to) become -inf; the block's token 0 is t0.
+template <int D, int C> __device__ __forceinline__ void hide(float* s, int t0, int g, int from, int to) {
 #pragma unroll
     for (int r = 0; r < Shape<D, C>::kScores; ++r) {
         const int token = t0 + Shape<D, C>::token(g, r);
         s[r] = token >= from && token < to ? s[r] : -INFINITY;
     }
-    const bool none = max(from, t0) >= min(to, t0 + kBlock);
-    fk = none ? 1.f : fk;
-    scale_v = none ? -INFINITY : scale_v;
 }
 
-// The factor of a block's scores: positive, so that hidden ones stay -inf.
-__device__ __forceinline__ float positive(float fk) { return fk < 1e-30f ? 1e-30f : fk; }
+// The factor of a block's scores, positive and finite, so that hidden ones stay -inf whatever the block's scale is.
+__device__ __forceinline__ float factor_of(float fk) { return __builtin_amdgcn_fmed3f(fk, 1e-30f, 3e38f); }
 
 // Values that a wave's lanes share, in scalar registers.
 __device__ __forceinline__ int one(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -572,11 +574,11 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
         for (int b = b0 + wave; b < b1; b += kWaves) {
             const Place next = place_at(a.c, t.seq, min(b + kWaves, b1 - 1), head);
             const int t0 = b * kBlock;
-            float fk = positive(factor * now.scale_k()), scale_v = log2_of(now.scale_v());
+            const float fk = factor_of(factor * now.scale_k()), scale_v = log2_of(now.scale_v());
             float s[S::kScores];
             codes.scores(q, s);
             codes.fetch_keys(block_codes(next), lane);
-            if (now.absent || t0 + kBlock > v.each_to || t0 < v.each_from) hide<D, C>(s, fk, scale_v, t0, g, c.from, now.absent ? 0 : c.to);
+            if (now.absent || t0 + kBlock > v.each_to || t0 < v.each_from) hide<D, C>(s, t0, g, c.from, now.absent ? 0 : c.to);
             const float top = st.top_of(s, fk);
             if (st.behind(top, scale_v)) st.catch_up(top, scale_v);
             half8 p[S::kSteps];
@@ -872,7 +874,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
             int buffer = 0;
             for (int b = b0; b < b1; ++b) {
                 const int t0 = b * kBlock;
-                float fk = positive(factor * now.scale_k()), scale_v = log2_of(now.scale_v());
+                const float fk = factor_of(factor * now.scale_k()), scale_v = log2_of(now.scale_v());
                 half8 y[2 * F];                        // fragments of keys, then of values
                 const auto read = [&](int i) { y[i] = stage[buffer][i >= F][i >= F ? i - F : i][lane]; };
 #pragma unroll
@@ -897,7 +899,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
                 float s[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = x[r];
-                if (now.absent || t0 + kBlock > each_to || t0 < each_from) hide<D, 32>(s, fk, scale_v, t0, h, c.from, now.absent ? 0 : c.to);
+                if (now.absent || t0 + kBlock > each_to || t0 < each_from) hide<D, 32>(s, t0, h, c.from, now.absent ? 0 : c.to);
                 const float top = st.top_of(s, fk);
                 if (st.behind(top, scale_v)) st.catch_up(top, scale_v);
                 half8 p[2];
