@@ -624,7 +624,7 @@ typedef struct {
  * query has seen 2^-34 of that); sums, maxima and the running output are FP32, and probabilities below 2^-126 may count as 0.
  * Tokens that a query does
  * not see add nothing, whatever their codes and scales hold; a NaN or an infinity in a query makes that
- * query's output NaN.  Scales are expected to be finite and >= 0; NaN codes of E4M3 (which iq_cache_append never writes)
+ * query's output NaN where it sees anything.  Scores times log2(e) have to lie in FP32's range.  Scales are expected to be finite and >= 0; NaN codes of E4M3 (which iq_cache_append never writes)
  * in tokens that a sequence holds may make any of that sequence's outputs of their head NaN.
  * The order of all sums is fixed by shapes, lengths and starts: calls repeat their bits.
  * tokens * q_heads up to 2^28 (IQ_EUNSUPPORTED).

@@ -54,6 +54,10 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // largest product on and steps of 2^-33 of that below.
 constexpr float kSlack = 6.f, kLift = 9.f;
 
+// From a maximum of this size on, FP32 steps of an exponent are no small part of 1: scores are taken less the maximum
+// before anything is added to them.
+constexpr float kFar = 0x1p20f;
+
 // Log2 of a block's values scale over 2^z, at least: what FP16 leaves nothing of, and FP32 enough for the sum, so that
 // blocks of small values or none (scale 0) still count in it.
 constexpr float kLeastRatio = -60.f, kMostRatio = 1000.f;                 // at most: 2^z is 0 until a value other than 0 is seen
@@ -243,12 +247,14 @@ template <int D, int C> struct State {
     using S = Shape<D, C>;
     typename S::Tile o[S::kTiles];
     float m, l, z;
+    int far;                     // whether some column's m is past kFar
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int j = 0; j < S::kTiles; ++j) o[j] = 0.f;
         m = z = -INFINITY;
         l = 0.f;
+        far = 0;
     }
     // The largest of the lane's scores, as an exponent of 2.
     static __device__ __forceinline__ float top_of(const float* s, float fk) {
@@ -262,25 +268,34 @@ template <int D, int C> struct State {
         const float past = top - m;
         return __any(past > kSlack || past + scale_v > z + kSlack);
     }
-    // Brings both up to the block's.  Rare.
+    // Brings both up to the block's, and takes the maximum off its scores if it is far.  Rare.
     __device__ __forceinline__ void catch_up(float top, float scale_v) {
         top = S::over_groups(top, false);
         const float now = fmaxf(m, top), fall = now == m ? 0.f : m - now, was = z + fall;
         z = fmaxf(was, top - now + scale_v);
         m = now;
+        far = __builtin_amdgcn_readfirstlane(__any(fabsf(now) >= kFar && now > -INFINITY));
         l *= exp2_fast(fall);
         const float by = z == was ? 1.f : exp2_fast(was - z);
 #pragma unroll
         for (int j = 0; j < S::kTiles; ++j) o[j] *= by;
     }
+    static __device__ __forceinline__ float least(float m) { return fmaxf(m, -3.402823466e+38f); }       // m is -inf until a token is seen
     // What turns a block's scores into what the second product takes: factor and offset of the exponents, their running
     // sum, and what makes a sum of probabilities over 2^m of it.
     struct Exponent {
         float factor, offset, weight, sum;
     };
-    __device__ __forceinline__ Exponent exponent(float fk, float scale_v) const {
+    __device__ __forceinline__ Exponent exponent(float* s, float fk, float scale_v) const {
         const float ratio = __builtin_amdgcn_fmed3f(scale_v - z, kLeastRatio, kMostRatio) + kLift;           // NaN, of 0 and 0: the least
-        return {fk, ratio - fmaxf(m, -1e37f), exp2_fast(-ratio), 0.f};             // m is -inf until a token is seen
+        Exponent x = {fk, ratio - least(m), exp2_fast(-ratio), 0.f};
+        if (far) {
+#pragma unroll
+            for (int r = 0; r < S::kScores; ++r) s[r] = s[r] * fk - least(m);
+            x.factor = 1.f;
+            x.offset = ratio;
+        }
+        return x;
     }
     // Elements r and r + 1, in the second product's order.  The sum is of what they are before FP16, which loses
     // those of a block whose values are small beside others'.
@@ -582,7 +597,7 @@ template <int D, int FMT, int C, bool DIRECT> __global__ __launch_bounds__(kThre
             const float top = st.top_of(s, fk);
             if (st.behind(top, scale_v)) st.catch_up(top, scale_v);
             half8 p[S::kSteps];
-            typename State<D, C>::Exponent ex = st.exponent(fk, scale_v);
+            typename State<D, C>::Exponent ex = st.exponent(s, fk, scale_v);
 #pragma unroll
             for (int r = 0; r < S::kScores; r += 2) st.probabilities(s, r, ex, p);
             st.add(ex);
@@ -903,7 +918,7 @@ template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) 
                 const float top = st.top_of(s, fk);
                 if (st.behind(top, scale_v)) st.catch_up(top, scale_v);
                 half8 p[2];
-                typename State<D, 32>::Exponent ex = st.exponent(fk, scale_v);
+                typename State<D, 32>::Exponent ex = st.exponent(s, fk, scale_v);
 #pragma unroll
                 for (int r = 0; r < 16; r += 2) st.probabilities(s, r, ex, p);
                 st.add(ex);

@@ -155,3 +155,42 @@ def test_bad_queries_that_see_nothing(iq, bad):  # noqa: F811
         assert torch.isnan(got[hurt & sees, 1]).all() and not got[~sees].any()
         want[hurt & sees, 1] = got[hurt & sees, 1] = 0
         assert torch.equal(got, want), (new, length)
+
+
+# ---- scores at the ends of their range ------------------------------------------------------
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("size", [2.0 ** 14, 2.0 ** 30, 2.0 ** 60, 2.0 ** 100, 2.0 ** 124])
+def test_scores_far_from_zero(iq, fmt, size):  # noqa: F811
+    """Scores of one sign, up to the ends of FP32: the query takes the token of the largest, and the mean of those that are equal
+    to it.  Keys are one code times a power of two, so scores are exact, differ by their own size where they differ, and
+    roundings of exponents do not show."""
+    dim, heads = 64, 2
+    for had, new in (([0], [1]), ([70], [3]), ([300], [40]), ([20], [170]), ([5000], [1])):
+        n = had[0] + new[0]
+        pages = -(-n // 32)
+        cache = iq.make_cache(pages, heads, dim, fmt, 32)
+        ao.fill(cache, 3)
+        one = 0x38 if fmt == "e4m3" else 1
+        cache.codes[:, :, :, 0] = one
+        cache.scales[..., 1] = 1.0
+        power = torch.randint(0, 3, (pages, heads, 1), generator=gen(n), device="cuda")
+        cache.scales[..., 0] = torch.exp2(-4.0 * power)
+        table = torch.arange(pages, dtype=I32, device="cuda")[None]
+        starts, lengths = torch.tensor([0, new[0]], dtype=I32, device="cuda"), torch.tensor([n], dtype=I32, device="cuda")
+        for t in (table, widened(table, 400)):
+            for sign in (1.0, -1.0):
+                q = torch.zeros(new[0], heads, dim, dtype=torch.bfloat16, device="cuda")
+                q[..., 9], q[..., 10] = sign * size, sign * size * 2.0 ** -9 * (2 - 2.0 ** -7)      # more digits than BF16 has
+                for kw in (dict(), dict(window=45)):
+                    got = iq.cache_attention(cache, q, t, lengths, starts, scale=1.0, **kw).cpu().double()
+                    codes, scales, _ = parts_of(model_of(cache), table[0].tolist(), n)
+                    at, key = torch.arange(had[0], n)[:, None], torch.arange(n)[None]
+                    seen = (key <= at) & (key > at - kw.get("window", 1 << 30))
+                    for h in range(heads):
+                        score = torch.where(seen, sign * scales[0, :, h], torch.tensor(-math.inf, dtype=torch.float64))
+                        p = (score == score.amax(1, keepdim=True)).double()
+                        p = p / p.sum(1, keepdim=True)
+                        want = p @ codes[1, :, h]
+                        # FP16 holds the equal probabilities alike to 2^-11, and sums of them in FP32
+                        e = (p @ codes[1, :, h].abs()) * (2.0 ** -10 + (2 * n + 64) * U) + TINY
+                        ao.assert_within(got[:, h].to(torch.float32), want, e + 2.0 ** -8 * (want.abs() + e), f"{had} {new} {sign} {kw}")
