@@ -26,14 +26,16 @@ template <typename T> struct alignas(16) Vec {
 };
 
 // Cosine and sine of 2 pi * position * turns.  The product has up to 31 + 53 bits and is
-// reduced to half a turn in 64 bits, so its error is 2^-53 of the angle, and
-// 2^-25 of a turn once it is FP32.
+// reduced to half a turn in 64 bits, so its error is 2^-53 of the angle; what FP32 leaves of the
+// reduced angle (up to 2^-25 half turns) turns the result once more, to first order.
 __device__ __forceinline__ float2 turn(int position, double turns, float amplitude, float way) {
     double t = (double)position * turns;
-    t -= __builtin_rint(t);
+    t = 2 * (t - __builtin_rint(t));
+    const float near = (float)t, rest = (float)(t - (double)near) * 3.14159265f;
     float s, c;
-    sincospif(2.f * (float)t, &s, &c);
-    return make_float2(c * amplitude, s * (amplitude * way));
+    sincospif(near, &s, &c);
+    const float cosine = __builtin_fmaf(-s, rest, c), sine = __builtin_fmaf(c, rest, s);
+    return make_float2(cosine * amplitude, sine * (amplitude * way));
 }
 
 // Turns the heads [head0, head1) of one token.  cs: cosine and sine of its pairs, in LDS.

@@ -194,3 +194,23 @@ def test_scores_far_from_zero(iq, fmt, size):  # noqa: F811
                         # FP16 holds the equal probabilities alike to 2^-11, and sums of them in FP32
                         e = (p @ codes[1, :, h].abs()) * (2.0 ** -10 + (2 * n + 64) * U) + TINY
                         ao.assert_within(got[:, h].to(torch.float32), want, e + 2.0 ** -8 * (want.abs() + e), f"{had} {new} {sign} {kw}")
+
+
+# ---- angles -----------------------------------------------------------------------------------
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotary_angles_keep_their_digits(iq, inter):  # noqa: F811
+    """Cosines and sines of angles that FP32 does not hold, read off pairs (1, 0): off by one step of the largest below 1 (the
+    functions' own, U in all) and half a step for what the rest of the angle adds.  An angle rounded to FP32 alone is off
+    by up to 2^-25 half turns, 1.57 U."""
+    g = gen(70)
+    x = torch.zeros(3, 2, 1024, device="cuda")
+    x[..., 0::2 if inter else 1][..., :512] = 1
+    a, b = (slice(0, None, 2), slice(1, None, 2)) if inter else (slice(0, 512), slice(512, None))
+    at = torch.tensor([1, -1, 3], dtype=I32, device="cuda")
+    for _ in range(100):
+        table = torch.rand(512, generator=g, device="cuda", dtype=torch.float64) - 0.5
+        for call, way in ((iq.rotary, 1), (iq.rotary_backward, -1)):
+            y = call(x, at, table, interleaved=inter).double()
+            t = at.double()[:, None] * table
+            t = ((t - t.round()) * (2 * math.pi * way))[:, None]
+            assert max((y[..., a] - torch.cos(t)).abs().max(), (y[..., b] - torch.sin(t)).abs().max()) <= 1.5 * U
