@@ -472,7 +472,8 @@ typedef enum {
 iq_status iq_rotary_table(int32_t rot, double base, int32_t scaling, double factor, double context, double low,
                           double high, double* table);
 
-/* Strides count elements; the elements of a head are contiguous. */
+/* Strides count elements; the elements of a head are contiguous.  Here and below nothing is asked of the stride of a
+ * dimension of one element. */
 typedef struct {
     int32_t dtype;                      /* iq_dtype of x and y */
     int32_t layout;                     /* iq_rotary_layout */

@@ -23,8 +23,11 @@ constexpr int64_t kMostWork = (int64_t)1 << 23;      // workgroups of a launch, 
 
 bool is_finite(double v) { return v - v == 0; }
 
-// Strides of [n, m] blocks of `dim` elements: not negative, products far inside 64 bits.
+// Strides of [n, m] blocks of `dim` elements: not negative, products far inside 64 bits.  Nothing is asked of one that
+// leads from the first block to none.
 iq_status check_strides(int64_t n, int64_t m, int64_t ld_n, int64_t ld_m) {
+    if (n <= 1) ld_n = 0;
+    if (m <= 1) ld_m = 0;
     if (ld_n < 0 || ld_m < 0) return IQ_EINVAL;
     if (ld_n > kMostStride || ld_m > kMostStride) return IQ_EUNSUPPORTED;
     if ((ld_n && n > kMostSpan / ld_n) || (ld_m && m > kMostSpan / ld_m)) return IQ_EUNSUPPORTED;
@@ -61,7 +64,7 @@ iq_status rotate(const iq_rotary_desc* d, const void* x, const int32_t* position
     if (st != IQ_OK) return st;
     if (d->tokens == 0 || d->heads == 0 || d->dim == 0) return IQ_OK;
     if (!x || !y || !positions || (d->rot > 0 && !table)) return IQ_EINVAL;
-    if (x == y && (d->ld_token != d->ld_token_out || d->ld_head != d->ld_head_out) && (d->tokens > 1 || d->heads > 1)) return IQ_EINVAL;
+    if (x == y && ((d->tokens > 1 && d->ld_token != d->ld_token_out) || (d->heads > 1 && d->ld_head != d->ld_head_out))) return IQ_EINVAL;
     const uintptr_t e = (uintptr_t)size_of(d->dtype);
     if (!aligned(x, e) || !aligned(y, e) || !aligned(positions, 4) || !aligned(table, 8)) return IQ_EALIGN;
     iqk::RotaryArgs a;
@@ -130,7 +133,7 @@ iq_status check_attention(const iq_cache_desc* d, const iq_attention_desc* a, co
     if (a->tokens * a->q_heads > ((int64_t)1 << 28)) return IQ_EUNSUPPORTED;
     const iq_status strides = check_strides(a->tokens, a->q_heads, a->ld_token, a->ld_head);
     if (strides != IQ_OK) return strides;
-    if (a->ld_token % 8 || a->ld_head % 8) return IQ_EALIGN;
+    if ((a->tokens > 1 && a->ld_token % 8) || (a->q_heads > 1 && a->ld_head % 8)) return IQ_EALIGN;
     return IQ_OK;
 }
 

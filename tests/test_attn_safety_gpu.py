@@ -214,3 +214,22 @@ def test_rotary_angles_keep_their_digits(iq, inter):  # noqa: F811
             t = at.double()[:, None] * table
             t = ((t - t.round()) * (2 * math.pi * way))[:, None]
             assert max((y[..., a] - torch.cos(t)).abs().max(), (y[..., b] - torch.sin(t)).abs().max()) <= 1.5 * U
+
+
+# ---- strides ------------------------------------------------------------------------------------
+def test_strides_of_single_tokens_and_heads(iq):  # noqa: F811
+    """A row of a buffer whose rows do not lie on 16 bytes, and one head of it: the stride that leads nowhere is not looked at."""
+    g = gen(71)
+    cache, q, table, lengths, starts = scene(iq, "int8", 1, 3, 64, 32, [70], [1], 7)
+    want = iq.cache_attention(cache, q, table, lengths)
+    odd = torch.as_strided(q, (1, 3, 64), (2051, 64, 1))
+    for t in (None, torch.empty_like(q)):
+        assert torch.equal(iq.cache_attention(cache, odd, table, lengths, out=t), want)
+    cache, q, table, lengths, starts = scene(iq, "int8", 1, 1, 64, 32, [70], [5], 7)
+    want = iq.cache_attention(cache, q, table, lengths, starts)
+    assert torch.equal(iq.cache_attention(cache, torch.as_strided(q, (5, 1, 64), (64, 67, 1)), table, lengths, starts), want)
+    turns, at = iq.rotary_table(64), torch.tensor([9], dtype=I32, device="cuda")
+    x = rand(g, 1, 3, 64)
+    want = iq.rotary(x, at, turns)
+    y = x.clone()
+    assert torch.equal(iq.rotary(y, at, turns, out=torch.as_strided(y, (1, 3, 64), (2051, 64, 1))), want) and torch.equal(y, want)
