@@ -467,7 +467,7 @@ typedef enum {
  *   table[i] = base^(-2 i / rot) / (2 pi), scaled.
  * A HOST function: `table` is host memory, and the other calls take a copy of
  * it in device memory.  rot even and >= 0; base > 0, factor > 0 and, for
- * IQ_ROTARY_PARTS, context > 0 and high > low, all finite (IQ_EINVAL).
+ * IQ_ROTARY_PARTS, context > 0 and high > low, all finite, and so the turns (IQ_EINVAL).
  */
 iq_status iq_rotary_table(int32_t rot, double base, int32_t scaling, double factor, double context, double low,
                           double high, double* table);

@@ -159,15 +159,17 @@ iq_status iq_rotary_table(int32_t rot, double base, int32_t scaling, double fact
     if (scaling == IQ_ROTARY_PARTS && !(is_finite(context) && is_finite(low) && is_finite(high) && context > 0 && high > low)) return IQ_EINVAL;
     const double tau = 6.283185307179586476925;
     const double b = scaling == IQ_ROTARY_BASE && rot > 2 ? base * pow(factor, (double)rot / (rot - 2)) : base;
-    for (int32_t i = 0; i < rot / 2; ++i) {
-        double turns = pow(b, -2.0 * i / rot) / tau;
-        if (scaling == IQ_ROTARY_LINEAR) turns /= factor;
-        if (scaling == IQ_ROTARY_PARTS) {
-            const double w = (turns * context - low) / (high - low), keep = w < 0 ? 0 : w > 1 ? 1 : w;
-            turns = turns / factor * (1 - keep) + turns * keep;
+    for (int pass = 0; pass < 2; ++pass)               // looked at first, then written
+        for (int32_t i = 0; i < rot / 2; ++i) {
+            double turns = pow(b, -2.0 * i / rot) / tau;
+            if (scaling == IQ_ROTARY_LINEAR) turns /= factor;
+            if (scaling == IQ_ROTARY_PARTS) {
+                const double w = (turns * context - low) / (high - low), keep = w < 0 ? 0 : w > 1 ? 1 : w;
+                turns = turns / factor * (1 - keep) + turns * keep;
+            }
+            if (!is_finite(turns)) return IQ_EINVAL;
+            if (pass) table[i] = turns;
         }
-        table[i] = turns;
-    }
     return IQ_OK;
 }
 

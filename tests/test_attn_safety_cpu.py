@@ -1,6 +1,4 @@
 """What the attention operators accept and refuse at the ends of their arguments, shown without a GPU."""
-import math
-
 import pytest
 import torch
 
@@ -20,3 +18,17 @@ def test_strides_that_are_not_used(iq):  # noqa: F811
     # in place, strides that differ where they are used
     for tokens, heads, s in ((1, 3, (192, 64, 192, 72)), (4, 1, (64, 64, 72, 64))):
         assert iq.iq_rotary(rotary_desc(iq, tokens=tokens, heads=heads, strides=s), FAKE, FAKE, FAKE, FAKE, None) == iq.IQ_EINVAL
+
+
+def test_rotary_tables_that_leave_the_range(iq):  # noqa: F811
+    """Finite arguments whose turns would not be are refused, and the table is left as it was."""
+    for args in ((64, 1e-300, "linear", 1e-300, 0.0), (64, 1e-200, "base", 1e-200, 0.0), (64, 1e4, "linear", 1e-310, 0.0), (64, 1e4, "parts", 1e-310, 4096.0)):
+        rot, base, scaling, factor, context = args
+        with pytest.raises(iq.IQError):
+            iq.rotary_table(rot, base, scaling, factor, context, device="cpu")
+        host = torch.full((rot // 2,), 7.0, dtype=torch.float64)
+        assert iq.iq_rotary_table(rot, base, iq.ROTARY_SCALINGS[scaling], factor, context, 1.0, 32.0, host.data_ptr()) == iq.IQ_EINVAL
+        assert (host == 7).all()
+    for args in ((64, 1e300), (64, 1e-3), (64, 1e308, "base", 1e300), (64, 1e4, "linear", 1e300), (64, 1e4, "parts", 1e3, 1e-300)):
+        table = iq.rotary_table(*args, device="cpu")
+        assert torch.isfinite(table).all() and table[0] > 0 and (table >= 0).all()
