@@ -988,7 +988,7 @@ def _rotary(call, what: str, x, positions, table, interleaved: bool, amplitude: 
             return done
     with _place(stream, x):
         torch = _torch()
-        _refuse_grad(x, out)
+        _refuse_grad(x, table, out)
         _heads_of(x, "x")
         dtype = _dtype_of(x, "x")
         tokens, heads, dim = x.shape
@@ -1079,7 +1079,7 @@ def cache_append(cache: "KVCache", k, v, page_table, lengths, starts=None, *, q=
         if done is not None:
             return done
     with _place(stream, k):
-        _refuse_grad(k, v, q)
+        _refuse_grad(k, v, q, rotary, cache.scales)
         dtype = _dtype_of(k, "k")
         for x, what, heads in ((k, "k", cache.heads), (v, "v", cache.heads), (q, "q", None)):
             if x is None:
@@ -1120,6 +1120,7 @@ def cache_read(cache: "KVCache", page_table, lengths, starts, tokens: int, out_d
             return done
     with _place(stream, cache.codes):
         codes = cache.codes
+        _refuse_grad(cache.scales, *(out or ()))
         d = _cache_desc(cache, page_table, lengths, starts, tokens, codes)
         dtype = _torch().bfloat16 if out_dtype is None else out_dtype
         if out is not None:
@@ -1147,7 +1148,7 @@ def cache_attention(cache: "KVCache", q, page_table, lengths, starts=None, *, sc
             return done
     with _place(stream, q):
         torch = _torch()
-        _refuse_grad(q, out)
+        _refuse_grad(q, cache.scales, out)
         _heads_of(q, "q")
         if q.dtype != torch.bfloat16:
             raise TypeError("q must be bfloat16")

@@ -1,4 +1,6 @@
 """What the attention operators accept and refuse at the ends of their arguments, shown without a GPU."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -32,3 +34,27 @@ def test_rotary_tables_that_leave_the_range(iq):  # noqa: F811
     for args in ((64, 1e300), (64, 1e-3), (64, 1e308, "base", 1e300), (64, 1e4, "linear", 1e300), (64, 1e4, "parts", 1e3, 1e-300)):
         table = iq.rotary_table(*args, device="cpu")
         assert torch.isfinite(table).all() and table[0] > 0 and (table >= 0).all()
+
+
+# ---- the binding ------------------------------------------------------------------------------
+def operands():
+    bf, i32 = torch.bfloat16, torch.int32
+    return SimpleNamespace(x=torch.zeros(4, 2, 64, dtype=bf), q=torch.zeros(4, 6, 64, dtype=bf), at=torch.zeros(4, dtype=i32),
+                           turns=torch.zeros(16, dtype=torch.float64), pages=torch.zeros(4, 3, dtype=i32), lengths=torch.ones(4, dtype=i32),
+                           starts=torch.zeros(5, dtype=i32))
+
+
+def test_tables_scales_and_results_that_require_gradients(iq):  # noqa: F811
+    """No graph is recorded for any operand, the table of a rotation, a cache's scales and given results among them."""
+    o, cache = operands(), iq.make_cache(6, 2, 64, device="cpu")
+    asks = iq.KVCache(cache.codes, cache.scales.zero_().clone().requires_grad_(), "e4m3", 2, 64, 64)
+    turns, leaf = o.turns.clone().requires_grad_(), o.x.clone().requires_grad_()
+    where = (o.pages, o.lengths, o.starts)
+    for call in (lambda: iq.rotary(o.x, o.at, turns), lambda: iq.rotary_backward(o.x, o.at, turns), lambda: iq.rotary(o.x, o.at, o.turns, out=leaf),
+                 lambda: iq.cache_append(cache, o.x, o.x, *where, q=o.q, rotary=turns), lambda: iq.cache_append(asks, o.x, o.x, *where),
+                 lambda: iq.cache_attention(asks, o.q, *where), lambda: iq.cache_read(asks, *where, 4),
+                 lambda: iq.cache_read(cache, *where, 4, out=(o.x.clone(), leaf))):
+        with pytest.raises(RuntimeError, match="no gradient passes"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="not on a GPU"):
+            call()
