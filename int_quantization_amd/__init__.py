@@ -1111,7 +1111,8 @@ def cache_append(cache: "KVCache", k, v, page_table, lengths, starts=None, *, q=
 def cache_read(cache: "KVCache", page_table, lengths, starts, tokens: int, out_dtype=None, *, out=None, stream=None):
     """Keys and values [tokens, heads, dim] (bfloat16 by default, or float32) of
     the last starts[b + 1] - starts[b] tokens of every sequence, at rows
-    starts[b] on (starts None: the last token of each); `out` a pair of tensors."""
+    starts[b] on (starts None: the last token of each); `out` a pair of tensors,
+    either of which may be None."""
     f32 = _packed_f32(out_dtype)
     if out is None and stream is None and f32 is not None and cache.fmt in CACHE_FORMATS:
         done = (_fast_calls or _bind_fast()).cache_read(cache.codes, cache.scales, CACHE_FORMATS[cache.fmt], cache.heads, cache.dim, cache.page,
@@ -1124,7 +1125,7 @@ def cache_read(cache: "KVCache", page_table, lengths, starts, tokens: int, out_d
         d = _cache_desc(cache, page_table, lengths, starts, tokens, codes)
         dtype = _torch().bfloat16 if out_dtype is None else out_dtype
         if out is not None:
-            dtype = out[0].dtype
+            dtype = next((o.dtype for o in out if o is not None), dtype)
         shape = (tokens, cache.heads, cache.dim)
         k, v = (_result(None if out is None else o, shape, dtype, codes, what) for o, what in zip(out or (None, None), ("out[0]", "out[1]")))
         _check(iq_cache_read(d, codes.data_ptr(), cache.scales.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), _ptr(starts), tokens,

@@ -58,3 +58,13 @@ def test_tables_scales_and_results_that_require_gradients(iq):  # noqa: F811
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="not on a GPU"):
             call()
+
+
+def test_one_given_result_of_a_read(iq):  # noqa: F811
+    """Either result of a read may be given alone; both are of its type."""
+    o, cache = operands(), iq.make_cache(6, 2, 64, device="cpu")
+    for out in ((o.x.clone(), None), (None, o.x.clone()), (None, o.x.float()), (None, None)):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            iq.cache_read(cache, o.pages, o.lengths, o.starts, 4, out=out)
+    with pytest.raises(TypeError):
+        iq.cache_read(cache, o.pages, o.lengths, o.starts, 4, out=(o.x.float(), o.x.clone()))
