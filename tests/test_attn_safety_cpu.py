@@ -1,9 +1,12 @@
 """What the attention operators accept and refuse at the ends of their arguments, shown without a GPU."""
+import os
+import subprocess
 from types import SimpleNamespace
 
 import pytest
 import torch
 
+from conftest import ROOT
 from test_attn_cpu import FAKE, attention_desc, cache_desc, iq, rotary_desc  # noqa: F401
 
 
@@ -68,3 +71,13 @@ def test_one_given_result_of_a_read(iq):  # noqa: F811
             iq.cache_read(cache, o.pages, o.lengths, o.starts, 4, out=out)
     with pytest.raises(TypeError):
         iq.cache_read(cache, o.pages, o.lengths, o.starts, 4, out=(o.x.float(), o.x.clone()))
+
+
+def test_shares_stay_in_range(tmp_path):
+    """What columns see, rows, shares and their places in the workspace, by the kernels' own functions, under any lengths and starts."""
+    exe = tmp_path / "check"
+    subprocess.run(["/opt/rocm/bin/hipcc", "-O1", "-Xarch_host", "-fsanitize=undefined", "-std=c++17", "--offload-arch=gfx950", "-x", "hip",
+                    os.path.join(ROOT, "tests", "attend_index_check.cpp"), "-I", os.path.join(ROOT, "include"), "-o", str(exe)], check=True,
+                   capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok" and not r.stderr, r.stdout + r.stderr

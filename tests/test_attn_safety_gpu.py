@@ -66,9 +66,9 @@ def answer(q, codes, scales, there, first, length, scale, causal, window):
     return o, e
 
 
-def check(iq, cache, q, table, lengths, starts, *, causal=True, window=0, scale=None, rows=None, what="", **kw):  # noqa: F811
-    """Runs cache_attention and holds its rows (those where `rows` is true) to `answer`."""
-    got = iq.cache_attention(cache, q, table, lengths, starts, causal=causal, window=window, scale=scale, **kw)
+def check(iq, cache, q, table, lengths, starts, *, causal=True, window=0, scale=None, rows=None, got=None, what="", **kw):  # noqa: F811
+    """Runs cache_attention (unless its result is given) and holds its rows (those where `rows` is true) to `answer`."""
+    got = got if got is not None else iq.cache_attention(cache, q, table, lengths, starts, causal=causal, window=window, scale=scale, **kw)
     model, scale = model_of(cache), cache.dim ** -0.5 if scale is None else scale
     for b, length in enumerate(lengths.tolist()):
         lo, hi = (int(starts[b]), int(starts[b + 1])) if starts is not None else (b, b + 1)
@@ -233,3 +233,43 @@ def test_strides_of_single_tokens_and_heads(iq):  # noqa: F811
     want = iq.rotary(x, at, turns)
     y = x.clone()
     assert torch.equal(iq.rotary(y, at, turns, out=torch.as_strided(y, (1, 3, 64), (2051, 64, 1))), want) and torch.equal(y, want)
+
+
+# ---- arrays of any content ------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_starts_and_lengths_of_any_content(iq, fmt):  # noqa: F811
+    """Starts that descend, are negative or point behind the rows, lengths past the table: nothing outside the operands changes,
+    and sequences whose entries are sound beside others answer as alone."""
+    g, heads, dim, n, guard = gen(80), 2, 64, 90, 64
+    odd = [-(1 << 31), (1 << 31) - 1, -1, 0, 40, 91, 1 << 30]
+    for width in (3, 300):
+        cache = iq.make_cache(40, heads, dim, fmt, 32)
+        ao.fill(cache, 6)
+        table = torch.full((5, width), -1, dtype=I32, device="cuda")
+        table[:, :3] = torch.randperm(36, generator=torch.Generator().manual_seed(2))[:15].view(5, 3).to(I32)
+        for k in range(len(odd)):
+            print("case", width, k, flush=True)
+            # sequence 0 has rows 0 to 29; the others' starts are anything
+            starts = torch.tensor([0, 30] + [odd[(k + 3 * i) % len(odd)] for i in range(4)], dtype=torch.int64).to(I32).cuda()
+            lengths = torch.tensor([77] + [odd[(2 * k + i) % len(odd)] for i in range(4)], dtype=torch.int64).to(I32).cuda()
+            q, k_, v = rand(g, n, 8, dim), rand(g, n, heads, dim), rand(g, n, heads, dim)
+            around = torch.full((2 * guard + n, 8, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+            out = around[guard:guard + n]
+            before = model_of(cache)
+            iq.cache_attention(cache, q, table, lengths, starts, out=out)
+            assert (around[:guard] == 7).all() and (around[guard + n:] == 7).all()
+            if not any(int(starts[i]) < 30 and int(starts[i + 1]) > int(starts[i]) for i in range(1, 5)):
+                check(iq, cache, q[:30], table[:1], lengths[:1], starts[:2], got=out[:30], what=f"{k}")
+            keys = torch.full((2 * guard + n, heads, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+            values = keys.clone()
+            iq.cache_read(cache, table, lengths, starts, n, out=(keys[guard:guard + n], values[guard:guard + n]))
+            for t in (keys, values):
+                assert (t[:guard] == 7).all() and (t[guard + n:] == 7).all()
+            after = model_of(cache)
+            assert torch.equal(before.codes, after.codes) and torch.equal(before.scales, after.scales)
+            iq.cache_append(cache, k_, v, table, lengths, starts, q=q)
+            free = torch.ones(40, dtype=torch.bool)
+            free[table[:, :3].cpu().long().flatten()] = False
+            after = model_of(cache)
+            assert torch.equal(before.codes[free], after.codes[free]) and torch.equal(before.scales[free], after.scales[free])
+            ao.fill(cache, 6)
