@@ -8,7 +8,7 @@ import torch
 
 import attn_oracle as ao
 from attn_oracle import TINY, U
-from test_attn_gpu import FORMATS, I32, gen, iq, model_of, rand, scene  # noqa: F401
+from test_attn_gpu import FORMATS, I32, ends, gen, iq, model_of, rand, same_memory, scene, tables  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -273,3 +273,88 @@ def test_starts_and_lengths_of_any_content(iq, fmt):  # noqa: F811
             after = model_of(cache)
             assert torch.equal(before.codes[free], after.codes[free]) and torch.equal(before.scales[free], after.scales[free])
             ao.fill(cache, 6)
+
+
+# ---- far offsets, calls at once, calls again -----------------------------------------------------------
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_cache_past_32_bits(iq, fmt):  # noqa: F811
+    """Pages that lie 5 GB into the memory, with scales to match: the bits of a small cache."""
+    heads, dim, page = 8, 128, 256
+    pages = 5 * 2 ** 30 // (heads * page * 2 * dim) + 40
+    g, had, new = gen(90), [700, 0, 90], [1, 300, 20]
+    total = [a + b for a, b in zip(had, new)]
+    whole = lambda t: torch.tensor(t, dtype=I32, device="cuda")  # noqa: E731
+    small, large = iq.make_cache(9, heads, dim, fmt, page), iq.make_cache(pages, heads, dim, fmt, page)
+    assert large.codes.numel() > 5 * 2 ** 30
+    near = whole([[0, 1, 2, -1], [3, 4, -1, -1], [5, -1, -1, -1]])
+    far = torch.where(near >= 0, pages - 9 + near, near)
+    n = sum(total)
+    k, v, q = rand(g, n, heads, dim), rand(g, n, heads, dim), rand(g, sum(new), 32, dim)
+    every, starts = whole([0, total[0], total[0] + total[1], n]), whole([0, 1, 301, 321])
+    turns, outs = iq.rotary_table(dim), []
+    for cache, table in ((small, near), (large, far)):
+        cache.codes.zero_()                                         # what no token writes is compared too
+        cache.scales.zero_()
+        iq.cache_append(cache, k, v, table, whole(total), every, rotary=turns)
+        outs.append([iq.cache_attention(cache, q, table, whole(total), starts), iq.cache_attention(cache, q[:3], table, whole(total)),
+                     *iq.cache_read(cache, table, whole(total), every, n)])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    assert torch.equal(small.codes[:6], large.codes[pages - 9:pages - 3]) and torch.equal(small.scales[:6], large.scales[pages - 9:pages - 3])
+
+
+def test_strides_past_32_bits(iq):  # noqa: F811
+    """Rows 2^31 elements apart."""
+    g, far = gen(91), (1 << 31) + 8
+    at, turns = torch.tensor([5, 70000], dtype=I32, device="cuda"), iq.rotary_table(64)
+    memory = torch.empty(far + 4 * 64, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(memory, (2, 4, 64), (far, 64, 1))
+    x.copy_(rand(g, 2, 4, 64))
+    near = x.contiguous()
+    want = iq.rotary(near, at, turns)
+    assert torch.equal(iq.rotary(x, at, turns), want)
+    cache, _, table, lengths, starts = scene(iq, "e4m3", 2, 2, 64, 32, [40, 90], [1, 1], 3)
+    assert torch.equal(iq.cache_attention(cache, x, table, lengths), iq.cache_attention(cache, near, table, lengths))
+    before = model_of(cache)
+    q = iq.cache_append(cache, x[:, :2], x[:, 2:], table, lengths, q=x, rotary=turns)
+    after = model_of(cache)
+    cache.codes.copy_(before.codes)
+    cache.scales.copy_(before.scales)
+    assert torch.equal(iq.cache_append(cache, near[:, :2], near[:, 2:], table, lengths, q=near, rotary=turns), q)
+    same_memory(cache, after)
+    assert iq.rotary(x, at, turns, out=x) is x and torch.equal(x.contiguous(), want)
+
+
+def test_calls_at_once(iq):  # noqa: F811
+    """Two streams in one cache: attention of some sequences while others are appended to, again and again."""
+    cache, q, table, lengths, starts = scene(iq, "int8", 2, 4, 128, 32, [3000, 200, 10, 64], [1, 130, 1, 40], 12)
+    k, v, turns = rand(gen(1), 172, 2, 128), rand(gen(2), 172, 2, 128), iq.rotary_table(128)
+    mine, yours = slice(0, 2), slice(2, 4)
+    first, rest = starts[:3].clone(), starts[2:] - starts[2]
+    want = iq.cache_attention(cache, q[:131], table[mine], lengths[mine], first)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for _ in range(30):
+        iq.cache_append(cache, k[131:], v[131:], table[yours], lengths[yours], rest, rotary=turns, stream=streams[0])
+        outs.append(iq.cache_attention(cache, q[:131], table[mine], lengths[mine], first, stream=streams[1]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    # appended thirty times over, the sequences hold what one append leaves
+    again = model_of(cache)
+    iq.cache_append(cache, k[131:], v[131:], table[yours], lengths[yours], rest, rotary=turns)
+    same_memory(cache, again)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_append_repeats_its_bits(iq, fmt):  # noqa: F811
+    g, had, new = gen(93), [5, 64, 0], [70, 3, 400]
+    total = [a + b for a, b in zip(had, new)]
+    table, pages = tables(total, 64, 1)
+    k, v, q = (rand(g, sum(new), h, 96) for h in (3, 3, 6))
+    turns, seen = iq.rotary_table(40), []
+    for _ in range(4):
+        cache = iq.make_cache(pages, 3, 96, fmt, 64)
+        ao.fill(cache, 1)
+        out = iq.cache_append(cache, k, v, table, torch.tensor(total, dtype=I32, device="cuda"), ends(new), q=q, rotary=turns)
+        seen.append((out, cache.codes, cache.scales))
+    assert all(torch.equal(a, b) for s in seen[1:] for a, b in zip(seen[0], s))
