@@ -579,8 +579,8 @@ typedef struct {
  * lose nothing by it above E4M3's subnormal range; INT8 codes are off by less than
  * one new step however often it happens).  A scale of 0, all elements being 0, counts
  * as none.  The cache holds finite values only: NaN is stored as 0, an infinity as the largest
- * code of its sign.  Codes of tokens that are not the sequence's are left as they were.
- * Sequences of one call must not share the pages that they append to; pages shared and only
+ * code of its sign (0 in a block whose scale is 0).  Codes of tokens that are not the sequence's are left as they were.
+ * The pages that one call appends to must be distinct, within a sequence and among sequences; pages shared and only
  * read are fine.  (tokens / 32 + 2 batch) * heads * 2 + tokens up to 2^23 (IQ_EUNSUPPORTED).
  */
 iq_status iq_cache_append(const iq_cache_desc* d, const iq_append_desc* a, const void* k, const void* v,
@@ -618,15 +618,20 @@ typedef struct {
  *   q   [tokens, q_heads, dim] BF16, 16-byte aligned, strides multiples of 8 elements (IQ_EALIGN)
  *   o   dense [tokens, q_heads, dim] BF16, 16-byte aligned; may be q where that is dense, otherwise they must not
  *       overlap.  A query that sees nothing gets zeros
- *   workspace  iq_cache_attention_workspace_bytes(d, a) bytes, 256-byte aligned, of any content
+ *   workspace  iq_cache_attention_workspace_bytes(d, a) bytes, 256-byte aligned, of any content: up to 120 MB, as
+ *       the GPU and not the call has it, where a sequence may have more than 64 pairs of a token and a query head for a key head
+ * Which kernels run goes by shapes, the page table's width among them, since lengths are read on the GPU: results change by
+ * roundings with it, and a table much wider than its sequences makes short calls slower (one token at 500 tokens 6.9 us,
+ * and 12.9 with a table for 131072).
  * Codes enter the matrix cores exactly, as FP16, and so do queries, scaled by a power of
  * two for each row (elements below 2^-28 of their row's largest lose digits); probabilities times
- * their block's values scale are rounded to FP16 (half a step: 2^-11; of those below 2^-23 of the largest such product that the
- * query has seen 2^-34 of that); sums, maxima and the running output are FP32, and probabilities below 2^-126 may count as 0.
- * Tokens that a query does
- * not see add nothing, whatever their codes and scales hold; a NaN or an infinity in a query makes that
- * query's output NaN where it sees anything.  Scores times log2(e) have to lie in FP32's range.  Scales are expected to be finite and >= 0; NaN codes of E4M3 (which iq_cache_append never writes)
- * in tokens that a sequence holds may make any of that sequence's outputs of their head NaN.
+ * their block's values scale are rounded to FP16 (half a step: 2^-11; of those below 2^-23 of the
+ * largest such product that the query has seen 2^-34 of that); sums, maxima and the running output
+ * are FP32, and probabilities below 2^-126 may count as 0.  Scores times log2(e) have to lie in FP32's range.
+ * Tokens that a query does not see add nothing, whatever their codes and scales hold, but for NaN
+ * codes of E4M3 (which iq_cache_append never writes) in tokens that the sequence holds: they may make
+ * any of that sequence's outputs of their head NaN.  Scales of seen tokens have to be finite and >= 0.  A
+ * NaN or an infinity in a query makes that query's output NaN where it sees anything.
  * The order of all sums is fixed by shapes, lengths and starts: calls repeat their bits.
  * tokens * q_heads up to 2^28 (IQ_EUNSUPPORTED).
  */

@@ -149,7 +149,8 @@ inline int few_columns(const AttendArgs& a) {
     return columns <= 16 ? 16 : 32;
 }
 
-// A row of this many blocks is not worth sharing: its workgroup takes it whole, without a search for its share and
+// A row of this many blocks is not worth sharing (blocks that the table has entries for, since the host does not know the
+// lengths: one token at 500 tokens takes 6.9 us, 12.9 with a table for 131072): its workgroup takes it whole, without a search for its share and
 // without the join's launch.  One sequence of 2000 tokens takes 14.4 us, 17.6 shared; of 4000 tokens 23.0 and 18.2.  Where
 // rows fill half the CUs twice as many blocks are not worth it: 16 sequences of 4000 tokens 26.8 and 34.0, 64 of 100 to 4000 tokens 62
 // and 78, but 4 of 4000 24.1 and 21.9.  kDirectRows bounds the launch where most sequences have no tokens.
@@ -173,7 +174,9 @@ inline Plans plans_of(const AttendArgs& a) {
     const int64_t rows = (int64_t)a.c.tokens * a.group;
     int64_t at = 0;
     const auto room = [&](int64_t bytes) { const int64_t here = at; at += (bytes + 255) / 256 * 256; return here; };
-    // which kernels some sequence may be for; of one sequence the host knows nothing better than that it has all rows
+    // Which kernels some sequence may be for; of one sequence the host knows nothing better than that it has all rows.  Without
+    // starts all is k_few's, whatever the group: 128 heads on each of 1 key head, 8 sequences of 4000 tokens 33 us and 39 in
+    // k_many, of 32000 50 and 56; on each of 8 key heads 67 and 74, but of 32000 tokens 322 and 211.
     const int limit = few_limit(a);
     const bool many = a.c.starts && rows > limit, few = !many || a.c.batch > 1;
     p.few.few = p.many.few = limit;

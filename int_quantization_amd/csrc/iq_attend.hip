@@ -198,7 +198,7 @@ template <int D, int C> __device__ __forceinline__ float load_query(float scale,
         }
 #pragma unroll
     for (int d = C; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-    // a query that is not finite answers NaN, whatever it sees: all its elements are
+    // a query that is not finite answers NaN where it sees anything: all its elements are
     const uint32_t bad = top >= 0x7F800000u ? 0xFFFFFFFFu : 0u;
     int e = (int)(top >> 23);                          // 0 for zeros and subnormals, 255 for infinities and NaN
     e = e == 255 ? 0 : max(e, 1) - 127 - 14;
@@ -246,7 +246,7 @@ template <int D, int C> struct State {
         const float past = top - m;
         return __any(past > kSlack || past + scale_v > z + kSlack);
     }
-    // Brings both up to the block's, and takes the maximum off its scores if it is far.  Rare.
+    // Brings both up to the block's.  Rare.
     __device__ __forceinline__ void catch_up(float top, float scale_v) {
         top = S::over_groups(top, false);
         const float now = fmaxf(m, top), fall = now == m ? 0.f : m - now, was = z + fall;
@@ -658,11 +658,12 @@ template <int D, int C> __global__ __launch_bounds__(kThreads) void k_join(Atten
 // ---- many columns: the work is products ----------------------------------------------------
 // A workgroup takes 128 columns, 32 to a wave.  Its waves turn a block's codes
 // into FP16 once, in LDS and in the order in which the matrix cores take them; two blocks are there, one read, one made.
-// The issue of instructions bounds it: for a block of 32 tokens a wave of 128 elements has 16 products (512 cycles) and
-// about 600 cycles of vector work (conversion, maxima, exponentials, rounding), and two waves of a SIMD overlap them to
-// about 1200 cycles for both kinds of both.  A prompt of 8192 tokens (32 heads of 128 on 8; 550 GFLOP) takes 585 to 690 us, 0.80 to
-// 0.94 PFLOP/s, and 20 for the join.  Priority for the wave in its products gains 5%; rows in the order of `row_at` 12%;
-// 64 columns a wave cost their output registers' copies (1506 us), three LDS buffers 690 to 723 against 698.
+// The issue of instructions bounds it: for a block of 32 tokens a wave of 128 elements has 16 products (512 cycles of a
+// SIMD's matrix core) and about 125 vector instructions beside them (570 cycles: conversion, maxima, exponentials,
+// rounding), and takes 1240 cycles.  So the matrix cores are busy 41% of the time and the vector units 45%: the two waves of a SIMD
+// hardly overlap one's products with the other's vector work.  A prompt of 8192 tokens (32 heads of 128 on 8; 550 GFLOP)
+// takes 590 to 650 us from card to card, 0.85 to 0.93 PFLOP/s, and 20 for the join.  Priority for the wave in its products gains 5%; rows
+// in the order of `row_at` 12%; 64 columns a wave cost their output registers' copies (1506 us), three LDS buffers 690 to 723 against 698.
 template <int D, int FMT> __global__ __launch_bounds__(kThreads, many_waves(D)) void k_many(AttendArgs a, Plan plan) {
     using S = Shape<D, 32>;
     constexpr int C = kManyColumns, J = D / 32, F = D / 16, N = (J + kWaves - 1) / kWaves;

@@ -166,8 +166,9 @@ __device__ __forceinline__ uint32_t bytes_between(int t, int lo, int hi) {
 // largest magnitude is found, and codes are written, so x is read once.  Values change places through LDS, where a row of
 // 32 codes has 36 bytes so that rows meet in fewer banks.  Queries are turned in the same launch, a workgroup to a token.
 //   VEC: rows that start on 16 bytes, rot a multiple of 16.
-// The bytes of q, k, v and the codes bound it: 8192 tokens of 32 + 2 * 8 heads of 128 (184 MB)
-// take 42 us, 4.4 TB/s; one token of them takes 5.4 us, the launch and a chain of four loads.
+// 8192 tokens of 32 + 2 * 8 heads of 128 (184 MB) take 42 us, 4.4 TB/s where a copy reaches 6.1: the vector units are busy 63%
+// of the time (a division for each element, conversions, addresses), LDS 28%, most of it conflicts of the values' byte
+// stores.  One token of them takes 5.4 us, the launch and a chain of four loads.
 constexpr int kPitch = 36;
 
 template <typename T, int FMT, bool VEC, int NI> __global__ __launch_bounds__(kThreads, 4) void k_append(AppendArgs a, int64_t slots, int per, bool vec_q) {
@@ -348,8 +349,9 @@ template <typename T, int FMT, bool VEC, int NI> __global__ __launch_bounds__(kT
 }
 
 // ---- read -------------------------------------------------------------------------
-// Keys and values of a block back to rows, 16 elements of a token to a thread; values change places in LDS.  Bytes bound
-// it: 8192 tokens of 8 heads of 128 to BF16 (50 MB, much of it from the last-level cache) take 11 us.
+// Keys and values of a block back to rows, 16 elements of a token to a thread; values change places in LDS.  8192 tokens of
+// 8 heads of 128 to BF16 (50 MB, much of it from the last-level cache) take 11 us, 8 at a copy's rate: a short launch's beginning
+// and end, for the CUs hold waves 44% of that time.
 template <typename T, int FMT> __global__ __launch_bounds__(kThreads) void k_read(ReadArgs a) {
     __shared__ __align__(16) uint8_t turned[256 * kPitch];
     const CacheArgs& c = a.c;

@@ -72,6 +72,8 @@ def check(iq, cache, q, table, lengths, starts, *, causal=True, window=0, scale=
     model, scale = model_of(cache), cache.dim ** -0.5 if scale is None else scale
     for b, length in enumerate(lengths.tolist()):
         lo, hi = (int(starts[b]), int(starts[b + 1])) if starts is not None else (b, b + 1)
+        if lo >= hi or length <= 0:
+            continue
         codes, scales, there = parts_of(model, table[b].tolist(), min(length, table.shape[1] * cache.page))
         o, e = answer(q[lo:hi].cpu(), codes, scales, there, length - (hi - lo), length, scale, causal, window)
         keep = slice(None) if rows is None else rows[lo:hi].cpu()
